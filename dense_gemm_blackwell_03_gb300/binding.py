@@ -13,6 +13,14 @@ import threading
 
 BF16 = 0
 FP16 = 1
+FP32 = 2
+
+E4M3 = 0
+E5M2 = 1
+
+BLOCK = 128
+BLOCK_ROW = 0
+BLOCK_SQUARE = 1
 
 SCHEDULE_AUTO = 0
 SCHEDULE_TILES = 1
@@ -38,6 +46,7 @@ EXPORTED = [
     "bwgemm_status_string", "bwgemm_version", "bwgemm_run_splitk_noalloc",
     "bwgemm_plan_read_trace", "bwgemm_tune", "bwgemm_plan_tuned_count",
     "bwgemm_probe_tensor_rate", "bwgemm_noalloc_scratch", "bwgemm_bench_load_path",
+    "bwgemm_quantize", "bwgemm_run_scaled",
 ]
 
 # layouts of bwgemm_bench_load_path
@@ -121,6 +130,18 @@ class Config(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class Scaled(ctypes.Structure):
+    """``bwgemm_scaled_t``: 8-bit values and their scales."""
+    _fields_ = [
+        ("values", ctypes.c_void_p),
+        ("ld", ctypes.c_int64),
+        ("scales", ctypes.c_void_p),
+        ("ld_scales", ctypes.c_int64),
+        ("type", ctypes.c_int32),
+        ("block", ctypes.c_int32),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -196,6 +217,13 @@ def load_library(build_if_missing: bool = False):
                                                ctypes.POINTER(ctypes.c_double),
                                                ctypes.POINTER(ctypes.c_double)]
         lib.bwgemm_bench_load_path.restype = st
+        ci = ctypes.c_int
+        lib.bwgemm_quantize.argtypes = [vp, vp, ci, i64, i64, i64, ci, ci, i32, vp, i64, vp, i64, vp, i64, vp,
+                                        i64, vp]
+        lib.bwgemm_quantize.restype = st
+        lib.bwgemm_run_scaled.argtypes = [vp, ctypes.POINTER(Scaled), ctypes.POINTER(Scaled), vp, i64, i64, i64,
+                                          i64, ci, i32, vp]
+        lib.bwgemm_run_scaled.restype = st
         _lib = lib
         return lib
 
@@ -215,6 +243,8 @@ def make_options(**kw) -> PlanOptions:
 
 _torch_mod = None
 _dtype_codes: dict = {}
+_all_dtype_codes: dict = {}  # with fp32, for the calls that take it
+_fp8_codes: dict = {}
 
 
 def _torch():
@@ -224,6 +254,8 @@ def _torch():
         import torch
         _torch_mod = torch
         _dtype_codes.update({torch.bfloat16: BF16, torch.float16: FP16})
+        _all_dtype_codes.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
+        _fp8_codes.update({torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2})
     return _torch_mod
 
 
@@ -241,6 +273,32 @@ def _ld(t) -> int:
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError("operands must be K-major / row-major (unit stride along the last dim)")
     return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.shape[1]), 1)
+
+
+def _padded_empty(rows: int, cols: int, dtype, device, multiple: int):
+    """An uninitialised rows x cols matrix whose rows start `multiple` elements apart or more."""
+    ld = -(-cols // multiple) * multiple
+    t = _torch().empty((rows, ld), dtype=dtype, device=device)
+    return t[:, :cols] if ld != cols else t
+
+
+def _scaled(values, scales, name: str) -> Scaled:
+    """The descriptor of 8-bit `values` (R x K) with `scales` ((K blocks) x (R or row blocks))."""
+    code = _fp8_codes.get(values.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float8_e4m3fn or float8_e5m2, got {values.dtype}")
+    if scales.dtype != _torch().float32:
+        raise TypeError(f"the scales of {name} must be float32, got {scales.dtype}")
+    rows, K = values.shape
+    ld = _ld(values)
+    if values.shape[0] == 1:
+        ld = -(-ld // 16) * 16  # a single row has no next one
+    kb, per = scales.shape
+    if kb != -(-K // BLOCK) or (per != rows and per != -(-rows // BLOCK)):
+        raise ValueError(f"the scales of {name} ({rows} x {K}) must be {-(-K // BLOCK)} x {rows} or "
+                         f"{-(-K // BLOCK)} x {-(-rows // BLOCK)}, got {tuple(scales.shape)}")
+    return Scaled(values.data_ptr(), ld, scales.data_ptr(), _ld(scales), code,
+                  BLOCK_ROW if per == rows else BLOCK_SQUARE)
 
 
 def select_config(num_sms: int, M: int, N: int, K: int, dtype: int = BF16, max_pairs: int = 0,
@@ -382,6 +440,91 @@ class Plan:
             raise BwgemmError(rc, "bwgemm_run_host")
         return out
 
+    def _check_tensor(self, name, t):
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} is on {t.device}, the plan on cuda:{self.device}")
+
+    def quantize(self, X, blocks: str = "row", transposed: bool = False, pow2: bool = False, dtype=None,
+                 stream=None):
+        """``bwgemm_quantize``: the 2-D CUDA tensor X (bf16, fp16 or fp32) in 8 bits
+        with one fp32 scale per 128 elements of a row (``blocks="row"``) or per
+        128 x 128 (``"square"``).
+
+        Returns ``(q, scales)``, and with `transposed` also ``(qt, scales_t)`` of
+        the transpose (its own blocks, along X's columns; with "square" the same
+        values).  `dtype`: torch.float8_e4m3fn (default) or torch.float8_e5m2;
+        `pow2` rounds the scales up to powers of two.  q's rows are padded to 16
+        bytes; scales are (column blocks) x rows, or x row blocks."""
+        torch = _torch()
+        dt = _all_dtype_codes.get(X.dtype)
+        if dt is None:
+            raise TypeError(f"quantize takes bfloat16, float16 or float32 tensors, got {X.dtype}")
+        if dtype is None:
+            dtype = torch.float8_e4m3fn
+        f8 = _fp8_codes.get(dtype)
+        if f8 is None:
+            raise TypeError(f"quantize makes float8_e4m3fn or float8_e5m2, got {dtype}")
+        if blocks not in ("row", "square"):
+            raise ValueError(f"blocks must be 'row' or 'square', got {blocks!r}")
+        self._check_tensor("X", X)
+        ldx = _ld(X)
+        rows, cols = X.shape
+        if rows == 1:
+            ldx = -(-ldx // 8) * 8  # a single row has no next one
+        square = blocks == "square"
+        kb, rb = -(-cols // BLOCK), -(-rows // BLOCK)
+        dev = X.device
+        q = _padded_empty(rows, cols, dtype, dev, 16)
+        s = torch.empty((kb, rb if square else rows), dtype=torch.float32, device=dev)
+        qt = st = None
+        args_t = (None, 0, None, 0)
+        if transposed:
+            qt = _padded_empty(cols, rows, dtype, dev, 16)
+            st = torch.empty((rb, kb if square else cols), dtype=torch.float32, device=dev)
+            args_t = (qt.data_ptr(), qt.stride(0), st.data_ptr(), st.stride(0))
+        h = (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+        rc = self.lib.bwgemm_quantize(self.handle, X.data_ptr(), dt, rows, cols, ldx,
+                                      BLOCK_SQUARE if square else BLOCK_ROW, f8, int(pow2), q.data_ptr(),
+                                      q.stride(0), s.data_ptr(), s.stride(0), *args_t, h)
+        if rc != 0:
+            raise BwgemmError(rc, "bwgemm_quantize")
+        return (q, s, qt, st) if transposed else (q, s)
+
+    def gemm_scaled(self, A, scale_a, B, scale_b, out=None, out_dtype=None, accumulate: bool = False, stream=None):
+        """``bwgemm_run_scaled``: ``out = A @ B.T`` of 8-bit CUDA tensors A (M x K) and
+        B (N x K) with their block scales, as `quantize` returns them.  `out_dtype`:
+        bf16 (default), fp16 or fp32; `accumulate` adds to an fp32 `out`."""
+        torch = _torch()
+        self._check_tensor("A", A)
+        self._check_tensor("B", B)
+        self._check_tensor("scale_a", scale_a)
+        self._check_tensor("scale_b", scale_b)
+        a = _scaled(A, scale_a, "A")
+        b = _scaled(B, scale_b, "B")
+        M, K = A.shape
+        N, Kb = B.shape
+        if Kb != K:
+            raise ValueError(f"K mismatch: A is {tuple(A.shape)}, B is {tuple(B.shape)}")
+        if out is None:
+            if accumulate:
+                raise ValueError("accumulate needs the out tensor to add to")
+            out = _padded_empty(M, N, out_dtype or torch.bfloat16, A.device, 8)
+        else:
+            self._check_tensor("out", out)
+            if tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
+                raise ValueError("out must be an M x N CUDA tensor of out_dtype")
+        dt = _all_dtype_codes.get(out.dtype)
+        if dt is None:
+            raise TypeError(f"gemm_scaled writes bfloat16, float16 or float32, got {out.dtype}")
+        ldc = _ld(out)
+        if M == 1:
+            ldc = -(-ldc // 8) * 8  # a single row has no next one
+        h = (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+        rc = self.lib.bwgemm_run_scaled(self.handle, a, b, out.data_ptr(), M, N, K, ldc, dt, int(accumulate), h)
+        if rc != 0:
+            raise BwgemmError(rc, "bwgemm_run_scaled")
+        return out
+
     def status(self, stream=None) -> int:
         """``bwgemm_get_status``: synchronises the stream, returns and clears the status."""
         return int(self.lib.bwgemm_get_status(self.handle, self._stream_handle(stream)))
@@ -448,3 +591,24 @@ def gemm(A, B, out=None, stream=None):
     if plan is None:
         plan = _plans[dev] = Plan(dev)
     return plan.gemm(A, B, out=out, stream=stream)
+
+
+def _default_plan(t) -> Plan:
+    """The cached default plan of a CUDA tensor's device."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("bwgemm takes CUDA tensors (it has no host path)")
+    plan = _plans.get(dev)
+    if plan is None:
+        plan = _plans[dev] = Plan(dev)
+    return plan
+
+
+def quantize(X, blocks="row", transposed=False, pow2=False, dtype=None, stream=None):
+    """`Plan.quantize` with a cached default plan per device."""
+    return _default_plan(X).quantize(X, blocks, transposed, pow2, dtype, stream)
+
+
+def gemm_scaled(A, scale_a, B, scale_b, out=None, out_dtype=None, accumulate=False, stream=None):
+    """`Plan.gemm_scaled` with a cached default plan per device."""
+    return _default_plan(A).gemm_scaled(A, scale_a, B, scale_b, out, out_dtype, accumulate, stream)

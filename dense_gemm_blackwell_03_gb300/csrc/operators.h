@@ -1,0 +1,93 @@
+// operators.h -- launch descriptions of the operators beside the 16-bit GEMM:
+// quantising to blocks of 128, the product of such matrices, and the
+// orthogonalisation.  Shared by their kernels' translation units and
+// operators.cpp, which checks the arguments and fills them in.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "../../include/bwgemm.h"
+
+namespace bwgemm {
+
+constexpr int kBlock = 128;  // elements of K, or rows, that share a scale
+
+// A block whose largest magnitude is below this is scaled as if it held it:
+// limit / amax then stays finite in fp32 and an all-zero block needs no case
+// of its own.
+constexpr float kSmallestAmax = 7.8886090522101181e-31f;  // 2^-100
+
+// ------------------------------------------------------------------ quantise
+struct QuantizeParams {
+    const void* x;       // rows x cols, ldx elements apart
+    int64_t ldx;
+    int64_t rows, cols;
+    uint8_t* q;          // rows x cols in 8 bits, ldq bytes apart
+    int64_t ldq;
+    float* s;            // [column block][row or row block], lds apart
+    int64_t lds;
+    uint8_t* qt;         // cols x rows in 8 bits (or null), ldqt bytes apart
+    int64_t ldqt;
+    float* st;           // [row block][column or column block], ldst apart
+    int64_t ldst;
+    int32_t pow2;        // 1: scales rounded up to powers of two
+};
+
+// fp8: 0 = e4m3, 1 = e5m2; square: one scale per 128 x 128 instead of 1 x 128.
+cudaError_t launch_quantize(int dtype, int fp8, bool square, const QuantizeParams& p, cudaStream_t stream, bool pdl);
+
+// ------------------------------------------------------------ scaled product
+// C[M x N] = sum over K blocks of sa * sb * (A block)(B block)^T.  The kernel
+// sees a lane-side operand (the MMA's M: one TMEM lane per row) and a
+// column-side operand (the MMA's N).  In order the lane side is A; swapped,
+// for few rows of A, it is B and the accumulator holds C transposed.
+struct ScaledParams {
+    int32_t lrows, crows, K;      // rows of the lane-side and column-side operands
+    int32_t num_kb;               // ceil(K / 128)
+    int32_t chunks;               // whole 128-element K chunks (0: no 3-D views)
+    int32_t num_l, num_c;         // blocks of lane rows and of columns
+    int32_t raster_group;         // lane blocks walked before stepping along the columns
+    int32_t dp_tiles, sk_tiles;   // tiles computed whole; tiles whose K iterations are spread over the workers
+    int64_t sk_iters;             // sk_tiles * num_kb
+    const float* ls;              // scale of lane row r, K block kb: ls[kb * ls_ld + (r >> ls_shift)]
+    int64_t ls_ld;
+    const float* cs;              // and of column c
+    int64_t cs_ld;
+    int32_t ls_shift, cs_shift;   // 0: a scale per row, 7: one per 128 rows
+    void* c;
+    int64_t ldc;
+    int32_t out_type;             // bwgemm_dtype_t of C
+    int32_t accumulate;           // 1: C += (fp32 only)
+    uint32_t idesc;
+    uint64_t timeout_ns;
+    uint32_t* status;
+    float* partials;              // fp32 partial tiles of stream-K pieces
+    uint32_t* counters;           // K blocks arrived per (tile, CTA, warp); zero between calls
+    int32_t stall_kblock;         // test hook, as in GemmParams
+};
+
+// Compiled forms: CTAs per MMA, columns per tile, operands swapped, and whether
+// the column side has a scale per column (the swapped forms always take one
+// per column and read one per 128 through it).
+struct ScaledVariant {
+    int cg, bn;
+    bool swap, colvec;
+};
+constexpr ScaledVariant kScaledVariants[] = {
+    {2, 256, false, false}, {2, 256, false, true}, {2, 128, false, false}, {2, 128, false, true},
+    {1, 128, true, true},   {1, 64, true, true},   {1, 32, true, true},    {1, 16, true, true},
+};
+constexpr int kNumScaledVariants = int(sizeof(kScaledVariants) / sizeof(kScaledVariants[0]));
+constexpr int kScaledKps = 2;  // K blocks per ring stage and TMA copy
+
+// l / c: the operands in boxes of 128 bytes x (128 | bn / cg) rows; l3 / c3:
+// their 3-D views of kScaledKps K blocks; out: C in 64-byte x 32-row boxes
+// (operands in order only).
+cudaError_t launch_scaled(int idx, const CUtensorMap& l, const CUtensorMap& c, const CUtensorMap& l3,
+                          const CUtensorMap& c3, const CUtensorMap& out, const ScaledParams& p, int grid,
+                          cudaStream_t stream, bool pdl);
+
+}  // namespace bwgemm

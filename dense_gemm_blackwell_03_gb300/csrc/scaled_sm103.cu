@@ -1,0 +1,74 @@
+// scaled_sm103.cu -- instantiates and launches the block-scaled 8-bit product
+// (scaled_kernel.cuh).
+#include "scaled_kernel.cuh"
+
+namespace bwgemm {
+namespace {
+
+template <int CG, int BN, bool SWAP, bool COLVEC>
+cudaError_t launch_sc(const CUtensorMap& l, const CUtensorMap& c, const CUtensorMap& l3, const CUtensorMap& c3,
+                      const CUtensorMap& out, const ScaledParams& p, int grid, cudaStream_t stream, bool pdl)
+{
+    using Cfg = ScaledConfig<CG, BN, SWAP, COLVEC>;
+    auto kernel = scaled_kernel<CG, BN, SWAP, COLVEC>;
+    if (grid % CG != 0)
+        return cudaErrorInvalidValue;
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+    if (err != cudaSuccess)
+        return err;
+    if (Cfg::kSplitRegs) {
+        // the warpgroups' shares must fit what the block is launched with: a
+        // share that does not would wait for registers for ever
+        static const int regs = [&] {
+            cudaFuncAttributes a;
+            return cudaFuncGetAttributes(&a, kernel) == cudaSuccess ? a.numRegs : 0;
+        }();
+        if (regs * Cfg::kThreads < 128 * Cfg::kRegsFirst + 32 * Cfg::kEpiWarps * Cfg::kRegsEpi ||
+            regs < Cfg::kRegsFirst || regs > Cfg::kRegsEpi)
+            return cudaErrorLaunchOutOfResources;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid), 1, 1);
+    cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (CG == 2) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = 2;
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kernel, l, c, l3, c3, out, p);
+}
+
+}  // namespace
+
+cudaError_t launch_scaled(int idx, const CUtensorMap& l, const CUtensorMap& c, const CUtensorMap& l3,
+                          const CUtensorMap& c3, const CUtensorMap& out, const ScaledParams& p, int grid,
+                          cudaStream_t stream, bool pdl)
+{
+    static_assert(kNumScaledVariants == 8, "one case per variant below, in the order of kScaledVariants");
+    switch (idx) {
+    case 0: return launch_sc<2, 256, false, false>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 1: return launch_sc<2, 256, false, true>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 2: return launch_sc<2, 128, false, false>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 3: return launch_sc<2, 128, false, true>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 4: return launch_sc<1, 128, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 5: return launch_sc<1, 64, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 6: return launch_sc<1, 32, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 7: return launch_sc<1, 16, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace bwgemm

@@ -48,7 +48,8 @@ typedef struct bwgemm_plan_s* bwgemm_plan_t;
 
 typedef enum {
     BWGEMM_BF16 = 0, /* bfloat16 inputs and output */
-    BWGEMM_FP16 = 1  /* IEEE binary16 inputs and output */
+    BWGEMM_FP16 = 1, /* IEEE binary16 inputs and output */
+    BWGEMM_FP32 = 2  /* binary32: only where a call says so (not the 16-bit product) */
 } bwgemm_dtype_t;
 
 typedef enum {
@@ -421,6 +422,80 @@ bwgemm_status_t bwgemm_run_splitk_noalloc(const void* A, const void* B, void* C,
 bwgemm_status_t bwgemm_noalloc_scratch(int32_t num_sms, int32_t max_pairs, int64_t M, int64_t N,
                                        int64_t K, int32_t split_k, uint64_t* partial_bytes,
                                        uint64_t* counter_bytes);
+
+/* ------------------------------------------------------------------------
+ * 8-bit matrices with a scale per block of 128, their product, and the
+ * orthogonalisation of an update: what a linear layer needs beside
+ * bwgemm_run to be trained and served in 8 bits.
+ *
+ * Such a matrix is a pair (values, scales).  Values: R x K in 8-bit floating
+ * point, row-major, rows `ld` bytes apart.  Scales: fp32, K blocks outermost:
+ * scales[kb * ld_scales + r] weights the elements kb * 128 .. kb * 128 + 127 of
+ * row r (BWGEMM_BLOCK_ROW), scales[kb * ld_scales + r / 128] those of 128 rows
+ * (BWGEMM_BLOCK_SQUARE).  Any fp32 scales are taken, powers of two or not.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+    BWGEMM_E4M3 = 0, /* 4 exponent, 3 mantissa bits; largest 448, no infinities */
+    BWGEMM_E5M2 = 1  /* 5 exponent, 2 mantissa bits; largest 57344              */
+} bwgemm_fp8_t;
+
+typedef enum {
+    BWGEMM_BLOCK_ROW = 0,   /* a scale per row and 128 elements of K  */
+    BWGEMM_BLOCK_SQUARE = 1 /* a scale per 128 rows and 128 elements  */
+} bwgemm_block_t;
+
+typedef struct {
+    const void* values;  /* 8-bit values, 16-byte aligned                          */
+    int64_t ld;          /* bytes between rows, a multiple of 16                   */
+    const float* scales; /* fp32 scales, 4-byte aligned                            */
+    int64_t ld_scales;   /* elements between K blocks (>= rows, or row blocks)     */
+    int32_t type;        /* bwgemm_fp8_t                                           */
+    int32_t block;       /* bwgemm_block_t                                         */
+} bwgemm_scaled_t;
+
+/*
+ * Quantise X (rows x cols, bf16, fp16 or fp32, row stride ldx elements) in
+ * blocks of 128.  For every block with largest magnitude a >= 2^-100 (smaller
+ * ones count as 2^-100): scale = a / limit (limit = 448 or 57344), value =
+ * round_to_nearest_even(x * (limit / a)); with pow2 != 0 the scale is the next
+ * power of two >= a / limit and value = round(x / scale).  All in fp32.  A NaN
+ * makes every value of its block NaN.
+ *
+ *   q, scales    : X itself (rows x cols), blocks along its rows (or 128 x 128)
+ *   qt, scales_t : the transpose (cols x rows), blocks along X's columns --
+ *                  what a product over rows contracts; with
+ *                  BWGEMM_BLOCK_SQUARE the same values and scales transposed.
+ *                  Both NULL: not wanted.  One read of X serves both.
+ *
+ * Scales are laid out as bwgemm_scaled_t says (for qt: [row block][column]).
+ * X, q and qt 16-byte aligned; ldx a multiple of 16 bytes, ldq and ldqt of 16;
+ * scales 4-byte aligned.  Device memory as for bwgemm_run.  Asynchronous, one
+ * launch (none for an empty X), no allocation, capturable.
+ */
+bwgemm_status_t bwgemm_quantize(bwgemm_plan_t plan, const void* X, bwgemm_dtype_t dtype, int64_t rows,
+                                int64_t cols, int64_t ldx, bwgemm_block_t block, bwgemm_fp8_t type,
+                                int32_t pow2, void* q, int64_t ldq, float* scales, int64_t ld_scales,
+                                void* qt, int64_t ldqt, float* scales_t, int64_t ld_scales_t, void* stream);
+
+/*
+ * C = A * B^T of two 8-bit matrices with scales, A of M rows, B of N rows, both
+ * K wide (K-major, as in bwgemm_run); either may be e4m3 or e5m2 and carry
+ * scales per row or per 128 rows.  The 128 products of a K block are summed by
+ * the tensor cores in fp32, weighted with both scales and added in fp32.
+ *
+ *   C : M x N bf16, fp16 or fp32 (`out`), row stride ldc elements, 16-byte
+ *       aligned, ldc a multiple of 16 bytes
+ *   accumulate : nonzero adds to C (fp32 only): a gradient over several
+ *       batches
+ *
+ * Everything else -- device memory, empty sizes (K == 0: C = 0, or unchanged
+ * when accumulating), asynchrony, capture, status after a timeout, the plan's
+ * workspace -- is as for bwgemm_run.  Results do not depend on timing: sums are
+ * in a fixed order for a shape.
+ */
+bwgemm_status_t bwgemm_run_scaled(bwgemm_plan_t plan, const bwgemm_scaled_t* A, const bwgemm_scaled_t* B,
+                                  void* C, int64_t M, int64_t N, int64_t K, int64_t ldc, bwgemm_dtype_t out,
+                                  int32_t accumulate, void* stream);
 
 /* Static text for a status code ("unknown status" for anything else). */
 const char* bwgemm_status_string(bwgemm_status_t status);
