@@ -8,7 +8,7 @@ it raises if the library is missing rather than computing anything on the host.
 """
 import importlib
 
-__all__ = ["BF16", "FP16", "BwgemmError", "Plan", "PlanOptions", "gemm", "gemm_scaled", "quantize",
+__all__ = ["BF16", "FP16", "BwgemmError", "Plan", "PlanOptions", "gemm", "gemm_scaled", "orthogonalize", "quantize",
            "library_path", "load_library", "select_config", "check_args"]
 
 

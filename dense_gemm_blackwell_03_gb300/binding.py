@@ -46,7 +46,7 @@ EXPORTED = [
     "bwgemm_status_string", "bwgemm_version", "bwgemm_run_splitk_noalloc",
     "bwgemm_plan_read_trace", "bwgemm_tune", "bwgemm_plan_tuned_count",
     "bwgemm_probe_tensor_rate", "bwgemm_noalloc_scratch", "bwgemm_bench_load_path",
-    "bwgemm_quantize", "bwgemm_run_scaled",
+    "bwgemm_quantize", "bwgemm_run_scaled", "bwgemm_orthogonalize", "bwgemm_orthogonalize_workspace",
 ]
 
 # layouts of bwgemm_bench_load_path
@@ -224,6 +224,12 @@ def load_library(build_if_missing: bool = False):
         lib.bwgemm_run_scaled.argtypes = [vp, ctypes.POINTER(Scaled), ctypes.POINTER(Scaled), vp, i64, i64, i64,
                                           i64, ci, i32, vp]
         lib.bwgemm_run_scaled.restype = st
+        lib.bwgemm_orthogonalize.argtypes = [vp, vp, ci, vp, ci, i64, i64, i64, i64, i64, i64, i64, i32,
+                                             ctypes.POINTER(ctypes.c_float), ctypes.c_float, ctypes.c_float, vp,
+                                             ctypes.c_uint64, vp]
+        lib.bwgemm_orthogonalize.restype = st
+        lib.bwgemm_orthogonalize_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(ctypes.c_uint64)]
+        lib.bwgemm_orthogonalize_workspace.restype = st
         _lib = lib
         return lib
 
@@ -525,6 +531,56 @@ class Plan:
             raise BwgemmError(rc, "bwgemm_run_scaled")
         return out
 
+    def orthogonalize(self, G, out=None, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                      scale: float = 1.0, stream=None):
+        """``bwgemm_orthogonalize``: the Newton-Schulz iteration on a CUDA matrix, or a
+        stack of them (3-D), in bf16, fp16 or fp32.  `coefficients`: one triple
+        (a, b, c) for every step, or one per step.  Returns `scale` times the
+        result in bf16, or in `out` (bf16 or fp16, G's shape)."""
+        torch = _torch()
+        dt = _all_dtype_codes.get(G.dtype)
+        if dt is None:
+            raise TypeError(f"orthogonalize takes bfloat16, float16 or float32 tensors, got {G.dtype}")
+        self._check_tensor("G", G)
+        if G.dim() not in (2, 3):
+            raise ValueError("G must be a matrix or a stack of matrices")
+        if out is None:
+            out = torch.empty(G.shape, dtype=torch.bfloat16, device=G.device)
+        else:
+            self._check_tensor("out", out)
+            if out.shape != G.shape:
+                raise ValueError("out must have G's shape")
+        dto = _dtype_code(out)
+        batch = G.shape[0] if G.dim() == 3 else 1
+        rows, cols = G.shape[-2:]
+        if cols > 1 and (G.stride(-1) != 1 or out.stride(-1) != 1):
+            raise ValueError("G and out need unit stride along the last dim")
+        lds = [max(int(t.stride(-2)), cols) if rows > 1 else max(int(cols), 1) for t in (G, out)]
+        strides = [int(t.stride(0)) if t.dim() == 3 else 0 for t in (G, out)]
+        flat = [float(v) for v in coefficients] if not hasattr(coefficients[0], "__len__") else \
+            [float(v) for triple in coefficients for v in triple]
+        if len(flat) == 3:
+            flat = flat * int(steps)
+        if len(flat) != 3 * int(steps):
+            raise ValueError("coefficients: one (a, b, c), or one for each step")
+        need = ctypes.c_uint64()
+        rc = self.lib.bwgemm_orthogonalize_workspace(batch, rows, cols, ctypes.byref(need))
+        if rc != 0:
+            raise BwgemmError(rc, "bwgemm_orthogonalize_workspace")
+        ws = torch.empty(need.value, dtype=torch.uint8, device=G.device)
+        if stream is None:
+            h = torch.cuda.current_stream(self.device).cuda_stream
+        else:
+            h = stream.cuda_stream
+            ws.record_stream(stream)
+        rc = self.lib.bwgemm_orthogonalize(self.handle, G.data_ptr(), dt, out.data_ptr(), dto, batch, rows, cols,
+                                           lds[0], strides[0], lds[1], strides[1], int(steps),
+                                           (ctypes.c_float * len(flat))(*flat), float(eps), float(scale),
+                                           ws.data_ptr(), need.value, h)
+        if rc != 0:
+            raise BwgemmError(rc, "bwgemm_orthogonalize")
+        return out
+
     def status(self, stream=None) -> int:
         """``bwgemm_get_status``: synchronises the stream, returns and clears the status."""
         return int(self.lib.bwgemm_get_status(self.handle, self._stream_handle(stream)))
@@ -612,3 +668,8 @@ def quantize(X, blocks="row", transposed=False, pow2=False, dtype=None, stream=N
 def gemm_scaled(A, scale_a, B, scale_b, out=None, out_dtype=None, accumulate=False, stream=None):
     """`Plan.gemm_scaled` with a cached default plan per device."""
     return _default_plan(A).gemm_scaled(A, scale_a, B, scale_b, out, out_dtype, accumulate, stream)
+
+
+def orthogonalize(G, out=None, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=1.0, stream=None):
+    """`Plan.orthogonalize` with a cached default plan per device."""
+    return _default_plan(G).orthogonalize(G, out, steps, coefficients, eps, scale, stream)

@@ -1,6 +1,8 @@
 // operators.cpp -- argument checks, tensor maps and work division of the
-// operators beside the 16-bit GEMM (quantise, block-scaled product).
+// operators beside the 16-bit GEMM (quantise, block-scaled product,
+// orthogonalisation).
 #include <algorithm>
+#include <cmath>
 
 #include "operators.h"
 #include "plan.h"
@@ -172,6 +174,101 @@ ScaledPlan plan_scaled(int num_sms, int max_pairs, int64_t M, int64_t N, int64_t
     return best;
 }
 
+// ---------------------------------------------------------- orthogonalisation
+constexpr int kOrthoMaxSteps = 64;
+// The first products of the iteration take X in two fp16 terms: those of the
+// second and third step (and the first, for fp32 input; 16-bit input is one
+// term exactly).
+//
+// Why: rounding X to fp16 puts an error of 2^-12 of its large singular
+// directions into its small ones, and the iteration multiplies small ones by up
+// to 3.44 a step until all are near one; the earlier the rounding, the more it
+// is amplified.  Rounding S and B matters less: S enters B beside a I.  Error
+// of the result against 64 bits (512 x 512, 5 steps), with X in one term
+// throughout / two terms in step 2 / in steps 2 and 3 / in steps 2 to 4:
+// N(0, 1) 1.2e-3 / 1.1e-3 / 1.1e-3 / 1.1e-3; eight directions 30 times the
+// rest 1.3e-2 / 2.9e-3 / 1.4e-3 / 1.3e-3; singular values 1 / i 1.8e-3 /
+// 1.1e-3 / 7e-4 / 7e-4.  (Rounding the result to bf16 alone is 1.7e-3.)
+constexpr int kTwoTermSteps = 3;
+
+struct OrthoLayout {
+    bool wide;                    // columns >= rows: X X^T contracts over columns
+    int64_t m, n;                 // the shorter and longer side
+    int64_t ldx, lds;             // fp16 elements between rows of X, and of S and B
+    int64_t x_stride, s_stride;   // per matrix
+    int parts;                    // blocks per matrix of the input pass
+    uint64_t hi[2], lo[2], s, b, sums, factors, total;  // byte offsets
+};
+
+OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols)
+{
+    auto pad = [](int64_t v) { return (v + 127) / 128 * 128; };
+    OrthoLayout l;
+    l.wide = rows <= cols;
+    l.m = std::min(rows, cols);
+    l.n = std::max(rows, cols);
+    l.ldx = pad(cols);
+    l.lds = pad(l.m);
+    l.x_stride = rows * l.ldx;
+    l.s_stride = l.m * l.lds;
+    // about 16K elements per block, and all matrices together a few blocks per SM
+    const int64_t want = (rows * cols + 16383) / 16384;
+    l.parts = int(std::max<int64_t>(1, std::min<int64_t>({want, (rows + 7) / 8, std::max<int64_t>(1, 1216 / batch)})));
+    uint64_t at = 0;
+    auto take = [&](uint64_t bytes) {
+        const uint64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    for (int i = 0; i < 2; ++i) {
+        l.hi[i] = take(uint64_t(batch) * l.x_stride * 2);
+        l.lo[i] = take(uint64_t(batch) * l.x_stride * 2);
+    }
+    l.s = take(uint64_t(batch) * l.s_stride * 2);
+    l.b = take(uint64_t(batch) * l.s_stride * 2);
+    l.sums = take(uint64_t(batch) * l.parts * 4);
+    l.factors = take(uint64_t(batch) * 2 * 4);
+    l.total = at;
+    return l;
+}
+
+// A stack of fp16 matrices as operand: boxes of two 64-column chunks of 128 rows.
+bwgemm_status_t encode_stack(CUtensorMap* map, const void* ptr, int64_t rows, int64_t ld, int64_t stride, int64_t batch)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc)
+        return BWGEMM_ERR_NO_DEVICE;
+    const cuuint64_t dims[4] = {64, cuuint64_t(rows), cuuint64_t(ld / 64), cuuint64_t(batch)};
+    const cuuint64_t strides[3] = {cuuint64_t(ld) * 2, 128, cuuint64_t(stride) * 2};
+    const cuuint32_t box[4] = {64, 128, 2, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? BWGEMM_OK
+               : BWGEMM_ERR_CUDA;
+}
+
+// A stack of 16-bit matrices as result: 32 x 32 boxes.
+bwgemm_status_t encode_result(CUtensorMap* map, int dtype, void* ptr, int64_t rows, int64_t cols, int64_t ld,
+                              int64_t stride, int64_t batch)
+{
+    const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(batch)};
+    const cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(stride) * 2};
+    const cuuint32_t box[3] = {32, 32, 1};
+    return encode(map, dtype == BWGEMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, ptr,
+                  dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+}
+
+bwgemm_status_t check_ortho(int64_t batch, int64_t rows, int64_t cols)
+{
+    if (batch < 0 || rows < 0 || cols < 0)
+        return BWGEMM_ERR_INVALID_ARG;
+    if (batch > 65535 || rows > (1 << 24) || cols > (1 << 24) || std::min(rows, cols) > (1 << 17))
+        return BWGEMM_ERR_UNSUPPORTED;
+    return BWGEMM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -317,6 +414,183 @@ bwgemm_status_t bwgemm_run_scaled(bwgemm_plan_t plan, const bwgemm_scaled_t* A, 
     if (launch_scaled(sel.variant, ml, mc, ml3, mc3, mo, p, sel.grid, s, plan->opts.pdl_off == 0) != cudaSuccess)
         return BWGEMM_ERR_CUDA;
     plan->launches += 1;
+    return BWGEMM_OK;
+}
+
+bwgemm_status_t bwgemm_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, uint64_t* bytes)
+{
+    if (!bytes)
+        return BWGEMM_ERR_INVALID_ARG;
+    *bytes = 0;
+    const bwgemm_status_t st = check_ortho(batch, rows, cols);
+    if (st != BWGEMM_OK || batch == 0 || rows == 0 || cols == 0)
+        return st;
+    *bytes = ortho_layout(batch, rows, cols).total;
+    return BWGEMM_OK;
+}
+
+bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_dtype_t dtype, void* X,
+                                     bwgemm_dtype_t out, int64_t batch, int64_t rows, int64_t cols, int64_t ldg,
+                                     int64_t stride_g, int64_t ldx, int64_t stride_x, int32_t steps,
+                                     const float* coefficients, float eps, float scale, void* workspace,
+                                     uint64_t workspace_bytes, void* stream)
+{
+    if (!plan || (dtype != BWGEMM_BF16 && dtype != BWGEMM_FP16 && dtype != BWGEMM_FP32) ||
+        (out != BWGEMM_BF16 && out != BWGEMM_FP16) || steps < 1 || steps > kOrthoMaxSteps || !(eps >= 0.f))
+        return BWGEMM_ERR_INVALID_ARG;
+    bwgemm_status_t st = check_ortho(batch, rows, cols);
+    if (st != BWGEMM_OK)
+        return st;
+    if (batch == 0 || rows == 0 || cols == 0)
+        return BWGEMM_OK;
+    if (!G || !X || !workspace || ldg < cols || ldx < cols ||
+        (batch > 1 && (stride_g < (rows - 1) * ldg + cols || stride_x < (rows - 1) * ldx + cols)))
+        return BWGEMM_ERR_INVALID_ARG;
+    if (ldg >= (1ll << 31) || ldx >= (1ll << 31) || stride_g >= (1ll << 38) || stride_x >= (1ll << 38))
+        return BWGEMM_ERR_UNSUPPORTED;
+    if (!aligned(G, element_size(dtype)) || !aligned(X, 2) || !aligned(workspace, 256))
+        return BWGEMM_ERR_ALIGNMENT;
+    const OrthoLayout l = ortho_layout(batch, rows, cols);
+    if (workspace_bytes < l.total)
+        return BWGEMM_ERR_WORKSPACE;
+    DeviceGuard guard(plan->device);
+    if (!guard.ok)
+        return BWGEMM_ERR_CUDA;
+    if ((st = check_resident({G, X, workspace}, plan->device)) != BWGEMM_OK)
+        return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool pdl = plan->opts.pdl_off == 0;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const int log2_scale = std::min(8, int(std::lround(0.5 * std::log2(double(l.m)))));
+    const int first_terms = dtype == BWGEMM_FP32 ? 2 : 1;
+
+    OrthoInput in = {};
+    in.g = G;
+    in.ldg = ldg;
+    in.stride_g = batch > 1 ? stride_g : 0;
+    in.dtype = dtype;
+    in.rows = int32_t(rows);
+    in.cols = int32_t(cols);
+    in.batch = int32_t(batch);
+    const int64_t per_vector = 16 / element_size(dtype);
+    in.vectors = aligned(G, 16) && ldg % per_vector == 0 && in.stride_g % per_vector == 0;
+    in.eps = eps;
+    in.log2_scale = log2_scale;
+    in.sums = reinterpret_cast<float*>(ws + l.sums);
+    in.parts = l.parts;
+    in.hi = reinterpret_cast<uint16_t*>(ws + l.hi[0]);
+    in.lo = first_terms == 2 ? reinterpret_cast<uint16_t*>(ws + l.lo[0]) : nullptr;
+    in.ld = l.ldx;
+    in.stride = l.x_stride;
+    in.factors = reinterpret_cast<float*>(ws + l.factors);
+    if (launch_ortho_input(in, s, pdl) != cudaSuccess)
+        return BWGEMM_ERR_CUDA;
+    plan->launches += 2;
+
+    // operand maps of X (two buffers, two terms), S and B, and their result maps
+    CUtensorMap x_op[2][2], x_res[2][2], s_op, s_res, b_op, b_res, final_res;
+    for (int i = 0; i < 2; ++i)
+        for (int t = 0; t < 2; ++t) {
+            void* at = ws + (t ? l.lo[i] : l.hi[i]);
+            if ((st = encode_stack(&x_op[i][t], at, rows, l.ldx, l.x_stride, batch)) != BWGEMM_OK ||
+                (st = encode_result(&x_res[i][t], BWGEMM_FP16, at, rows, l.ldx, l.ldx, l.x_stride, batch)) != BWGEMM_OK)
+                return st;
+        }
+    if ((st = encode_stack(&s_op, ws + l.s, l.m, l.lds, l.s_stride, batch)) != BWGEMM_OK ||
+        (st = encode_result(&s_res, BWGEMM_FP16, ws + l.s, l.m, l.lds, l.lds, l.s_stride, batch)) != BWGEMM_OK ||
+        (st = encode_stack(&b_op, ws + l.b, l.m, l.lds, l.s_stride, batch)) != BWGEMM_OK ||
+        (st = encode_result(&b_res, BWGEMM_FP16, ws + l.b, l.m, l.lds, l.lds, l.s_stride, batch)) != BWGEMM_OK)
+        return st;
+    // a TMA store needs 16-byte rows, and clips a row's end only in whole
+    // 16-byte pieces
+    const bool plain = !aligned(X, 16) || ldx % 8 != 0 || cols % 8 != 0 || (batch > 1 && stride_x % 8 != 0);
+    final_res = x_res[0][0];
+    if (!plain && (st = encode_result(&final_res, out, X, rows, cols, ldx, batch > 1 ? stride_x : rows * ldx, batch)) !=
+                      BWGEMM_OK)
+        return st;
+
+    // One product: square tiles of 256 on CTA pairs (1024 SM cycles per 128 of
+    // K, bound by the MMAs) or of 128 on single CTAs (about 740, bound by the
+    // copies of both operands), whichever takes fewer cycles in its waves.
+    const int pairs = plan->max_active[find_variant(2, 256, false, 1)];
+    OrthoParams p0 = {};
+    p0.batch = int32_t(batch);
+    p0.timeout_ns = plan->opts.timeout_ns ? plan->opts.timeout_ns : 4000000000ull;
+    p0.status = plan->d_status;
+    p0.stall_kblock = plan->opts.stall_kblock;
+    auto product = [&](int form, OrthoParams p, int64_t K, const CUtensorMap& a, const CUtensorMap& b,
+                       const CUtensorMap& a2, const CUtensorMap& b2, const CUtensorMap& res, const CUtensorMap& res2) {
+        p.steps_k = int32_t((K + 127) / 128);
+        int64_t tiles[3] = {};
+        for (int cg = 1; cg <= 2; ++cg) {
+            const int64_t r = (p.rows + 128 * cg - 1) / (128 * cg), c = (p.cols + 128 * cg - 1) / (128 * cg);
+            tiles[cg] = p.symmetric ? r * (r + 1) / 2 : r * c;
+        }
+        const int64_t t1 = tiles[1] * batch, t2 = tiles[2] * batch;
+        const int64_t cost1 = (t1 + plan->num_sms - 1) / plan->num_sms * 740, cost2 = (t2 + pairs - 1) / pairs * 1024;
+        const int cg = cost1 < cost2 ? 1 : 2;
+        if (tiles[cg] * batch >= (1ll << 31))
+            return BWGEMM_ERR_UNSUPPORTED;
+        p.num_r = int32_t((p.rows + 128 * cg - 1) / (128 * cg));
+        p.num_c = int32_t((p.cols + 128 * cg - 1) / (128 * cg));
+        p.tiles = int32_t(tiles[cg]);
+        const int64_t workers = std::min<int64_t>(tiles[cg] * batch, cg == 2 ? pairs : plan->num_sms);
+        if (launch_ortho(form, cg, a, b, a2, b2, res, res2, p, int(workers * cg), s, pdl) != cudaSuccess)
+            return BWGEMM_ERR_CUDA;
+        plan->launches += 1;
+        return BWGEMM_OK;
+    };
+
+    const float down = std::ldexp(1.f, -log2_scale);
+    int cur = 0;
+    for (int i = 0; i < steps; ++i) {
+        const float a = coefficients ? coefficients[3 * i] : 3.4445f;
+        const float b = coefficients ? coefficients[3 * i + 1] : -4.7750f;
+        const float c = coefficients ? coefficients[3 * i + 2] : 2.0315f;
+        const CUtensorMap& x = x_op[cur][0];
+        // S = X X^T over the longer side
+        OrthoParams p = p0;
+        p.rows = p.cols = int32_t(l.m);
+        p.terms = 1;
+        p.symmetric = 1;
+        p.alpha = i == 0 ? 1.f : down * down;
+        p.alpha_dev = i == 0 ? in.factors + batch : nullptr;
+        p.store_cols = int32_t(l.lds);
+        if ((st = product(l.wide ? kOrthoNT : kOrthoTN, p, l.n, x, x, x, x, s_res, s_res)) != BWGEMM_OK)
+            return st;
+        // B = a I + b S + c S S
+        p.alpha = c;
+        p.alpha_dev = nullptr;
+        p.beta = b;
+        p.diag = a;
+        p.e = reinterpret_cast<const uint16_t*>(ws + l.s);
+        p.lde = l.lds;
+        p.stride_e = l.s_stride;
+        if ((st = product(kOrthoNT, p, l.m, s_op, s_op, s_op, s_op, b_res, b_res)) != BWGEMM_OK)
+            return st;
+        // X <- B X, or X B with X stored upright
+        const bool last = i == steps - 1;
+        p = p0;
+        p.rows = int32_t(rows);
+        p.cols = int32_t(cols);
+        p.terms = i == 0 ? first_terms : (i < kTwoTermSteps ? 2 : 1);
+        p.alpha = last ? scale * (i == 0 ? 1.f : down) : (i == 0 ? 1.f / down : 1.f);
+        p.alpha_dev = i == 0 ? in.factors : nullptr;
+        p.store_cols = int32_t(last ? cols : l.ldx);
+        p.low = !last && i + 1 < kTwoTermSteps;
+        p.out_bf16 = last && out == BWGEMM_BF16;
+        p.plain_store = last && plain;
+        p.out = static_cast<uint16_t*>(X);
+        p.ldo = ldx;
+        p.stride_o = batch > 1 ? stride_x : 0;
+        const CUtensorMap &x2 = p.terms == 2 ? x_op[cur][1] : x, &res = last ? final_res : x_res[cur ^ 1][0],
+                          &res2 = x_res[cur ^ 1][1];
+        st = l.wide ? product(kOrthoNN, p, l.m, b_op, x, b_op, x2, res, res2)
+                    : product(kOrthoNT, p, l.m, x, b_op, x2, b_op, res, res2);
+        if (st != BWGEMM_OK)
+            return st;
+        cur ^= 1;
+    }
     return BWGEMM_OK;
 }
 

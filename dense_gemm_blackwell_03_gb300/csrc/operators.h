@@ -90,4 +90,57 @@ cudaError_t launch_scaled(int idx, const CUtensorMap& l, const CUtensorMap& c, c
                           const CUtensorMap& c3, const CUtensorMap& out, const ScaledParams& p, int grid,
                           cudaStream_t stream, bool pdl);
 
+// -------------------------------------------------------- orthogonalisation
+// One product of the iteration over a stack of matrices, fp16 operands:
+//   D = alpha * A B^T + beta * E + diag * I
+// A and B: `rows` / `cols` wide on their output side and K deep, each K-major
+// or (a_mn / b_mn) MN-major, i.e. stored transposed.
+struct OrthoParams {
+    int32_t rows, cols;          // of D
+    int32_t steps_k;             // ceil(K / 128)
+    int32_t terms;               // 1, or 2: A or B is the sum of two fp16 matrices (maps a2 / b2)
+    int32_t num_r, num_c;        // tiles along rows and columns
+    int32_t tiles, batch;        // tiles per matrix; matrices
+    int32_t symmetric;           // 1: only tiles on and below the diagonal, stored twice
+    float alpha, beta, diag;
+    const float* alpha_dev;      // a further factor per matrix (null: 1)
+    const uint16_t* e;           // E, fp16 (null: none), lde elements apart, stride_e per matrix
+    int64_t lde, stride_e;
+    int32_t store_cols;          // columns that may be stored (D's padded width)
+    int32_t low;                 // 1: also store what fp16 rounding lost (map out2)
+    int32_t out_bf16;            // 1: D is bf16 instead of fp16
+    int32_t plain_store;         // 1: D's rows cannot be written by TMA: element by element to `out`
+    uint16_t* out;
+    int64_t ldo, stride_o;
+    uint64_t timeout_ns;
+    uint32_t* status;
+    int32_t stall_kblock;
+};
+
+// Which side each operand of a product is stored along.
+enum : int { kOrthoNT = 0, kOrthoNN = 1, kOrthoTN = 2 };  // A, B: K K | K MN | MN MN
+constexpr int ortho_tile(int cg) { return 128 * cg; }
+
+cudaError_t launch_ortho(int form, int cg, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2,
+                         const CUtensorMap& b2, const CUtensorMap& out, const CUtensorMap& out2, const OrthoParams& p,
+                         int grid, cudaStream_t stream, bool pdl);
+
+// The input pass: sums of squares, then G as fp16 in the workspace.
+struct OrthoInput {
+    const void* g;               // rows x cols, ldg apart, stride_g per matrix
+    int64_t ldg, stride_g;
+    int32_t dtype;
+    int32_t rows, cols, batch;
+    int32_t vectors;             // 1: rows start on 16-byte boundaries
+    float eps;
+    int32_t log2_scale;          // X is stored times 2^log2_scale
+    float* sums;                 // [batch][parts]
+    int32_t parts;               // blocks per matrix of the first kernel
+    uint16_t* hi;                // fp16, `ld` apart, `stride` per matrix; columns up to ld are zeroed
+    uint16_t* lo;                // what fp16 lost (null: nothing is)
+    int64_t ld, stride;
+    float* factors;              // [2][batch]: stored -> true X, and its square
+};
+cudaError_t launch_ortho_input(const OrthoInput& p, cudaStream_t stream, bool pdl);
+
 }  // namespace bwgemm

@@ -1,0 +1,467 @@
+// ortho_kernel.cuh -- the products of the Newton-Schulz iteration
+//
+//   S = X X^T     B = a I + b S + c S S     X <- B X
+//
+// on fp16 operands with fp32 accumulation: one persistent, warp-specialised
+// tcgen05 kernel for all three, over a stack of matrices.
+//
+// Symmetry: S and S S are computed on and below the diagonal of tiles only
+// (m^2 n + m^3 instead of twice that); the epilogue stores an off-diagonal box
+// a second time, transposed in shared memory.  The polynomial's b S and a I are
+// added to the fp32 sums before their one rounding.
+//
+// Orientation: X is kept as it comes, its longer side along rows or columns.
+// With more columns the first product contracts over columns (both operands
+// K-major) and the last over rows of X (B K-major, X MN-major); with more rows
+// the first contracts over rows (both MN-major) and the last is X B (both
+// K-major).  tcgen05 reads either major order, so nothing is ever transposed
+// in memory.
+//
+// Two terms: where `terms` is 2 the K loop runs twice, the second time with the
+// operand's low part (what fp16 rounding lost) -- the sum of both products in
+// one accumulator.
+//
+// Each stage of the ring holds 128 of K of both operands (64 KiB), one 32 KiB
+// copy each (box {64, 128 rows, 2 chunks}); the same box serves K-major (rows =
+// output rows, chunks along K) and MN-major (rows = K, chunks along the
+// output).  Roles, TMEM double buffering and bounded waits are as in the main
+// GEMM kernel.
+#pragma once
+
+#include "gemm_kernel.cuh"
+#include "operators.h"
+
+namespace bwgemm {
+
+constexpr int kOrthoK = 128;  // of K per stage
+
+template <int CG>
+struct OrthoConfig {
+    static constexpr int kTile = 128 * CG;                 // rows and columns of a tile
+    static constexpr int kEpiWarps = 8;
+    static constexpr int kThreads = 32 * (2 + kEpiWarps);
+    static constexpr int kCols = kTile / 2;                // columns per epilogue warp
+    static constexpr int kOperandBytes = 128 * kOrthoK * 2;  // 32 KiB: this CTA's 128 rows of A, or of B
+    static constexpr int kStages = 3;
+    static constexpr int kTmemCols = 2 * kTile;
+    static constexpr int kStoreBytes = 2048;               // a 32 x 32 box of 16-bit values
+    static constexpr int kOffA = 0;
+    static constexpr int kOffB = kStages * kOperandBytes;
+    static constexpr int kOffStore = 2 * kStages * kOperandBytes;
+    static constexpr int kOffBar = kOffStore + kEpiWarps * 2 * kStoreBytes;
+    static constexpr int kNumBars = 2 * kStages + 4 + 1;   // full, empty, acc_full[2], acc_empty[2], drain
+    static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars;
+    static constexpr int kOffAbort = kOffTmemSlot + 4;
+    static constexpr int kSmemBytes = kOffAbort + 4 + 1024;
+    static_assert(kSmemBytes <= 227 * 1024, "exceeds the 227 KiB shared memory of one CTA");
+};
+
+// Shared-memory descriptor of an MN-major operand block: 128-byte rows of 64
+// output elements, one row per k, 128-byte swizzle (8 k per 1 KiB atom: stride
+// byte offset); the next 64 output elements lie a whole chunk of kOrthoK rows
+// further (leading byte offset).
+__device__ __forceinline__ uint64_t make_sdesc_mn(uint32_t smem)
+{
+    uint64_t d = 0;
+    d |= uint64_t((smem & 0x3FFFFu) >> 4);
+    d |= uint64_t((kOrthoK * 128) >> 4) << 16;
+    d |= uint64_t(1024 >> 4) << 32;
+    d |= uint64_t(1) << 46;
+    d |= uint64_t(2) << 61;
+    return d;
+}
+
+__device__ __forceinline__ bool ortho_wait(uint32_t bar, uint32_t parity, const OrthoParams& p,
+                                           volatile uint32_t* abort_flag, uint32_t code)
+{
+    if (ptx::mbar_try_wait(bar, parity))
+        return true;
+    WaitClock clock;
+#pragma unroll 1
+    while (true) {
+        if (ptx::mbar_try_wait(bar, parity))
+            return true;
+        if (*abort_flag)
+            return false;
+        if (clock.expired(p.timeout_ns)) {
+            atomicOr(p.status, code);
+            *abort_flag = 1u;
+            return false;
+        }
+    }
+}
+
+struct OrthoTile {
+    int r, c, matrix;
+};
+
+__device__ __forceinline__ OrthoTile ortho_tile_at(const OrthoParams& p, int t)
+{
+    OrthoTile x;
+    x.matrix = t / p.tiles;
+    const int i = t - x.matrix * p.tiles;
+    if (p.symmetric) {
+        // row r of the triangle holds tiles r (r + 1) / 2 .. + r
+        int r = int((sqrtf(8.f * float(i) + 1.f) - 1.f) * 0.5f);
+        while (r * (r + 1) / 2 > i)
+            --r;
+        while ((r + 1) * (r + 2) / 2 <= i)
+            ++r;
+        x.r = r;
+        x.c = i - r * (r + 1) / 2;
+    } else {
+        // groups of 8 tile rows, walked down before stepping along the columns
+        const int per_group = 8 * p.num_c;
+        const int g = i / per_group;
+        const int height = min(p.num_r - 8 * g, 8);
+        const int local = i - g * per_group;
+        x.r = 8 * g + local % height;
+        x.c = local / height;
+    }
+    return x;
+}
+
+// The warp's staging buffers: boxes alternate between two.
+struct OrthoStore {
+    uint32_t buf;
+    int n;
+    __device__ __forceinline__ uint32_t claim(int lane)
+    {
+        if (lane == 0)
+            ptx::bulk_wait_group_read<1>();
+        __syncwarp();
+        return buf + uint32_t((n++ & 1) * 2048);
+    }
+};
+
+// One 32 x 32 box, lane = row, 16 packed words = its columns, into `sb` with
+// the 64-byte swizzle of the store maps (16-byte piece XOR bits 7-8 of the
+// offset), or transposed.
+__device__ __forceinline__ void ortho_stage(const uint32_t (&w)[16], uint32_t sb, int lane, bool transposed)
+{
+    if (!transposed) {
+        const uint32_t row = sb + uint32_t(lane * 64);
+        const uint32_t swz = uint32_t((lane >> 1) & 3);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch)
+            ptx::st_shared_v4(row + ((uint32_t(ch) ^ swz) << 4), w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            ptx::st_shared_u16(sb + uint32_t(i * 64) + ((uint32_t(lane >> 3) ^ uint32_t((i >> 1) & 3)) << 4) +
+                                   uint32_t((lane & 7) * 2),
+                               uint16_t((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xFFFFu)));
+    }
+}
+
+template <int CG, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
+    ortho_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                 const __grid_constant__ CUtensorMap tmap_a2, const __grid_constant__ CUtensorMap tmap_b2,
+                 const __grid_constant__ CUtensorMap tmap_out, const __grid_constant__ CUtensorMap tmap_out2,
+                 const OrthoParams p)
+{
+    using Cfg = OrthoConfig<CG>;
+    constexpr int STAGES = Cfg::kStages;
+    constexpr int TILE = Cfg::kTile;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;
+    const int worker = int(blockIdx.x) / CG;
+    const int workers = int(gridDim.x) / CG;
+    const int total = p.tiles * p.batch;
+    const int steps = p.steps_k * p.terms;
+    const uint32_t sA = base + Cfg::kOffA;
+    const uint32_t sB = base + Cfg::kOffB;
+    const uint32_t bar_full = base + Cfg::kOffBar;
+    const uint32_t bar_empty = bar_full + 8 * STAGES;
+    const uint32_t bar_acc_full = bar_empty + 8 * STAGES;
+    const uint32_t bar_acc_empty = bar_acc_full + 16;
+    const uint32_t bar_drain = bar_acc_empty + 16;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffTmemSlot);
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffAbort);
+
+    if (threadIdx.x == 64) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(bar_full + 8 * s, 1);
+            ptx::mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(bar_acc_full + 8 * b, 1);
+            ptx::mbar_init(bar_acc_empty + 8 * b, CG * Cfg::kEpiWarps);
+        }
+        ptx::mbar_init(bar_drain, 1);
+        *abort_flag = 0u;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tensormap(&tmap_a);
+        ptx::prefetch_tensormap(&tmap_b);
+        ptx::prefetch_tensormap(&tmap_out);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc<CG>(ptx::smem_addr(tmem_slot), Cfg::kTmemCols);
+        ptx::tmem_relinquish<CG>();
+    }
+    ptx::tc_fence_before_sync();
+    if constexpr (CG == 2)
+        ptx::cluster_sync();
+    else
+        __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    ptx::launch_dependents();
+    uint32_t armed_mask = 0, armed_parity = 0;
+
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        ptx::grid_dependency_wait();
+        const uint32_t leader_full = CG == 2 ? ptx::map_to_cta(bar_full, 0) : bar_full;
+        int s = 0, n = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int t = worker; ok && t < total; t += workers) {
+            const OrthoTile x = ortho_tile_at(p, t);
+            const int a0 = x.r * TILE + int(rank) * 128;  // this CTA's output rows, and columns of B
+            const int b0 = x.c * TILE + int(rank) * 128;
+#pragma unroll 1
+            for (int i = 0; i < steps; ++i, ++n) {
+                ok = __all_sync(0xffffffffu,
+                                ortho_wait(bar_empty + 8 * s, phase ^ 1u, p, abort_flag, kStatusProducerTimeout));
+                if (!ok)
+                    break;
+                const bool stall = p.stall_kblock >= 0 && blockIdx.x == 0 && p.stall_kblock == n;
+                if (!stall && rank == 0) {
+                    armed_mask |= 1u << s;
+                    armed_parity = (armed_parity & ~(1u << s)) | (phase << s);
+                }
+                if (!stall && ptx::elect_one()) {
+                    const bool second = i >= p.steps_k;
+                    const int k = (second ? i - p.steps_k : i) * kOrthoK;
+                    const CUtensorMap* ma = second ? &tmap_a2 : &tmap_a;
+                    const CUtensorMap* mb = second ? &tmap_b2 : &tmap_b;
+                    const uint32_t fb = leader_full + 8 * s;
+                    const uint32_t dA = sA + uint32_t(s * Cfg::kOperandBytes), dB = sB + uint32_t(s * Cfg::kOperandBytes);
+                    const int ra = A_MN ? k : a0, ca = (A_MN ? a0 : k) / 64;
+                    const int rb = B_MN ? k : b0, cb = (B_MN ? b0 : k) / 64;
+                    if (rank == 0)
+                        ptx::mbar_arrive_expect_tx(fb, uint32_t(CG * 2 * Cfg::kOperandBytes));
+                    if constexpr (CG == 2) {
+                        ptx::tma_load_4d_pair(dA, ma, fb, 0, ra, ca, x.matrix);
+                        ptx::tma_load_4d_pair(dB, mb, fb, 0, rb, cb, x.matrix);
+                    } else {
+                        ptx::tma_load_4d(dA, ma, fb, 0, ra, ca, x.matrix);
+                        ptx::tma_load_4d(dB, mb, fb, 0, rb, cb, x.matrix);
+                    }
+                }
+                __syncwarp();
+                if (++s == STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1 && rank == 0) {
+        // ---------------------------------------------------------- MMA issue
+        // A K-major block holds two chunks of 64 k, 16 KiB apart, 32 bytes per
+        // MMA; an MN-major one 128 k in rows of 128 bytes, 2 KiB per MMA.
+        const uint64_t a_desc0 = A_MN ? make_sdesc_mn(sA) : make_sdesc_sw128(sA);
+        const uint64_t b_desc0 = B_MN ? make_sdesc_mn(sB) : make_sdesc_sw128(sB);
+        const uint32_t idesc = make_idesc(BWGEMM_FP16, 128 * CG, TILE) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+        const uint32_t tmem0 = __shfl_sync(0xffffffffu, tmem_base, 0);
+        int s = 0, b = 0;
+        uint32_t phase = 0, bphase = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int t = worker; ok && t < total; t += workers) {
+            ok = __all_sync(0xffffffffu,
+                            ortho_wait(bar_acc_empty + 8 * b, bphase ^ 1u, p, abort_flag, kStatusMmaTimeout));
+#pragma unroll 1
+            for (int i = 0; ok && i < steps; ++i) {
+                ok = __all_sync(0xffffffffu, ortho_wait(bar_full + 8 * s, phase, p, abort_flag, kStatusMmaTimeout));
+                if (!ok)
+                    break;
+                ptx::tc_fence_after_sync();
+                if (ptx::elect_one()) {
+                    const uint64_t ad = a_desc0 + uint64_t((s * Cfg::kOperandBytes) >> 4);
+                    const uint64_t bd = b_desc0 + uint64_t((s * Cfg::kOperandBytes) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < kOrthoK / 16; ++kk) {
+                        const uint32_t k_major = uint32_t((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                        const uint32_t mn_major = uint32_t(kk * 2048) >> 4;
+                        ptx::mma_f16<CG>(tmem0 + uint32_t(b * TILE), ad + (A_MN ? mn_major : k_major),
+                                         bd + (B_MN ? mn_major : k_major), idesc, (i > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    if constexpr (CG == 2) {
+                        ptx::mma_commit_pair(bar_empty + 8 * s, 0x3);
+                        if (i == steps - 1)
+                            ptx::mma_commit_pair(bar_acc_full + 8 * b, 0x3);
+                    } else {
+                        ptx::mma_commit(bar_empty + 8 * s);
+                        if (i == steps - 1)
+                            ptx::mma_commit(bar_acc_full + 8 * b);
+                    }
+                }
+                __syncwarp();
+                if (++s == STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (++b == 2) {
+                b = 0;
+                bphase ^= 1u;
+            }
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------------------ epilogue
+        ptx::grid_dependency_wait();
+        const int e = warp - 2;
+        const int q = warp & 3;
+        OrthoStore store = {base + uint32_t(Cfg::kOffStore + e * 2 * Cfg::kStoreBytes), 0};
+        int b = 0;
+        uint32_t bphase = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int t = worker; ok && t < total; t += workers) {
+            const OrthoTile x = ortho_tile_at(p, t);
+            const int row0 = x.r * TILE + int(rank) * 128 + 32 * q;
+            const int col0 = x.c * TILE + (e >> 2) * Cfg::kCols;
+            const int row = row0 + lane;
+            const float alpha = p.alpha_dev ? p.alpha * ptx::ld_global_cg_f32(p.alpha_dev + x.matrix) : p.alpha;
+            const bool mirror = p.symmetric && x.r != x.c;
+            ok = __all_sync(0xffffffffu,
+                            ortho_wait(bar_acc_full + 8 * b, bphase, p, abort_flag, kStatusEpilogueTimeout));
+            if (!ok)
+                break;
+            ptx::tc_fence_after_sync();
+            const uint32_t taddr = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(b * TILE + (e >> 2) * Cfg::kCols);
+#pragma unroll 1
+            for (int c = 0; c < Cfg::kCols; c += 32) {
+                const int col = col0 + c;
+                uint4 add[4];
+                const bool has = p.e != nullptr && row < p.rows && col < p.store_cols;
+                if (has) {
+                    const uint16_t* src = p.e + x.matrix * p.stride_e + row * p.lde + col;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        add[i] = ptx::ld_global_cg_v4(src + 8 * i);
+                }
+                uint32_t v[32];
+                ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c), v);
+                ptx::tmem_ld_wait();
+                if (c + 32 >= Cfg::kCols)
+                    release_accumulator<CG>(bar_acc_empty + 8 * b, lane, 0);
+                // the box itself, and its mirror image: columns of D from its rows, up
+                // to the padded width (zeros there, which later products read)
+                const bool direct = row0 < p.rows && col < p.store_cols;
+                const bool mirrored = mirror && col < p.rows && row0 < p.store_cols;
+                if (!direct && !mirrored)
+                    continue;
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float f[2] = {alpha * __uint_as_float(v[2 * i]), alpha * __uint_as_float(v[2 * i + 1])};
+                    if (has) {
+                        const uint32_t w = (&add[i >> 2].x)[i & 3];
+                        const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                        f[0] = fmaf(p.beta, g.x, f[0]);
+                        f[1] = fmaf(p.beta, g.y, f[1]);
+                    }
+                    if (p.diag != 0.f) {
+                        f[0] += row == col + 2 * i ? p.diag : 0.f;
+                        f[1] += row == col + 2 * i + 1 ? p.diag : 0.f;
+                    }
+                    hi[i] = pack2(__float_as_uint(f[0]), __float_as_uint(f[1]), p.out_bf16 ? 0 : 1);
+                    if (p.low) {
+                        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
+                        lo[i] = pack2(__float_as_uint(f[0] - h.x), __float_as_uint(f[1] - h.y), 1);
+                    }
+                }
+                auto put = [&](const uint32_t(&w)[16], const CUtensorMap* map, bool transposed) {
+                    const uint32_t sb = store.claim(lane);
+                    ortho_stage(w, sb, lane, transposed);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::tma_store_3d(map, sb, transposed ? row0 : col, transposed ? col : row0, x.matrix);
+                        ptx::bulk_commit_group();
+                    }
+                };
+                if (p.plain_store) {
+                    // the caller's rows are not on 16-byte boundaries: the box goes
+                    // through shared memory and out a row at a time, lane = column
+                    const uint32_t sb = store.claim(lane);
+                    ortho_stage(hi, sb, lane, false);
+                    __syncwarp();
+                    if (col + lane < p.cols) {
+                        uint16_t* dst = p.out + x.matrix * p.stride_o + row0 * p.ldo + col + lane;
+                        const int n = min(32, p.rows - row0);
+#pragma unroll 1
+                        for (int i = 0; i < n; ++i)
+                            dst[i * p.ldo] = ptx::ld_shared_u16(
+                                sb + uint32_t(i * 64) + ((uint32_t(lane >> 3) ^ uint32_t((i >> 1) & 3)) << 4) +
+                                uint32_t((lane & 7) * 2));
+                    }
+                    __syncwarp();
+                } else {
+                    if (direct)
+                        put(hi, &tmap_out, false);
+                    if (mirrored)
+                        put(hi, &tmap_out, true);
+                    if (p.low && direct)
+                        put(lo, &tmap_out2, false);
+                }
+            }
+            if (++b == 2) {
+                b = 0;
+                bphase ^= 1u;
+            }
+        }
+        if (lane == 0)
+            ptx::bulk_wait_group_all();
+        __syncwarp();
+    }
+
+    // --------------------------------------------------------------- teardown
+    // as in the other kernels: after an abort, drain MMAs and loads (bounded)
+    // before TMEM and shared memory are released
+    __syncwarp();
+    __syncthreads();
+    if (*abort_flag) {
+        if (warp == 1 && rank == 0) {
+            if (ptx::elect_one()) {
+                if constexpr (CG == 2)
+                    ptx::mma_commit_pair(bar_drain, 0x1);
+                else
+                    ptx::mma_commit(bar_drain);
+            }
+            __syncwarp();
+            drain_wait(bar_drain, 0u, kDrainNs);
+        }
+        if (warp == 0) {
+#pragma unroll 1
+            for (int s = 0; s < STAGES; ++s)
+                if ((armed_mask >> s) & 1u)
+                    drain_wait(bar_full + 8 * s, (armed_parity >> s) & 1u, kDrainNs);
+            if (lane == 0)
+                settle(kSettleNs);
+        }
+        __syncwarp();
+        __syncthreads();
+    }
+    ptx::tc_fence_before_sync();
+    if constexpr (CG == 2)
+        ptx::cluster_sync();
+    if (warp == 1) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc<CG>(tmem_base, Cfg::kTmemCols);
+    }
+}
+
+}  // namespace bwgemm

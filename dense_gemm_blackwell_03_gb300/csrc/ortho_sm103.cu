@@ -1,0 +1,225 @@
+// ortho_sm103.cu -- the Newton-Schulz products' instances and launches
+// (ortho_kernel.cuh), and the pass that brings the input into the workspace.
+#include <type_traits>
+
+#include "ortho_kernel.cuh"
+
+namespace bwgemm {
+namespace {
+
+template <int CG, bool A_MN, bool B_MN>
+cudaError_t launch_one(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2, const CUtensorMap& b2,
+                       const CUtensorMap& out, const CUtensorMap& out2, const OrthoParams& p, int grid,
+                       cudaStream_t stream, bool pdl)
+{
+    using Cfg = OrthoConfig<CG>;
+    auto kernel = ortho_kernel<CG, A_MN, B_MN>;
+    if (grid % CG != 0)
+        return cudaErrorInvalidValue;
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+    if (err != cudaSuccess)
+        return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid), 1, 1);
+    cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (CG == 2) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = 2;
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kernel, a, b, a2, b2, out, out2, p);
+}
+
+// ------------------------------------------------------------ the input pass
+// Both kernels are bound by HBM traffic: one read of G for the norm, one read
+// of G and one write of X (from L2 where G fits it).  A warp takes whole rows.
+constexpr int kInThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v)
+{
+    if constexpr (std::is_same<T, float>::value)
+        return v;
+    else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        return __bfloat162float(v);
+    else
+        return __half2float(v);
+}
+
+__device__ __forceinline__ float block_sum(float v, float* shared)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, d);
+    if ((threadIdx.x & 31) == 0)
+        shared[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kInThreads / 32; ++w)
+        s += shared[w];
+    __syncthreads();
+    return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kInThreads) ortho_sums_kernel(const OrthoInput p)
+{
+    __shared__ float shared[kInThreads / 32];
+    constexpr int V = 16 / int(sizeof(T));
+    const int lane = threadIdx.x & 31;
+    const int first = int(blockIdx.x) * (kInThreads / 32) + int(threadIdx.x >> 5);
+    const int step = int(gridDim.x) * (kInThreads / 32);
+    const T* g = static_cast<const T*>(p.g) + int64_t(blockIdx.y) * p.stride_g;
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    float sum = 0.f;
+    for (int r = first; r < p.rows; r += step) {
+        const T* row = g + int64_t(r) * p.ldg;
+        int c = 0;
+        if (p.vectors) {
+            const int whole = p.cols / V * V;
+#pragma unroll 4
+            for (c = lane * V; c < whole; c += 32 * V) {
+                const uint4 w = ptx::ld_global_cg_v4(row + c);
+                const T* x = reinterpret_cast<const T*>(&w);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float f = to_f32(x[i]);
+                    sum = fmaf(f, f, sum);
+                }
+            }
+            c = whole;
+        }
+        for (c += lane; c < p.cols; c += 32) {
+            const float f = to_f32(row[c]);
+            sum = fmaf(f, f, sum);
+        }
+    }
+    sum = block_sum(sum, shared);
+    if (threadIdx.x == 0)
+        p.sums[int64_t(blockIdx.y) * p.parts + blockIdx.x] = sum;
+}
+
+// X is stored as G times a power of two near 2^log2_scale / (|G| + eps): exact
+// for bf16 and fp16 input (but for elements below fp16's range, 2^-24 and less
+// of the largest), with elements around 2^log2_scale / sqrt(rows cols), clear
+// of fp16's subnormals.  The rest of the factor is applied to fp32 sums.
+template <typename T>
+__global__ void __launch_bounds__(kInThreads) ortho_convert_kernel(const OrthoInput p)
+{
+    __shared__ float shared[kInThreads / 32];
+    constexpr int V = 8;  // columns per lane and step
+    const int lane = threadIdx.x & 31;
+    const int first = int(blockIdx.x) * (kInThreads / 32) + int(threadIdx.x >> 5);
+    const int step = int(gridDim.x) * (kInThreads / 32);
+    const int64_t mat = blockIdx.y;
+    const T* g = static_cast<const T*>(p.g) + mat * p.stride_g;
+    uint16_t* hi = p.hi + mat * p.stride;
+    uint16_t* lo = p.lo ? p.lo + mat * p.stride : nullptr;
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    float sum = 0.f;
+    for (int i = threadIdx.x; i < p.parts; i += kInThreads)
+        sum += ptx::ld_global_cg_f32(p.sums + mat * p.parts + i);
+    const float norm = sqrtf(block_sum(sum, shared)) + p.eps;
+    int e = 0;
+    if (norm > 0.f && norm <= 3.0e38f)
+        e = min(max(p.log2_scale - ilogbf(norm), -120), 120);
+    const float up = ldexpf(1.f, e);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        const float f = ldexpf(1.f / norm, -e);
+        p.factors[mat] = f;
+        p.factors[p.batch + mat] = f * f;
+    }
+    for (int r = first; r < p.rows; r += step) {
+        const T* row = g + int64_t(r) * p.ldg;
+        for (int c = lane * V; c < int(p.ld); c += 32 * V) {
+            float x[V];
+            if (p.vectors && c + V <= p.cols) {
+                uint4 w[sizeof(T) / 2];
+#pragma unroll
+                for (int i = 0; i < int(sizeof(T) / 2); ++i)
+                    w[i] = ptx::ld_global_cg_v4(reinterpret_cast<const uint4*>(row + c) + i);
+                const T* t = reinterpret_cast<const T*>(w);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    x[i] = to_f32(t[i]) * up;
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    x[i] = c + i < p.cols ? to_f32(row[c + i]) * up : 0.f;
+            }
+            uint32_t h[V / 2], l[V / 2];
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                const __half2 a = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+                const float2 b = __half22float2(a);
+                const __half2 d = __floats2half2_rn(x[2 * i] - b.x, x[2 * i + 1] - b.y);
+                h[i] = *reinterpret_cast<const uint32_t*>(&a);
+                l[i] = *reinterpret_cast<const uint32_t*>(&d);
+            }
+            *reinterpret_cast<uint4*>(hi + int64_t(r) * p.ld + c) = make_uint4(h[0], h[1], h[2], h[3]);
+            if (lo)
+                *reinterpret_cast<uint4*>(lo + int64_t(r) * p.ld + c) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_input(const OrthoInput& p, cudaStream_t stream, bool pdl)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(p.parts), unsigned(p.batch), 1);
+    cfg.blockDim = dim3(kInThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, ortho_sums_kernel<T>, p);
+    return err != cudaSuccess ? err : cudaLaunchKernelEx(&cfg, ortho_convert_kernel<T>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_ortho_input(const OrthoInput& p, cudaStream_t stream, bool pdl)
+{
+    switch (p.dtype) {
+    case BWGEMM_BF16: return launch_input<__nv_bfloat16>(p, stream, pdl);
+    case BWGEMM_FP16: return launch_input<__half>(p, stream, pdl);
+    case BWGEMM_FP32: return launch_input<float>(p, stream, pdl);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_ortho(int form, int cg, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2,
+                         const CUtensorMap& b2, const CUtensorMap& out, const CUtensorMap& out2, const OrthoParams& p,
+                         int grid, cudaStream_t stream, bool pdl)
+{
+    switch (form * 2 + (cg - 1)) {
+    case kOrthoNT * 2: return launch_one<1, false, false>(a, b, a2, b2, out, out2, p, grid, stream, pdl);
+    case kOrthoNT * 2 + 1: return launch_one<2, false, false>(a, b, a2, b2, out, out2, p, grid, stream, pdl);
+    case kOrthoNN * 2: return launch_one<1, false, true>(a, b, a2, b2, out, out2, p, grid, stream, pdl);
+    case kOrthoNN * 2 + 1: return launch_one<2, false, true>(a, b, a2, b2, out, out2, p, grid, stream, pdl);
+    case kOrthoTN * 2: return launch_one<1, true, true>(a, b, a2, b2, out, out2, p, grid, stream, pdl);
+    case kOrthoTN * 2 + 1: return launch_one<2, true, true>(a, b, a2, b2, out, out2, p, grid, stream, pdl);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace bwgemm

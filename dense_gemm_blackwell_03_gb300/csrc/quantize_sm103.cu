@@ -46,7 +46,7 @@ struct Row8 {
         if (valid >= 8) {
 #pragma unroll
             for (int i = 0; i < kWords; i += 4) {
-                const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src) + i / 4);
+                const uint4 v = ptx::ld_global_cs_v4(reinterpret_cast<const uint4*>(src) + i / 4);
                 w[i] = v.x;
                 w[i + 1] = v.y;
                 w[i + 2] = v.z;

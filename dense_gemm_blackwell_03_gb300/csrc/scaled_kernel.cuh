@@ -591,10 +591,11 @@ __global__ void __launch_bounds__(ScaledConfig<CG, BN, SWAP, COLVEC>::kThreads, 
                 float* part = p.partials + (size_t(worker) * 2 + seg.slot) * stride + mine;
 #pragma unroll
                 for (int j = 0; j < COLS / 4; ++j) {
-                    float4 v;
-                    ptx::unpack_f32x2(acc[2 * j], v.x, v.y);
-                    ptx::unpack_f32x2(acc[2 * j + 1], v.z, v.w);
-                    __stcg(reinterpret_cast<float4*>(part + size_t(j) * 128), v);
+                    float a, b2, c, d;
+                    ptx::unpack_f32x2(acc[2 * j], a, b2);
+                    ptx::unpack_f32x2(acc[2 * j + 1], c, d);
+                    ptx::st_global_cg_v4(part + size_t(j) * 128, make_uint4(__float_as_uint(a), __float_as_uint(b2),
+                                                                            __float_as_uint(c), __float_as_uint(d)));
                 }
                 __threadfence();
                 __syncwarp();
@@ -622,11 +623,9 @@ __global__ void __launch_bounds__(ScaledConfig<CG, BN, SWAP, COLVEC>::kThreads, 
                         const float* src = p.partials + (size_t(w) * 2 + wslot) * stride + mine;
 #pragma unroll
                         for (int j = 0; j < COLS / 4; ++j) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + size_t(j) * 128));
-                            acc[2 * j] = ptx::fma_f32x2(
-                                ptx::pack_f32x2(__float_as_uint(v.x), __float_as_uint(v.y)), one2, acc[2 * j]);
-                            acc[2 * j + 1] = ptx::fma_f32x2(
-                                ptx::pack_f32x2(__float_as_uint(v.z), __float_as_uint(v.w)), one2, acc[2 * j + 1]);
+                            const uint4 v = ptx::ld_global_cg_v4(src + size_t(j) * 128);
+                            acc[2 * j] = ptx::fma_f32x2(ptx::pack_f32x2(v.x, v.y), one2, acc[2 * j]);
+                            acc[2 * j + 1] = ptx::fma_f32x2(ptx::pack_f32x2(v.z, v.w), one2, acc[2 * j + 1]);
                         }
                     }
                 }

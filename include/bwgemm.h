@@ -497,6 +497,44 @@ bwgemm_status_t bwgemm_run_scaled(bwgemm_plan_t plan, const bwgemm_scaled_t* A, 
                                   void* C, int64_t M, int64_t N, int64_t K, int64_t ldc, bwgemm_dtype_t out,
                                   int32_t accumulate, void* stream);
 
+/*
+ * Orthogonalise a stack of matrices by Newton-Schulz products, as the Muon
+ * optimiser does with a weight's momentum: with X = G / (|G|_F + eps),
+ *
+ *     `steps` times:  S = X X^T;  X <- a X + (b S + c S S) X
+ *
+ * (X^T X and X (...) when there are more rows than columns -- the same result),
+ * which drives all singular values towards one; the result is `scale` * X.
+ *
+ *   G : batch x rows x cols, bf16, fp16 or fp32 (`dtype`), row stride ldg and
+ *       matrix stride stride_g in elements (any; rows on 16-byte boundaries are
+ *       read in vectors).  Read only.
+ *   X : the result, bf16 or fp16 (`out`), strides ldx and stride_x (rows on
+ *       16-byte boundaries and cols a multiple of 8 are stored by TMA).  May be
+ *       G itself only if the types and strides are the same.
+ *   steps : 1..64
+ *   coefficients : host array of `steps` triples (a, b, c), read before the
+ *       call returns; NULL = (3.4445, -4.7750, 2.0315) in every step
+ *   eps >= 0; workspace: device memory, 256-byte aligned, of at least
+ *       bwgemm_orthogonalize_workspace() bytes (else BWGEMM_ERR_WORKSPACE),
+ *       holding nothing of use before or after
+ *
+ * Products take fp16 operands -- X in two terms where one would cost accuracy
+ * -- and sum in fp32; the norm is summed in fp32.  The relative error before
+ * the result's rounding is about 1e-3 for the default steps.  A matrix of
+ * zeros gives zeros; one holding a NaN or an infinity gives NaNs.
+ * Asynchronous: 2 + 3 steps launches, no allocation, capturable; errors as for
+ * bwgemm_run.
+ */
+bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_dtype_t dtype, void* X,
+                                     bwgemm_dtype_t out, int64_t batch, int64_t rows, int64_t cols, int64_t ldg,
+                                     int64_t stride_g, int64_t ldx, int64_t stride_x, int32_t steps,
+                                     const float* coefficients, float eps, float scale, void* workspace,
+                                     uint64_t workspace_bytes, void* stream);
+
+/* Host-only: the workspace bytes of bwgemm_orthogonalize for these sizes. */
+bwgemm_status_t bwgemm_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, uint64_t* bytes);
+
 /* Static text for a status code ("unknown status" for anything else). */
 const char* bwgemm_status_string(bwgemm_status_t status);
 
