@@ -56,9 +56,9 @@ bwgemm_status_t encode(CUtensorMap* map, CUtensorMapDataType type, uint32_t rank
 }
 
 // An 8-bit operand in boxes of 128 bytes x box_rows, and its 3-D view in boxes
-// of kScaledKps whole K blocks (dimension 2: K blocks, 128 bytes apart).
+// of `kps` whole K blocks (dimension 2: K blocks, 128 bytes apart).
 bwgemm_status_t encode_operand(CUtensorMap* map, CUtensorMap* map3, const bwgemm_scaled_t& x, int64_t rows, int64_t K,
-                               uint32_t box_rows)
+                               uint32_t box_rows, int kps)
 {
     const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
     const cuuint64_t strides[1] = {cuuint64_t(x.ld)};
@@ -69,11 +69,11 @@ bwgemm_status_t encode_operand(CUtensorMap* map, CUtensorMap* map3, const bwgemm
         return st;
     *map3 = *map;
     const int64_t chunks = K / kBlock;
-    if (chunks < kScaledKps)
+    if (chunks < kps)
         return BWGEMM_OK;
     const cuuint64_t dims3[3] = {cuuint64_t(kBlock), cuuint64_t(rows), cuuint64_t(chunks)};
     const cuuint64_t strides3[2] = {cuuint64_t(x.ld), cuuint64_t(kBlock)};
-    const cuuint32_t box3[3] = {uint32_t(kBlock), box_rows, uint32_t(kScaledKps)};
+    const cuuint32_t box3[3] = {uint32_t(kBlock), box_rows, uint32_t(kps)};
     return encode(map3, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, x.values, dims3, strides3, box3, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
@@ -98,78 +98,87 @@ bwgemm_status_t check_operand(const bwgemm_scaled_t* x, int64_t rows, int64_t K)
 // The compiled form and the division of the work for one product.
 struct ScaledPlan {
     int variant;
-    int workers, grid;
-    int num_l, num_c, dp_tiles, sk_tiles;
-    int64_t sk_iters;
+    int workers;
+    int l_rows, num_l, num_c, dp_tiles, sk_tiles;
+    int32_t sk_iters;
     int raster;
 };
 
-// Microseconds of one K block of a tile on its CTA (or pair): the larger of the
-// MMAs and of the bytes' way from L2 into shared memory.
-double block_us(const ScaledVariant& v)
+// Microseconds of one K block of a tile on its CTA: the bytes' way from L2 into
+// shared memory (150 GB/s and SM), or the handshake with the epilogue and its
+// additions (measured per form), whichever is longer.
+double block_us(const ScaledVariant& v, int l_rows)
 {
-    const double mma = 2.0 * 128 * v.bn * 128 / (v.bn >= 64 ? 16384.0 : 8192.0) / 1.9e3;
-    const double bytes = (128.0 + double(v.bn) / v.cg) * 128;
-    return std::max(mma, bytes / 150e3);
+    const double step = v.bn == 256 ? 0.56 : v.bn == 128 ? 0.32 : v.bn == 64 ? 0.17 : 0.1;
+    return std::max(step, (l_rows + v.bn) * 128.0 / 150e3);
 }
 
-ScaledPlan plan_scaled(int num_sms, int max_pairs, int64_t M, int64_t N, int64_t K, bool b_square,
-                       uint64_t workspace_bytes)
+ScaledPlan plan_scaled(int num_sms, int64_t M, int64_t N, int64_t K, bool b_square, uint64_t workspace_bytes)
 {
     const int64_t kb = blocks_of(K);
+    const int W = num_sms;
+    const double hbm_us = double(M + N) * double(K) / 6.5e6;  // both operands once
     ScaledPlan best = {};
     double best_us = 0;
     for (int i = 0; i < kNumScaledVariants; ++i) {
         const ScaledVariant& v = kScaledVariants[i];
         if (!v.swap && v.colvec == b_square)
             continue;  // the other form of the same tile
-        ScaledPlan s = {};
-        s.variant = i;
         const int64_t lrows = v.swap ? N : M, crows = v.swap ? M : N;
-        const int64_t nl = (lrows + v.cg * 128 - 1) / (v.cg * 128), nc = (crows + v.bn - 1) / v.bn;
-        const int64_t tiles = nl * nc;
-        if (tiles > (1ll << 30))
-            continue;
-        const int W = v.cg == 2 ? max_pairs : num_sms;
-        s.num_l = int(nl);
-        s.num_c = int(nc);
-        // whole tiles for the full waves; the rest in K iterations over all
-        // workers unless it nearly fills a wave itself, at least four K blocks
-        // a piece (a shorter piece costs more in partial sums than it saves)
-        const int64_t full = tiles / W * W, rest = tiles - full;
-        const uint64_t slot_bytes = uint64_t(v.cg) * 128 * v.bn * 4;
-        const bool room = kCounterRegionBytes + uint64_t(W) * 2 * slot_bytes <= workspace_bytes &&
-                          uint64_t(rest) * uint64_t(v.cg) * 8 * 4 <= kCounterRegionBytes;
-        const bool spread = rest > 0 && rest * 100 < int64_t(W) * 90 && room && (full > 0 || rest * kb / 4 > rest);
-        s.workers = W;
-        if (spread) {
-            s.dp_tiles = int(full);
-            s.sk_tiles = int(rest);
-            s.sk_iters = rest * kb;
-            if (full == 0)
-                s.workers = int(std::max<int64_t>(std::min<int64_t>(W, s.sk_iters / 4), 1));
-        } else {
-            s.dp_tiles = int(tiles);
-            s.workers = int(std::min<int64_t>(tiles, W));
-        }
-        s.grid = s.workers * v.cg;
-        const double us = block_us(v);
-        const double waves = double((s.dp_tiles + s.workers - 1) / s.workers);
-        double t = waves * double(kb) * us;
-        if (spread) {
-            const double pieces = double(s.workers) / double(rest);
-            t += double((s.sk_iters + s.workers - 1) / s.workers) * us;
-            // a piece's partial tile out, and the pieces of a tile in again by one CTA
-            if (pieces > 1.0)
-                t += (1.0 + pieces) * 128.0 * v.bn * 4 / 200e3 + 1.0;
-        }
-        if (best_us == 0 || t < best_us) {
-            best_us = t;
-            best = s;
+        const int64_t nc = (crows + v.bn - 1) / v.bn;
+        // tiles of 128 lane rows; in the swapped form also lower ones, as high as
+        // makes the tiles fill whole waves
+        for (int low = 0; low <= (v.swap ? 1 : 0); ++low) {
+            ScaledPlan s = {};
+            s.variant = i;
+            s.l_rows = 128;
+            if (low) {
+                const int64_t waves = ((lrows + 127) / 128 * nc + W - 1) / W;
+                const int64_t blocks = std::max<int64_t>(waves * W / nc, 1);
+                s.l_rows = int(std::min<int64_t>(128, ((lrows + blocks - 1) / blocks + 7) / 8 * 8));
+            }
+            const int64_t nl = (lrows + s.l_rows - 1) / s.l_rows, tiles = nl * nc;
+            if (tiles > (1ll << 30))
+                continue;
+            s.num_l = int(nl);
+            s.num_c = int(nc);
+            // whole tiles, or whole tiles for the full waves and the rest in K
+            // iterations over all workers, at least four K blocks a piece
+            const int64_t full = tiles / W * W, rest = tiles - full;
+            const uint64_t slot_bytes = uint64_t(128) * v.bn * 4;
+            const bool room = kCounterRegionBytes + uint64_t(W) * 2 * slot_bytes <= workspace_bytes &&
+                              uint64_t(rest) * 8 * 4 <= kCounterRegionBytes;
+            for (int spread = 0; spread <= (rest > 0 && room && rest * kb < (1ll << 30) ? 1 : 0); ++spread) {
+                s.workers = int(std::min<int64_t>(tiles, W));
+                s.dp_tiles = int(tiles);
+                s.sk_tiles = 0;
+                s.sk_iters = 0;
+                if (spread) {
+                    s.dp_tiles = int(full);
+                    s.sk_tiles = int(rest);
+                    s.sk_iters = int32_t(rest * kb);
+                    s.workers = full == 0 ? std::max(std::min(W, s.sk_iters / 4), 1) : W;
+                }
+                const double us = block_us(v, s.l_rows);
+                double t = double((s.dp_tiles + s.workers - 1) / s.workers) * double(kb) * us;
+                if (spread) {
+                    // a piece's partial tile out, the fence and the counter, and the
+                    // pieces of a tile in again by one CTA
+                    const double pieces = double(s.workers) / double(rest);
+                    t += double((s.sk_iters + s.workers - 1) / s.workers) * us;
+                    t += 4.0 + (1.0 + pieces) * 128.0 * v.bn * 4 / 200e3;
+                }
+                // bound by HBM, the form with the least work of its own is taken
+                t = std::max(t, hbm_us) + 0.1 * t;
+                if (best_us == 0 || t < best_us) {
+                    best_us = t;
+                    best = s;
+                }
+            }
         }
     }
     const ScaledVariant& v = kScaledVariants[best.variant];
-    best.raster = v.swap ? best.num_l : 8;
+    best.raster = v.swap ? best.num_l : 16;
     best.raster = std::max(1, std::min(best.raster, best.num_l));
     return best;
 }
@@ -358,8 +367,7 @@ bwgemm_status_t bwgemm_run_scaled(bwgemm_plan_t plan, const bwgemm_scaled_t* A, 
         return st;
 
     const ScaledPlan sel =
-        plan_scaled(plan->num_sms, plan->max_active[find_variant(2, 256, false, 1)], M, N, K,
-                    B->block == BWGEMM_BLOCK_SQUARE, plan->workspace_bytes);
+        plan_scaled(plan->num_sms, M, N, K, B->block == BWGEMM_BLOCK_SQUARE, plan->workspace_bytes);
     const ScaledVariant& v = kScaledVariants[sel.variant];
     const bwgemm_scaled_t& L = v.swap ? *B : *A;
     const bwgemm_scaled_t& R = v.swap ? *A : *B;
@@ -368,7 +376,10 @@ bwgemm_status_t bwgemm_run_scaled(bwgemm_plan_t plan, const bwgemm_scaled_t* A, 
     p.crows = int32_t(v.swap ? M : N);
     p.K = int32_t(K);
     p.num_kb = int32_t(blocks_of(K));
-    p.chunks = K / kBlock >= kScaledKps ? int32_t(K / kBlock) : 0;
+    const int kps = scaled_kps(v.bn, v.swap);
+    p.chunks = K / kBlock >= kps ? int32_t(K / kBlock) : 0;
+    p.stages = scaled_stages(v.bn, v.swap, sel.l_rows);
+    p.l_rows = sel.l_rows;
     p.num_l = sel.num_l;
     p.num_c = sel.num_c;
     p.raster_group = sel.raster;
@@ -387,7 +398,7 @@ bwgemm_status_t bwgemm_run_scaled(bwgemm_plan_t plan, const bwgemm_scaled_t* A, 
     p.accumulate = accumulate ? 1 : 0;
     // the instruction descriptor of the 16-bit products with the operand types
     // of kind::f8f6f4 (e4m3 = 0, e5m2 = 1) in the same fields
-    p.idesc = (make_idesc(BWGEMM_FP16, 128 * v.cg, v.bn) & ~((7u << 7) | (7u << 10))) | (uint32_t(L.type) << 7) |
+    p.idesc = (make_idesc(BWGEMM_FP16, 128, v.bn) & ~((7u << 7) | (7u << 10))) | (uint32_t(L.type) << 7) |
               (uint32_t(R.type) << 10);
     p.timeout_ns = plan->opts.timeout_ns ? plan->opts.timeout_ns : 4000000000ull;
     p.status = plan->d_status;
@@ -396,8 +407,8 @@ bwgemm_status_t bwgemm_run_scaled(bwgemm_plan_t plan, const bwgemm_scaled_t* A, 
     p.stall_kblock = plan->opts.stall_kblock;
 
     CUtensorMap ml, ml3, mc, mc3, mo;
-    if ((st = encode_operand(&ml, &ml3, L, p.lrows, K, uint32_t(kRowsPerCta))) != BWGEMM_OK ||
-        (st = encode_operand(&mc, &mc3, R, p.crows, K, uint32_t(v.bn / v.cg))) != BWGEMM_OK)
+    if ((st = encode_operand(&ml, &ml3, L, p.lrows, K, uint32_t(sel.l_rows), kps)) != BWGEMM_OK ||
+        (st = encode_operand(&mc, &mc3, R, p.crows, K, uint32_t(v.bn), kps)) != BWGEMM_OK)
         return st;
     mo = ml;
     if (!v.swap) {
@@ -411,7 +422,7 @@ bwgemm_status_t bwgemm_run_scaled(bwgemm_plan_t plan, const bwgemm_scaled_t* A, 
                          CU_TENSOR_MAP_L2_PROMOTION_NONE)) != BWGEMM_OK)
             return st;
     }
-    if (launch_scaled(sel.variant, ml, mc, ml3, mc3, mo, p, sel.grid, s, plan->opts.pdl_off == 0) != cudaSuccess)
+    if (launch_scaled(sel.variant, ml, mc, ml3, mc3, mo, p, sel.workers, s, plan->opts.pdl_off == 0) != cudaSuccess)
         return BWGEMM_ERR_CUDA;
     plan->launches += 1;
     return BWGEMM_OK;

@@ -48,10 +48,12 @@ struct ScaledParams {
     int32_t lrows, crows, K;      // rows of the lane-side and column-side operands
     int32_t num_kb;               // ceil(K / 128)
     int32_t chunks;               // whole 128-element K chunks (0: no 3-D views)
+    int32_t l_rows;               // lane rows per tile (swapped form: a multiple of 8, at most 128)
+    int32_t stages;               // of the ring (swapped form)
     int32_t num_l, num_c;         // blocks of lane rows and of columns
     int32_t raster_group;         // lane blocks walked before stepping along the columns
     int32_t dp_tiles, sk_tiles;   // tiles computed whole; tiles whose K iterations are spread over the workers
-    int64_t sk_iters;             // sk_tiles * num_kb
+    int32_t sk_iters;             // sk_tiles * num_kb
     const float* ls;              // scale of lane row r, K block kb: ls[kb * ls_ld + (r >> ls_shift)]
     int64_t ls_ld;
     const float* cs;              // and of column c
@@ -69,22 +71,31 @@ struct ScaledParams {
     int32_t stall_kblock;         // test hook, as in GemmParams
 };
 
-// Compiled forms: CTAs per MMA, columns per tile, operands swapped, and whether
-// the column side has a scale per column (the swapped forms always take one
-// per column and read one per 128 through it).
+// Compiled forms: columns per tile (128 lane rows each), operands swapped, and
+// whether the column side has a scale per column (the swapped forms always take
+// one per column and read one per 128 through it).
 struct ScaledVariant {
-    int cg, bn;
+    int bn;
     bool swap, colvec;
 };
 constexpr ScaledVariant kScaledVariants[] = {
-    {2, 256, false, false}, {2, 256, false, true}, {2, 128, false, false}, {2, 128, false, true},
-    {1, 128, true, true},   {1, 64, true, true},   {1, 32, true, true},    {1, 16, true, true},
+    {256, false, false}, {256, false, true}, {128, false, false}, {128, false, true},
+    {128, true, true},   {64, true, true},   {32, true, true},    {16, true, true},
 };
 constexpr int kNumScaledVariants = int(sizeof(kScaledVariants) / sizeof(kScaledVariants[0]));
-constexpr int kScaledKps = 2;  // K blocks per ring stage and TMA copy
+// K blocks per ring stage and TMA copy, and the ring: stages of kps * (l_rows +
+// bn) rows of 128 bytes
+constexpr int scaled_kps(int bn, bool swap) { return swap && bn <= 32 ? 4 : 2; }
+constexpr int kScaledRingBytes = 192 * 1024;
+constexpr int kScaledMaxStages = 10;
+constexpr int scaled_stages(int bn, bool swap, int l_rows)
+{
+    const int n = kScaledRingBytes / (scaled_kps(bn, swap) * (l_rows + bn) * kBlock);
+    return n < kScaledMaxStages ? n : kScaledMaxStages;
+}
 
-// l / c: the operands in boxes of 128 bytes x (128 | bn / cg) rows; l3 / c3:
-// their 3-D views of kScaledKps K blocks; out: C in 64-byte x 32-row boxes
+// l / c: the operands in boxes of 128 bytes x (128 | bn) rows; l3 / c3:
+// their 3-D views of scaled_kps() K blocks; out: C in 64-byte x 32-row boxes
 // (operands in order only).
 cudaError_t launch_scaled(int idx, const CUtensorMap& l, const CUtensorMap& c, const CUtensorMap& l3,
                           const CUtensorMap& c3, const CUtensorMap& out, const ScaledParams& p, int grid,

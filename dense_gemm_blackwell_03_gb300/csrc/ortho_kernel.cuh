@@ -28,8 +28,8 @@
 // GEMM kernel.
 #pragma once
 
-#include "gemm_kernel.cuh"
 #include "operators.h"
+#include "pipeline.cuh"
 
 namespace bwgemm {
 
@@ -69,26 +69,6 @@ __device__ __forceinline__ uint64_t make_sdesc_mn(uint32_t smem)
     d |= uint64_t(1) << 46;
     d |= uint64_t(2) << 61;
     return d;
-}
-
-__device__ __forceinline__ bool ortho_wait(uint32_t bar, uint32_t parity, const OrthoParams& p,
-                                           volatile uint32_t* abort_flag, uint32_t code)
-{
-    if (ptx::mbar_try_wait(bar, parity))
-        return true;
-    WaitClock clock;
-#pragma unroll 1
-    while (true) {
-        if (ptx::mbar_try_wait(bar, parity))
-            return true;
-        if (*abort_flag)
-            return false;
-        if (clock.expired(p.timeout_ns)) {
-            atomicOr(p.status, code);
-            *abort_flag = 1u;
-            return false;
-        }
-    }
 }
 
 struct OrthoTile {
@@ -232,7 +212,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
 #pragma unroll 1
             for (int i = 0; i < steps; ++i, ++n) {
                 ok = __all_sync(0xffffffffu,
-                                ortho_wait(bar_empty + 8 * s, phase ^ 1u, p, abort_flag, kStatusProducerTimeout));
+                                pipe_wait(bar_empty + 8 * s, phase ^ 1u, p, abort_flag, kStatusProducerTimeout));
                 if (!ok)
                     break;
                 const bool stall = p.stall_kblock >= 0 && blockIdx.x == 0 && p.stall_kblock == n;
@@ -280,10 +260,10 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
 #pragma unroll 1
         for (int t = worker; ok && t < total; t += workers) {
             ok = __all_sync(0xffffffffu,
-                            ortho_wait(bar_acc_empty + 8 * b, bphase ^ 1u, p, abort_flag, kStatusMmaTimeout));
+                            pipe_wait(bar_acc_empty + 8 * b, bphase ^ 1u, p, abort_flag, kStatusMmaTimeout));
 #pragma unroll 1
             for (int i = 0; ok && i < steps; ++i) {
-                ok = __all_sync(0xffffffffu, ortho_wait(bar_full + 8 * s, phase, p, abort_flag, kStatusMmaTimeout));
+                ok = __all_sync(0xffffffffu, pipe_wait(bar_full + 8 * s, phase, p, abort_flag, kStatusMmaTimeout));
                 if (!ok)
                     break;
                 ptx::tc_fence_after_sync();
@@ -336,7 +316,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
             const float alpha = p.alpha_dev ? p.alpha * ptx::ld_global_cg_f32(p.alpha_dev + x.matrix) : p.alpha;
             const bool mirror = p.symmetric && x.r != x.c;
             ok = __all_sync(0xffffffffu,
-                            ortho_wait(bar_acc_full + 8 * b, bphase, p, abort_flag, kStatusEpilogueTimeout));
+                            pipe_wait(bar_acc_full + 8 * b, bphase, p, abort_flag, kStatusEpilogueTimeout));
             if (!ok)
                 break;
             ptx::tc_fence_after_sync();
@@ -356,7 +336,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                 ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c), v);
                 ptx::tmem_ld_wait();
                 if (c + 32 >= Cfg::kCols)
-                    release_accumulator<CG>(bar_acc_empty + 8 * b, lane, 0);
+                    hand_back<CG>(bar_acc_empty + 8 * b, lane);
                 // the box itself, and its mirror image: columns of D from its rows, up
                 // to the padded width (zeros there, which later products read)
                 const bool direct = row0 < p.rows && col < p.store_cols;

@@ -8,23 +8,32 @@
 // overwrites) and the outer sum lives in the epilogue warps' registers: while
 // the MMAs of the next block run into another TMEM buffer, eight warps read
 // the finished block and add it, weighted, to their running sums with paired
-// fp32 FMAs.  Per 128 x 256 block of a CTA that is 512 cycles of MMA beside
-// 256 cycles of TMEM reads and 128 (a scale per 128 columns) or about 320 (one
-// per column) issue slots per scheduler, so the tensor pipe stays the bound.
+// fp32 FMAs.
 //
-//   warp 0      TMA producer: a ring of stages of two K blocks (64 KiB for a
-//               256 x 256 pair tile), one 3-D copy per operand and stage -- a
-//               copy of two blocks moves about 1.7 times the bytes per second
-//               and SM of single-block copies.
-//   warp 1      TMEM allocator and (even CTA) MMA issuer: 4 tcgen05.mma of
-//               K = 32 per block, kBufs accumulators in turn.
-//   the others  epilogue: 8 warps, two per TMEM lane quarter with half the
+// What bounds it, on large products: per K block of a 128 x 256 tile the MMAs
+// take 512 cycles, the FMAs 256 (512 with a scale per column, which is one more
+// multiplication each), and the path of a block through the epilogue -- barrier,
+// two TMEM loads, additions, hand-back, each waiting for the one before -- about
+// 1050; the two TMEM buffers let that overlap only with the next block's MMAs.
+// 8192 x 28672 x 8192 runs at 2.2 PFLOP/s, with a scale per column 8192^3 at 1.55;
+// the same kernel without the additions at 2.5.  Tried and slower: CTA pairs (half
+// the copies, but every hand-back crosses the pair; 2.1), 192 columns with twelve
+// epilogue warps of 64 (1.9), 128 columns (1.7), TMEM loads of 32 columns.
+// On few rows of A it is bound by HBM: see the swapped form.
+//
+//   warp 0      TMA producer: a ring of stages of several K blocks, one 3-D copy
+//               per operand and stage (fewer, larger copies: a stage costs its
+//               barrier round trip whatever its size).
+//   warp 1      TMEM allocator and MMA issuer: 4 tcgen05.mma of K = 32 per block,
+//               kBufs accumulators in turn.  Narrow tiles: warp 2 issues too.
+//   warp 3      the scales.
+//   warps 4..   epilogue: 8 warps, two per TMEM lane quarter with half the
 //               columns each (tiles of 128 and 256 columns), else 4.
 //
-// The scales reach each epilogue warp through a small ring of its own in shared
-// memory filled with 4-byte asynchronous copies a few blocks ahead (across tile
-// boundaries too), so neither their latency nor a barrier between warps stands
-// in the loop.
+// The scales come through a ring of their own in shared memory, filled by a
+// warp with 4-byte asynchronous copies as far ahead as it holds (across tile
+// boundaries too): the epilogue neither computes an address nor waits for a
+// load, and the scales need no alignment.
 //
 // Work: the last, partial wave of tiles is spread over all workers in K
 // iterations (stream-K).  A worker's piece of a tile goes to an fp32 partial in
@@ -33,50 +42,62 @@
 // waits for anybody.
 //
 // Swapped form (few rows of A): the weights fill the 128 lanes, A's rows are
-// the MMA's N, C leaves through plain stores (a warp's 32 lanes are 32
-// consecutive columns of C).
+// the MMA's N (16 to 128), C leaves through plain stores (a warp's 32 lanes are
+// 32 consecutive columns of C).  Tiles may hold fewer than 128 weight rows, so
+// that they fill the SMs without splitting K, and up to four K blocks share an
+// accumulator hand-over.  One row on an 8192 x 8192 weight takes 19.6 us (10.0 at
+// the copy rate of HBM), 64 rows on 28672 x 8192 take 51.6 us (35.7).
 #pragma once
 
-#include "gemm_kernel.cuh"
 #include "operators.h"
+#include "pipeline.cuh"
 
 namespace bwgemm {
 
-template <int CG, int BN, bool SWAP, bool COLVEC>
+template <int BN, bool SWAP, bool COLVEC>
 struct ScaledConfig {
-    static constexpr int kKps = kScaledKps;
-    static constexpr int kEpiWarps = BN >= 128 ? 8 : 4;
-    // 256 columns: 128 running sums per thread need more registers than an even
-    // share of the file (168 at ten warps and more).  The launch then has three
-    // warpgroups -- producer, MMA and two idle warps in the first -- and the
-    // first gives registers to the two of the epilogue: 128 x 56 + 256 x 224 =
-    // 64512, the 384 x 168 that the block is launched with (the launch code
-    // checks the compiled count).
-    static constexpr bool kSplitRegs = BN == 256;
-    static constexpr int kFirstEpi = kSplitRegs ? 4 : 2;
+    static constexpr int kKps = scaled_kps(BN, SWAP);
+    // Four warps of producer, MMA issue and scales, then the epilogue.  With eight
+    // epilogue warps a thread has 64 or 128 running sums and 64 loaded values,
+    // more registers than an even share of the file (168 at twelve warps), and
+    // the first warpgroup gives some of its own: 128 x 56 + 256 x 224 = 64512, the
+    // 384 x 168 that the block is launched with (the launch code checks the
+    // compiled count).
+    static constexpr int kCols = BN >= 128 ? BN / 2 : BN;   // columns per epilogue warp
+    static constexpr int kEpiWarps = 4 * (BN / kCols);
+    static constexpr int kFirstEpi = 4;
     static constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+    static constexpr bool kSplitRegs = BN >= 128;
     static constexpr int kRegsFirst = 56, kRegsEpi = 224;
-    static constexpr int kCols = BN >= 128 ? BN / 2 : BN;  // columns per epilogue warp
+    static constexpr int kLoadCols = 64;  // columns per TMEM load: of one K block, or of several
     static constexpr int kLBlock = kRowsPerCta * kBlock;   // one K block of the lane side: 16 KiB
-    static constexpr int kCRows = BN / CG;                 // column-side rows this CTA copies
-    static constexpr int kCBlock = kCRows * kBlock;
-    static constexpr int kLBytes = kKps * kLBlock;
+    static constexpr int kCBlock = BN * kBlock;
+    // the ring: whole stages of the lane side, then of the column side; with
+    // fewer lane rows (swapped form) more stages fit
     static constexpr int kCBytes = kKps * kCBlock;
-    static constexpr int kStages = (192 * 1024) / (kLBytes + kCBytes);
-    static constexpr int kBufs = BN == 256 ? 2 : 4;        // accumulators in TMEM
-    static constexpr int kTmemCols = kBufs * BN;
+    static constexpr int kMaxStages = SWAP ? kScaledMaxStages : scaled_stages(BN, SWAP, kRowsPerCta);
+    // K blocks per handshake between the MMAs and the epilogue, each in columns
+    // of its own: a handshake takes either about 0.3 us, more than a narrow
+    // block's MMAs and additions (1 x 28672 x 8192: 53 us one by one, 46 joined)
+    static constexpr int kJoin = !SWAP ? 1 : BN <= 32 ? 4 : BN == 64 ? 2 : 1;
+    static constexpr int kIssuers = kJoin > 1 ? 2 : 1;     // MMA warps
+    static constexpr int kBufCols = kJoin * BN;
+    static constexpr int kBufs = kBufCols == 256 ? 2 : 4;  // such accumulators in TMEM
+    static constexpr int kTmemCols = kBufs * kBufCols;
     static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM allocation");
-    // per warp: scale slots of 32 lane scales and the column scales (or 32
-    // copies of the one scale of its columns)
-    static constexpr int kSlots = COLVEC && BN == 256 ? 3 : 4;
-    static constexpr int kSlotBytes = 4 * (32 + (COLVEC ? kCols : 32));
+    // a scale slot holds four K blocks' scales: [lane][block], and [column group
+    // of a warp][block] or, with a scale per column, [block][column]
+    static constexpr int kGroup = 4;
+    static constexpr int kColScaleOff = 4 * kGroup * kRowsPerCta;
+    static constexpr int kSlotBytes = kColScaleOff + 4 * kGroup * (COLVEC ? BN : 4);
+    static constexpr int kSlots = COLVEC && BN > 128 ? 2 : 3;
+    static constexpr int kScaleThreads = 32;
     static constexpr int kStoreBytes = 2048;  // a 64-byte x 32-row output box
-    static constexpr int kOffL = 0;
-    static constexpr int kOffC = kStages * kLBytes;
-    static constexpr int kOffStore = kOffC + kStages * kCBytes;
+    static constexpr int kOffStore = kScaledRingBytes;
     static constexpr int kOffScale = kOffStore + (SWAP ? 0 : kEpiWarps * kStoreBytes);
-    static constexpr int kOffBar = kOffScale + kEpiWarps * kSlots * kSlotBytes;
-    static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 1;  // full, empty, acc_full, acc_empty, drain
+    static constexpr int kOffBar = kOffScale + kSlots * kSlotBytes;
+    // full, empty, acc_full, acc_empty, scale_full, scale_empty, drain
+    static constexpr int kNumBars = 2 * (kMaxStages + kBufs + kSlots) + 1;
     static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars;
     static constexpr int kOffAbort = kOffTmemSlot + 4;
     static constexpr int kSmemBytes = kOffAbort + 4 + 1024;  // + slack to align the base to 1 KiB
@@ -96,13 +117,13 @@ struct ScaledSegment {
 // The pieces of work of one worker: its share of the stream-K iterations, then
 // whole tiles.  Every role walks the same sequence.
 struct ScaledIter {
-    long long it, it_begin, it_end;
+    int it, it_begin, it_end;
     int t, step;
 
-    static __device__ __forceinline__ long long begin(const ScaledParams& p, int worker, int workers)
+    static __device__ __forceinline__ int begin(const ScaledParams& p, int worker, int workers)
     {
         const long long prod = (long long)worker * p.sk_iters;
-        return prod < (1ll << 32) ? (long long)(unsigned(prod) / unsigned(workers)) : prod / workers;
+        return prod < (1ll << 32) ? int(unsigned(prod) / unsigned(workers)) : int(prod / workers);
     }
     __device__ __forceinline__ void init(const ScaledParams& p, int worker, int workers)
     {
@@ -114,9 +135,9 @@ struct ScaledIter {
     __device__ __forceinline__ bool next(const ScaledParams& p, ScaledSegment& s)
     {
         if (it < it_end) {
-            const int tile = int(it / p.num_kb);
-            s.kb0 = int(it - (long long)tile * p.num_kb);
-            s.kb1 = int(min((long long)p.num_kb, s.kb0 + (it_end - it)));
+            const int tile = it / p.num_kb;
+            s.kb0 = it - tile * p.num_kb;
+            s.kb1 = min(p.num_kb, s.kb0 + (it_end - it));
             s.whole = s.kb0 == 0 && s.kb1 == p.num_kb;
             s.slot = it == it_begin ? 0 : 1;
             s.tile = p.dp_tiles + tile;
@@ -142,76 +163,16 @@ struct ScaledIter {
     }
 };
 
-__device__ __forceinline__ bool scaled_wait(uint32_t bar, uint32_t parity, const ScaledParams& p,
-                                            volatile uint32_t* abort_flag, uint32_t code)
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[N])
 {
-    if (ptx::mbar_try_wait(bar, parity))
-        return true;
-    WaitClock clock;
-#pragma unroll 1
-    while (true) {
-        if (ptx::mbar_try_wait(bar, parity))
-            return true;
-        if (*abort_flag)
-            return false;
-        if (clock.expired(p.timeout_ns)) {
-            atomicOr(p.status, code);
-            *abort_flag = 1u;
-            return false;
-        }
-    }
+    if constexpr (N == 64)
+        ptx::tmem_ld_32x32b_x64(taddr, r);
+    else if constexpr (N == 32)
+        ptx::tmem_ld_32x32b_x32(taddr, r);
+    else
+        ptx::tmem_ld_32x32b_x16(taddr, r);
 }
-
-// Fills one epilogue warp's ring of scale slots, K block after K block of the
-// warp's segments: slot i % SLOTS holds the i-th block's.
-template <int CG, int BN, bool SWAP, bool COLVEC>
-struct ScaleFeed {
-    using Cfg = ScaledConfig<CG, BN, SWAP, COLVEC>;
-    ScaledIter iter;
-    ScaledSegment seg;
-    int kb, n;
-    bool live;
-
-    __device__ __forceinline__ void init(const ScaledParams& p, int worker, int workers)
-    {
-        iter.init(p, worker, workers);
-        live = iter.next(p, seg);
-        kb = seg.kb0;
-        n = 0;
-    }
-    // Start the copies of one block's scales (an empty group once all are read).
-    __device__ __forceinline__ void issue(const ScaledParams& p, uint32_t ring, int rank, int q, int col, int lane)
-    {
-        if (live) {
-            const uint32_t slot = ring + uint32_t((n % Cfg::kSlots) * Cfg::kSlotBytes);
-            const int row = (seg.l_blk * CG + rank) * kRowsPerCta + 32 * q + lane;
-            const bool in = row < p.lrows;
-            ptx::cp_async_4(slot + 4 * lane, p.ls + (in ? int64_t(kb) * p.ls_ld + (row >> p.ls_shift) : 0), in ? 4 : 0);
-            if constexpr (COLVEC) {
-#pragma unroll
-                for (int i = 0; i < (Cfg::kCols + 31) / 32; ++i) {
-                    if (Cfg::kCols >= 32 || lane < Cfg::kCols) {
-                        const int c = seg.c_blk * BN + col + 32 * i + lane;
-                        const bool cin = c < p.crows;
-                        ptx::cp_async_4(slot + 128 + 4 * (32 * i + lane),
-                                        p.cs + (cin ? int64_t(kb) * p.cs_ld + (c >> p.cs_shift) : 0), cin ? 4 : 0);
-                    }
-                }
-            } else {
-                const int c = seg.c_blk * BN + col;  // the warp's columns share one block of 128
-                const bool cin = c < p.crows;
-                ptx::cp_async_4(slot + 128 + 4 * lane, p.cs + (cin ? int64_t(kb) * p.cs_ld + (c >> p.cs_shift) : 0),
-                                cin ? 4 : 0);
-            }
-            if (++kb == seg.kb1) {
-                live = iter.next(p, seg);
-                kb = seg.kb0;
-            }
-            ++n;
-        }
-        ptx::cp_async_commit();
-    }
-};
 
 __device__ __forceinline__ void scaled_store_one(const ScaledParams& p, int64_t row, int64_t col, float v)
 {
@@ -226,16 +187,17 @@ __device__ __forceinline__ void scaled_store_one(const ScaledParams& p, int64_t 
     }
 }
 
-// One thread's finished row piece (kCols sums of lane row `row`) to C.
-template <int CG, int BN, bool SWAP, bool COLVEC>
-__device__ __forceinline__ void scaled_store(const uint64_t (&acc)[ScaledConfig<CG, BN, SWAP, COLVEC>::kCols / 2],
+// A warp's finished sums (kCols of lane row row0 + lane, `rows` of them in the
+// tile) to C.
+template <int BN, bool SWAP, bool COLVEC>
+__device__ __forceinline__ void scaled_store(const uint64_t (&acc)[ScaledConfig<BN, SWAP, COLVEC>::kCols / 2],
                                              const ScaledParams& p, const CUtensorMap* tmap_out, uint32_t buf,
-                                             int row0, int col0, int lane)
+                                             int row0, int rows, int col0, int lane)
 {
-    using Cfg = ScaledConfig<CG, BN, SWAP, COLVEC>;
+    using Cfg = ScaledConfig<BN, SWAP, COLVEC>;
     if constexpr (SWAP) {
         const int n = row0 + lane;  // column of C
-        if (n < p.lrows) {
+        if (lane < rows && n < p.lrows) {
 #pragma unroll
             for (int j = 0; j < Cfg::kCols / 2; ++j) {
                 float lo, hi;
@@ -321,14 +283,13 @@ __device__ __forceinline__ void scaled_store(const uint64_t (&acc)[ScaledConfig<
     }
 }
 
-template <int CG, int BN, bool SWAP, bool COLVEC>
-__global__ void __launch_bounds__(ScaledConfig<CG, BN, SWAP, COLVEC>::kThreads, 1)
+template <int BN, bool SWAP, bool COLVEC>
+__global__ void __launch_bounds__(ScaledConfig<BN, SWAP, COLVEC>::kThreads, 1)
     scaled_kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUtensorMap tmap_c,
                   const __grid_constant__ CUtensorMap tmap_l3, const __grid_constant__ CUtensorMap tmap_c3,
                   const __grid_constant__ CUtensorMap tmap_out, const ScaledParams p)
 {
-    using Cfg = ScaledConfig<CG, BN, SWAP, COLVEC>;
-    constexpr int STAGES = Cfg::kStages;
+    using Cfg = ScaledConfig<BN, SWAP, COLVEC>;
     constexpr int KPS = Cfg::kKps;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -336,34 +297,48 @@ __global__ void __launch_bounds__(ScaledConfig<CG, BN, SWAP, COLVEC>::kThreads, 
     uint8_t* smem = smem_raw + (base - raw);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;
-    const int worker = int(blockIdx.x) / CG;
-    const int workers = int(gridDim.x) / CG;
-    const uint32_t sL = base + Cfg::kOffL;
-    const uint32_t sC = base + Cfg::kOffC;
+    const int worker = int(blockIdx.x);
+    const int workers = int(gridDim.x);
+    // Lane rows of a tile, and the bytes of one K block of them: 128, or fewer
+    // (swapped form) where that gives every CTA a tile of its own.  The MMAs then
+    // read on into whatever lies behind the rows -- later stages, or the column
+    // side, which is larger than the rows left out; the lanes that this fills are
+    // not stored.
+    const int l_rows = SWAP ? p.l_rows : kRowsPerCta;
+    const int l_block = l_rows * kBlock;
+    const int l_bytes = KPS * l_block;
+    const int stages = SWAP ? p.stages : Cfg::kMaxStages;
+    const uint32_t sL = base;
+    const uint32_t sC = base + uint32_t(stages * l_bytes);
     const uint32_t bar_full = base + Cfg::kOffBar;              // + 8 * stage
-    const uint32_t bar_empty = bar_full + 8 * STAGES;           // + 8 * stage
-    const uint32_t bar_acc_full = bar_empty + 8 * STAGES;       // + 8 * buffer
+    const uint32_t bar_empty = bar_full + 8 * Cfg::kMaxStages;           // + 8 * stage
+    const uint32_t bar_acc_full = bar_empty + 8 * Cfg::kMaxStages;       // + 8 * buffer
     const uint32_t bar_acc_empty = bar_acc_full + 8 * Cfg::kBufs;
-    const uint32_t bar_drain = bar_acc_empty + 8 * Cfg::kBufs;  // after an abort: the issued MMAs completed
+    const uint32_t bar_scale_full = bar_acc_empty + 8 * Cfg::kBufs;   // + 8 * slot
+    const uint32_t bar_scale_empty = bar_scale_full + 8 * Cfg::kSlots;
+    const uint32_t bar_drain = bar_scale_empty + 8 * Cfg::kSlots;  // after an abort: the issued MMAs completed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffTmemSlot);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffAbort);
 
-    // K blocks of the stage that starts at block kb of a segment: two when both
-    // are whole chunks of the 3-D views, else one (a ragged last block, or a
-    // single one left over)
+    // K blocks of the stage that starts at block kb of a segment: KPS when all are
+    // whole chunks of the 3-D views, else one (a ragged last block, or single
+    // ones left over)
     auto blocks_at = [&](int kb, int kb1) { return kb + KPS <= min(p.chunks, kb1) ? KPS : 1; };
 
     if (threadIdx.x == 64) {
-        for (int s = 0; s < STAGES; ++s) {
-            ptx::mbar_init(bar_full + 8 * s, 1);   // the even CTA's producer's arrive.expect_tx (+ bytes)
-            ptx::mbar_init(bar_empty + 8 * s, 1);  // one tcgen05.commit
+        for (int s = 0; s < Cfg::kMaxStages; ++s) {
+            ptx::mbar_init(bar_full + 8 * s, 1);   // the producer's arrive.expect_tx (+ bytes)
+            ptx::mbar_init(bar_empty + 8 * s, Cfg::kIssuers);  // a tcgen05.commit of each MMA warp
         }
         for (int b = 0; b < Cfg::kBufs; ++b) {
-            ptx::mbar_init(bar_acc_full + 8 * b, 1);
-            ptx::mbar_init(bar_acc_empty + 8 * b, CG * Cfg::kEpiWarps);
+            ptx::mbar_init(bar_acc_full + 8 * b, Cfg::kIssuers);
+            ptx::mbar_init(bar_acc_empty + 8 * b, Cfg::kEpiWarps);
         }
-        ptx::mbar_init(bar_drain, 1);
+        for (int i = 0; i < Cfg::kSlots; ++i) {
+            ptx::mbar_init(bar_scale_full + 8 * i, Cfg::kScaleThreads);
+            ptx::mbar_init(bar_scale_empty + 8 * i, Cfg::kEpiWarps);
+        }
+        ptx::mbar_init(bar_drain, Cfg::kIssuers);
         *abort_flag = 0u;
         ptx::fence_mbar_init();
     }
@@ -378,14 +353,11 @@ __global__ void __launch_bounds__(ScaledConfig<CG, BN, SWAP, COLVEC>::kThreads, 
             ptx::prefetch_tensormap(&tmap_out);
     }
     if (warp == 1) {
-        ptx::tmem_alloc<CG>(ptx::smem_addr(tmem_slot), Cfg::kTmemCols);
-        ptx::tmem_relinquish<CG>();
+        ptx::tmem_alloc<1>(ptx::smem_addr(tmem_slot), Cfg::kTmemCols);
+        ptx::tmem_relinquish<1>();
     }
     ptx::tc_fence_before_sync();
-    if constexpr (CG == 2)
-        ptx::cluster_sync();  // both CTAs' barriers exist before either copies or commits to them
-    else
-        __syncthreads();
+    __syncthreads();
     ptx::tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
     ptx::launch_dependents();
@@ -397,7 +369,6 @@ __global__ void __launch_bounds__(ScaledConfig<CG, BN, SWAP, COLVEC>::kThreads, 
         if (warp == 0) {
             // ------------------------------------------------------ TMA producer
             ptx::grid_dependency_wait();
-            const uint32_t leader_full = CG == 2 ? ptx::map_to_cta(bar_full, 0) : bar_full;
             ScaledIter iter;
             ScaledSegment seg;
             iter.init(p, worker, workers);
@@ -405,54 +376,49 @@ __global__ void __launch_bounds__(ScaledConfig<CG, BN, SWAP, COLVEC>::kThreads, 
             uint32_t phase = 0;
             bool ok = true;
             while (ok && iter.next(p, seg)) {
-                const int l_row = (seg.l_blk * CG + int(rank)) * kRowsPerCta;
-                const int c_row = seg.c_blk * BN + int(rank) * Cfg::kCRows;
+                const int l_row = seg.l_blk * l_rows;
+                const int c_row = seg.c_blk * BN;
     #pragma unroll 1
                 for (int kb = seg.kb0; kb < seg.kb1; ++i) {
                     const int nkb = blocks_at(kb, seg.kb1);
                     ok = __all_sync(0xffffffffu,
-                                    scaled_wait(bar_empty + 8 * s, phase ^ 1u, p, abort_flag, kStatusProducerTimeout));
+                                    pipe_wait(bar_empty + 8 * s, phase ^ 1u, p, abort_flag, kStatusProducerTimeout));
                     if (!ok)
                         break;
                     // test hook: the producer of CTA 0 never fills this stage of the launch
                     const bool stall = p.stall_kblock >= 0 && blockIdx.x == 0 && p.stall_kblock == i;
-                    if (!stall && rank == 0) {
+                    if (!stall) {
                         armed_mask |= 1u << s;
                         armed_parity = (armed_parity & ~(1u << s)) | (phase << s);
                     }
                     if (!stall && ptx::elect_one()) {
-                        const uint32_t fb = leader_full + 8 * s;
-                        const uint32_t dL = sL + uint32_t(s * Cfg::kLBytes), dC = sC + uint32_t(s * Cfg::kCBytes);
-                        if (rank == 0)
-                            ptx::mbar_arrive_expect_tx(fb, uint32_t(CG * nkb * (Cfg::kLBlock + Cfg::kCBlock)));
-                        if constexpr (CG == 2) {
-                            if (nkb == KPS) {
-                                ptx::tma_load_3d_pair(dL, &tmap_l3, fb, 0, l_row, kb);
-                                ptx::tma_load_3d_pair(dC, &tmap_c3, fb, 0, c_row, kb);
-                            } else {
-                                ptx::tma_load_2d_pair(dL, &tmap_l, fb, kb * kBlock, l_row);
-                                ptx::tma_load_2d_pair(dC, &tmap_c, fb, kb * kBlock, c_row);
-                            }
+                        const uint32_t fb = bar_full + 8 * s;
+                        const uint32_t dL = sL + uint32_t(s * l_bytes), dC = sC + uint32_t(s * Cfg::kCBytes);
+                        ptx::mbar_arrive_expect_tx(fb, uint32_t(nkb * (l_block + Cfg::kCBlock)));
+                        if (nkb == KPS) {
+                            ptx::tma_load_3d(dL, &tmap_l3, fb, 0, l_row, kb);
+                            ptx::tma_load_3d(dC, &tmap_c3, fb, 0, c_row, kb);
                         } else {
-                            if (nkb == KPS) {
-                                ptx::tma_load_3d(dL, &tmap_l3, fb, 0, l_row, kb);
-                                ptx::tma_load_3d(dC, &tmap_c3, fb, 0, c_row, kb);
-                            } else {
-                                ptx::tma_load_2d(dL, &tmap_l, fb, kb * kBlock, l_row);
-                                ptx::tma_load_2d(dC, &tmap_c, fb, kb * kBlock, c_row);
-                            }
+                            ptx::tma_load_2d(dL, &tmap_l, fb, kb * kBlock, l_row);
+                            ptx::tma_load_2d(dC, &tmap_c, fb, kb * kBlock, c_row);
                         }
                     }
                     __syncwarp();
                     kb += nkb;
-                    if (++s == STAGES) {
+                    if (++s == stages) {
                         s = 0;
                         phase ^= 1u;
                     }
                 }
             }
-        } else if (warp == 1 && rank == 0) {
+        } else if (warp <= Cfg::kIssuers) {
             // ---------------------------------------------------------- MMA issue
+            // With joint accumulators warps 1 and 2 take every other block of a
+            // stage: one warp's serial path through waits, issue and
+            // commits is some 600 cycles a block, more than a narrow block needs
+            // otherwise.  Both wait for every stage and accumulator, and a stage is
+            // free, an accumulator full, when both have committed.
+            const int w = warp - 1;
             const uint64_t l_desc0 = make_sdesc_sw128(sL);
             const uint64_t c_desc0 = make_sdesc_sw128(sC);
             const uint32_t tmem0 = __shfl_sync(0xffffffffu, tmem_base, 0);
@@ -463,47 +429,124 @@ __global__ void __launch_bounds__(ScaledConfig<CG, BN, SWAP, COLVEC>::kThreads, 
             uint32_t phase = 0, bphase = 0;
             bool ok = true;
             while (ok && iter.next(p, seg)) {
-    #pragma unroll 1
+                int sub = 0;  // block of the joint accumulator
+#pragma unroll 1
                 for (int kb = seg.kb0; ok && kb < seg.kb1;) {
                     const int nkb = blocks_at(kb, seg.kb1);
-                    ok = __all_sync(0xffffffffu, scaled_wait(bar_full + 8 * s, phase, p, abort_flag, kStatusMmaTimeout));
-    #pragma unroll 1
-                    for (int c = 0; ok && c < nkb; ++c) {
-                        ok = __all_sync(0xffffffffu, scaled_wait(bar_acc_empty + 8 * b, bphase ^ 1u, p, abort_flag,
-                                                                 kStatusMmaTimeout));
+                    ok = __all_sync(0xffffffffu, pipe_wait(bar_full + 8 * s, phase, p, abort_flag, kStatusMmaTimeout));
+                    // block c of the stage into column block d of the accumulator
+                    auto issue = [&](int c, int d) {
+                        const uint64_t ld = l_desc0 + uint64_t((s * l_bytes + c * l_block) >> 4);
+                        const uint64_t cd = c_desc0 + uint64_t((s * Cfg::kCBytes + c * Cfg::kCBlock) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            ptx::mma_f8<1>(tmem0 + uint32_t(b * Cfg::kBufCols + d * BN), ld + uint64_t(2 * kk),
+                                           cd + uint64_t(2 * kk), p.idesc, kk > 0 ? 1u : 0u);
+                    };
+                    if constexpr (Cfg::kIssuers == 2) {
+                        static_assert(Cfg::kJoin % KPS == 0, "a stage lies in one accumulator");
+                        if (ok && sub == 0)
+                            ok = __all_sync(0xffffffffu, pipe_wait(bar_acc_empty + 8 * b, bphase ^ 1u, p, abort_flag,
+                                                                   kStatusMmaTimeout));
                         if (!ok)
                             break;
                         ptx::tc_fence_after_sync();
+                        const bool last = sub + nkb >= Cfg::kJoin || kb + nkb == seg.kb1;
                         if (ptx::elect_one()) {
-                            const uint64_t ld = l_desc0 + uint64_t((s * Cfg::kLBytes + c * Cfg::kLBlock) >> 4);
-                            const uint64_t cd = c_desc0 + uint64_t((s * Cfg::kCBytes + c * Cfg::kCBlock) >> 4);
-    #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                ptx::mma_f8<CG>(tmem0 + uint32_t(b * BN), ld + uint64_t(2 * kk), cd + uint64_t(2 * kk),
-                                                p.idesc, kk > 0 ? 1u : 0u);
-                            if constexpr (CG == 2) {
-                                if (c == nkb - 1)
-                                    ptx::mma_commit_pair(bar_empty + 8 * s, 0x3);
-                                ptx::mma_commit_pair(bar_acc_full + 8 * b, 0x3);
-                            } else {
+                            for (int c = w; c < nkb; c += 2)
+                                issue(c, sub + c);
+                            ptx::mma_commit(bar_empty + 8 * s);
+                            if (last)
+                                ptx::mma_commit(bar_acc_full + 8 * b);
+                        }
+                        __syncwarp();
+                        sub += nkb;
+                        if (last) {
+                            sub = 0;
+                            b = (b + 1) & (Cfg::kBufs - 1);
+                            bphase ^= b == 0 ? 1u : 0u;
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; ok && c < nkb; ++c) {
+                            ok = __all_sync(0xffffffffu, pipe_wait(bar_acc_empty + 8 * b, bphase ^ 1u, p, abort_flag,
+                                                                   kStatusMmaTimeout));
+                            if (!ok)
+                                break;
+                            ptx::tc_fence_after_sync();
+                            if (ptx::elect_one()) {
+                                issue(c, 0);
                                 if (c == nkb - 1)
                                     ptx::mma_commit(bar_empty + 8 * s);
                                 ptx::mma_commit(bar_acc_full + 8 * b);
                             }
-                        }
-                        __syncwarp();
-                        if (++b == Cfg::kBufs) {
-                            b = 0;
-                            bphase ^= 1u;
+                            __syncwarp();
+                            b = (b + 1) & (Cfg::kBufs - 1);
+                            bphase ^= b == 0 ? 1u : 0u;
                         }
                     }
                     kb += nkb;
-                    if (++s == STAGES) {
+                    if (++s == stages) {
                         s = 0;
                         phase ^= 1u;
                     }
                 }
             }
+        } else if (warp == 3) {
+            // -------------------------------------------------------- scales
+            // Each thread's arrival on a slot comes when its copies have landed, so the
+            // warp runs ahead of the epilogue as far as the slots allow.
+            ptx::grid_dependency_wait();
+            ScaledIter iter;
+            ScaledSegment seg;
+            iter.init(p, worker, workers);
+            int slot = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            while (ok && iter.next(p, seg)) {
+                const int row0 = seg.l_blk * l_rows;
+                const int col0 = seg.c_blk * BN;
+#pragma unroll 1
+                for (int kb = seg.kb0; kb < seg.kb1; kb += Cfg::kGroup) {
+                    ok = __all_sync(0xffffffffu, pipe_wait(bar_scale_empty + 8 * slot, phase ^ 1u, p, abort_flag,
+                                                           kStatusProducerTimeout));
+                    if (!ok)
+                        break;
+                    const int n = min(Cfg::kGroup, seg.kb1 - kb);
+#pragma unroll 1
+                    for (int g = 0; g < n; ++g) {
+                        const uint32_t dst = base + uint32_t(Cfg::kOffScale + slot * Cfg::kSlotBytes);
+                        const uint32_t dst_c = dst + Cfg::kColScaleOff;
+                        const float* ls = p.ls + int64_t(kb + g) * p.ls_ld;
+                        const float* cs = p.cs + int64_t(kb + g) * p.cs_ld;
+#pragma unroll
+                        for (int i = 0; i < kRowsPerCta / 32; ++i) {
+                            const int row = row0 + 32 * i + lane;
+                            ptx::cp_async_4(dst + 4 * (Cfg::kGroup * (32 * i + lane) + g),
+                                            ls + (row < p.lrows ? row >> p.ls_shift : 0), row < p.lrows ? 4 : 0);
+                        }
+                        if constexpr (COLVEC) {
+#pragma unroll
+                            for (int i = 0; i < (BN + 31) / 32; ++i) {
+                                const int col = col0 + 32 * i + lane;
+                                if (BN >= 32 || lane < BN)
+                                    ptx::cp_async_4(dst_c + 4 * (BN * g + 32 * i + lane),
+                                                    cs + (col < p.crows ? col >> p.cs_shift : 0), col < p.crows ? 4 : 0);
+                            }
+                        } else if (lane < BN / Cfg::kCols) {
+                            const int col = col0 + lane * Cfg::kCols;  // a warp's columns share one block of 128
+                            ptx::cp_async_4(dst_c + 4 * (Cfg::kGroup * lane + g),
+                                            cs + (col < p.crows ? col >> p.cs_shift : 0), col < p.crows ? 4 : 0);
+                        }
+                    }
+                    ptx::cp_async_arrive(bar_scale_full + 8 * slot);
+                    if (++slot == Cfg::kSlots) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            ptx::cp_async_wait_all();
         }
     } else {
         // ------------------------------------------------------------ epilogue
@@ -514,18 +557,12 @@ __global__ void __launch_bounds__(ScaledConfig<CG, BN, SWAP, COLVEC>::kThreads, 
         const int e = warp - Cfg::kFirstEpi;
         const int q = warp & 3;            // the TMEM lane quarter this warp may access
         const int col = (e >> 2) * COLS;   // its first column of the tile
-        const uint32_t ring = base + uint32_t(Cfg::kOffScale + e * Cfg::kSlots * Cfg::kSlotBytes);
         const uint32_t store_buf = base + uint32_t(Cfg::kOffStore + e * Cfg::kStoreBytes);
-        ScaleFeed<CG, BN, SWAP, COLVEC> feed;
-        feed.init(p, worker, workers);
-#pragma unroll 1
-        for (int i = 0; i < Cfg::kSlots - 1; ++i)
-            feed.issue(p, ring, int(rank), q, col, lane);
         ScaledIter iter;
         ScaledSegment seg;
         iter.init(p, worker, workers);
         int b = 0, slot = 0;
-        uint32_t bphase = 0;
+        uint32_t bphase = 0, sphase = 0;
         bool ok = true;
         while (ok && iter.next(p, seg)) {
             uint64_t acc[COLS / 2];
@@ -533,61 +570,87 @@ __global__ void __launch_bounds__(ScaledConfig<CG, BN, SWAP, COLVEC>::kThreads, 
             for (int j = 0; j < COLS / 2; ++j)
                 acc[j] = 0ull;
 #pragma unroll 1
-            for (int kb = seg.kb0; kb < seg.kb1; ++kb) {
-                ptx::cp_async_wait<Cfg::kSlots - 2>();
-                __syncwarp();  // every lane's part of the slot has landed, and the slot before it has been read
-                feed.issue(p, ring, int(rank), q, col, lane);
-                const uint32_t sl = ring + uint32_t(slot * Cfg::kSlotBytes);
-                float scale = ptx::ld_shared_f32(sl + 4 * lane);
-                if constexpr (!COLVEC)
-                    scale *= ptx::ld_shared_f32(sl + 128 + 4 * lane);
-                const uint64_t scale2 = ptx::pack_f32x2(__float_as_uint(scale), __float_as_uint(scale));
-                ok = __all_sync(0xffffffffu, scaled_wait(bar_acc_full + 8 * b, bphase, p, abort_flag,
-                                                         kStatusEpilogueTimeout));
-                if (!ok)
-                    break;
-                ptx::tc_fence_after_sync();
-                const uint32_t taddr = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(b * BN + col);
-                uint32_t r[2][16];
-                ptx::tmem_ld_32x32b_x16(taddr, r[0]);
+            for (int kb = seg.kb0; ok && kb < seg.kb1; kb += Cfg::kGroup) {
+                // the group's four scales of this lane, with its warp's column
+                // scales where it has one per block
+                ok = __all_sync(0xffffffffu, pipe_wait(bar_scale_full + 8 * slot, sphase, p, abort_flag,
+                                                       kStatusEpilogueTimeout));
+                const uint32_t sl = base + uint32_t(Cfg::kOffScale + slot * Cfg::kSlotBytes);
+                const uint32_t scale_empty = bar_scale_empty + 8 * slot;
+                float4 ls = ptx::ld_shared_f32x4(sl + 16 * (32 * q + lane));
+                if constexpr (!COLVEC) {
+                    const float4 cs = ptx::ld_shared_f32x4(sl + Cfg::kColScaleOff + 16 * (e >> 2));
+                    ls = make_float4(ls.x * cs.x, ls.y * cs.y, ls.z * cs.z, ls.w * cs.w);
+                }
+                if (++slot == Cfg::kSlots) {
+                    slot = 0;
+                    sphase ^= 1u;
+                }
 #pragma unroll
-                for (int c = 0; c < COLS; c += 16) {
-                    ptx::tmem_ld_wait();
-                    if (c + 16 < COLS)
-                        ptx::tmem_ld_32x32b_x16(taddr + uint32_t(c + 16), r[((c >> 4) + 1) & 1]);
-                    else
-                        release_accumulator<CG>(bar_acc_empty + 8 * b, lane, 0);
-                    const uint32_t(&v)[16] = r[(c >> 4) & 1];
+                for (int g = 0; g < Cfg::kGroup; g += Cfg::kJoin) {
+                    if (!ok || kb + g >= seg.kb1)
+                        break;
+                    const int blocks = min(Cfg::kJoin, seg.kb1 - kb - g);  // in this accumulator
+                    ok = __all_sync(0xffffffffu, pipe_wait(bar_acc_full + 8 * b, bphase, p, abort_flag,
+                                                           kStatusEpilogueTimeout));
+                    if (!ok)
+                        break;
+                    ptx::tc_fence_after_sync();
+                    const uint32_t taddr = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(b * Cfg::kBufCols + col);
+                    const uint32_t empty = bar_acc_empty + 8 * b;
+                    b = (b + 1) & (Cfg::kBufs - 1);
+                    bphase ^= b == 0 ? 1u : 0u;
+                    constexpr int LD = Cfg::kLoadCols;
+                    constexpr int TOTAL = Cfg::kJoin * COLS;  // columns this warp reads
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        uint64_t x0 = ptx::pack_f32x2(v[2 * j], v[2 * j + 1]);
-                        uint64_t x1 = ptx::pack_f32x2(v[2 * j + 2], v[2 * j + 3]);
-                        if constexpr (COLVEC) {
-                            uint64_t c0, c1;
-                            ptx::ld_shared_v2_b64(sl + 128 + 4 * uint32_t(c + 2 * j), c0, c1);
-                            x0 = ptx::mul_f32x2(x0, c0);
-                            x1 = ptx::mul_f32x2(x1, c1);
+                    for (int i = 0; i < TOTAL; i += LD) {
+                        uint32_t v[LD];
+                        tmem_load<LD>(taddr + uint32_t(i), v);
+                        ptx::tmem_ld_wait();
+                        if (i + LD == TOTAL)
+                            hand_back<1>(empty, lane);
+                        // the piece's columns, K block by K block
+#pragma unroll
+                        for (int part = 0; part < LD; part += COLS < LD ? COLS : LD) {
+                            const int sub = (i + part) / COLS;
+                            if (sub > 0 && sub >= blocks)
+                                continue;
+                            const int k = g + sub;
+                            const float scale = k == 0 ? ls.x : k == 1 ? ls.y : k == 2 ? ls.z : ls.w;
+                            const uint64_t scale2 = ptx::pack_f32x2(__float_as_uint(scale), __float_as_uint(scale));
+                            const uint32_t sc = sl + Cfg::kColScaleOff + 4 * (BN * k + col);
+                            const int c0 = (i + part) % COLS;  // first column
+#pragma unroll
+                            for (int j = 0; j < (COLS < LD ? COLS : LD); j += 4) {
+                                uint64_t x0 = ptx::pack_f32x2(v[part + j], v[part + j + 1]);
+                                uint64_t x1 = ptx::pack_f32x2(v[part + j + 2], v[part + j + 3]);
+                                if constexpr (COLVEC) {
+                                    uint64_t m0, m1;
+                                    ptx::ld_shared_v2_b64(sc + 4 * uint32_t(c0 + j), m0, m1);
+                                    x0 = ptx::mul_f32x2(x0, m0);
+                                    x1 = ptx::mul_f32x2(x1, m1);
+                                }
+                                acc[(c0 + j) / 2] = ptx::fma_f32x2(x0, scale2, acc[(c0 + j) / 2]);
+                                acc[(c0 + j) / 2 + 1] = ptx::fma_f32x2(x1, scale2, acc[(c0 + j) / 2 + 1]);
+                            }
                         }
-                        acc[c / 2 + j] = ptx::fma_f32x2(x0, scale2, acc[c / 2 + j]);
-                        acc[c / 2 + j + 1] = ptx::fma_f32x2(x1, scale2, acc[c / 2 + j + 1]);
                     }
                 }
-                if (++b == Cfg::kBufs) {
-                    b = 0;
-                    bphase ^= 1u;
-                }
-                if (++slot == Cfg::kSlots)
-                    slot = 0;
+                // relaxed: the slot's scales have been read into registers and used by
+                // now, in every lane
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive_relaxed(scale_empty);
             }
             if (!ok)
                 break;
-            const int row0 = (seg.l_blk * CG + int(rank)) * kRowsPerCta + 32 * q;
+            const int row0 = seg.l_blk * l_rows + 32 * q;
             bool done = seg.whole;
             if (!done) {
                 // publish this piece; whoever brings the tile's last K block adds
                 // all pieces in worker order
-                const size_t stride = size_t(CG) * Cfg::kPartialFloats;
-                const size_t mine = rank * size_t(Cfg::kPartialFloats) + size_t(e) * (32 * COLS) + 4 * lane;
+                const size_t stride = Cfg::kPartialFloats;
+                const size_t mine = size_t(e) * (32 * COLS) + 4 * lane;
                 float* part = p.partials + (size_t(worker) * 2 + seg.slot) * stride + mine;
 #pragma unroll
                 for (int j = 0; j < COLS / 4; ++j) {
@@ -600,7 +663,7 @@ __global__ void __launch_bounds__(ScaledConfig<CG, BN, SWAP, COLVEC>::kThreads, 
                 __threadfence();
                 __syncwarp();
                 const int st = seg.tile - p.dp_tiles;
-                uint32_t* counter = p.counters + (size_t(st) * CG + rank) * Cfg::kEpiWarps + e;
+                uint32_t* counter = p.counters + size_t(st) * Cfg::kEpiWarps + e;
                 uint32_t before = 0;
                 if (lane == 0)
                     before = ptx::atom_add_acq_rel_gpu(counter, uint32_t(seg.kb1 - seg.kb0));
@@ -631,9 +694,8 @@ __global__ void __launch_bounds__(ScaledConfig<CG, BN, SWAP, COLVEC>::kThreads, 
                 }
             }
             if (done)
-                scaled_store<CG, BN, SWAP, COLVEC>(acc, p, &tmap_out, store_buf, row0, seg.c_blk * BN + col, lane);
+                scaled_store<BN, SWAP, COLVEC>(acc, p, &tmap_out, store_buf, row0, l_rows - 32 * q, seg.c_blk * BN + col, lane);
         }
-        ptx::cp_async_wait<0>();
         if (!SWAP && lane == 0)
             ptx::bulk_wait_group_all();
         __syncwarp();
@@ -641,24 +703,19 @@ __global__ void __launch_bounds__(ScaledConfig<CG, BN, SWAP, COLVEC>::kThreads, 
 
     // --------------------------------------------------------------- teardown
     // After an abort, drain the MMAs and the loads this CTA armed (bounded) and
-    // settle before TMEM and shared memory are released; the even CTA's barriers
-    // count both CTAs' loads and neither CTA leaves before the other.
+    // settle before TMEM and shared memory are released.
     __syncwarp();
     __syncthreads();
     if (*abort_flag) {
-        if (warp == 1 && rank == 0) {
-            if (ptx::elect_one()) {
-                if constexpr (CG == 2)
-                    ptx::mma_commit_pair(bar_drain, 0x1);
-                else
-                    ptx::mma_commit(bar_drain);
-            }
+        if (warp >= 1 && warp <= Cfg::kIssuers) {
+            if (ptx::elect_one())
+                ptx::mma_commit(bar_drain);
             __syncwarp();
             drain_wait(bar_drain, 0u, kDrainNs);
         }
         if (warp == 0) {
 #pragma unroll 1
-            for (int s = 0; s < STAGES; ++s)
+            for (int s = 0; s < stages; ++s)
                 if ((armed_mask >> s) & 1u)
                     drain_wait(bar_full + 8 * s, (armed_parity >> s) & 1u, kDrainNs);
             if (lane == 0)
@@ -668,11 +725,10 @@ __global__ void __launch_bounds__(ScaledConfig<CG, BN, SWAP, COLVEC>::kThreads, 
         __syncthreads();
     }
     ptx::tc_fence_before_sync();
-    if constexpr (CG == 2)
-        ptx::cluster_sync();
+    __syncthreads();
     if (warp == 1) {
         ptx::tc_fence_after_sync();
-        ptx::tmem_dealloc<CG>(tmem_base, Cfg::kTmemCols);
+        ptx::tmem_dealloc<1>(tmem_base, Cfg::kTmemCols);
     }
 }
 

@@ -5,14 +5,12 @@
 namespace bwgemm {
 namespace {
 
-template <int CG, int BN, bool SWAP, bool COLVEC>
+template <int BN, bool SWAP, bool COLVEC>
 cudaError_t launch_sc(const CUtensorMap& l, const CUtensorMap& c, const CUtensorMap& l3, const CUtensorMap& c3,
                       const CUtensorMap& out, const ScaledParams& p, int grid, cudaStream_t stream, bool pdl)
 {
-    using Cfg = ScaledConfig<CG, BN, SWAP, COLVEC>;
-    auto kernel = scaled_kernel<CG, BN, SWAP, COLVEC>;
-    if (grid % CG != 0)
-        return cudaErrorInvalidValue;
+    using Cfg = ScaledConfig<BN, SWAP, COLVEC>;
+    auto kernel = scaled_kernel<BN, SWAP, COLVEC>;
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
     if (err != cudaSuccess)
         return err;
@@ -32,22 +30,11 @@ cudaError_t launch_sc(const CUtensorMap& l, const CUtensorMap& c, const CUtensor
     cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
     cfg.dynamicSmemBytes = Cfg::kSmemBytes;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    unsigned n = 0;
-    if (CG == 2) {
-        attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = 2;
-        attr[n].val.clusterDim.y = 1;
-        attr[n].val.clusterDim.z = 1;
-        ++n;
-    }
-    if (pdl) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n].val.programmaticStreamSerializationAllowed = 1;
-        ++n;
-    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = n;
+    cfg.numAttrs = pdl ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, l, c, l3, c3, out, p);
 }
 
@@ -59,14 +46,14 @@ cudaError_t launch_scaled(int idx, const CUtensorMap& l, const CUtensorMap& c, c
 {
     static_assert(kNumScaledVariants == 8, "one case per variant below, in the order of kScaledVariants");
     switch (idx) {
-    case 0: return launch_sc<2, 256, false, false>(l, c, l3, c3, out, p, grid, stream, pdl);
-    case 1: return launch_sc<2, 256, false, true>(l, c, l3, c3, out, p, grid, stream, pdl);
-    case 2: return launch_sc<2, 128, false, false>(l, c, l3, c3, out, p, grid, stream, pdl);
-    case 3: return launch_sc<2, 128, false, true>(l, c, l3, c3, out, p, grid, stream, pdl);
-    case 4: return launch_sc<1, 128, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
-    case 5: return launch_sc<1, 64, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
-    case 6: return launch_sc<1, 32, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
-    case 7: return launch_sc<1, 16, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 0: return launch_sc<256, false, false>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 1: return launch_sc<256, false, true>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 2: return launch_sc<128, false, false>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 3: return launch_sc<128, false, true>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 4: return launch_sc<128, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 5: return launch_sc<64, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 6: return launch_sc<32, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 7: return launch_sc<16, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
     default: return cudaErrorInvalidValue;
     }
 }
