@@ -14,5 +14,7 @@ __all__ = ["BF16", "FP16", "BwgemmError", "Plan", "PlanOptions", "gemm", "gemm_s
 
 def __getattr__(name):
     if name in __all__:
-        return getattr(importlib.import_module(".binding", __name__), name)
+        value = getattr(importlib.import_module(".binding", __name__), name)
+        globals()[name] = value  # found directly from now on
+        return value
     raise AttributeError(name)

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 BF16 = 0
@@ -221,8 +222,8 @@ def load_library(build_if_missing: bool = False):
         lib.bwgemm_quantize.argtypes = [vp, vp, ci, i64, i64, i64, ci, ci, i32, vp, i64, vp, i64, vp, i64, vp,
                                         i64, vp]
         lib.bwgemm_quantize.restype = st
-        lib.bwgemm_run_scaled.argtypes = [vp, ctypes.POINTER(Scaled), ctypes.POINTER(Scaled), vp, i64, i64, i64,
-                                          i64, ci, i32, vp]
+        # the two bwgemm_scaled_t as plain addresses: the fastest argument to pass
+        lib.bwgemm_run_scaled.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, ci, i32, vp]
         lib.bwgemm_run_scaled.restype = st
         lib.bwgemm_orthogonalize.argtypes = [vp, vp, ci, vp, ci, i64, i64, i64, i64, i64, i64, i64, i32,
                                              ctypes.POINTER(ctypes.c_float), ctypes.c_float, ctypes.c_float, vp,
@@ -282,29 +283,36 @@ def _ld(t) -> int:
 
 
 def _padded_empty(rows: int, cols: int, dtype, device, multiple: int):
-    """An uninitialised rows x cols matrix whose rows start `multiple` elements apart or more."""
+    """An uninitialised rows x cols matrix whose rows start a multiple of `multiple` elements apart."""
     ld = -(-cols // multiple) * multiple
-    t = _torch().empty((rows, ld), dtype=dtype, device=device)
-    return t[:, :cols] if ld != cols else t
+    if ld == cols:
+        return _torch_mod.empty((rows, cols), dtype=dtype, device=device)
+    return _torch_mod.empty_strided((rows, cols), (ld, 1), dtype=dtype, device=device)
 
 
-def _scaled(values, scales, name: str) -> Scaled:
-    """The descriptor of 8-bit `values` (R x K) with `scales` ((K blocks) x (R or row blocks))."""
+# bwgemm_scaled_t as a packed record (native sizes and alignment)
+_SCALED = struct.Struct("@PqPqii")
+assert _SCALED.size == ctypes.sizeof(Scaled)
+
+
+def _pack_scaled(into: Scaled, values, scales, name: str):
+    """Describe 8-bit `values` (R x K) with `scales` ((K blocks) x (R or row blocks))
+    in `into`; returns (R, K)."""
     code = _fp8_codes.get(values.dtype)
     if code is None:
         raise TypeError(f"{name} must be float8_e4m3fn or float8_e5m2, got {values.dtype}")
-    if scales.dtype != _torch().float32:
+    if scales.dtype is not _torch_mod.float32:
         raise TypeError(f"the scales of {name} must be float32, got {scales.dtype}")
     rows, K = values.shape
-    ld = _ld(values)
-    if values.shape[0] == 1:
-        ld = -(-ld // 16) * 16  # a single row has no next one
-    kb, per = scales.shape
-    if kb != -(-K // BLOCK) or (per != rows and per != -(-rows // BLOCK)):
+    blocks, per = scales.shape
+    rb = -(-rows // BLOCK)
+    if blocks != -(-K // BLOCK) or (per != rows and per != rb):
         raise ValueError(f"the scales of {name} ({rows} x {K}) must be {-(-K // BLOCK)} x {rows} or "
-                         f"{-(-K // BLOCK)} x {-(-rows // BLOCK)}, got {tuple(scales.shape)}")
-    return Scaled(values.data_ptr(), ld, scales.data_ptr(), _ld(scales), code,
-                  BLOCK_ROW if per == rows else BLOCK_SQUARE)
+                         f"{-(-K // BLOCK)} x {rb}, got {tuple(scales.shape)}")
+    ld = _ld(values) if rows > 1 else -(-K // 16) * 16  # a single row has no next one
+    _SCALED.pack_into(into, 0, values.data_ptr(), ld, scales.data_ptr(), _ld(scales), code,
+                      BLOCK_ROW if per == rows else BLOCK_SQUARE)
+    return rows, K
 
 
 def select_config(num_sms: int, M: int, N: int, K: int, dtype: int = BF16, max_pairs: int = 0,
@@ -365,6 +373,8 @@ class Plan:
         if rc != 0:
             raise BwgemmError(rc, "bwgemm_create_plan")
         self.handle = h
+        self._a, self._b = Scaled(), Scaled()  # gemm_scaled's operands, rewritten by every call
+        self._a_at, self._b_at = ctypes.addressof(self._a), ctypes.addressof(self._b)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -450,6 +460,12 @@ class Plan:
         if t.get_device() != self.device:
             raise ValueError(f"{name} is on {t.device}, the plan on cuda:{self.device}")
 
+    def _stream(self, stream) -> int:
+        """The raw handle of `stream`, or of the device's current stream."""
+        if stream is None:
+            return _torch_mod._C._cuda_getCurrentRawStream(self.device)
+        return stream.cuda_stream
+
     def quantize(self, X, blocks: str = "row", transposed: bool = False, pow2: bool = False, dtype=None,
                  stream=None):
         """``bwgemm_quantize``: the 2-D CUDA tensor X (bf16, fp16 or fp32) in 8 bits
@@ -479,42 +495,42 @@ class Plan:
             ldx = -(-ldx // 8) * 8  # a single row has no next one
         square = blocks == "square"
         kb, rb = -(-cols // BLOCK), -(-rows // BLOCK)
+        per, per_t = (rb, kb) if square else (rows, cols)
         dev = X.device
         q = _padded_empty(rows, cols, dtype, dev, 16)
-        s = torch.empty((kb, rb if square else rows), dtype=torch.float32, device=dev)
-        qt = st = None
+        s = torch.empty((kb, per), dtype=torch.float32, device=dev)
+        result = (q, s)
         args_t = (None, 0, None, 0)
         if transposed:
             qt = _padded_empty(cols, rows, dtype, dev, 16)
-            st = torch.empty((rb, kb if square else cols), dtype=torch.float32, device=dev)
-            args_t = (qt.data_ptr(), qt.stride(0), st.data_ptr(), st.stride(0))
-        h = (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+            st = torch.empty((rb, per_t), dtype=torch.float32, device=dev)
+            args_t = (qt.data_ptr(), -(-rows // 16) * 16, st.data_ptr(), per_t)
+            result = (q, s, qt, st)
         rc = self.lib.bwgemm_quantize(self.handle, X.data_ptr(), dt, rows, cols, ldx,
                                       BLOCK_SQUARE if square else BLOCK_ROW, f8, int(pow2), q.data_ptr(),
-                                      q.stride(0), s.data_ptr(), s.stride(0), *args_t, h)
+                                      -(-cols // 16) * 16, s.data_ptr(), per, *args_t, self._stream(stream))
         if rc != 0:
             raise BwgemmError(rc, "bwgemm_quantize")
-        return (q, s, qt, st) if transposed else (q, s)
+        return result
 
     def gemm_scaled(self, A, scale_a, B, scale_b, out=None, out_dtype=None, accumulate: bool = False, stream=None):
         """``bwgemm_run_scaled``: ``out = A @ B.T`` of 8-bit CUDA tensors A (M x K) and
         B (N x K) with their block scales, as `quantize` returns them.  `out_dtype`:
         bf16 (default), fp16 or fp32; `accumulate` adds to an fp32 `out`."""
         torch = _torch()
-        self._check_tensor("A", A)
-        self._check_tensor("B", B)
-        self._check_tensor("scale_a", scale_a)
-        self._check_tensor("scale_b", scale_b)
-        a = _scaled(A, scale_a, "A")
-        b = _scaled(B, scale_b, "B")
-        M, K = A.shape
-        N, Kb = B.shape
+        dev = self.device
+        if (A.get_device() != dev or B.get_device() != dev or scale_a.get_device() != dev
+                or scale_b.get_device() != dev):
+            for name, t in (("A", A), ("scale_a", scale_a), ("B", B), ("scale_b", scale_b)):
+                self._check_tensor(name, t)
+        M, K = _pack_scaled(self._a, A, scale_a, "A")
+        N, Kb = _pack_scaled(self._b, B, scale_b, "B")
         if Kb != K:
             raise ValueError(f"K mismatch: A is {tuple(A.shape)}, B is {tuple(B.shape)}")
         if out is None:
             if accumulate:
                 raise ValueError("accumulate needs the out tensor to add to")
-            out = _padded_empty(M, N, out_dtype or torch.bfloat16, A.device, 8)
+            out = _padded_empty(M, N, torch.bfloat16 if out_dtype is None else out_dtype, A.device, 8)
         else:
             self._check_tensor("out", out)
             if tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
@@ -522,11 +538,9 @@ class Plan:
         dt = _all_dtype_codes.get(out.dtype)
         if dt is None:
             raise TypeError(f"gemm_scaled writes bfloat16, float16 or float32, got {out.dtype}")
-        ldc = _ld(out)
-        if M == 1:
-            ldc = -(-ldc // 8) * 8  # a single row has no next one
-        h = (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
-        rc = self.lib.bwgemm_run_scaled(self.handle, a, b, out.data_ptr(), M, N, K, ldc, dt, int(accumulate), h)
+        ldc = _ld(out) if M > 1 else -(-N // 8) * 8  # a single row has no next one
+        rc = self.lib.bwgemm_run_scaled(self.handle, self._a_at, self._b_at, out.data_ptr(), M, N, K, ldc, dt,
+                                        int(accumulate), self._stream(stream))
         if rc != 0:
             raise BwgemmError(rc, "bwgemm_run_scaled")
         return out
@@ -568,10 +582,8 @@ class Plan:
         if rc != 0:
             raise BwgemmError(rc, "bwgemm_orthogonalize_workspace")
         ws = torch.empty(need.value, dtype=torch.uint8, device=G.device)
-        if stream is None:
-            h = torch.cuda.current_stream(self.device).cuda_stream
-        else:
-            h = stream.cuda_stream
+        h = self._stream(stream)
+        if stream is not None:
             ws.record_stream(stream)
         rc = self.lib.bwgemm_orthogonalize(self.handle, G.data_ptr(), dt, out.data_ptr(), dto, batch, rows, cols,
                                            lds[0], strides[0], lds[1], strides[1], int(steps),

@@ -4,6 +4,7 @@
 // operators.cpp, which checks the arguments and fills them in.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda.h>
@@ -19,6 +20,25 @@ constexpr int kBlock = 128;  // elements of K, or rows, that share a scale
 // limit / amax then stays finite in fp32 and an all-zero block needs no case
 // of its own.
 constexpr float kSmallestAmax = 7.8886090522101181e-31f;  // 2^-100
+
+// Allow `kernel` its dynamic shared memory on the current device, once per
+// device (the call costs more than looking it up).  `done`: a bit per device,
+// one word per kernel.
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<uint64_t>& done)
+{
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess)
+        return err;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_relaxed) & bit)
+        return cudaSuccess;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_relaxed);
+    return err;
+}
 
 // ------------------------------------------------------------------ quantise
 struct QuantizeParams {

@@ -16,7 +16,8 @@ cudaError_t launch_one(const CUtensorMap& a, const CUtensorMap& b, const CUtenso
     auto kernel = ortho_kernel<CG, A_MN, B_MN>;
     if (grid % CG != 0)
         return cudaErrorInvalidValue;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_smem(kernel, Cfg::kSmemBytes, allowed);
     if (err != cudaSuccess)
         return err;
     cudaLaunchConfig_t cfg = {};

@@ -11,7 +11,8 @@ cudaError_t launch_sc(const CUtensorMap& l, const CUtensorMap& c, const CUtensor
 {
     using Cfg = ScaledConfig<BN, SWAP, COLVEC>;
     auto kernel = scaled_kernel<BN, SWAP, COLVEC>;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemBytes);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_smem(kernel, Cfg::kSmemBytes, allowed);
     if (err != cudaSuccess)
         return err;
     if (Cfg::kSplitRegs) {
