@@ -211,7 +211,7 @@ struct OrthoLayout {
 
 OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols)
 {
-    auto pad = [](int64_t v) { return (v + 127) / 128 * 128; };
+    auto pad = [](int64_t v) { return (v + 63) / 64 * 64; };  // whole 64-column chunks
     OrthoLayout l;
     l.wide = rows <= cols;
     l.m = std::min(rows, cols);
@@ -522,30 +522,47 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
 
     // One product: square tiles of 256 on CTA pairs (1024 SM cycles per 128 of
     // K, bound by the MMAs) or of 128 on single CTAs (about 740, bound by the
-    // copies of both operands), whichever takes fewer cycles in its waves.
+    // copies of both operands), whichever takes fewer cycles in its waves; a
+    // deep K of few 128-tiles in slices, which cost some 8000 cycles to join and
+    // 800 for each (32 x 22101 x 54: 1222 us whole, 896 in slices).
     const int pairs = plan->max_active[find_variant(2, 256, false, 1)];
     OrthoParams p0 = {};
     p0.batch = int32_t(batch);
     p0.timeout_ns = plan->opts.timeout_ns ? plan->opts.timeout_ns : 4000000000ull;
     p0.status = plan->d_status;
     p0.stall_kblock = plan->opts.stall_kblock;
+    p0.counters = reinterpret_cast<uint32_t*>(plan->d_workspace);
+    p0.partials = reinterpret_cast<float*>(plan->d_workspace + kCounterRegionBytes);
     auto product = [&](int form, OrthoParams p, int64_t K, const CUtensorMap& a, const CUtensorMap& b,
                        const CUtensorMap& a2, const CUtensorMap& b2, const CUtensorMap& res, const CUtensorMap& res2) {
         p.steps_k = int32_t((K + 127) / 128);
+        const int64_t steps_all = int64_t(p.steps_k) * p.terms;
         int64_t tiles[3] = {};
         for (int cg = 1; cg <= 2; ++cg) {
             const int64_t r = (p.rows + 128 * cg - 1) / (128 * cg), c = (p.cols + 128 * cg - 1) / (128 * cg);
-            tiles[cg] = p.symmetric ? r * (r + 1) / 2 : r * c;
+            tiles[cg] = (p.symmetric ? r * (r + 1) / 2 : r * c) * batch;
         }
-        const int64_t t1 = tiles[1] * batch, t2 = tiles[2] * batch;
-        const int64_t cost1 = (t1 + plan->num_sms - 1) / plan->num_sms * 740, cost2 = (t2 + pairs - 1) / pairs * 1024;
-        const int cg = cost1 < cost2 ? 1 : 2;
-        if (tiles[cg] * batch >= (1ll << 31))
+        int64_t best = (tiles[2] + pairs - 1) / pairs * steps_all * 1024;
+        int cg = 2;
+        p.splits = 1;
+        const int64_t most = std::min<int64_t>(plan->num_sms / std::max<int64_t>(tiles[1], 1), steps_all / 4);
+        const bool room = kCounterRegionBytes + uint64_t(plan->num_sms) * 128 * 128 * 4 <= plan->workspace_bytes;
+        for (int64_t splits = 1; splits <= std::max<int64_t>(1, room ? most : 1); ++splits) {
+            const int64_t cost = (tiles[1] * splits + plan->num_sms - 1) / plan->num_sms *
+                                     ((steps_all + splits - 1) / splits) * 740 +
+                                 (splits > 1 ? 8000 + 800 * splits : 0);
+            if (cost < best) {
+                best = cost;
+                cg = 1;
+                p.splits = int32_t(splits);
+            }
+        }
+        if (tiles[cg] * p.splits >= (1ll << 31))
             return BWGEMM_ERR_UNSUPPORTED;
         p.num_r = int32_t((p.rows + 128 * cg - 1) / (128 * cg));
         p.num_c = int32_t((p.cols + 128 * cg - 1) / (128 * cg));
-        p.tiles = int32_t(tiles[cg]);
-        const int64_t workers = std::min<int64_t>(tiles[cg] * batch, cg == 2 ? pairs : plan->num_sms);
+        p.tiles = int32_t(tiles[cg] / batch);
+        const int64_t workers = std::min<int64_t>(tiles[cg] * p.splits, cg == 2 ? pairs : plan->num_sms);
         if (launch_ortho(form, cg, a, b, a2, b2, res, res2, p, int(workers * cg), s, pdl) != cudaSuccess)
             return BWGEMM_ERR_CUDA;
         plan->launches += 1;

@@ -132,6 +132,9 @@ struct OrthoParams {
     int32_t terms;               // 1, or 2: A or B is the sum of two fp16 matrices (maps a2 / b2)
     int32_t num_r, num_c;        // tiles along rows and columns
     int32_t tiles, batch;        // tiles per matrix; matrices
+    int32_t splits;              // slices of K per tile (1: whole)
+    float* partials;             // their fp32 sums
+    uint32_t* counters;          // slices arrived per (tile, CTA, warp); zero between launches
     int32_t symmetric;           // 1: only tiles on and below the diagonal, stored twice
     float alpha, beta, diag;
     const float* alpha_dev;      // a further factor per matrix (null: 1)

@@ -21,6 +21,9 @@
 // operand's low part (what fp16 rounding lost) -- the sum of both products in
 // one accumulator.
 //
+// Few tiles and a deep K (long, narrow matrices): the tiles of S are cut into
+// slices of K whose fp32 sums meet in global memory and are added in order.
+//
 // Each stage of the ring holds 128 of K of both operands (64 KiB), one 32 KiB
 // copy each (box {64, 128 rows, 2 chunks}); the same box serves K-major (rows =
 // output rows, chunks along K) and MN-major (rows = K, chunks along the
@@ -73,13 +76,19 @@ __device__ __forceinline__ uint64_t make_sdesc_mn(uint32_t smem)
 
 struct OrthoTile {
     int r, c, matrix;
+    int slice, k0, k1;  // slice of K: steps [k0, k1)
 };
 
 __device__ __forceinline__ OrthoTile ortho_tile_at(const OrthoParams& p, int t)
 {
     OrthoTile x;
-    x.matrix = t / p.tiles;
-    const int i = t - x.matrix * p.tiles;
+    const int whole = t / p.splits;
+    const int steps = p.steps_k * p.terms;
+    x.slice = t - whole * p.splits;
+    x.k0 = x.slice * steps / p.splits;
+    x.k1 = (x.slice + 1) * steps / p.splits;
+    x.matrix = whole / p.tiles;
+    const int i = whole - x.matrix * p.tiles;
     if (p.symmetric) {
         // row r of the triangle holds tiles r (r + 1) / 2 .. + r
         int r = int((sqrtf(8.f * float(i) + 1.f) - 1.f) * 0.5f);
@@ -153,8 +162,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
     const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;
     const int worker = int(blockIdx.x) / CG;
     const int workers = int(gridDim.x) / CG;
-    const int total = p.tiles * p.batch;
-    const int steps = p.steps_k * p.terms;
+    const int total = p.tiles * p.batch * p.splits;  // a unit is a tile, or a slice of its K
     const uint32_t sA = base + Cfg::kOffA;
     const uint32_t sB = base + Cfg::kOffB;
     const uint32_t bar_full = base + Cfg::kOffBar;
@@ -210,7 +218,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
             const int a0 = x.r * TILE + int(rank) * 128;  // this CTA's output rows, and columns of B
             const int b0 = x.c * TILE + int(rank) * 128;
 #pragma unroll 1
-            for (int i = 0; i < steps; ++i, ++n) {
+            for (int i = x.k0; i < x.k1; ++i, ++n) {
                 ok = __all_sync(0xffffffffu,
                                 pipe_wait(bar_empty + 8 * s, phase ^ 1u, p, abort_flag, kStatusProducerTimeout));
                 if (!ok)
@@ -259,10 +267,11 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
         bool ok = true;
 #pragma unroll 1
         for (int t = worker; ok && t < total; t += workers) {
+            const OrthoTile x = ortho_tile_at(p, t);
             ok = __all_sync(0xffffffffu,
                             pipe_wait(bar_acc_empty + 8 * b, bphase ^ 1u, p, abort_flag, kStatusMmaTimeout));
 #pragma unroll 1
-            for (int i = 0; ok && i < steps; ++i) {
+            for (int i = x.k0; ok && i < x.k1; ++i) {
                 ok = __all_sync(0xffffffffu, pipe_wait(bar_full + 8 * s, phase, p, abort_flag, kStatusMmaTimeout));
                 if (!ok)
                     break;
@@ -275,15 +284,15 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                         const uint32_t k_major = uint32_t((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
                         const uint32_t mn_major = uint32_t(kk * 2048) >> 4;
                         ptx::mma_f16<CG>(tmem0 + uint32_t(b * TILE), ad + (A_MN ? mn_major : k_major),
-                                         bd + (B_MN ? mn_major : k_major), idesc, (i > 0 || kk > 0) ? 1u : 0u);
+                                         bd + (B_MN ? mn_major : k_major), idesc, (i > x.k0 || kk > 0) ? 1u : 0u);
                     }
                     if constexpr (CG == 2) {
                         ptx::mma_commit_pair(bar_empty + 8 * s, 0x3);
-                        if (i == steps - 1)
+                        if (i == x.k1 - 1)
                             ptx::mma_commit_pair(bar_acc_full + 8 * b, 0x3);
                     } else {
                         ptx::mma_commit(bar_empty + 8 * s);
-                        if (i == steps - 1)
+                        if (i == x.k1 - 1)
                             ptx::mma_commit(bar_acc_full + 8 * b);
                     }
                 }
@@ -321,8 +330,8 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                 break;
             ptx::tc_fence_after_sync();
             const uint32_t taddr = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(b * TILE + (e >> 2) * Cfg::kCols);
-#pragma unroll 1
-            for (int c = 0; c < Cfg::kCols; c += 32) {
+            // 32 columns of the finished sums (this lane's row) to D
+            auto finish = [&](int c, const uint32_t(&v)[32]) {
                 const int col = col0 + c;
                 uint4 add[4];
                 const bool has = p.e != nullptr && row < p.rows && col < p.store_cols;
@@ -332,17 +341,12 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                     for (int i = 0; i < 4; ++i)
                         add[i] = ptx::ld_global_cg_v4(src + 8 * i);
                 }
-                uint32_t v[32];
-                ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c), v);
-                ptx::tmem_ld_wait();
-                if (c + 32 >= Cfg::kCols)
-                    hand_back<CG>(bar_acc_empty + 8 * b, lane);
                 // the box itself, and its mirror image: columns of D from its rows, up
                 // to the padded width (zeros there, which later products read)
                 const bool direct = row0 < p.rows && col < p.store_cols;
                 const bool mirrored = mirror && col < p.rows && row0 < p.store_cols;
                 if (!direct && !mirrored)
-                    continue;
+                    return;
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -396,6 +400,66 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                         put(hi, &tmap_out, true);
                     if (p.low && direct)
                         put(lo, &tmap_out2, false);
+                }
+            };
+            if (p.splits == 1) {
+#pragma unroll 1
+                for (int c = 0; c < Cfg::kCols; c += 32) {
+                    uint32_t v[32];
+                    ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c), v);
+                    ptx::tmem_ld_wait();
+                    if (c + 32 >= Cfg::kCols)
+                        hand_back<CG>(bar_acc_empty + 8 * b, lane);
+                    finish(c, v);
+                }
+            } else {
+                // a slice of K: publish its sums; the warp that completes the tile adds
+                // all slices in order, whichever came last
+                const size_t stride = size_t(CG) * 128 * TILE;  // floats of a tile's slice
+                float* const part = p.partials + (size_t(t) / p.splits * p.splits) * stride +
+                                    (rank * 8 + e) * size_t(32 * Cfg::kCols) + 4 * lane;
+#pragma unroll 1
+                for (int c = 0; c < Cfg::kCols; c += 32) {
+                    uint32_t v[32];
+                    ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c), v);
+                    ptx::tmem_ld_wait();
+                    if (c + 32 >= Cfg::kCols)
+                        hand_back<CG>(bar_acc_empty + 8 * b, lane);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        ptx::st_global_cg_v4(part + x.slice * stride + c * 32 + i * 128,
+                                             make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                }
+                __threadfence();
+                __syncwarp();
+                uint32_t* counter = p.counters + (size_t(t) / p.splits * CG + rank) * 8 + e;
+                uint32_t before = 0;
+                if (lane == 0)
+                    before = ptx::atom_add_acq_rel_gpu(counter, 1u);
+                before = __shfl_sync(0xffffffffu, before, 0);
+                if (before + 1 == uint32_t(p.splits)) {
+                    if (lane == 0)
+                        *counter = 0u;  // ready for the next launch
+                    __threadfence();
+#pragma unroll 1
+                    for (int c = 0; c < Cfg::kCols; c += 32) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = 0u;
+#pragma unroll 1
+                        for (int k = 0; k < p.splits; ++k) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const uint4 w = ptx::ld_global_cg_v4(part + k * stride + c * 32 + i * 128);
+                                v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + __uint_as_float(w.x));
+                                v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + __uint_as_float(w.y));
+                                v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + __uint_as_float(w.z));
+                                v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + __uint_as_float(w.w));
+                            }
+                        }
+                        finish(c, v);
+                    }
                 }
             }
             if (++b == 2) {

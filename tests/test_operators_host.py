@@ -63,9 +63,9 @@ def test_orthogonalize_workspace_sizes(lib):
     assert workspace(lib, -1, 8, 8)[0] == INVALID
     assert workspace(lib, 1 << 16, 8, 8)[0] == UNSUP
     assert workspace(lib, 1, 1 << 25, 8)[0] == UNSUP
-    # four fp16 matrices of G's size (columns padded to 128), two of the short side's
+    # four fp16 matrices of G's size (columns padded to 64), two of the short side's
     for batch, rows, cols in ((1, 300, 1000), (3, 1000, 300), (2, 512, 512), (1, 1, 1)):
-        pad = lambda v: -(-v // 128) * 128  # noqa: E731
+        pad = lambda v: -(-v // 64) * 64  # noqa: E731
         rc, n = workspace(lib, batch, rows, cols)
         m = min(rows, cols)
         need = batch * 2 * (4 * rows * pad(cols) + 2 * m * pad(m))
