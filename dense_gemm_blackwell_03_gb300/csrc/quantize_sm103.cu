@@ -83,15 +83,46 @@ struct Row8 {
     }
 };
 
+// Magnitudes are compared as bit patterns: the same order for finite values,
+// and a NaN, larger than infinity, reaches the scale of its block.  16-bit
+// types two at a time.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+template <typename T>
+struct Mag {
+    static constexpr int kWords = Row8<T>::kWords;
+    static constexpr bool kPairs = sizeof(T) == 2;
+    static __device__ __forceinline__ uint32_t of(uint32_t w) { return w & (kPairs ? 0x7FFF7FFFu : 0x7FFFFFFFu); }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b)
+    {
+        if constexpr (kPairs)
+            return max_u16x2(a, b);
+        else
+            return max(a, b);
+    }
+    // the larger of a word's values, and a value's fp32 bits
+    static __device__ __forceinline__ uint32_t fold(uint32_t w) { return kPairs ? max(w & 0xFFFFu, w >> 16) : w; }
+    static __device__ __forceinline__ uint32_t f32_bits(uint32_t m)
+    {
+        if constexpr (std::is_same<T, float>::value)
+            return m;
+        else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+            return m << 16;
+        else
+            return __float_as_uint(__half2float(__ushort_as_half(uint16_t(m))));
+    }
+};
+
 template <int F8>
 __device__ __forceinline__ uint32_t cvt2(float lo, float hi)
 {
     return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, F8 == 0 ? __NV_E4M3 : __NV_E5M2));
 }
-
-// Magnitudes are compared as bit patterns: the same order for finite values,
-// and a NaN, larger than infinity, reaches the scale of its block.
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
 struct Scale {
     float scale, factor;
@@ -113,8 +144,14 @@ __device__ __forceinline__ Scale make_scale(uint32_t amax_bits, bool pow2)
     return r;
 }
 
+// CTAs per SM: as many as registers allow without keeping the values unpacked
+// (the compiler would otherwise take 182 for bf16 in both directions, one CTA per
+// SM: 103 us on 8192 x 8192)
+template <typename T, bool BOTH>
+constexpr int kQuantCtas = sizeof(T) == 4 ? 2 : BOTH ? 3 : 4;
+
 template <typename T, int F8, bool SQUARE, bool BOTH>
-__global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantizeParams p, const int kblocks)
+__global__ void __launch_bounds__(kQuantThreads, kQuantCtas<T, BOTH>) quantize_kernel(const QuantizeParams p, const int kblocks)
 {
     __shared__ uint32_t s_max[BOTH && !SQUARE ? kWarps * kBlock : kWarps];
     __shared__ float s_factor[BOTH && !SQUARE ? kBlock : 1];
@@ -139,15 +176,24 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantizeP
         x[i].load(static_cast<const T*>(p.x) + (in ? row * p.ldx + col0 + c0 : 0), in ? valid : 0);
     }
 
-    float factor[8];  // of the thread's rows
-    uint32_t rmax[8];
+    using M = Mag<T>;
+    float factor[8];   // of the thread's rows
+    uint32_t rmax[8];  // bits of the rows' largest magnitudes
+    uint32_t cmax[M::kWords];
+#pragma unroll
+    for (int j = 0; j < M::kWords; ++j)
+        cmax[j] = 0u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            m = max(m, magnitude(x[i].get(j)));
-        rmax[i] = m;
+        for (int j = 0; j < M::kWords; ++j) {
+            const uint32_t v = M::of(x[i].w[j]);
+            m = M::larger(m, v);
+            if constexpr (BOTH && !SQUARE)
+                cmax[j] = M::larger(cmax[j], v);
+        }
+        rmax[i] = M::fold(m);
     }
     if constexpr (SQUARE) {
         uint32_t m = 0;
@@ -161,7 +207,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantizeP
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
             m = max(m, s_max[w]);
-        const Scale sc = make_scale<F8>(m, pow2);
+        const Scale sc = make_scale<F8>(M::f32_bits(m), pow2);
         if (threadIdx.x == 0) {
             p.s[int64_t(kb) * p.lds + rb] = sc.scale;
             if (BOTH)
@@ -185,7 +231,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantizeP
             }
         }
         const uint32_t m = max(rmax[0], __shfl_xor_sync(0xFFFFFFFFu, rmax[0], 1));
-        const Scale sc = make_scale<F8>(m, pow2);
+        const Scale sc = make_scale<F8>(M::f32_bits(m), pow2);
         const int64_t row = row0 + r0 + (g >> 1);
         if ((g & 1) == 0 && row < p.rows)
             p.s[int64_t(kb) * p.lds + row] = sc.scale;
@@ -215,23 +261,22 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantizeP
 
     if constexpr (BOTH) {
         if constexpr (!SQUARE) {
+            constexpr int per = 8 / M::kWords;  // columns per word
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    m = max(m, magnitude(x[i].get(j)));
-                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+            for (int j = 0; j < M::kWords; ++j) {
+                const uint32_t m = M::larger(cmax[j], __shfl_xor_sync(0xFFFFFFFFu, cmax[j], 16));
                 if (half == 0)
-                    s_max[warp * kBlock + c0 + j] = m;
+                    s_max[warp * (kBlock / per) + M::kWords * g + j] = m;
             }
             __syncthreads();
             if (threadIdx.x < kBlock) {
                 uint32_t m = 0;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
-                    m = max(m, s_max[w * kBlock + threadIdx.x]);
-                const Scale sc = make_scale<F8>(m, pow2);
+                    m = M::larger(m, s_max[w * (kBlock / per) + threadIdx.x / per]);
+                if constexpr (M::kPairs)
+                    m = (threadIdx.x & 1) ? m >> 16 : m & 0xFFFFu;
+                const Scale sc = make_scale<F8>(M::f32_bits(m), pow2);
                 s_factor[threadIdx.x] = sc.factor;
                 if (col0 + threadIdx.x < p.cols)
                     p.st[rb * p.ldst + col0 + threadIdx.x] = sc.scale;
