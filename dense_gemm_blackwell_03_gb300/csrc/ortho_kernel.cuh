@@ -330,42 +330,55 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                 break;
             ptx::tc_fence_after_sync();
             const uint32_t taddr = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(b * TILE + (e >> 2) * Cfg::kCols);
+            // The epilogue is bound by its own instructions (8 warps share four
+            // schedulers with the issuing ones, and a 256-wide tile is 128 columns a
+            // thread), so what only some products need is tested once per 32
+            // columns, and fp32 values go in pairs.
+            const uint64_t alpha2 = ptx::pack_f32x2(__float_as_uint(alpha), __float_as_uint(alpha));
+            const uint64_t beta2 = ptx::pack_f32x2(__float_as_uint(p.beta), __float_as_uint(p.beta));
+            const bool e_row = p.e != nullptr && row < p.rows;
+            const uint16_t* const e_at = p.e + x.matrix * p.stride_e + row * p.lde + col0;
             // 32 columns of the finished sums (this lane's row) to D
             auto finish = [&](int c, const uint32_t(&v)[32]) {
                 const int col = col0 + c;
-                uint4 add[4];
-                const bool has = p.e != nullptr && row < p.rows && col < p.store_cols;
-                if (has) {
-                    const uint16_t* src = p.e + x.matrix * p.stride_e + row * p.lde + col;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        add[i] = ptx::ld_global_cg_v4(src + 8 * i);
-                }
                 // the box itself, and its mirror image: columns of D from its rows, up
                 // to the padded width (zeros there, which later products read)
                 const bool direct = row0 < p.rows && col < p.store_cols;
                 const bool mirrored = mirror && col < p.rows && row0 < p.store_cols;
                 if (!direct && !mirrored)
                     return;
-                uint32_t hi[16], lo[16];
+                uint64_t f[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float f[2] = {alpha * __uint_as_float(v[2 * i]), alpha * __uint_as_float(v[2 * i + 1])};
-                    if (has) {
+                for (int i = 0; i < 16; ++i)
+                    f[i] = ptx::mul_f32x2(ptx::pack_f32x2(v[2 * i], v[2 * i + 1]), alpha2);
+                if (e_row && col < p.store_cols) {
+                    uint4 add[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        add[i] = ptx::ld_global_cg_v4(e_at + c + 8 * i);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
                         const uint32_t w = (&add[i >> 2].x)[i & 3];
                         const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&w));
-                        f[0] = fmaf(p.beta, g.x, f[0]);
-                        f[1] = fmaf(p.beta, g.y, f[1]);
+                        f[i] = ptx::fma_f32x2(ptx::pack_f32x2(__float_as_uint(g.x), __float_as_uint(g.y)), beta2, f[i]);
                     }
-                    if (p.diag != 0.f) {
-                        f[0] += row == col + 2 * i ? p.diag : 0.f;
-                        f[1] += row == col + 2 * i + 1 ? p.diag : 0.f;
+                }
+                if (p.diag != 0.f && row0 < col + 32 && col < row0 + 32) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float lo, hi;
+                        ptx::unpack_f32x2(f[i], lo, hi);
+                        lo += row == col + 2 * i ? p.diag : 0.f;
+                        hi += row == col + 2 * i + 1 ? p.diag : 0.f;
+                        f[i] = ptx::pack_f32x2(__float_as_uint(lo), __float_as_uint(hi));
                     }
-                    hi[i] = pack2(__float_as_uint(f[0]), __float_as_uint(f[1]), p.out_bf16 ? 0 : 1);
-                    if (p.low) {
-                        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
-                        lo[i] = pack2(__float_as_uint(f[0] - h.x), __float_as_uint(f[1] - h.y), 1);
-                    }
+                }
+                uint32_t hi[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float a, b2;
+                    ptx::unpack_f32x2(f[i], a, b2);
+                    hi[i] = pack2(__float_as_uint(a), __float_as_uint(b2), p.out_bf16 ? 0 : 1);
                 }
                 auto put = [&](const uint32_t(&w)[16], const CUtensorMap* map, bool transposed) {
                     const uint32_t sb = store.claim(lane);
@@ -398,8 +411,17 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                         put(hi, &tmap_out, false);
                     if (mirrored)
                         put(hi, &tmap_out, true);
-                    if (p.low && direct)
+                    if (p.low && direct) {
+                        uint32_t lo[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float a, b2;
+                            ptx::unpack_f32x2(f[i], a, b2);
+                            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
+                            lo[i] = pack2(__float_as_uint(a - h.x), __float_as_uint(b2 - h.y), 1);
+                        }
                         put(lo, &tmap_out2, false);
+                    }
                 }
             };
             if (p.splits == 1) {

@@ -730,21 +730,11 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v)
 
 // Plain 16-byte global accesses that stay where they are written: behind the
 // dependency wait or an acquire, whatever the compiler knows of the address.
-// (cg: through L2; cs: streamed, evicted first.)
+// (cg: through L2.)
 __device__ __forceinline__ uint4 ld_global_cg_v4(const void* p)
 {
     uint4 v;
     asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
-                 : "memory");
-    return v;
-}
-
-__device__ __forceinline__ uint4 ld_global_cs_v4(const void* p)
-{
-    uint4 v;
-    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p)
                  : "memory");
