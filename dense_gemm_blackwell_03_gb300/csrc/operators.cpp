@@ -258,15 +258,17 @@ bwgemm_status_t encode_stack(CUtensorMap* map, const void* ptr, int64_t rows, in
                : BWGEMM_ERR_CUDA;
 }
 
-// A stack of 16-bit matrices as result: 32 x 32 boxes.
+// A stack of 16-bit matrices as result: boxes of 64 columns x 32 rows, or turned
+// ones of 32 columns x 64 rows.
 bwgemm_status_t encode_result(CUtensorMap* map, int dtype, void* ptr, int64_t rows, int64_t cols, int64_t ld,
-                              int64_t stride, int64_t batch)
+                              int64_t stride, int64_t batch, bool turned = false)
 {
     const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(batch)};
     const cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(stride) * 2};
-    const cuuint32_t box[3] = {32, 32, 1};
+    const cuuint32_t box[3] = {turned ? 32u : 64u, turned ? 64u : 32u, 1};
     return encode(map, dtype == BWGEMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, ptr,
-                  dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+                  dims, strides, box, turned ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 bwgemm_status_t check_ortho(int64_t batch, int64_t rows, int64_t cols)
@@ -499,7 +501,7 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
     plan->launches += 2;
 
     // operand maps of X (two buffers, two terms), S and B, and their result maps
-    CUtensorMap x_op[2][2], x_res[2][2], s_op, s_res, b_op, b_res, final_res;
+    CUtensorMap x_op[2][2], x_res[2][2], s_op, s_res, s_turned, b_op, b_res, b_turned, final_res;
     for (int i = 0; i < 2; ++i)
         for (int t = 0; t < 2; ++t) {
             void* at = ws + (t ? l.lo[i] : l.hi[i]);
@@ -509,6 +511,8 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
         }
     if ((st = encode_stack(&s_op, ws + l.s, l.m, l.lds, l.s_stride, batch)) != BWGEMM_OK ||
         (st = encode_result(&s_res, BWGEMM_FP16, ws + l.s, l.m, l.lds, l.lds, l.s_stride, batch)) != BWGEMM_OK ||
+        (st = encode_result(&s_turned, BWGEMM_FP16, ws + l.s, l.m, l.lds, l.lds, l.s_stride, batch, true)) != BWGEMM_OK ||
+        (st = encode_result(&b_turned, BWGEMM_FP16, ws + l.b, l.m, l.lds, l.lds, l.s_stride, batch, true)) != BWGEMM_OK ||
         (st = encode_stack(&b_op, ws + l.b, l.m, l.lds, l.s_stride, batch)) != BWGEMM_OK ||
         (st = encode_result(&b_res, BWGEMM_FP16, ws + l.b, l.m, l.lds, l.lds, l.s_stride, batch)) != BWGEMM_OK)
         return st;
@@ -584,7 +588,7 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
         p.alpha = i == 0 ? 1.f : down * down;
         p.alpha_dev = i == 0 ? in.factors + batch : nullptr;
         p.store_cols = int32_t(l.lds);
-        if ((st = product(l.wide ? kOrthoNT : kOrthoTN, p, l.n, x, x, x, x, s_res, s_res)) != BWGEMM_OK)
+        if ((st = product(l.wide ? kOrthoNT : kOrthoTN, p, l.n, x, x, x, x, s_res, s_turned)) != BWGEMM_OK)
             return st;
         // B = a I + b S + c S S
         p.alpha = c;
@@ -594,7 +598,7 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
         p.e = reinterpret_cast<const uint16_t*>(ws + l.s);
         p.lde = l.lds;
         p.stride_e = l.s_stride;
-        if ((st = product(kOrthoNT, p, l.m, s_op, s_op, s_op, s_op, b_res, b_res)) != BWGEMM_OK)
+        if ((st = product(kOrthoNT, p, l.m, s_op, s_op, s_op, s_op, b_res, b_turned)) != BWGEMM_OK)
             return st;
         // X <- B X, or X B with X stored upright
         const bool last = i == steps - 1;

@@ -155,6 +155,7 @@ struct OrthoParams {
 enum : int { kOrthoNT = 0, kOrthoNN = 1, kOrthoTN = 2 };  // A, B: K K | K MN | MN MN
 constexpr int ortho_tile(int cg) { return 128 * cg; }
 
+// out: D in 64 x 32 boxes; out2: its low part, or (symmetric) D in turned boxes
 cudaError_t launch_ortho(int form, int cg, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& a2,
                          const CUtensorMap& b2, const CUtensorMap& out, const CUtensorMap& out2, const OrthoParams& p,
                          int grid, cudaStream_t stream, bool pdl);

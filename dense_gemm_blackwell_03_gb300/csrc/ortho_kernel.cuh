@@ -47,11 +47,11 @@ struct OrthoConfig {
     static constexpr int kOperandBytes = 128 * kOrthoK * 2;  // 32 KiB: this CTA's 128 rows of A, or of B
     static constexpr int kStages = 3;
     static constexpr int kTmemCols = 2 * kTile;
-    static constexpr int kStoreBytes = 2048;               // a 32 x 32 box of 16-bit values
+    static constexpr int kStoreBytes = 4096;               // a warp's 32 x 64 16-bit values
     static constexpr int kOffA = 0;
     static constexpr int kOffB = kStages * kOperandBytes;
     static constexpr int kOffStore = 2 * kStages * kOperandBytes;
-    static constexpr int kOffBar = kOffStore + kEpiWarps * 2 * kStoreBytes;
+    static constexpr int kOffBar = kOffStore + kEpiWarps * kStoreBytes;
     static constexpr int kNumBars = 2 * kStages + 4 + 1;   // full, empty, acc_full[2], acc_empty[2], drain
     static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars;
     static constexpr int kOffAbort = kOffTmemSlot + 4;
@@ -110,37 +110,27 @@ __device__ __forceinline__ OrthoTile ortho_tile_at(const OrthoParams& p, int t)
     return x;
 }
 
-// The warp's staging buffers: boxes alternate between two.
-struct OrthoStore {
-    uint32_t buf;
-    int n;
-    __device__ __forceinline__ uint32_t claim(int lane)
-    {
-        if (lane == 0)
-            ptx::bulk_wait_group_read<1>();
-        __syncwarp();
-        return buf + uint32_t((n++ & 1) * 2048);
-    }
-};
-
-// One 32 x 32 box, lane = row, 16 packed words = its columns, into `sb` with
-// the 64-byte swizzle of the store maps (16-byte piece XOR bits 7-8 of the
-// offset), or transposed.
-__device__ __forceinline__ void ortho_stage(const uint32_t (&w)[16], uint32_t sb, int lane, bool transposed)
+// Convert-and-store works on 64 columns of a warp's 32 rows at a time (lane = row,
+// 32 packed words = its columns), staged in 4 KiB of the warp's shared memory:
+// rows of 128 bytes with the 128-byte swizzle of the result maps (16-byte piece
+// XOR row mod 8), or turned, 64 rows of 64 bytes with the 64-byte swizzle (piece
+// XOR (row / 2) mod 4).
+__device__ __forceinline__ void ortho_stage(const uint32_t (&w)[32], uint32_t sb, int lane)
 {
-    if (!transposed) {
-        const uint32_t row = sb + uint32_t(lane * 64);
-        const uint32_t swz = uint32_t((lane >> 1) & 3);
+    const uint32_t row = sb + uint32_t(lane * 128);
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch)
-            ptx::st_shared_v4(row + ((uint32_t(ch) ^ swz) << 4), w[4 * ch], w[4 * ch + 1], w[4 * ch + 2], w[4 * ch + 3]);
-    } else {
+    for (int ch = 0; ch < 8; ++ch)
+        ptx::st_shared_v4(row + ((uint32_t(ch) ^ uint32_t(lane & 7)) << 4), w[4 * ch], w[4 * ch + 1], w[4 * ch + 2],
+                          w[4 * ch + 3]);
+}
+
+__device__ __forceinline__ void ortho_stage_turned(const uint32_t (&w)[32], uint32_t sb, int lane)
+{
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            ptx::st_shared_u16(sb + uint32_t(i * 64) + ((uint32_t(lane >> 3) ^ uint32_t((i >> 1) & 3)) << 4) +
-                                   uint32_t((lane & 7) * 2),
-                               uint16_t((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xFFFFu)));
-    }
+    for (int i = 0; i < 64; ++i)
+        ptx::st_shared_u16(sb + uint32_t(i * 64) + ((uint32_t(lane >> 3) ^ uint32_t((i >> 1) & 3)) << 4) +
+                               uint32_t((lane & 7) * 2),
+                           uint16_t((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xFFFFu)));
 }
 
 template <int CG, bool A_MN, bool B_MN>
@@ -312,7 +302,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
         ptx::grid_dependency_wait();
         const int e = warp - 2;
         const int q = warp & 3;
-        OrthoStore store = {base + uint32_t(Cfg::kOffStore + e * 2 * Cfg::kStoreBytes), 0};
+        const uint32_t sb = base + uint32_t(Cfg::kOffStore + e * Cfg::kStoreBytes);
         int b = 0;
         uint32_t bphase = 0;
         bool ok = true;
@@ -324,22 +314,27 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
             const int row = row0 + lane;
             const float alpha = p.alpha_dev ? p.alpha * ptx::ld_global_cg_f32(p.alpha_dev + x.matrix) : p.alpha;
             const bool mirror = p.symmetric && x.r != x.c;
-            ok = __all_sync(0xffffffffu,
-                            pipe_wait(bar_acc_full + 8 * b, bphase, p, abort_flag, kStatusEpilogueTimeout));
-            if (!ok)
-                break;
-            ptx::tc_fence_after_sync();
-            const uint32_t taddr = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(b * TILE + (e >> 2) * Cfg::kCols);
             // The epilogue is bound by its own instructions (8 warps share four
             // schedulers with the issuing ones, and a 256-wide tile is 128 columns a
-            // thread), so what only some products need is tested once per 32
+            // thread), so what only some products need is tested once per 64
             // columns, and fp32 values go in pairs.
             const uint64_t alpha2 = ptx::pack_f32x2(__float_as_uint(alpha), __float_as_uint(alpha));
             const uint64_t beta2 = ptx::pack_f32x2(__float_as_uint(p.beta), __float_as_uint(p.beta));
+            // E's 64 columns, loaded before the sums are waited for, later ones a
+            // piece ahead
             const bool e_row = p.e != nullptr && row < p.rows;
             const uint16_t* const e_at = p.e + x.matrix * p.stride_e + row * p.lde + col0;
-            // 32 columns of the finished sums (this lane's row) to D
-            auto finish = [&](int c, const uint32_t(&v)[32]) {
+            uint4 add[8];
+            auto fetch = [&](int c) {
+                if (e_row && c < Cfg::kCols && col0 + c < p.store_cols) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        add[i] = ptx::ld_global_cg_v4(e_at + c + 8 * i);
+                }
+            };
+            fetch(0);
+            // 64 columns of the finished sums (this lane's row) to D
+            auto finish = [&](int c, const uint32_t(&v)[64]) {
                 const int col = col0 + c;
                 // the box itself, and its mirror image: columns of D from its rows, up
                 // to the padded width (zeros there, which later products read)
@@ -347,25 +342,22 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                 const bool mirrored = mirror && col < p.rows && row0 < p.store_cols;
                 if (!direct && !mirrored)
                     return;
-                uint64_t f[16];
+                uint64_t f[32];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < 32; ++i)
                     f[i] = ptx::mul_f32x2(ptx::pack_f32x2(v[2 * i], v[2 * i + 1]), alpha2);
                 if (e_row && col < p.store_cols) {
-                    uint4 add[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        add[i] = ptx::ld_global_cg_v4(e_at + c + 8 * i);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < 32; ++i) {
                         const uint32_t w = (&add[i >> 2].x)[i & 3];
                         const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&w));
                         f[i] = ptx::fma_f32x2(ptx::pack_f32x2(__float_as_uint(g.x), __float_as_uint(g.y)), beta2, f[i]);
                     }
                 }
-                if (p.diag != 0.f && row0 < col + 32 && col < row0 + 32) {
+                fetch(c + 64);
+                if (p.diag != 0.f && row0 < col + 64 && col < row0 + 32) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < 32; ++i) {
                         float lo, hi;
                         ptx::unpack_f32x2(f[i], lo, hi);
                         lo += row == col + 2 * i ? p.diag : 0.f;
@@ -373,64 +365,80 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                         f[i] = ptx::pack_f32x2(__float_as_uint(lo), __float_as_uint(hi));
                     }
                 }
-                uint32_t hi[16];
+                uint32_t w[32];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float a, b2;
-                    ptx::unpack_f32x2(f[i], a, b2);
-                    hi[i] = pack2(__float_as_uint(a), __float_as_uint(b2), p.out_bf16 ? 0 : 1);
+                for (int i = 0; i < 32; ++i) {
+                    float lo, hi;
+                    ptx::unpack_f32x2(f[i], lo, hi);
+                    w[i] = pack2(__float_as_uint(lo), __float_as_uint(hi), p.out_bf16 ? 0 : 1);
                 }
-                auto put = [&](const uint32_t(&w)[16], const CUtensorMap* map, bool transposed) {
-                    const uint32_t sb = store.claim(lane);
-                    ortho_stage(w, sb, lane, transposed);
+                auto claim = [&] {  // the store before has read the staging block
+                    if (lane == 0)
+                        ptx::bulk_wait_group_read<0>();
+                    __syncwarp();
+                };
+                auto put = [&](const CUtensorMap* map, int at_col, int at_row) {
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        ptx::tma_store_3d(map, sb, transposed ? row0 : col, transposed ? col : row0, x.matrix);
+                        ptx::tma_store_3d(map, sb, at_col, at_row, x.matrix);
                         ptx::bulk_commit_group();
                     }
                 };
                 if (p.plain_store) {
-                    // the caller's rows are not on 16-byte boundaries: the box goes
-                    // through shared memory and out a row at a time, lane = column
-                    const uint32_t sb = store.claim(lane);
-                    ortho_stage(hi, sb, lane, false);
+                    // the caller's rows are not on 16-byte boundaries: the block goes
+                    // through shared memory and out a row at a time, two columns a lane
                     __syncwarp();
-                    if (col + lane < p.cols) {
-                        uint16_t* dst = p.out + x.matrix * p.stride_o + row0 * p.ldo + col + lane;
-                        const int n = min(32, p.rows - row0);
+                    ortho_stage(w, sb, lane);
+                    __syncwarp();
+                    uint16_t* dst = p.out + x.matrix * p.stride_o + row0 * p.ldo + col;
+                    const int n = min(32, p.rows - row0);
 #pragma unroll 1
-                        for (int i = 0; i < n; ++i)
-                            dst[i * p.ldo] = ptx::ld_shared_u16(
-                                sb + uint32_t(i * 64) + ((uint32_t(lane >> 3) ^ uint32_t((i >> 1) & 3)) << 4) +
-                                uint32_t((lane & 7) * 2));
-                    }
-                    __syncwarp();
-                } else {
-                    if (direct)
-                        put(hi, &tmap_out, false);
-                    if (mirrored)
-                        put(hi, &tmap_out, true);
-                    if (p.low && direct) {
-                        uint32_t lo[16];
+                    for (int i = 0; i < n; ++i)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float a, b2;
-                            ptx::unpack_f32x2(f[i], a, b2);
-                            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
-                            lo[i] = pack2(__float_as_uint(a - h.x), __float_as_uint(b2 - h.y), 1);
-                        }
-                        put(lo, &tmap_out2, false);
+                        for (int k = lane; k < 64; k += 32)
+                            if (col + k < p.cols)
+                                dst[i * p.ldo + k] = ptx::ld_shared_u16(
+                                    sb + uint32_t(i * 128) + ((uint32_t(k >> 3) ^ uint32_t(i & 7)) << 4) +
+                                    uint32_t((k & 7) * 2));
+                    return;
+                }
+                if (direct) {
+                    claim();
+                    ortho_stage(w, sb, lane);
+                    put(&tmap_out, col, row0);
+                }
+                if (mirrored) {
+                    claim();
+                    ortho_stage_turned(w, sb, lane);
+                    put(&tmap_out2, row0, col);
+                }
+                if (p.low && direct) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float lo, hi;
+                        ptx::unpack_f32x2(f[i], lo, hi);
+                        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                        w[i] = pack2(__float_as_uint(lo - h.x), __float_as_uint(hi - h.y), 1);
                     }
+                    claim();
+                    ortho_stage(w, sb, lane);
+                    put(&tmap_out2, col, row0);
                 }
             };
+            ok = __all_sync(0xffffffffu,
+                            pipe_wait(bar_acc_full + 8 * b, bphase, p, abort_flag, kStatusEpilogueTimeout));
+            if (!ok)
+                break;
+            ptx::tc_fence_after_sync();
+            const uint32_t taddr = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(b * TILE + (e >> 2) * Cfg::kCols);
             if (p.splits == 1) {
 #pragma unroll 1
-                for (int c = 0; c < Cfg::kCols; c += 32) {
-                    uint32_t v[32];
-                    ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c), v);
+                for (int c = 0; c < Cfg::kCols; c += 64) {
+                    uint32_t v[64];
+                    ptx::tmem_ld_32x32b_x64(taddr + uint32_t(c), v);
                     ptx::tmem_ld_wait();
-                    if (c + 32 >= Cfg::kCols)
+                    if (c + 64 >= Cfg::kCols)
                         hand_back<CG>(bar_acc_empty + 8 * b, lane);
                     finish(c, v);
                 }
@@ -464,15 +472,15 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                         *counter = 0u;  // ready for the next launch
                     __threadfence();
 #pragma unroll 1
-                    for (int c = 0; c < Cfg::kCols; c += 32) {
-                        uint32_t v[32];
+                    for (int c = 0; c < Cfg::kCols; c += 64) {
+                        uint32_t v[64];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
+                        for (int i = 0; i < 64; ++i)
                             v[i] = 0u;
 #pragma unroll 1
                         for (int k = 0; k < p.splits; ++k) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
+                            for (int i = 0; i < 16; ++i) {
                                 const uint4 w = ptx::ld_global_cg_v4(part + k * stride + c * 32 + i * 128);
                                 v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + __uint_as_float(w.x));
                                 v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + __uint_as_float(w.y));
