@@ -297,7 +297,8 @@ assert _SCALED.size == ctypes.sizeof(Scaled)
 
 def _pack_scaled(into: Scaled, values, scales, name: str):
     """Describe 8-bit `values` (R x K) with `scales` ((K blocks) x (R or row blocks))
-    in `into`; returns (R, K)."""
+    in `into`; returns (R, K).  (Strides are read here, not through _ld: this is
+    the per-call path.)"""
     code = _fp8_codes.get(values.dtype)
     if code is None:
         raise TypeError(f"{name} must be float8_e4m3fn or float8_e5m2, got {values.dtype}")
@@ -305,13 +306,18 @@ def _pack_scaled(into: Scaled, values, scales, name: str):
         raise TypeError(f"the scales of {name} must be float32, got {scales.dtype}")
     rows, K = values.shape
     blocks, per = scales.shape
-    rb = -(-rows // BLOCK)
-    if blocks != -(-K // BLOCK) or (per != rows and per != rb):
+    square = per != rows
+    if blocks != (K + 127) >> 7 or (square and per != (rows + 127) >> 7):
         raise ValueError(f"the scales of {name} ({rows} x {K}) must be {-(-K // BLOCK)} x {rows} or "
-                         f"{-(-K // BLOCK)} x {rb}, got {tuple(scales.shape)}")
-    ld = _ld(values) if rows > 1 else -(-K // 16) * 16  # a single row has no next one
-    _SCALED.pack_into(into, 0, values.data_ptr(), ld, scales.data_ptr(), _ld(scales), code,
-                      BLOCK_ROW if per == rows else BLOCK_SQUARE)
+                         f"{-(-K // BLOCK)} x {-(-rows // BLOCK)}, got {tuple(scales.shape)}")
+    ld, unit = values.stride()
+    lds, unit_s = scales.stride()
+    if (unit != 1 and K > 1) or (unit_s != 1 and per > 1):
+        raise ValueError(f"{name} and its scales need unit stride along the last dim")
+    if rows <= 1:
+        ld = (K + 15) & -16  # a single row has no next one
+    _SCALED.pack_into(into, 0, values.data_ptr(), ld, scales.data_ptr(), lds if blocks > 1 else per, code,
+                      BLOCK_SQUARE if square else BLOCK_ROW)
     return rows, K
 
 
@@ -488,13 +494,18 @@ class Plan:
             raise TypeError(f"quantize makes float8_e4m3fn or float8_e5m2, got {dtype}")
         if blocks not in ("row", "square"):
             raise ValueError(f"blocks must be 'row' or 'square', got {blocks!r}")
-        self._check_tensor("X", X)
-        ldx = _ld(X)
+        if X.get_device() != self.device:
+            self._check_tensor("X", X)
+        if X.dim() != 2:
+            raise ValueError("X must be 2-D")
         rows, cols = X.shape
-        if rows == 1:
-            ldx = -(-ldx // 8) * 8  # a single row has no next one
+        ldx, unit = X.stride()
+        if unit != 1 and cols > 1:
+            raise ValueError("X must be row-major (unit stride along the last dim)")
+        if rows <= 1:
+            ldx = (cols + 7) & -8  # a single row has no next one
         square = blocks == "square"
-        kb, rb = -(-cols // BLOCK), -(-rows // BLOCK)
+        kb, rb = (cols + 127) >> 7, (rows + 127) >> 7
         per, per_t = (rb, kb) if square else (rows, cols)
         dev = X.device
         q = _padded_empty(rows, cols, dtype, dev, 16)
@@ -504,11 +515,13 @@ class Plan:
         if transposed:
             qt = _padded_empty(cols, rows, dtype, dev, 16)
             st = torch.empty((rb, per_t), dtype=torch.float32, device=dev)
-            args_t = (qt.data_ptr(), -(-rows // 16) * 16, st.data_ptr(), per_t)
+            args_t = (qt.data_ptr(), (rows + 15) & -16, st.data_ptr(), per_t)
             result = (q, s, qt, st)
         rc = self.lib.bwgemm_quantize(self.handle, X.data_ptr(), dt, rows, cols, ldx,
                                       BLOCK_SQUARE if square else BLOCK_ROW, f8, int(pow2), q.data_ptr(),
-                                      -(-cols // 16) * 16, s.data_ptr(), per, *args_t, self._stream(stream))
+                                      (cols + 15) & -16, s.data_ptr(), per, *args_t,
+                                      _torch_mod._C._cuda_getCurrentRawStream(self.device) if stream is None
+                                      else stream.cuda_stream)
         if rc != 0:
             raise BwgemmError(rc, "bwgemm_quantize")
         return result
@@ -530,17 +543,22 @@ class Plan:
         if out is None:
             if accumulate:
                 raise ValueError("accumulate needs the out tensor to add to")
-            out = _padded_empty(M, N, torch.bfloat16 if out_dtype is None else out_dtype, A.device, 8)
+            if out_dtype is None:
+                out_dtype = torch.bfloat16
+            ldc = (N + 7) & -8
+            out = _padded_empty(M, N, out_dtype, A.device, 8)
         else:
             self._check_tensor("out", out)
             if tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
                 raise ValueError("out must be an M x N CUDA tensor of out_dtype")
-        dt = _all_dtype_codes.get(out.dtype)
+            out_dtype = out.dtype
+            ldc = _ld(out) if M > 1 else (N + 7) & -8  # a single row has no next one
+        dt = _all_dtype_codes.get(out_dtype)
         if dt is None:
-            raise TypeError(f"gemm_scaled writes bfloat16, float16 or float32, got {out.dtype}")
-        ldc = _ld(out) if M > 1 else -(-N // 8) * 8  # a single row has no next one
+            raise TypeError(f"gemm_scaled writes bfloat16, float16 or float32, got {out_dtype}")
         rc = self.lib.bwgemm_run_scaled(self.handle, self._a_at, self._b_at, out.data_ptr(), M, N, K, ldc, dt,
-                                        int(accumulate), self._stream(stream))
+                                        1 if accumulate else 0,
+                                        torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
         if rc != 0:
             raise BwgemmError(rc, "bwgemm_run_scaled")
         return out

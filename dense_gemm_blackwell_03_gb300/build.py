@@ -21,7 +21,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libbwgemm.so")
 
 SOURCES = ["gemm_sm103.cu", "skinny_sm103.cu", "wholek_sm103.cu", "api.cpp", "planner.cpp", "noalloc.cu", "probe.cu",
-           "microbench.cu", "quantize_sm103.cu", "scaled_sm103.cu", "ortho_sm103.cu", "operators.cpp"]
+           "microbench.cu", "quantize_sm103.cu", "scaled_sm103.cu", "scaled_few_sm103.cu", "ortho_sm103.cu", "operators.cpp"]
 HEADERS = ["ptx.cuh", "gemm_kernel.cuh", "skinny_kernel.cuh", "wholek_kernel.cuh", "kernel_params.h", "internal.h", "tuned_table.h",
            "plan.h", "operators.h", "scaled_kernel.cuh", "ortho_kernel.cuh", "pipeline.cuh"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -113,6 +113,24 @@ double block_us(const ScaledVariant& v, int l_rows)
     return std::max(step, (l_rows + v.bn) * 128.0 / 150e3);
 }
 
+// Whether the kernel for few rows of A takes the product, by both kernels' time:
+// fitted in microseconds to M = 1, 8, 9 and 16 on 18 shapes.  Few rows: the bytes,
+// the K blocks that a warp takes one after another, and the CTAs; tiles: the K
+// blocks of a tile, split over CTAs where they are many, or the bytes.  Measured,
+// few rows against tiles: 1 x 1024 x 1024 1.7 and 6.9, 1 x 4096 x 4096 4.8 and 11.2,
+// 8 x 8192 x 8192 18.0 and 18.1, 1 x 16384 x 8192 30.6 and 24.0, 1 x 128 x 28672
+// 13.9 and 28.8, 1 x 28672 x 1024 10.2 and 7.9; 16 x 4096 x 8192 15.7 and 20.1,
+// 16 x 8192 x 4096 13.0 and 11.7.
+bool takes_few_rows(int64_t M, int64_t N, int64_t K)
+{
+    if (M > kScaledFewRows)
+        return false;
+    const double bytes = double(N) * double(K), kb = double(blocks_of(K));
+    const double few = 1.5 + bytes / (M <= 8 ? 5.2e6 : 3.3e6) + 0.25 * kb / 8 + 75e-6 * double(N);
+    const double tiles = 4.5 + std::max(std::min(0.2 * kb, 15.0), bytes / 6.5e6);
+    return few <= tiles;
+}
+
 ScaledPlan plan_scaled(int num_sms, int64_t M, int64_t N, int64_t K, bool b_square, uint64_t workspace_bytes)
 {
     const int64_t kb = blocks_of(K);
@@ -367,6 +385,32 @@ bwgemm_status_t bwgemm_run_scaled(bwgemm_plan_t plan, const bwgemm_scaled_t* A, 
     }
     if ((st = check_resident({A->values, A->scales, B->values, B->scales, C}, plan->device)) != BWGEMM_OK)
         return st;
+
+    if (takes_few_rows(M, N, K)) {
+        FewParams f = {};
+        f.w = static_cast<const uint8_t*>(B->values);
+        f.x = static_cast<const uint8_t*>(A->values);
+        f.ldw = B->ld;
+        f.ldx = A->ld;
+        f.ws = B->scales;
+        f.xs = A->scales;
+        f.ws_ld = B->ld_scales;
+        f.xs_ld = A->ld_scales;
+        f.ws_shift = B->block == BWGEMM_BLOCK_SQUARE ? 7 : 0;
+        f.xs_shift = A->block == BWGEMM_BLOCK_SQUARE ? 7 : 0;
+        f.M = int32_t(M);
+        f.N = int32_t(N);
+        f.K = int32_t(K);
+        f.num_kb = int32_t(blocks_of(K));
+        f.c = C;
+        f.ldc = ldc;
+        f.out_type = out;
+        f.accumulate = accumulate ? 1 : 0;
+        if (launch_scaled_few(B->type, A->type, f, s, plan->opts.pdl_off == 0) != cudaSuccess)
+            return BWGEMM_ERR_CUDA;
+        plan->launches += 1;
+        return BWGEMM_OK;
+    }
 
     const ScaledPlan sel =
         plan_scaled(plan->num_sms, M, N, K, B->block == BWGEMM_BLOCK_SQUARE, plan->workspace_bytes);

@@ -121,6 +121,23 @@ cudaError_t launch_scaled(int idx, const CUtensorMap& l, const CUtensorMap& c, c
                           const CUtensorMap& c3, const CUtensorMap& out, const ScaledParams& p, int grid,
                           cudaStream_t stream, bool pdl);
 
+// The same product for at most kScaledFewRows rows of A (scaled_few_sm103.cu).
+struct FewParams {
+    const uint8_t* w;            // weights, N x K, ldw bytes apart
+    const uint8_t* x;            // A, M x K
+    int64_t ldw, ldx;
+    const float* ws;             // scales as in ScaledParams
+    const float* xs;
+    int64_t ws_ld, xs_ld;
+    int32_t ws_shift, xs_shift;
+    int32_t M, N, K, num_kb;
+    void* c;
+    int64_t ldc;
+    int32_t out_type, accumulate;
+};
+constexpr int kScaledFewRows = 16;
+cudaError_t launch_scaled_few(int w_type, int x_type, const FewParams& p, cudaStream_t stream, bool pdl);
+
 // -------------------------------------------------------- orthogonalisation
 // One product of the iteration over a stack of matrices, fp16 operands:
 //   D = alpha * A B^T + beta * E + diag * I

@@ -7,11 +7,8 @@ namespace bwgemm {
 
 // Bounded wait on an mbarrier phase: gives up after p.timeout_ns (recording
 // `code` in the status word) or as soon as another role of this CTA gave up.
-// The way through is a loop of a few instructions, and the clock and the abort
-// flag are looked at once in many probes, out of its way: a role's loop runs
-// once per K block, in a few hundred cycles, and with the whole wait inlined in
-// its middle the MMA issuer of the block-scaled product took some 500 cycles a
-// block to fetch and run its own instructions.
+// The way through is a loop of a few instructions; the clock and the abort flag
+// are looked at once in many probes, out of its way.
 template <typename Params>
 __device__ __forceinline__ bool pipe_wait(uint32_t bar, uint32_t parity, const Params& p, volatile uint32_t* abort_flag,
                                           uint32_t code)

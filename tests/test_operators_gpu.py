@@ -264,6 +264,50 @@ def test_scaled_forms(plan, M, a_square, b_square, kinds):
     check_product(plan, M, 700, 900, a_square=a_square, b_square=b_square, a_kind=kinds[0], b_kind=kinds[1], seed=M)
 
 
+# the kernel for few rows: both groups of eight, every pair of types and kind of block,
+# one to many K blocks per warp
+@pytest.mark.parametrize("a_square", [False, True])
+@pytest.mark.parametrize("b_square", [False, True])
+@pytest.mark.parametrize("kinds", [("e4m3", "e4m3"), ("e5m2", "e4m3"), ("e4m3", "e5m2"), ("e5m2", "e5m2")])
+@pytest.mark.parametrize("M,N,K", [(1, 259, 2056), (7, 131, 4200), (8, 1001, 128), (9, 130, 3900), (16, 77, 1030)])
+def test_scaled_few_rows_forms(plan, M, N, K, a_square, b_square, kinds):
+    check_product(plan, M, N, K, a_square=a_square, b_square=b_square, a_kind=kinds[0], b_kind=kinds[1], seed=M)
+
+
+# so many weights that tiles take even a few rows
+@pytest.mark.parametrize("M", [1, 5, 13])
+@pytest.mark.parametrize("b_square", [False, True])
+def test_scaled_few_rows_many_weights(plan, M, b_square):
+    check_product(plan, M, 20008, 6100, b_square=b_square, seed=M)
+
+
+@pytest.mark.parametrize("M", [2, 12])
+def test_scaled_few_rows_in_the_last_bytes(plan, M):
+    # operands that end with the last value of their last row, a sum onto C in place
+    N, K, ld = 40, 1030, 1040
+    A, sa, a = random_scaled(M, K, "e4m3", False, 5)
+    B, sb, b = random_scaled(N, K, "e4m3", True, 6)
+    tight = []
+    for x, rows in ((A, M), (B, N)):
+        y = torch.zeros((rows - 1) * ld + K, dtype=torch.uint8, device="cuda").as_strided((rows, K), (ld, 1))
+        y.copy_(x.view(torch.uint8))
+        tight.append(y.view(torch.float8_e4m3fn))
+    C = torch.ones(M, N, device="cuda")
+    plan.gemm_scaled(tight[0], sa, tight[1], sb, out=C, accumulate=True)
+    exact, bound = product_bound(a, b, "fp32")
+    assert (np.abs(host(C) - (exact + 1)) <= bound + 2.0 ** -24 * (np.abs(exact) + 1)).all()
+
+
+@pytest.mark.parametrize("M", [3, 11])
+def test_scaled_few_rows_nan_stays_in_its_row(plan, M):
+    A, sa, _ = random_scaled(M, 1100, "e4m3", False, 1)
+    B, sb, _ = random_scaled(90, 1100, "e4m3", True, 2)
+    want = plan.gemm_scaled(A, sa, B, sb, out_dtype=torch.float32)
+    A.view(torch.uint8)[M - 1, 1099] = 0x7F
+    got = plan.gemm_scaled(A, sa, B, sb, out_dtype=torch.float32)
+    assert torch.isnan(got[M - 1]).all() and torch.equal(got[: M - 1], want[: M - 1])
+
+
 @pytest.mark.parametrize("M,N,K", [(2000, 3000, 768), (4096, 300, 2048), (130, 9000, 1024), (64, 20000, 384),
                                    (1, 512, 30000), (300, 128, 20000)])
 def test_scaled_many_tiles(plan, M, N, K):
@@ -422,7 +466,7 @@ def test_scaled_refusals(plan):
     torch.cuda.synchronize()
 
 
-@pytest.mark.parametrize("M", [8, 300])
+@pytest.mark.parametrize("M", [24, 300])
 def test_scaled_timeout_is_reported(M):
     # the producer of CTA 0 never fills a stage: the bounded waits run out and
     # the plan works again afterwards
