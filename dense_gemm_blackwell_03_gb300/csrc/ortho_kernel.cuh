@@ -48,6 +48,8 @@ struct OrthoConfig {
     static constexpr int kStages = 3;
     static constexpr int kTmemCols = 2 * kTile;
     static constexpr int kStoreBytes = 4096;               // a warp's 32 x 64 16-bit values
+    static constexpr int kIdleBytes = 2 * kStages * kOperandBytes / kEpiWarps;  // of the idle ring, per warp
+    static_assert(kIdleBytes % 1024 == 0 && kIdleBytes >= kCols / 64 * 2 * kStoreBytes, "boxes of a tile");
     static constexpr int kOffA = 0;
     static constexpr int kOffB = kStages * kOperandBytes;
     static constexpr int kOffStore = 2 * kStages * kOperandBytes;
@@ -197,7 +199,6 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
-        ptx::grid_dependency_wait();
         const uint32_t leader_full = CG == 2 ? ptx::map_to_cta(bar_full, 0) : bar_full;
         int s = 0, n = 0;
         uint32_t phase = 0;
@@ -229,6 +230,10 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                     const int rb = B_MN ? k : b0, cb = (B_MN ? b0 : k) / 64;
                     if (rank == 0)
                         ptx::mbar_arrive_expect_tx(fb, uint32_t(CG * 2 * Cfg::kOperandBytes));
+                    // as late as can be: all before it, its instructions' way into the cache
+                    // too (1200 to 2000 cycles), overlaps the product before
+                    if (n == 0)
+                        ptx::grid_dependency_wait();
                     if constexpr (CG == 2) {
                         ptx::tma_load_4d_pair(dA, ma, fb, 0, ra, ca, x.matrix);
                         ptx::tma_load_4d_pair(dB, mb, fb, 0, rb, cb, x.matrix);
@@ -314,6 +319,10 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
             const int row = row0 + lane;
             const float alpha = p.alpha_dev ? p.alpha * ptx::ld_global_cg_f32(p.alpha_dev + x.matrix) : p.alpha;
             const bool mirror = p.symmetric && x.r != x.c;
+            // The CTA's last tile: once its sums are there, the ring has been read and
+            // takes the result's boxes, so that none waits for the one before it to leave.
+            const bool idle = t + workers >= total;
+            uint32_t box = idle ? base + uint32_t(e * Cfg::kIdleBytes) : sb;
             // The epilogue is bound by its own instructions (8 warps share four
             // schedulers with the issuing ones, and a 256-wide tile is 128 columns a
             // thread), so what only some products need is tested once per 64
@@ -321,15 +330,18 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
             const uint64_t alpha2 = ptx::pack_f32x2(__float_as_uint(alpha), __float_as_uint(alpha));
             const uint64_t beta2 = ptx::pack_f32x2(__float_as_uint(p.beta), __float_as_uint(p.beta));
             // E's 64 columns, loaded before the sums are waited for, later ones a
-            // piece ahead
-            const bool e_row = p.e != nullptr && row < p.rows;
-            const uint16_t* const e_at = p.e + x.matrix * p.stride_e + row * p.lde + col0;
+            // piece ahead: four rows of 128 bytes at a time (eight lanes each), turned
+            // to a row per lane through the staging block
+            const uint16_t* const e_at = p.e + x.matrix * p.stride_e + (row0 + (lane >> 3)) * p.lde + col0 + 8 * (lane & 7);
             uint4 add[8];
             auto fetch = [&](int c) {
-                if (e_row && c < Cfg::kCols && col0 + c < p.store_cols) {
+                if (p.e != nullptr && c < Cfg::kCols) {
+                    const bool in = col0 + c + 8 * (lane & 7) < p.store_cols;
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        add[i] = ptx::ld_global_cg_v4(e_at + c + 8 * i);
+                        add[i] = in && row0 + 4 * i + (lane >> 3) < p.rows
+                                     ? ptx::ld_global_cg_v4(e_at + c + 4 * i * p.lde)
+                                     : make_uint4(0u, 0u, 0u, 0u);
                 }
             };
             fetch(0);
@@ -342,17 +354,38 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                 const bool mirrored = mirror && col < p.rows && row0 < p.store_cols;
                 if (!direct && !mirrored)
                     return;
+                auto claim = [&] {  // the store before has read the staging block
+                    if (idle)
+                        return;
+                    if (lane == 0)
+                        ptx::bulk_wait_group_read<0>();
+                    __syncwarp();
+                };
                 uint64_t f[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     f[i] = ptx::mul_f32x2(ptx::pack_f32x2(v[2 * i], v[2 * i + 1]), alpha2);
-                if (e_row && col < p.store_cols) {
+                if (p.e != nullptr) {
+                    claim();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const uint32_t w = (&add[i >> 2].x)[i & 3];
-                        const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&w));
-                        f[i] = ptx::fma_f32x2(ptx::pack_f32x2(__float_as_uint(g.x), __float_as_uint(g.y)), beta2, f[i]);
+                    for (int i = 0; i < 8; ++i)
+                        ptx::st_shared_v4(box + uint32_t((4 * i + (lane >> 3)) * 128) +
+                                              (uint32_t((lane & 7) ^ ((4 * i + (lane >> 3)) & 7)) << 4),
+                                          add[i].x, add[i].y, add[i].z, add[i].w);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        uint32_t w[4];
+                        ptx::ld_shared_v4(box + uint32_t(lane * 128) + (uint32_t((i >> 2) ^ (lane & 7)) << 4), w[0], w[1],
+                                          w[2], w[3]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                            f[i + k] = ptx::fma_f32x2(ptx::pack_f32x2(__float_as_uint(g.x), __float_as_uint(g.y)), beta2,
+                                                      f[i + k]);
+                        }
                     }
+                    __syncwarp();
                 }
                 fetch(c + 64);
                 if (p.diag != 0.f && row0 < col + 64 && col < row0 + 32) {
@@ -372,18 +405,15 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                     ptx::unpack_f32x2(f[i], lo, hi);
                     w[i] = pack2(__float_as_uint(lo), __float_as_uint(hi), p.out_bf16 ? 0 : 1);
                 }
-                auto claim = [&] {  // the store before has read the staging block
-                    if (lane == 0)
-                        ptx::bulk_wait_group_read<0>();
-                    __syncwarp();
-                };
                 auto put = [&](const CUtensorMap* map, int at_col, int at_row) {
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        ptx::tma_store_3d(map, sb, at_col, at_row, x.matrix);
+                        ptx::tma_store_3d(map, box, at_col, at_row, x.matrix);
                         ptx::bulk_commit_group();
                     }
+                    if (idle)
+                        box += Cfg::kStoreBytes;
                 };
                 if (p.plain_store) {
                     // the caller's rows are not on 16-byte boundaries: the block goes
@@ -405,12 +435,12 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                 }
                 if (direct) {
                     claim();
-                    ortho_stage(w, sb, lane);
+                    ortho_stage(w, box, lane);
                     put(&tmap_out, col, row0);
                 }
                 if (mirrored) {
                     claim();
-                    ortho_stage_turned(w, sb, lane);
+                    ortho_stage_turned(w, box, lane);
                     put(&tmap_out2, row0, col);
                 }
                 if (p.low && direct) {
@@ -422,7 +452,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                         w[i] = pack2(__float_as_uint(lo - h.x), __float_as_uint(hi - h.y), 1);
                     }
                     claim();
-                    ortho_stage(w, sb, lane);
+                    ortho_stage(w, box, lane);
                     put(&tmap_out2, col, row0);
                 }
             };

@@ -370,7 +370,6 @@ __global__ void __launch_bounds__(ScaledConfig<BN, SWAP, COLVEC>::kThreads, 1)
             ptx::setmaxnreg_dec<Cfg::kRegsFirst>();
         if (warp == 0) {
             // ------------------------------------------------------ TMA producer
-            ptx::grid_dependency_wait();
             ScaledIter iter;
             ScaledSegment seg;
             iter.init(p, worker, workers);
@@ -397,6 +396,8 @@ __global__ void __launch_bounds__(ScaledConfig<BN, SWAP, COLVEC>::kThreads, 1)
                         const uint32_t fb = bar_full + 8 * s;
                         const uint32_t dL = sL + uint32_t(s * l_bytes), dC = sC + uint32_t(s * Cfg::kCBytes);
                         ptx::mbar_arrive_expect_tx(fb, uint32_t(nkb * (l_block + Cfg::kCBlock)));
+                        if (i == 0)  // all before it overlaps the kernel before
+                            ptx::grid_dependency_wait();
                         if (nkb == KPS) {
                             ptx::tma_load_3d(dL, &tmap_l3, fb, 0, l_row, kb);
                             ptx::tma_load_3d(dC, &tmap_c3, fb, 0, c_row, kb);
@@ -498,13 +499,12 @@ __global__ void __launch_bounds__(ScaledConfig<BN, SWAP, COLVEC>::kThreads, 1)
             // -------------------------------------------------------- scales
             // Each thread's arrival on a slot comes when its copies have landed, so the
             // warp runs ahead of the epilogue as far as the slots allow.
-            ptx::grid_dependency_wait();
             ScaledIter iter;
             ScaledSegment seg;
             iter.init(p, worker, workers);
             int slot = 0;
             uint32_t phase = 0;
-            bool ok = true;
+            bool ok = true, first = true;
             while (ok && iter.next(p, seg)) {
                 const int row0 = seg.l_blk * l_rows;
                 const int col0 = seg.c_blk * BN;
@@ -514,6 +514,9 @@ __global__ void __launch_bounds__(ScaledConfig<BN, SWAP, COLVEC>::kThreads, 1)
                                                            kStatusProducerTimeout));
                     if (!ok)
                         break;
+                    if (first)
+                        ptx::grid_dependency_wait();
+                    first = false;
                     const int n = min(Cfg::kGroup, seg.kb1 - kb);
 #pragma unroll 1
                     for (int g = 0; g < n; ++g) {
