@@ -216,6 +216,13 @@ constexpr int kOrthoMaxSteps = 64;
 // N(0, 1) 1.2e-3 / 1.1e-3 / 1.1e-3 / 1.1e-3; eight directions 30 times the
 // rest 1.3e-2 / 2.9e-3 / 1.4e-3 / 1.3e-3; singular values 1 / i 1.8e-3 /
 // 1.1e-3 / 7e-4 / 7e-4.  (Rounding the result to bf16 alone is 1.7e-3.)
+// Rounding B in the same steps matters where all singular values are close (long
+// matrices, or nearly orthogonal ones): its diagonal is then one value that rounds
+// one way, an error of the whole result.  The diagonal blocks of 128 of B keep
+// their low part: largest error over 60 matrices of 16 to 128 rows, up to 4096
+// columns, N(0, 1), as a multiple of the bf16 rounding of the result: 2.34
+// without, 1.42 with it (1.48 in steps 2 and 3 alone); 512 x 16384 1.82 and 1.28.
+// It costs a K step per 128 rows of the tile, 16 x 512 x 1344 212 -> 226 us.
 constexpr int kTwoTermSteps = 3;
 
 struct OrthoLayout {
@@ -252,7 +259,7 @@ OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols)
         l.lo[i] = take(uint64_t(batch) * l.x_stride * 2);
     }
     l.s = take(uint64_t(batch) * l.s_stride * 2);
-    l.b = take(uint64_t(batch) * l.s_stride * 2);
+    l.b = take(uint64_t(batch) * l.s_stride * 2 * 2);  // B and its low part
     l.sums = take(uint64_t(batch) * l.parts * 4);
     l.factors = take(uint64_t(batch) * 2 * 4);
     l.total = at;
@@ -556,9 +563,9 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
     if ((st = encode_stack(&s_op, ws + l.s, l.m, l.lds, l.s_stride, batch)) != BWGEMM_OK ||
         (st = encode_result(&s_res, BWGEMM_FP16, ws + l.s, l.m, l.lds, l.lds, l.s_stride, batch)) != BWGEMM_OK ||
         (st = encode_result(&s_turned, BWGEMM_FP16, ws + l.s, l.m, l.lds, l.lds, l.s_stride, batch, true)) != BWGEMM_OK ||
-        (st = encode_result(&b_turned, BWGEMM_FP16, ws + l.b, l.m, l.lds, l.lds, l.s_stride, batch, true)) != BWGEMM_OK ||
-        (st = encode_stack(&b_op, ws + l.b, l.m, l.lds, l.s_stride, batch)) != BWGEMM_OK ||
-        (st = encode_result(&b_res, BWGEMM_FP16, ws + l.b, l.m, l.lds, l.lds, l.s_stride, batch)) != BWGEMM_OK)
+        (st = encode_result(&b_turned, BWGEMM_FP16, ws + l.b, l.m, l.lds, l.lds, l.s_stride, 2 * batch, true)) != BWGEMM_OK ||
+        (st = encode_stack(&b_op, ws + l.b, l.m, l.lds, l.s_stride, 2 * batch)) != BWGEMM_OK ||
+        (st = encode_result(&b_res, BWGEMM_FP16, ws + l.b, l.m, l.lds, l.lds, l.s_stride, 2 * batch)) != BWGEMM_OK)
         return st;
     // a TMA store needs 16-byte rows, and clips a row's end only in whole
     // 16-byte pieces
@@ -584,20 +591,20 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
     auto product = [&](int form, OrthoParams p, int64_t K, const CUtensorMap& a, const CUtensorMap& b,
                        const CUtensorMap& a2, const CUtensorMap& b2, const CUtensorMap& res, const CUtensorMap& res2) {
         p.steps_k = int32_t((K + 127) / 128);
-        const int64_t steps_all = int64_t(p.steps_k) * p.terms;
+        auto steps_all = [&](int cg) { return int64_t(p.steps_k) * p.terms + (p.low_side ? cg : 0); };
         int64_t tiles[3] = {};
         for (int cg = 1; cg <= 2; ++cg) {
             const int64_t r = (p.rows + 128 * cg - 1) / (128 * cg), c = (p.cols + 128 * cg - 1) / (128 * cg);
             tiles[cg] = (p.symmetric ? r * (r + 1) / 2 : r * c) * batch;
         }
-        int64_t best = (tiles[2] + pairs - 1) / pairs * steps_all * 1024;
+        int64_t best = (tiles[2] + pairs - 1) / pairs * steps_all(2) * 1024;
         int cg = 2;
         p.splits = 1;
-        const int64_t most = std::min<int64_t>(plan->num_sms / std::max<int64_t>(tiles[1], 1), steps_all / 4);
+        const int64_t most = std::min<int64_t>(plan->num_sms / std::max<int64_t>(tiles[1], 1), steps_all(1) / 4);
         const bool room = kCounterRegionBytes + uint64_t(plan->num_sms) * 128 * 128 * 4 <= plan->workspace_bytes;
         for (int64_t splits = 1; splits <= std::max<int64_t>(1, room ? most : 1); ++splits) {
             const int64_t cost = (tiles[1] * splits + plan->num_sms - 1) / plan->num_sms *
-                                     ((steps_all + splits - 1) / splits) * 740 +
+                                     ((steps_all(1) + splits - 1) / splits) * 740 +
                                  (splits > 1 ? 8000 + 800 * splits : 0);
             if (cost < best) {
                 best = cost;
@@ -639,6 +646,7 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
         p.alpha_dev = nullptr;
         p.beta = b;
         p.diag = a;
+        p.low = i < kTwoTermSteps;
         p.e = reinterpret_cast<const uint16_t*>(ws + l.s);
         p.lde = l.lds;
         p.stride_e = l.s_stride;
@@ -650,6 +658,7 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
         p.rows = int32_t(rows);
         p.cols = int32_t(cols);
         p.terms = i == 0 ? first_terms : (i < kTwoTermSteps ? 2 : 1);
+        p.low_side = i >= kTwoTermSteps ? 0 : l.wide ? 1 : 2;
         p.alpha = last ? scale * (i == 0 ? 1.f : down) : (i == 0 ? 1.f / down : 1.f);
         p.alpha_dev = i == 0 ? in.factors : nullptr;
         p.store_cols = int32_t(last ? cols : l.ldx);

@@ -147,6 +147,8 @@ struct OrthoParams {
     int32_t rows, cols;          // of D
     int32_t steps_k;             // ceil(K / 128)
     int32_t terms;               // 1, or 2: A or B is the sum of two fp16 matrices (maps a2 / b2)
+    int32_t low_side;            // 0: none; then a step per 128 of the tile's diagonal block with the
+                                 // low part of A (1) or B (2), stored `batch` matrices further
     int32_t num_r, num_c;        // tiles along rows and columns
     int32_t tiles, batch;        // tiles per matrix; matrices
     int32_t splits;              // slices of K per tile (1: whole)
@@ -158,7 +160,8 @@ struct OrthoParams {
     const uint16_t* e;           // E, fp16 (null: none), lde elements apart, stride_e per matrix
     int64_t lde, stride_e;
     int32_t store_cols;          // columns that may be stored (D's padded width)
-    int32_t low;                 // 1: also store what fp16 rounding lost (map out2)
+    int32_t low;                 // 1: also store what fp16 rounding lost (map out2; symmetric: of the
+                                 // diagonal's tiles, `batch` matrices further)
     int32_t out_bf16;            // 1: D is bf16 instead of fp16
     int32_t plain_store;         // 1: D's rows cannot be written by TMA: element by element to `out`
     uint16_t* out;

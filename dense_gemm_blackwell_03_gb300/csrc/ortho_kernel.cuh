@@ -21,6 +21,11 @@
 // operand's low part (what fp16 rounding lost) -- the sum of both products in
 // one accumulator.
 //
+// The diagonal: where X's singular values are close together, B is close to a
+// multiple of I, and fp16 rounds all of its diagonal the same way -- a relative
+// error of the whole result.  In the first steps the diagonal tiles of B keep
+// their low part too, and the product with X takes one more K step with it.
+//
 // Few tiles and a deep K (long, narrow matrices): the tiles of S are cut into
 // slices of K whose fp32 sums meet in global memory and are added in order.
 //
@@ -81,11 +86,19 @@ struct OrthoTile {
     int slice, k0, k1;  // slice of K: steps [k0, k1)
 };
 
+// K steps of a tile: the operands' terms, and the low part of its diagonal block.
+template <int CG>
+__device__ __forceinline__ int ortho_steps(const OrthoParams& p)
+{
+    return p.steps_k * p.terms + (p.low_side ? CG : 0);
+}
+
+template <int CG>
 __device__ __forceinline__ OrthoTile ortho_tile_at(const OrthoParams& p, int t)
 {
     OrthoTile x;
     const int whole = t / p.splits;
-    const int steps = p.steps_k * p.terms;
+    const int steps = ortho_steps<CG>(p);
     x.slice = t - whole * p.splits;
     x.k0 = x.slice * steps / p.splits;
     x.k1 = (x.slice + 1) * steps / p.splits;
@@ -205,7 +218,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
         bool ok = true;
 #pragma unroll 1
         for (int t = worker; ok && t < total; t += workers) {
-            const OrthoTile x = ortho_tile_at(p, t);
+            const OrthoTile x = ortho_tile_at<CG>(p, t);
             const int a0 = x.r * TILE + int(rank) * 128;  // this CTA's output rows, and columns of B
             const int b0 = x.c * TILE + int(rank) * 128;
 #pragma unroll 1
@@ -220,8 +233,18 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                     armed_parity = (armed_parity & ~(1u << s)) | (phase << s);
                 }
                 if (!stall && ptx::elect_one()) {
-                    const bool second = i >= p.steps_k;
-                    const int k = (second ? i - p.steps_k : i) * kOrthoK;
+                    const bool low = i >= p.steps_k * p.terms;
+                    const bool second = !low && i >= p.steps_k;
+                    int k = (second ? i - p.steps_k : i) * kOrthoK, za = x.matrix, zb = x.matrix;
+                    if (low) {
+                        // the block of 128 of the diagonal that this CTA's rows (columns)
+                        // lie in; past the last matrix the copy brings zeros
+                        const int j = i - p.steps_k * p.terms;
+                        const int z = j == int(rank) ? x.matrix + p.batch : 2 * p.batch;
+                        k = (p.low_side == 1 ? x.r : x.c) * TILE + j * kOrthoK;
+                        za = p.low_side == 1 ? z : za;
+                        zb = p.low_side == 1 ? zb : z;
+                    }
                     const CUtensorMap* ma = second ? &tmap_a2 : &tmap_a;
                     const CUtensorMap* mb = second ? &tmap_b2 : &tmap_b;
                     const uint32_t fb = leader_full + 8 * s;
@@ -235,11 +258,11 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                     if (n == 0)
                         ptx::grid_dependency_wait();
                     if constexpr (CG == 2) {
-                        ptx::tma_load_4d_pair(dA, ma, fb, 0, ra, ca, x.matrix);
-                        ptx::tma_load_4d_pair(dB, mb, fb, 0, rb, cb, x.matrix);
+                        ptx::tma_load_4d_pair(dA, ma, fb, 0, ra, ca, za);
+                        ptx::tma_load_4d_pair(dB, mb, fb, 0, rb, cb, zb);
                     } else {
-                        ptx::tma_load_4d(dA, ma, fb, 0, ra, ca, x.matrix);
-                        ptx::tma_load_4d(dB, mb, fb, 0, rb, cb, x.matrix);
+                        ptx::tma_load_4d(dA, ma, fb, 0, ra, ca, za);
+                        ptx::tma_load_4d(dB, mb, fb, 0, rb, cb, zb);
                     }
                 }
                 __syncwarp();
@@ -262,7 +285,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
         bool ok = true;
 #pragma unroll 1
         for (int t = worker; ok && t < total; t += workers) {
-            const OrthoTile x = ortho_tile_at(p, t);
+            const OrthoTile x = ortho_tile_at<CG>(p, t);
             ok = __all_sync(0xffffffffu,
                             pipe_wait(bar_acc_empty + 8 * b, bphase ^ 1u, p, abort_flag, kStatusMmaTimeout));
 #pragma unroll 1
@@ -313,7 +336,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
         bool ok = true;
 #pragma unroll 1
         for (int t = worker; ok && t < total; t += workers) {
-            const OrthoTile x = ortho_tile_at(p, t);
+            const OrthoTile x = ortho_tile_at<CG>(p, t);
             const int row0 = x.r * TILE + int(rank) * 128 + 32 * q;
             const int col0 = x.c * TILE + (e >> 2) * Cfg::kCols;
             const int row = row0 + lane;
@@ -405,11 +428,11 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                     ptx::unpack_f32x2(f[i], lo, hi);
                     w[i] = pack2(__float_as_uint(lo), __float_as_uint(hi), p.out_bf16 ? 0 : 1);
                 }
-                auto put = [&](const CUtensorMap* map, int at_col, int at_row) {
+                auto put = [&](const CUtensorMap* map, int at_col, int at_row, int z) {
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        ptx::tma_store_3d(map, box, at_col, at_row, x.matrix);
+                        ptx::tma_store_3d(map, box, at_col, at_row, z);
                         ptx::bulk_commit_group();
                     }
                     if (idle)
@@ -436,14 +459,14 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                 if (direct) {
                     claim();
                     ortho_stage(w, box, lane);
-                    put(&tmap_out, col, row0);
+                    put(&tmap_out, col, row0, x.matrix);
                 }
                 if (mirrored) {
                     claim();
                     ortho_stage_turned(w, box, lane);
-                    put(&tmap_out2, row0, col);
+                    put(&tmap_out2, row0, col, x.matrix);
                 }
-                if (p.low && direct) {
+                if (p.low && direct && !mirror) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         float lo, hi;
@@ -453,7 +476,10 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                     }
                     claim();
                     ortho_stage(w, box, lane);
-                    put(&tmap_out2, col, row0);
+                    if (p.symmetric)
+                        put(&tmap_out, col, row0, x.matrix + p.batch);
+                    else
+                        put(&tmap_out2, col, row0, x.matrix);
                 }
             };
             ok = __all_sync(0xffffffffu,

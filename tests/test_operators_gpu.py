@@ -653,6 +653,17 @@ def test_orthogonalize_refusals(plan):
     torch.cuda.synchronize()
 
 
+# Singular values close together: B is close to a multiple of I, whose rounding
+# would show in the whole result.  Tolerance: 1.45 times the rounding of the result
+# to bf16 (1.7e-3) in a simulation of every other rounding, and a quarter more.
+@pytest.mark.parametrize("rows,cols", [(20, 2816), (41, 1860), (3500, 27), (64, 5000), (384, 9000), (6000, 200)])
+@pytest.mark.parametrize("seed", range(4))
+def test_orthogonalize_even_singular_values(plan, rows, cols, seed):
+    g = np.random.default_rng(seed).standard_normal((rows, cols)).astype(np.float32)
+    g = torch.from_numpy(g).to(torch.bfloat16)
+    assert rel(plan.orthogonalize(g.cuda()), orthogonalize_ref(host(g))) <= 3.1e-3
+
+
 def test_orthogonalize_timeout_is_reported():
     g = torch.from_numpy(gradient(256, 512, 4)).to(torch.bfloat16).cuda()
     with binding.Plan(0, stall_kblock=1, timeout_ns=20_000_000) as p:
