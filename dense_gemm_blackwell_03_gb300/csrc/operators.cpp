@@ -245,9 +245,10 @@ OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols)
     l.lds = pad(l.m);
     l.x_stride = rows * l.ldx;
     l.s_stride = l.m * l.lds;
-    // about 16K elements per block, and all matrices together a few blocks per SM
-    const int64_t want = (rows * cols + 16383) / 16384;
-    l.parts = int(std::max<int64_t>(1, std::min<int64_t>({want, (rows + 7) / 8, std::max<int64_t>(1, 1216 / batch)})));
+    // 8K elements per block (a thread's pieces in flight), and all matrices
+    // together a few blocks per SM
+    const int64_t want = (rows * l.ldx + 8191) / 8192;
+    l.parts = int(std::max<int64_t>(1, std::min<int64_t>(want, 1216 / batch)));
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         const uint64_t here = at;
@@ -578,40 +579,46 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
     // One product: square tiles of 256 on CTA pairs (1024 SM cycles per 128 of
     // K, bound by the MMAs) or of 128 on single CTAs (about 740, bound by the
     // copies of both operands), whichever takes fewer cycles in its waves; a
-    // deep K of few 128-tiles in slices, which cost some 8000 cycles to join and
-    // 800 for each (32 x 22101 x 54: 1222 us whole, 896 in slices).
+    // deep K of few tiles in slices, whose join costs a kernel more and the way of
+    // its bytes (us for the whole call, whole and in slices: 128 x 20000 335 and 93,
+    // 1024 x 4096 185 and 163, 300 x 1000 88 and 85; 2048 x 8192, whole, 538 and 546).
     const int pairs = plan->max_active[find_variant(2, 256, false, 1)];
     OrthoParams p0 = {};
     p0.batch = int32_t(batch);
     p0.timeout_ns = plan->opts.timeout_ns ? plan->opts.timeout_ns : 4000000000ull;
     p0.status = plan->d_status;
     p0.stall_kblock = plan->opts.stall_kblock;
-    p0.counters = reinterpret_cast<uint32_t*>(plan->d_workspace);
     p0.partials = reinterpret_cast<float*>(plan->d_workspace + kCounterRegionBytes);
     auto product = [&](int form, OrthoParams p, int64_t K, const CUtensorMap& a, const CUtensorMap& b,
                        const CUtensorMap& a2, const CUtensorMap& b2, const CUtensorMap& res, const CUtensorMap& res2) {
         p.steps_k = int32_t((K + 127) / 128);
-        auto steps_all = [&](int cg) { return int64_t(p.steps_k) * p.terms + (p.low_side ? cg : 0); };
-        int64_t tiles[3] = {};
-        for (int cg = 1; cg <= 2; ++cg) {
-            const int64_t r = (p.rows + 128 * cg - 1) / (128 * cg), c = (p.cols + 128 * cg - 1) / (128 * cg);
-            tiles[cg] = (p.symmetric ? r * (r + 1) / 2 : r * c) * batch;
-        }
-        int64_t best = (tiles[2] + pairs - 1) / pairs * steps_all(2) * 1024;
-        int cg = 2;
-        p.splits = 1;
-        const int64_t most = std::min<int64_t>(plan->num_sms / std::max<int64_t>(tiles[1], 1), steps_all(1) / 4);
-        const bool room = kCounterRegionBytes + uint64_t(plan->num_sms) * 128 * 128 * 4 <= plan->workspace_bytes;
-        for (int64_t splits = 1; splits <= std::max<int64_t>(1, room ? most : 1); ++splits) {
-            const int64_t cost = (tiles[1] * splits + plan->num_sms - 1) / plan->num_sms *
-                                     ((steps_all(1) + splits - 1) / splits) * 740 +
-                                 (splits > 1 ? 8000 + 800 * splits : 0);
-            if (cost < best) {
-                best = cost;
-                cg = 1;
-                p.splits = int32_t(splits);
+        int64_t tiles[3] = {}, best = 0;
+        int cg = 0;
+        for (int g = 1; g <= 2; ++g) {
+            const int64_t r = (p.rows + 128 * g - 1) / (128 * g), c = (p.cols + 128 * g - 1) / (128 * g);
+            tiles[g] = (p.symmetric ? r * (r + 1) / 2 : r * c) * batch;
+            const int64_t steps_all = int64_t(p.steps_k) * p.terms + (p.low_side ? g : 0);
+            const int64_t workers = g == 2 ? pairs : plan->num_sms;
+            int64_t most = 1;
+            if (p.symmetric && !p.e) {
+                const int64_t room = (int64_t(plan->workspace_bytes) - int64_t(kCounterRegionBytes)) / (g * g * 128 * 128 * 4);
+                most = std::max<int64_t>(1, std::min(std::min(workers, room) / tiles[g], steps_all / 2));
+            }
+            for (int64_t splits = 1; splits <= most; ++splits) {
+                const int64_t cost = (tiles[g] * splits + workers - 1) / workers * ((steps_all + splits - 1) / splits) *
+                                         (g == 2 ? 1024 : 740) +
+                                     (splits > 1 ? 3000 + tiles[g] * splits * g * g * 65536 / 1250 : 0);
+                if (cg == 0 || cost < best) {
+                    best = cost;
+                    cg = g;
+                    p.splits = int32_t(splits);
+                }
             }
         }
+        // of the join's CTAs some 2000 at most (24 tiles of 256 in three slices with
+        // eight warps a piece, five of them idle: 13 us a product more than with one)
+        for (p.join_share = 8; p.join_share > 1 && (p.join_share > p.splits || tiles[cg] * cg * cg * 16 * p.join_share > 2048);)
+            p.join_share /= 2;
         if (tiles[cg] * p.splits >= (1ll << 31))
             return BWGEMM_ERR_UNSUPPORTED;
         p.num_r = int32_t((p.rows + 128 * cg - 1) / (128 * cg));
@@ -620,7 +627,7 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
         const int64_t workers = std::min<int64_t>(tiles[cg] * p.splits, cg == 2 ? pairs : plan->num_sms);
         if (launch_ortho(form, cg, a, b, a2, b2, res, res2, p, int(workers * cg), s, pdl) != cudaSuccess)
             return BWGEMM_ERR_CUDA;
-        plan->launches += 1;
+        plan->launches += p.splits > 1 ? 2 : 1;
         return BWGEMM_OK;
     };
 
@@ -639,6 +646,9 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
         p.alpha = i == 0 ? 1.f : down * down;
         p.alpha_dev = i == 0 ? in.factors + batch : nullptr;
         p.store_cols = int32_t(l.lds);
+        p.out = reinterpret_cast<uint16_t*>(ws + l.s);
+        p.ldo = l.lds;
+        p.stride_o = l.s_stride;
         if ((st = product(l.wide ? kOrthoNT : kOrthoTN, p, l.n, x, x, x, x, s_res, s_turned)) != BWGEMM_OK)
             return st;
         // B = a I + b S + c S S

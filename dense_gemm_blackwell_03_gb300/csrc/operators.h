@@ -153,7 +153,7 @@ struct OrthoParams {
     int32_t tiles, batch;        // tiles per matrix; matrices
     int32_t splits;              // slices of K per tile (1: whole)
     float* partials;             // their fp32 sums
-    uint32_t* counters;          // slices arrived per (tile, CTA, warp); zero between launches
+    int32_t join_share;          // warps that add the slices of one piece: 1, 2, 4 or 8
     int32_t symmetric;           // 1: only tiles on and below the diagonal, stored twice
     float alpha, beta, diag;
     const float* alpha_dev;      // a further factor per matrix (null: 1)
@@ -164,7 +164,7 @@ struct OrthoParams {
                                  // diagonal's tiles, `batch` matrices further)
     int32_t out_bf16;            // 1: D is bf16 instead of fp16
     int32_t plain_store;         // 1: D's rows cannot be written by TMA: element by element to `out`
-    uint16_t* out;
+    uint16_t* out;               // D, for plain stores and for slices
     int64_t ldo, stride_o;
     uint64_t timeout_ns;
     uint32_t* status;

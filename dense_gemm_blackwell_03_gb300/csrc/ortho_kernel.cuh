@@ -27,7 +27,8 @@
 // their low part too, and the product with X takes one more K step with it.
 //
 // Few tiles and a deep K (long, narrow matrices): the tiles of S are cut into
-// slices of K whose fp32 sums meet in global memory and are added in order.
+// slices of K whose fp32 sums go to global memory; a second kernel adds them in
+// order, with as many CTAs as there is data.
 //
 // Each stage of the ring holds 128 of K of both operands (64 KiB), one 32 KiB
 // copy each (box {64, 128 rows, 2 chunks}); the same box serves K-major (rows =
@@ -499,11 +500,9 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                     finish(c, v);
                 }
             } else {
-                // a slice of K: publish its sums; the warp that completes the tile adds
-                // all slices in order, whichever came last
-                const size_t stride = size_t(CG) * 128 * TILE;  // floats of a tile's slice
-                float* const part = p.partials + (size_t(t) / p.splits * p.splits) * stride +
-                                    (rank * 8 + e) * size_t(32 * Cfg::kCols) + 4 * lane;
+                // a slice of K: its sums to global memory, where ortho_join_kernel adds
+                // them; lanes next to each other, so a warp's store is 512 bytes
+                float* const part = p.partials + (size_t(t) * CG + rank) * (128 * TILE) + e * (32 * Cfg::kCols) + 4 * lane;
 #pragma unroll 1
                 for (int c = 0; c < Cfg::kCols; c += 32) {
                     uint32_t v[32];
@@ -511,40 +510,11 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                     ptx::tmem_ld_wait();
                     if (c + 32 >= Cfg::kCols)
                         hand_back<CG>(bar_acc_empty + 8 * b, lane);
+                    if (row0 < p.store_cols && col0 + c < p.store_cols) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        ptx::st_global_cg_v4(part + x.slice * stride + c * 32 + i * 128,
-                                             make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
-                }
-                __threadfence();
-                __syncwarp();
-                uint32_t* counter = p.counters + (size_t(t) / p.splits * CG + rank) * 8 + e;
-                uint32_t before = 0;
-                if (lane == 0)
-                    before = ptx::atom_add_acq_rel_gpu(counter, 1u);
-                before = __shfl_sync(0xffffffffu, before, 0);
-                if (before + 1 == uint32_t(p.splits)) {
-                    if (lane == 0)
-                        *counter = 0u;  // ready for the next launch
-                    __threadfence();
-#pragma unroll 1
-                    for (int c = 0; c < Cfg::kCols; c += 64) {
-                        uint32_t v[64];
-#pragma unroll
-                        for (int i = 0; i < 64; ++i)
-                            v[i] = 0u;
-#pragma unroll 1
-                        for (int k = 0; k < p.splits; ++k) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const uint4 w = ptx::ld_global_cg_v4(part + k * stride + c * 32 + i * 128);
-                                v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + __uint_as_float(w.x));
-                                v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + __uint_as_float(w.y));
-                                v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + __uint_as_float(w.z));
-                                v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + __uint_as_float(w.w));
-                            }
-                        }
-                        finish(c, v);
+                        for (int i = 0; i < 8; ++i)
+                            ptx::st_global_cg_v4(part + c * 32 + i * 128,
+                                                 make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
                     }
                 }
             }
@@ -591,6 +561,67 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
     if (warp == 1) {
         ptx::tc_fence_after_sync();
         ptx::tmem_dealloc<CG>(tmem_base, Cfg::kTmemCols);
+    }
+}
+
+// Adds the slices of a symmetric product's tiles: D = alpha times the sums, stored
+// twice where the tile lies below the diagonal.  A warp takes 32 rows x 4 columns of
+// a tile (512 bytes of a slice) and every join_share-th slice; the sums of that many
+// warps meet in shared memory, in order.
+constexpr int kJoinWarps = 8;
+
+template <int CG>
+__global__ void __launch_bounds__(32 * kJoinWarps) ortho_join_kernel(const OrthoParams p)
+{
+    using Cfg = OrthoConfig<CG>;
+    constexpr int TILE = Cfg::kTile, CHUNKS = Cfg::kCols / 32;
+    __shared__ float4 sums[kJoinWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int share = p.join_share, first = warp % share;
+    const int piece = int(blockIdx.x) * (kJoinWarps / share) + warp / share;
+    const int i = piece % 8, c = piece / 8 % CHUNKS * 32, e = piece / (8 * CHUNKS) % 8, rank = piece / (64 * CHUNKS);
+    const int t = int(blockIdx.y) * p.splits;
+    const OrthoTile x = ortho_tile_at<CG>(p, t);
+    const int row0 = x.r * TILE + rank * 128 + 32 * ((e + 2) & 3), row = row0 + lane;
+    const int col = x.c * TILE + (e >> 2) * Cfg::kCols + c + 4 * i;
+    const bool mirror = x.r != x.c;
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    const float* at = p.partials + (size_t(t) * CG + rank) * (128 * TILE) + e * (32 * Cfg::kCols) + c * 32 + i * 128 + 4 * lane;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if ((row0 < p.rows && col < p.store_cols) || (mirror && col < p.rows && row0 < p.store_cols)) {
+#pragma unroll 8
+        for (int k = first; k < p.splits; k += share) {
+            const uint4 v = ptx::ld_global_cg_v4(at + size_t(k) * (CG * 128 * TILE));
+            f.x += __uint_as_float(v.x);
+            f.y += __uint_as_float(v.y);
+            f.z += __uint_as_float(v.z);
+            f.w += __uint_as_float(v.w);
+        }
+    }
+    sums[warp][lane] = f;
+    __syncthreads();
+    if (first != 0)
+        return;
+#pragma unroll 1
+    for (int k = 1; k < share; ++k) {
+        const float4 g = sums[warp + k][lane];
+        f.x += g.x;
+        f.y += g.y;
+        f.z += g.z;
+        f.w += g.w;
+    }
+    const float alpha = p.alpha_dev ? p.alpha * ptx::ld_global_cg_f32(p.alpha_dev + x.matrix) : p.alpha;
+    const uint32_t lo = pack2(__float_as_uint(f.x * alpha), __float_as_uint(f.y * alpha), 1);
+    const uint32_t hi = pack2(__float_as_uint(f.z * alpha), __float_as_uint(f.w * alpha), 1);
+    uint16_t* const out = p.out + x.matrix * p.stride_o;
+    if (row < p.rows && col < p.store_cols)
+        *reinterpret_cast<uint2*>(out + row * p.ldo + col) = make_uint2(lo, hi);
+    if (mirror && row < p.store_cols) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (col + k < p.rows)
+                out[(col + k) * p.ldo + row] = uint16_t((k < 2 ? lo : hi) >> (k & 1 ? 16 : 0));
     }
 }
 

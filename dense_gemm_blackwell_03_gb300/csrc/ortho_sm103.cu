@@ -41,12 +41,25 @@ cudaError_t launch_one(const CUtensorMap& a, const CUtensorMap& b, const CUtenso
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, kernel, a, b, a2, b2, out, out2, p);
+    err = cudaLaunchKernelEx(&cfg, kernel, a, b, a2, b2, out, out2, p);
+    if (err != cudaSuccess || p.splits == 1)
+        return err;
+    cudaLaunchConfig_t join = {};
+    join.gridDim = dim3(unsigned(CG * 8 * Cfg::kCols / 4 / kJoinWarps * p.join_share), unsigned(p.tiles * p.batch), 1);
+    join.blockDim = dim3(32 * kJoinWarps, 1, 1);
+    join.stream = stream;
+    join.attrs = pdl ? attr + n - 1 : nullptr;  // the dependency's
+    join.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&join, ortho_join_kernel<CG>, p);
 }
 
 // ------------------------------------------------------------ the input pass
 // Both kernels are bound by HBM traffic: one read of G for the norm, one read
-// of G and one write of X (from L2 where G fits it).  A warp takes whole rows.
+// of G and one write of X (from L2 where G fits it).  A thread takes 8 elements of
+// X's padded rows at a time, neighbours next to each other whatever the shape, four
+// such pieces in flight.  (A warp per row left most SMs without work on long or
+// narrow matrices: both kernels 95 us on 300 x 28000 and 87 on 24000 x 17, of calls
+// that now take 169 and 89.)
 constexpr int kInThreads = 256;
 
 template <typename T>
@@ -76,40 +89,74 @@ __device__ __forceinline__ float block_sum(float v, float* shared)
     return s;
 }
 
+// Eight elements of a row of G from column c on, zeros past its end.
+template <typename T>
+struct Eight {
+    uint4 w[sizeof(T) / 2];
+
+    __device__ __forceinline__ void load(const OrthoInput& p, const T* g, int row, int c)
+    {
+        const T* at = g + int64_t(row) * p.ldg + c;
+        if (p.vectors && c + 8 <= p.cols) {
+#pragma unroll
+            for (int i = 0; i < int(sizeof(T) / 2); ++i)
+                w[i] = ptx::ld_global_cg_v4(reinterpret_cast<const uint4*>(at) + i);
+        } else {
+            T* t = reinterpret_cast<T*>(w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                t[i] = c + i < p.cols ? at[i] : T(0.f);
+        }
+    }
+
+    __device__ __forceinline__ float operator[](int i) const { return to_f32(reinterpret_cast<const T*>(w)[i]); }
+};
+
+// This thread's pieces of a matrix, in the order of memory, all threads of the
+// grid's row of blocks apart: calls f(piece, row, column) for each.
+template <typename T, typename F>
+__device__ __forceinline__ void each_piece(const OrthoInput& p, const T* g, F&& f)
+{
+    constexpr int kFlight = 4;
+    const int per_row = int(p.ld / 8);
+    const int threads = int(gridDim.x) * kInThreads, at = int(blockIdx.x) * kInThreads + int(threadIdx.x);
+    const int rows = threads / per_row, pieces = threads % per_row;
+    int row = at / per_row, piece = at % per_row;
+    while (row < p.rows) {
+        Eight<T> x[kFlight];
+        int r[kFlight], c[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            r[i] = row;
+            c[i] = 8 * piece;
+            if (row < p.rows)
+                x[i].load(p, g, row, c[i]);
+            row += rows;
+            piece += pieces;
+            if (piece >= per_row) {
+                piece -= per_row;
+                ++row;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i)
+            if (r[i] < p.rows)
+                f(x[i], r[i], c[i]);
+    }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kInThreads) ortho_sums_kernel(const OrthoInput p)
 {
     __shared__ float shared[kInThreads / 32];
-    constexpr int V = 16 / int(sizeof(T));
-    const int lane = threadIdx.x & 31;
-    const int first = int(blockIdx.x) * (kInThreads / 32) + int(threadIdx.x >> 5);
-    const int step = int(gridDim.x) * (kInThreads / 32);
-    const T* g = static_cast<const T*>(p.g) + int64_t(blockIdx.y) * p.stride_g;
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     float sum = 0.f;
-    for (int r = first; r < p.rows; r += step) {
-        const T* row = g + int64_t(r) * p.ldg;
-        int c = 0;
-        if (p.vectors) {
-            const int whole = p.cols / V * V;
-#pragma unroll 4
-            for (c = lane * V; c < whole; c += 32 * V) {
-                const uint4 w = ptx::ld_global_cg_v4(row + c);
-                const T* x = reinterpret_cast<const T*>(&w);
+    each_piece(p, static_cast<const T*>(p.g) + int64_t(blockIdx.y) * p.stride_g, [&](const Eight<T>& x, int, int) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float f = to_f32(x[i]);
-                    sum = fmaf(f, f, sum);
-                }
-            }
-            c = whole;
-        }
-        for (c += lane; c < p.cols; c += 32) {
-            const float f = to_f32(row[c]);
-            sum = fmaf(f, f, sum);
-        }
-    }
+        for (int i = 0; i < 8; ++i)
+            sum = fmaf(x[i], x[i], sum);
+    });
     sum = block_sum(sum, shared);
     if (threadIdx.x == 0)
         p.sums[int64_t(blockIdx.y) * p.parts + blockIdx.x] = sum;
@@ -123,10 +170,6 @@ template <typename T>
 __global__ void __launch_bounds__(kInThreads) ortho_convert_kernel(const OrthoInput p)
 {
     __shared__ float shared[kInThreads / 32];
-    constexpr int V = 8;  // columns per lane and step
-    const int lane = threadIdx.x & 31;
-    const int first = int(blockIdx.x) * (kInThreads / 32) + int(threadIdx.x >> 5);
-    const int step = int(gridDim.x) * (kInThreads / 32);
     const int64_t mat = blockIdx.y;
     const T* g = static_cast<const T*>(p.g) + mat * p.stride_g;
     uint16_t* hi = p.hi + mat * p.stride;
@@ -146,38 +189,21 @@ __global__ void __launch_bounds__(kInThreads) ortho_convert_kernel(const OrthoIn
         p.factors[mat] = f;
         p.factors[p.batch + mat] = f * f;
     }
-    for (int r = first; r < p.rows; r += step) {
-        const T* row = g + int64_t(r) * p.ldg;
-        for (int c = lane * V; c < int(p.ld); c += 32 * V) {
-            float x[V];
-            if (p.vectors && c + V <= p.cols) {
-                uint4 w[sizeof(T) / 2];
+    each_piece(p, g, [&](const Eight<T>& x, int row, int c) {
+        uint32_t h[4], l[4];
 #pragma unroll
-                for (int i = 0; i < int(sizeof(T) / 2); ++i)
-                    w[i] = ptx::ld_global_cg_v4(reinterpret_cast<const uint4*>(row + c) + i);
-                const T* t = reinterpret_cast<const T*>(w);
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    x[i] = to_f32(t[i]) * up;
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    x[i] = c + i < p.cols ? to_f32(row[c + i]) * up : 0.f;
-            }
-            uint32_t h[V / 2], l[V / 2];
-#pragma unroll
-            for (int i = 0; i < V / 2; ++i) {
-                const __half2 a = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-                const float2 b = __half22float2(a);
-                const __half2 d = __floats2half2_rn(x[2 * i] - b.x, x[2 * i + 1] - b.y);
-                h[i] = *reinterpret_cast<const uint32_t*>(&a);
-                l[i] = *reinterpret_cast<const uint32_t*>(&d);
-            }
-            *reinterpret_cast<uint4*>(hi + int64_t(r) * p.ld + c) = make_uint4(h[0], h[1], h[2], h[3]);
-            if (lo)
-                *reinterpret_cast<uint4*>(lo + int64_t(r) * p.ld + c) = make_uint4(l[0], l[1], l[2], l[3]);
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = make_float2(x[2 * i] * up, x[2 * i + 1] * up);
+            const __half2 a = __floats2half2_rn(v.x, v.y);
+            const float2 b = __half22float2(a);
+            const __half2 d = __floats2half2_rn(v.x - b.x, v.y - b.y);
+            h[i] = *reinterpret_cast<const uint32_t*>(&a);
+            l[i] = *reinterpret_cast<const uint32_t*>(&d);
         }
-    }
+        *reinterpret_cast<uint4*>(hi + int64_t(row) * p.ld + c) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (lo)
+            *reinterpret_cast<uint4*>(lo + int64_t(row) * p.ld + c) = make_uint4(l[0], l[1], l[2], l[3]);
+    });
 }
 
 template <typename T>

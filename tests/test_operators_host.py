@@ -63,12 +63,13 @@ def test_orthogonalize_workspace_sizes(lib):
     assert workspace(lib, -1, 8, 8)[0] == INVALID
     assert workspace(lib, 1 << 16, 8, 8)[0] == UNSUP
     assert workspace(lib, 1, 1 << 25, 8)[0] == UNSUP
-    # four fp16 matrices of G's size (columns padded to 64), two of the short side's
+    # four fp16 matrices of G's size (columns padded to 64), three of the short side's (S, B
+    # and B's low part)
     for batch, rows, cols in ((1, 300, 1000), (3, 1000, 300), (2, 512, 512), (1, 1, 1)):
         pad = lambda v: -(-v // 64) * 64  # noqa: E731
         rc, n = workspace(lib, batch, rows, cols)
         m = min(rows, cols)
-        need = batch * 2 * (4 * rows * pad(cols) + 2 * m * pad(m))
+        need = batch * 2 * (4 * rows * pad(cols) + 3 * m * pad(m))
         assert rc == 0 and need <= n <= need + (1 << 20)
     # the two orientations hold the same matrices
     assert abs(workspace(lib, 1, 1024, 4096)[1] - workspace(lib, 1, 4096, 1024)[1]) < (1 << 20)
