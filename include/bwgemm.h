@@ -519,12 +519,14 @@ bwgemm_status_t bwgemm_run_scaled(bwgemm_plan_t plan, const bwgemm_scaled_t* A, 
  *       bwgemm_orthogonalize_workspace() bytes (else BWGEMM_ERR_WORKSPACE),
  *       holding nothing of use before or after
  *
- * Products take fp16 operands -- X in two terms where one would cost accuracy
- * -- and sum in fp32; the norm is summed in fp32.  The relative error before
- * the result's rounding is about 1e-3 for the default steps.  A matrix of
+ * Products take fp16 operands -- X and the polynomial's diagonal in two terms
+ * where one would cost accuracy -- and sum in fp32; the norm is summed in fp32.
+ * The relative error before the result's rounding is about 1e-3 for the default
+ * steps (1.7e-3 where all singular values are close).  A matrix of
  * zeros gives zeros; one holding a NaN or an infinity gives NaNs.
- * Asynchronous: 2 + 3 steps launches, no allocation, capturable; errors as for
- * bwgemm_run.
+ * Asynchronous: 2 + 3 steps launches, one more per step where S is cut into
+ * slices of K (in the plan's workspace); no allocation, capturable; errors as
+ * for bwgemm_run.
  */
 bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_dtype_t dtype, void* X,
                                      bwgemm_dtype_t out, int64_t batch, int64_t rows, int64_t cols, int64_t ldg,
