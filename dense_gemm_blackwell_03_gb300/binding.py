@@ -466,12 +466,6 @@ class Plan:
         if t.get_device() != self.device:
             raise ValueError(f"{name} is on {t.device}, the plan on cuda:{self.device}")
 
-    def _stream(self, stream) -> int:
-        """The raw handle of `stream`, or of the device's current stream."""
-        if stream is None:
-            return _torch_mod._C._cuda_getCurrentRawStream(self.device)
-        return stream.cuda_stream
-
     def quantize(self, X, blocks: str = "row", transposed: bool = False, pow2: bool = False, dtype=None,
                  stream=None):
         """``bwgemm_quantize``: the 2-D CUDA tensor X (bf16, fp16 or fp32) in 8 bits
@@ -484,6 +478,9 @@ class Plan:
         `pow2` rounds the scales up to powers of two.  q's rows are padded to 16
         bytes; scales are (column blocks) x rows, or x row blocks."""
         torch = _torch()
+        if stream is not None:  # results come from that stream's memory, free there and then
+            with torch.cuda.stream(stream):
+                return self.quantize(X, blocks, transposed, pow2, dtype)
         dt = _all_dtype_codes.get(X.dtype)
         if dt is None:
             raise TypeError(f"quantize takes bfloat16, float16 or float32 tensors, got {X.dtype}")
@@ -520,8 +517,7 @@ class Plan:
         rc = self.lib.bwgemm_quantize(self.handle, X.data_ptr(), dt, rows, cols, ldx,
                                       BLOCK_SQUARE if square else BLOCK_ROW, f8, int(pow2), q.data_ptr(),
                                       (cols + 15) & -16, s.data_ptr(), per, *args_t,
-                                      _torch_mod._C._cuda_getCurrentRawStream(self.device) if stream is None
-                                      else stream.cuda_stream)
+                                      torch._C._cuda_getCurrentRawStream(self.device))
         if rc != 0:
             raise BwgemmError(rc, "bwgemm_quantize")
         return result
@@ -531,6 +527,9 @@ class Plan:
         B (N x K) with their block scales, as `quantize` returns them.  `out_dtype`:
         bf16 (default), fp16 or fp32; `accumulate` adds to an fp32 `out`."""
         torch = _torch()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.gemm_scaled(A, scale_a, B, scale_b, out, out_dtype, accumulate)
         dev = self.device
         if (A.get_device() != dev or B.get_device() != dev or scale_a.get_device() != dev
                 or scale_b.get_device() != dev):
@@ -558,7 +557,7 @@ class Plan:
             raise TypeError(f"gemm_scaled writes bfloat16, float16 or float32, got {out_dtype}")
         rc = self.lib.bwgemm_run_scaled(self.handle, self._a_at, self._b_at, out.data_ptr(), M, N, K, ldc, dt,
                                         1 if accumulate else 0,
-                                        torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+                                        torch._C._cuda_getCurrentRawStream(dev))
         if rc != 0:
             raise BwgemmError(rc, "bwgemm_run_scaled")
         return out
@@ -570,6 +569,9 @@ class Plan:
         (a, b, c) for every step, or one per step.  Returns `scale` times the
         result in bf16, or in `out` (bf16 or fp16, G's shape)."""
         torch = _torch()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.orthogonalize(G, out, steps, coefficients, eps, scale)
         dt = _all_dtype_codes.get(G.dtype)
         if dt is None:
             raise TypeError(f"orthogonalize takes bfloat16, float16 or float32 tensors, got {G.dtype}")
@@ -600,13 +602,11 @@ class Plan:
         if rc != 0:
             raise BwgemmError(rc, "bwgemm_orthogonalize_workspace")
         ws = torch.empty(need.value, dtype=torch.uint8, device=G.device)
-        h = self._stream(stream)
-        if stream is not None:
-            ws.record_stream(stream)
         rc = self.lib.bwgemm_orthogonalize(self.handle, G.data_ptr(), dt, out.data_ptr(), dto, batch, rows, cols,
                                            lds[0], strides[0], lds[1], strides[1], int(steps),
                                            (ctypes.c_float * len(flat))(*flat), float(eps), float(scale),
-                                           ws.data_ptr(), need.value, h)
+                                           ws.data_ptr(), need.value,
+                                           torch._C._cuda_getCurrentRawStream(self.device))
         if rc != 0:
             raise BwgemmError(rc, "bwgemm_orthogonalize")
         return out

@@ -674,6 +674,27 @@ def test_orthogonalize_timeout_is_reported():
         assert rel(p.orthogonalize(g), orthogonalize_ref(host(g))) <= 4.1e-3
 
 
+@pytest.mark.parametrize("op", ["quantize", "gemm_scaled", "orthogonalize"])
+def test_other_streams_results_are_not_this_streams_memory(plan, op):
+    # memory freed here may still be read by work pending here, which the other
+    # stream does not wait for
+    x = torch.randn(512, 1024, device="cuda").to(torch.bfloat16)
+    q, s = plan.quantize(x)
+    call = {"quantize": lambda st: plan.quantize(x, stream=st)[0], "orthogonalize": lambda st: plan.orthogonalize(x, stream=st),
+            "gemm_scaled": lambda st: plan.gemm_scaled(q, s, q, s, stream=st)}[op]
+    torch.cuda.synchronize()
+    want = call(None)
+    freed = want.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    at = freed.data_ptr()
+    del freed
+    got = call(side)
+    side.synchronize()
+    assert got.data_ptr() != at
+    assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+
+
 # ----------------------------------------------------------------- together
 def dequantized(q, s):
     rows, cols = q.shape
