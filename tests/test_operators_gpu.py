@@ -653,6 +653,22 @@ def test_orthogonalize_refusals(plan):
     torch.cuda.synchronize()
 
 
+# deep K in slices, tiles of 128 and of 256, above and below the diagonal
+@pytest.mark.parametrize("rows,cols", [(1024, 9000), (9000, 700), (520, 6001), (129, 30000)])
+def test_orthogonalize_slices(plan, rows, cols):
+    g = torch.from_numpy(gradient(rows, cols, rows)).to(torch.bfloat16).cuda()
+    x = plan.orthogonalize(g)
+    assert torch.equal(plan.orthogonalize(g), x)
+    assert rel(x, orthogonalize_ref(host(g))) <= 4.1e-3
+
+
+def test_orthogonalize_small_workspace():
+    # no room for slices: whole tiles
+    g = torch.from_numpy(gradient(200, 9000, 1)).to(torch.bfloat16).cuda()
+    with binding.Plan(0, workspace_bytes=(1 << 20) + 4096) as p:
+        assert rel(p.orthogonalize(g), orthogonalize_ref(host(g))) <= 4.1e-3
+
+
 # Singular values close together: B is close to a multiple of I, whose rounding
 # would show in the whole result.  Tolerance: 1.45 times the rounding of the result
 # to bf16 (1.7e-3) in a simulation of every other rounding, and a quarter more.
