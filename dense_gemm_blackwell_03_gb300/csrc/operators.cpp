@@ -117,10 +117,10 @@ double block_us(const ScaledVariant& v, int l_rows)
 // fitted in microseconds to M = 1, 8, 9 and 16 on 18 shapes.  Few rows: the bytes,
 // the K blocks that a warp takes one after another, and the CTAs; tiles: the K
 // blocks of a tile, split over CTAs where they are many, or the bytes.  Measured,
-// few rows against tiles: 1 x 1024 x 1024 1.7 and 6.9, 1 x 4096 x 4096 4.8 and 11.2,
-// 8 x 8192 x 8192 18.0 and 18.1, 1 x 16384 x 8192 30.6 and 24.0, 1 x 128 x 28672
-// 13.9 and 28.8, 1 x 28672 x 1024 10.2 and 7.9; 16 x 4096 x 8192 15.7 and 20.1,
-// 16 x 8192 x 4096 13.0 and 11.7.
+// few rows against tiles: 1 x 1024 x 1024 1.7 and 6.9, 1 x 4096 x 4096 4.9 and 11.2,
+// 8 x 8192 x 8192 18.6 and 18.1, 1 x 16384 x 8192 30.0 and 24.0, 1 x 128 x 28672
+// 9.0 and 28.8, 1 x 28672 x 1024 10.3 and 7.9; 16 x 4096 x 8192 15.7 and 20.1,
+// 16 x 8192 x 4096 12.8 and 11.7.
 bool takes_few_rows(int64_t M, int64_t N, int64_t K)
 {
     if (M > kScaledFewRows)

@@ -2,9 +2,9 @@
 // of A (one generated token, a few beams): C = A B^T as in scaled_kernel.cuh.
 //
 // The weights' bytes are the time: N x K read once.  A tile of a few rows does
-// not repay tcgen05's path (copies into shared memory, barriers, an accumulator
-// handed over per K block) until there are many of them, so here the weights go
-// from memory straight into the registers of mma.sync: 8 weight rows are the
+// not repay tcgen05's path (copies by TMA, barriers, an accumulator handed over per K
+// block) until there are many of them, so here every lane copies the pieces that it
+// needs itself and gives them to mma.sync from registers: 8 weight rows are the
 // columns of m16n8k32, the rows of A its 16 rows.  The contraction does not care
 // which K a position stands for as long as both operands agree, so every lane
 // loads whole 16-byte pieces: lane (g, q) takes bytes 16 q and 64 + 16 q of weight
@@ -12,16 +12,17 @@
 // consume a block.  The block's fresh accumulator is weighted with both scales and
 // added to the running sums.
 //
-// Measured at one row: 1024 x 1024 1.7 us (tiles: 6.9), 4096 x 4096 4.8 (11.2),
-// 8192 x 8192 17.3 (18.8), 3.9 TB/s: the loads in flight bound it, and what a
-// block waits for besides them, its scales and A's piece out of L1 or L2.  Larger
-// products are left to the tiles' copies, which keep more bytes in flight.
+// Measured at one row: 1024 x 1024 1.7 us (tiles: 6.9), 4096 x 4096 4.9 (11.2),
+// 8192 x 8192 16.7 (18.8), 4 TB/s; 128 x 28672 9.0 (28.8).  Neither deeper rings nor
+// more or fewer CTAs per SM help, and a persistent form that copies ahead into the
+// next rows is slower (19.1) by the instructions it adds: a warp's own way through a
+// block bounds it.  Larger products are left to the tiles.
 //
 // A CTA takes 8 weight rows -- many small CTAs, so that the last ones do not run
-// alone (16 rows: 18.4 us) -- and its eight warps take the K blocks in turn, kAhead
-// blocks in flight each, and add their sums through shared memory in warp order.
-// Two blocks ahead and four CTAs per SM were the best of 2, 4, 6 and 3 to 5: deeper
-// needs the registers of a CTA (four ahead at the same bound spill: 20.2 us).
+// alone (16 rows: 18.4 us) -- and its eight warps take the K blocks in turn, kRing
+// blocks in flight each (asynchronous copies, which need no registers: with two
+// blocks in registers 17.3 us, and 14.8 on 128 x 28672), the scales one block ahead,
+// and add their sums through shared memory in warp order.
 #include "operators.h"
 #include "ptx.cuh"
 
@@ -34,7 +35,8 @@ namespace {
 constexpr int kFewWarps = 8;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kFewRows = 8;  // weight rows per CTA
-constexpr int kAhead = 2;    // blocks of weights in flight per warp
+constexpr int kRing = 4;     // blocks of weights in flight per warp
+constexpr int kFewSmem = kFewWarps * kRing * 1024;
 
 // 16 bytes of a row at byte k, zeros from byte `len` on, where nothing is read
 // (a row may end inside them).
@@ -76,6 +78,7 @@ __device__ __forceinline__ void mma_fp8(float (&d)[4], uint32_t a0, uint32_t a1,
 template <int NT, int F8W, int F8X>
 __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 3) scaled_few_kernel(const FewParams p)
 {
+    extern __shared__ __align__(16) uint8_t few_smem[];
     __shared__ float part[kFewWarps][8 * NT][kFewRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, q = lane & 3;
@@ -95,11 +98,22 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 3) scaled_few_kerne
     for (int t = 0; t < NT; ++t)
         sum[t][0] = sum[t][1] = 0.f;
 
-    // the block's sums, weighted, onto the running ones; x(t, h) is A's part
-    auto add = [&](const uint4& lo, const uint4& hi, int kb, auto&& x) {
+    struct Scales {
+        float w0, w1, x[NT];
+    };
+    auto scales_of = [&](int kb) {
+        Scales f;
         const float* ws = p.ws + int64_t(kb) * p.ws_ld;
         const float* xs = p.xs + int64_t(kb) * p.xs_ld;
-        const float w0 = ptx::ld_global_ca_f32(ws + ws_of[0]), w1 = ptx::ld_global_ca_f32(ws + ws_of[1]);
+        f.w0 = ptx::ld_global_ca_f32(ws + ws_of[0]);
+        f.w1 = ptx::ld_global_ca_f32(ws + ws_of[1]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            f.x[t] = ptx::ld_global_ca_f32(xs + (m_of[t] >> p.xs_shift));
+        return f;
+    };
+    // the block's sums, weighted, onto the running ones; x(t, h) is A's part
+    auto add = [&](const uint4& lo, const uint4& hi, const Scales& f, auto&& x) {
         float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -113,43 +127,46 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 3) scaled_few_kerne
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const float s = ptx::ld_global_ca_f32(xs + (m_of[t] >> p.xs_shift));
-            sum[t][0] = fmaf(d[2 * t], s * w0, sum[t][0]);
-            sum[t][1] = fmaf(d[2 * t + 1], s * w1, sum[t][1]);
+            sum[t][0] = fmaf(d[2 * t], f.x[t] * f.w0, sum[t][0]);
+            sum[t][1] = fmaf(d[2 * t + 1], f.x[t] * f.w1, sum[t][1]);
         }
     };
 
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
     const int whole = p.K / kBlock;
-    uint4 w[kAhead][2];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-        const int kb = warp + i * kFewWarps;
+    // every lane copies and reads its own pieces only: nobody waits for anybody
+    const uint32_t ring = ptx::smem_addr(few_smem) + uint32_t(warp * kRing * 1024 + 16 * lane);
+    auto fetch = [&](int kb, int slot) {
         if (kb < whole) {
-            w[i][0] = ptx::ld_global_stream_v4(w_at + int64_t(kb) * kBlock);
-            w[i][1] = ptx::ld_global_stream_v4(w_at + int64_t(kb) * kBlock + 64);
+            ptx::cp_async_16(ring + uint32_t(slot * 1024), w_at + int64_t(kb) * kBlock);
+            ptx::cp_async_16(ring + uint32_t(slot * 1024 + 512), w_at + int64_t(kb) * kBlock + 64);
         }
-    }
-#pragma unroll 1
-    for (int kb0 = warp; kb0 < whole; kb0 += kAhead * kFewWarps) {
+        ptx::cp_async_commit();
+    };
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int kb = kb0 + i * kFewWarps;
-            if (kb < whole) {
-                add(w[i][0], w[i][1], kb,
-                    [&](int t, int h) { return ptx::ld_global_ca_v4(x_at[t] + int64_t(kb) * kBlock + 64 * h); });
-                const int next = kb + kAhead * kFewWarps;
-                if (next < whole) {
-                    w[i][0] = ptx::ld_global_stream_v4(w_at + int64_t(next) * kBlock);
-                    w[i][1] = ptx::ld_global_stream_v4(w_at + int64_t(next) * kBlock + 64);
-                }
-            }
-        }
+    for (int i = 0; i < kRing; ++i)
+        fetch(warp + i * kFewWarps, i);
+    int slot = 0;
+    Scales next = {};
+    if (warp < whole)
+        next = scales_of(warp);
+#pragma unroll 1
+    for (int kb = warp; kb < whole; kb += kFewWarps) {
+        const Scales f = next;
+        if (kb + kFewWarps < whole)
+            next = scales_of(kb + kFewWarps);
+        ptx::cp_async_wait_group<kRing - 1>();
+        uint4 lo, hi;
+        ptx::ld_shared_v4(ring + uint32_t(slot * 1024), lo.x, lo.y, lo.z, lo.w);
+        ptx::ld_shared_v4(ring + uint32_t(slot * 1024 + 512), hi.x, hi.y, hi.z, hi.w);
+        add(lo, hi, f, [&](int t, int h) { return ptx::ld_global_ca_v4(x_at[t] + int64_t(kb) * kBlock + 64 * h); });
+        fetch(kb + kRing * kFewWarps, slot);
+        slot = slot + 1 == kRing ? 0 : slot + 1;
     }
     if (whole < p.num_kb && warp == whole % kFewWarps) {  // the last block, cut off by the end of the rows
         const int k = whole * kBlock + 16 * q;
-        add(load_ragged(w_at - 16 * q, k, p.K), load_ragged(w_at - 16 * q, k + 64, p.K), whole,
+        add(load_ragged(w_at - 16 * q, k, p.K), load_ragged(w_at - 16 * q, k + 64, p.K), scales_of(whole),
             [&](int t, int h) { return load_ragged(x_at[t] - 16 * q, k + 64 * h, p.K); });
     }
 
@@ -181,6 +198,7 @@ template <int NT, int F8W, int F8X>
 cudaError_t launch_few(const FewParams& p, cudaStream_t stream, bool pdl)
 {
     cudaLaunchConfig_t cfg = {};
+    cfg.dynamicSmemBytes = kFewSmem;
     cfg.gridDim = dim3(unsigned((p.N + kFewRows - 1) / kFewRows), 1, 1);
     cfg.blockDim = dim3(kFewThreads, 1, 1);
     cfg.stream = stream;
