@@ -589,7 +589,8 @@ class Plan:
         rows, cols = G.shape[-2:]
         if cols > 1 and (G.stride(-1) != 1 or out.stride(-1) != 1):
             raise ValueError("G and out need unit stride along the last dim")
-        lds = [max(int(t.stride(-2)), cols) if rows > 1 else max(int(cols), 1) for t in (G, out)]
+        # the true strides: rows closer than their length (expanded, overlapping) are refused
+        lds = [int(t.stride(-2)) if rows > 1 else max(int(cols), 1) for t in (G, out)]
         strides = [int(t.stride(0)) if t.dim() == 3 else 0 for t in (G, out)]
         flat = [float(v) for v in coefficients] if not hasattr(coefficients[0], "__len__") else \
             [float(v) for triple in coefficients for v in triple]

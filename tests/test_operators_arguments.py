@@ -1,0 +1,63 @@
+"""What the Python calls of the operators hand to the library (no GPU): a plan
+over a library that only records, host tensors in place of CUDA ones."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+from dense_gemm_blackwell_03_gb300 import binding
+
+
+class Recorder:
+    """The library's operator calls: their arguments are kept, nothing runs."""
+
+    def __init__(self, real):
+        self.calls = []
+        self.bwgemm_orthogonalize_workspace = real.bwgemm_orthogonalize_workspace
+
+    def bwgemm_orthogonalize(self, *args):
+        names = ("plan", "G", "dtype", "X", "out", "batch", "rows", "cols", "ldg", "stride_g", "ldx", "stride_x", "steps",
+                 "coefficients", "eps", "scale", "workspace", "workspace_bytes", "stream")
+        self.calls.append(dict(zip(names, args, strict=True)))
+        return 0
+
+
+@pytest.fixture
+def plan(monkeypatch):
+    real = binding.load_library(build_if_missing=True)
+    binding._torch()
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
+    p = binding.Plan.__new__(binding.Plan)
+    p.lib, p.handle, p.device = Recorder(real), ctypes.c_void_p(), -1  # -1: get_device() of a host tensor
+    yield p
+    p.handle = None
+
+
+# ------------------------------------------------------------ orthogonalise
+def test_orthogonalize_passes_the_strides_there_are(plan):
+    dense = torch.zeros(3, 8, 40, dtype=torch.bfloat16)
+    out = torch.zeros(3, 10, 64, dtype=torch.bfloat16)[:, 1:9, :40]
+    plan.orthogonalize(dense, out=out)
+    plan.orthogonalize(dense[0, :1], out=out[0, :1])  # a single row has no next one
+    plan.orthogonalize(dense[0, :, :1], out=out[0, :, :1])
+    stack, row, column = plan.lib.calls
+    assert [stack[k] for k in ("ldg", "stride_g", "ldx", "stride_x")] == [40, 320, 64, 640]
+    assert row["ldg"] == row["ldx"] == 40
+    assert (column["ldg"], column["ldx"]) == (40, 64)
+
+
+@pytest.mark.parametrize("make", [lambda: torch.zeros(1, 40, dtype=torch.bfloat16).expand(8, 40),
+                                  lambda: torch.zeros(200, dtype=torch.bfloat16).as_strided((8, 40), (16, 1)),
+                                  lambda: torch.zeros(8, 1, dtype=torch.bfloat16)[:1].expand(8, 1),
+                                  lambda: torch.zeros(3, 1, 40, dtype=torch.bfloat16).expand(3, 8, 40)])
+def test_orthogonalize_rows_closer_than_their_length_reach_the_library_as_they_are(plan, make):
+    # which refuses them: it reads (writes) ldg (ldx) elements a row
+    t = make()
+    dense = torch.zeros(t.shape, dtype=torch.bfloat16)
+    plan.orthogonalize(t, out=dense)
+    plan.orthogonalize(dense, out=t)
+    as_g, as_x = plan.lib.calls
+    assert as_g["ldg"] == t.stride(-2) < t.shape[-1] and as_g["ldx"] == dense.stride(-2)
+    assert as_x["ldx"] == t.stride(-2) < t.shape[-1] and as_x["ldg"] == dense.stride(-2)

@@ -1,0 +1,37 @@
+"""GPU tests of the operators at the edges of their arguments: layouts that are
+refused, and forms that only some sizes take.  Plain forms in 64 bits."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from dense_gemm_blackwell_03_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+INVALID = 1
+
+
+@pytest.fixture(scope="module")
+def plan():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    binding.load_library(build_if_missing=True)
+    p = binding.Plan(0)
+    yield p
+    assert p.status() == 0
+    p.close()
+
+
+# ------------------------------------------------------------ orthogonalise
+@pytest.mark.parametrize("shape", [(64, 128), (3, 64, 128)])
+def test_orthogonalize_refuses_rows_closer_than_their_length(plan, shape):
+    dense = torch.ones(shape, dtype=torch.bfloat16, device="cuda")
+    room = torch.ones(3 * 64 * 128, dtype=torch.bfloat16, device="cuda")
+    expanded = torch.ones(shape[:-2] + (1, 128), dtype=torch.bfloat16, device="cuda").expand(shape)
+    overlapping = room.as_strided(shape, (64 * 128, 120, 1)[-len(shape):])
+    for bad in (expanded, overlapping):
+        for kw in (dict(G=bad), dict(G=dense, out=bad)):
+            with pytest.raises(binding.BwgemmError) as e:
+                plan.orthogonalize(**kw)
+            assert e.value.status == INVALID
+    assert (room == 1).all() and (expanded == 1).all()
