@@ -551,7 +551,9 @@ class Plan:
             if tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
                 raise ValueError("out must be an M x N CUDA tensor of out_dtype")
             out_dtype = out.dtype
-            ldc = _ld(out) if M > 1 else (N + 7) & -8  # a single row has no next one
+            ldc = _ld(out)
+            if M <= 1:
+                ldc = (N + 7) & -8  # a single row has no next one
         dt = _all_dtype_codes.get(out_dtype)
         if dt is None:
             raise TypeError(f"gemm_scaled writes bfloat16, float16 or float32, got {out_dtype}")

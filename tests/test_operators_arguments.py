@@ -23,6 +23,11 @@ class Recorder:
         self.calls.append(dict(zip(names, args, strict=True)))
         return 0
 
+    def bwgemm_run_scaled(self, *args):
+        names = ("plan", "A", "B", "C", "M", "N", "K", "ldc", "out", "accumulate", "stream")
+        self.calls.append(dict(zip(names, args, strict=True)))
+        return 0
+
 
 @pytest.fixture
 def plan(monkeypatch):
@@ -31,6 +36,8 @@ def plan(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
     p = binding.Plan.__new__(binding.Plan)
     p.lib, p.handle, p.device = Recorder(real), ctypes.c_void_p(), -1  # -1: get_device() of a host tensor
+    p._a, p._b = binding.Scaled(), binding.Scaled()
+    p._a_at, p._b_at = ctypes.addressof(p._a), ctypes.addressof(p._b)
     yield p
     p.handle = None
 
@@ -61,3 +68,30 @@ def test_orthogonalize_rows_closer_than_their_length_reach_the_library_as_they_a
     as_g, as_x = plan.lib.calls
     assert as_g["ldg"] == t.stride(-2) < t.shape[-1] and as_g["ldx"] == dense.stride(-2)
     assert as_x["ldx"] == t.stride(-2) < t.shape[-1] and as_x["ldg"] == dense.stride(-2)
+
+
+# ------------------------------------------------------------ scaled product
+def scaled(rows, K):
+    return (torch.zeros(rows, K, dtype=torch.uint8).view(torch.float8_e4m3fn),
+            torch.ones(-(-K // 128), rows))
+
+
+@pytest.mark.parametrize("make", [lambda: torch.zeros(64, 2)[:, :1].t(),             # a column seen as a row
+                                  lambda: torch.zeros(1, 128)[:, ::2],
+                                  lambda: torch.zeros(1, 1).expand(1, 64),
+                                  lambda: torch.zeros(1, 64, 2)[:, :, 0]])
+@pytest.mark.parametrize("K", [256, 0])
+def test_scaled_product_refuses_a_strided_row_as_result(plan, make, K):
+    out = make()
+    assert out.shape == (1, 64) and out.stride(1) != 1
+    with pytest.raises(ValueError, match="unit stride"):
+        plan.gemm_scaled(*scaled(1, K), *scaled(64, K), out=out)
+    assert plan.lib.calls == []
+
+
+def test_scaled_product_row_and_column_results(plan):
+    plan.gemm_scaled(*scaled(1, 256), *scaled(61, 256), out=torch.zeros(1, 61))
+    plan.gemm_scaled(*scaled(1, 256), *scaled(61, 256), out=torch.zeros(5, 80)[2:3, 16:77])
+    plan.gemm_scaled(*scaled(5, 256), *scaled(1, 256), out=torch.zeros(5, 80)[:, 16:17])
+    plan.gemm_scaled(*scaled(1, 256), *scaled(1, 256), out=torch.zeros(5, 80)[:1, 16:17])
+    assert [(c["M"], c["N"], c["ldc"]) for c in plan.lib.calls] == [(1, 61, 64), (1, 61, 64), (5, 1, 80), (1, 1, 8)]

@@ -35,3 +35,20 @@ def test_orthogonalize_refuses_rows_closer_than_their_length(plan, shape):
                 plan.orthogonalize(**kw)
             assert e.value.status == INVALID
     assert (room == 1).all() and (expanded == 1).all()
+
+
+# ------------------------------------------------------------ scaled product
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("K", [256, 0])
+def test_scaled_product_refuses_a_strided_row_as_result(plan, dtype, K):
+    a, sa = plan.quantize(torch.ones(1, 256, device="cuda"))
+    b, sb = plan.quantize(torch.ones(32, 256, device="cuda"))
+    operands = (a[:, :K], sa[:K // 128], b[:, :K], sb[:K // 128])
+    held = torch.full((32, 8), 5.0, dtype=dtype, device="cuda")
+    wide = torch.full((1, 64), 5.0, dtype=dtype, device="cuda")
+    for out in (held[:, :1].t(), wide[:, ::2]):
+        with pytest.raises(ValueError, match="unit stride"):
+            plan.gemm_scaled(*operands, out=out)
+    assert (held == 5).all() and (wide == 5).all()
+    plan.gemm_scaled(*operands, out=wide[:, 32:])  # in place: 32 elements and nothing else
+    assert (wide[:, :32] == 5).all() and torch.equal(wide[:, 32:], plan.gemm_scaled(*operands, out_dtype=dtype))
