@@ -44,10 +44,12 @@ class _ScaledLinear(torch.autograd.Function):
 
 
 def _aligned_rows(t):
+    """t, or a copy of it, in rows as `quantize` reads them: apart from each other (the
+    gradient of a sum over rows is one row expanded) and on 16-byte boundaries."""
     per = 16 // t.element_size()
-    if t.stride(1) == 1 and t.stride(0) % per == 0 and t.data_ptr() % 16 == 0:
-        return t
     rows, cols = t.shape
+    if t.stride(1) == 1 and t.stride(0) >= cols and t.stride(0) % per == 0 and t.data_ptr() % 16 == 0:
+        return t
     wide = torch.empty((rows, -(-cols // per) * per), dtype=t.dtype, device=t.device)
     wide[:, :cols] = t
     return wide[:, :cols]

@@ -52,3 +52,21 @@ def test_scaled_product_refuses_a_strided_row_as_result(plan, dtype, K):
     assert (held == 5).all() and (wide == 5).all()
     plan.gemm_scaled(*operands, out=wide[:, 32:])  # in place: 32 elements and nothing else
     assert (wide[:, :32] == 5).all() and torch.equal(wide[:, 32:], plan.gemm_scaled(*operands, out_dtype=dtype))
+
+
+# ----------------------------------------------------------- a linear layer
+@pytest.mark.parametrize("outer", [136, 61])
+@pytest.mark.parametrize("loss", [lambda y, v: (y.sum(0) * v).sum(), lambda y, v: y.sum(), lambda y, v: (y.t() @ y).sum()])
+def test_linear_gradients_of_expanded_and_transposed_gradients(plan, outer, loss):
+    # the same bits as for the same gradient laid out densely
+    from dense_gemm_blackwell_03_gb300.linear_training import scaled_linear
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x, w, v = (torch.randn(*s, generator=gen, device="cuda") for s in ((96, 200), (outer, 200), (outer,)))
+    x.requires_grad_()
+    w.requires_grad_()
+    y = scaled_linear(x, w)
+    at = y.detach().requires_grad_()
+    dy, = torch.autograd.grad(loss(at, v), at)
+    want = torch.autograd.grad(y, (x, w), dy.clone(memory_format=torch.contiguous_format), retain_graph=True)
+    got = torch.autograd.grad(loss(y, v), (x, w))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
