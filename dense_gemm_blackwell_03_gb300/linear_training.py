@@ -31,6 +31,7 @@ class _ScaledLinear(torch.autograd.Function):
         return binding.gemm_scaled(xq, xs, wq, ws, out_dtype=x.dtype)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable  # computed outside the graph: a second derivative raises
     def backward(ctx, dy):
         xtq, xts, wtq, wts = ctx.saved_tensors
         # quantize reads rows on 16-byte boundaries; autograd may hand in any layout
@@ -57,7 +58,7 @@ def _aligned_rows(t):
 
 def scaled_linear(x, weight):
     """``x @ weight.T`` of CUDA matrices x (tokens x K) and weight (N x K), computed in 8 bits;
-    differentiable in both."""
+    differentiable in both, once."""
     return _ScaledLinear.apply(_aligned_rows(x), _aligned_rows(weight))
 
 

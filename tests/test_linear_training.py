@@ -70,3 +70,13 @@ def test_rows_are_copied_unless_the_quantiser_reads_them(make):
     assert got.data_ptr() % 16 == 0
     dense = torch.ones(4, 8)
     assert linear_training._aligned_rows(dense) is dense
+
+
+def test_a_second_derivative_raises(plain):
+    # the backward pass is computed in 8 bits outside the graph: a gradient penalty
+    # through it would silently lose its terms
+    x, w = leaves(12, 16, 24)
+    y = linear_training.scaled_linear(x, w)
+    gx, = torch.autograd.grad((y ** 3).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="twice"):
+        gx.square().sum().backward()
