@@ -222,7 +222,7 @@ def load_library(build_if_missing: bool = False):
         lib.bwgemm_quantize.argtypes = [vp, vp, ci, i64, i64, i64, ci, ci, i32, vp, i64, vp, i64, vp, i64, vp,
                                         i64, vp]
         lib.bwgemm_quantize.restype = st
-        # the two bwgemm_scaled_t as plain addresses: the fastest argument to pass
+        # the two bwgemm_scaled_t as addresses or packed bytes: the fastest arguments to pass
         lib.bwgemm_run_scaled.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, ci, i32, vp]
         lib.bwgemm_run_scaled.restype = st
         lib.bwgemm_orthogonalize.argtypes = [vp, vp, ci, vp, ci, i64, i64, i64, i64, i64, i64, i64, i32,
@@ -295,10 +295,11 @@ _SCALED = struct.Struct("@PqPqii")
 assert _SCALED.size == ctypes.sizeof(Scaled)
 
 
-def _pack_scaled(into: Scaled, values, scales, name: str):
-    """Describe 8-bit `values` (R x K) with `scales` ((K blocks) x (R or row blocks))
-    in `into`; returns (R, K).  (Strides are read here, not through _ld: this is
-    the per-call path.)"""
+def _pack_scaled(values, scales, name: str):
+    """8-bit `values` (R x K) with `scales` ((K blocks) x (R or row blocks)) as the bytes
+    of a bwgemm_scaled_t, R and K.  (A record of its own for every call: other threads
+    run while the library reads it.  Strides are read here, not through _ld: this is the
+    per-call path.)"""
     code = _fp8_codes.get(values.dtype)
     if code is None:
         raise TypeError(f"{name} must be float8_e4m3fn or float8_e5m2, got {values.dtype}")
@@ -316,9 +317,9 @@ def _pack_scaled(into: Scaled, values, scales, name: str):
         raise ValueError(f"{name} and its scales need unit stride along the last dim")
     if rows <= 1:
         ld = (K + 15) & -16  # a single row has no next one
-    _SCALED.pack_into(into, 0, values.data_ptr(), ld, scales.data_ptr(), lds if blocks > 1 else per, code,
-                      BLOCK_SQUARE if square else BLOCK_ROW)
-    return rows, K
+    record = _SCALED.pack(values.data_ptr(), ld, scales.data_ptr(), lds if blocks > 1 else per, code,
+                          BLOCK_SQUARE if square else BLOCK_ROW)
+    return record, rows, K
 
 
 def select_config(num_sms: int, M: int, N: int, K: int, dtype: int = BF16, max_pairs: int = 0,
@@ -379,8 +380,6 @@ class Plan:
         if rc != 0:
             raise BwgemmError(rc, "bwgemm_create_plan")
         self.handle = h
-        self._a, self._b = Scaled(), Scaled()  # gemm_scaled's operands, rewritten by every call
-        self._a_at, self._b_at = ctypes.addressof(self._a), ctypes.addressof(self._b)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -535,8 +534,8 @@ class Plan:
                 or scale_b.get_device() != dev):
             for name, t in (("A", A), ("scale_a", scale_a), ("B", B), ("scale_b", scale_b)):
                 self._check_tensor(name, t)
-        M, K = _pack_scaled(self._a, A, scale_a, "A")
-        N, Kb = _pack_scaled(self._b, B, scale_b, "B")
+        a, M, K = _pack_scaled(A, scale_a, "A")
+        b, N, Kb = _pack_scaled(B, scale_b, "B")
         if Kb != K:
             raise ValueError(f"K mismatch: A is {tuple(A.shape)}, B is {tuple(B.shape)}")
         if out is None:
@@ -557,7 +556,7 @@ class Plan:
         dt = _all_dtype_codes.get(out_dtype)
         if dt is None:
             raise TypeError(f"gemm_scaled writes bfloat16, float16 or float32, got {out_dtype}")
-        rc = self.lib.bwgemm_run_scaled(self.handle, self._a_at, self._b_at, out.data_ptr(), M, N, K, ldc, dt,
+        rc = self.lib.bwgemm_run_scaled(self.handle, a, b, out.data_ptr(), M, N, K, ldc, dt,
                                         1 if accumulate else 0,
                                         torch._C._cuda_getCurrentRawStream(dev))
         if rc != 0:

@@ -3,6 +3,7 @@ over a library that only records, host tensors in place of CUDA ones."""
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import pytest
 import torch
@@ -15,6 +16,7 @@ class Recorder:
 
     def __init__(self, real):
         self.calls = []
+        self.before = lambda: None
         self.bwgemm_orthogonalize_workspace = real.bwgemm_orthogonalize_workspace
 
     def bwgemm_orthogonalize(self, *args):
@@ -24,6 +26,7 @@ class Recorder:
         return 0
 
     def bwgemm_run_scaled(self, *args):
+        self.before()
         names = ("plan", "A", "B", "C", "M", "N", "K", "ldc", "out", "accumulate", "stream")
         self.calls.append(dict(zip(names, args, strict=True)))
         return 0
@@ -36,8 +39,6 @@ def plan(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
     p = binding.Plan.__new__(binding.Plan)
     p.lib, p.handle, p.device = Recorder(real), ctypes.c_void_p(), -1  # -1: get_device() of a host tensor
-    p._a, p._b = binding.Scaled(), binding.Scaled()
-    p._a_at, p._b_at = ctypes.addressof(p._a), ctypes.addressof(p._b)
     yield p
     p.handle = None
 
@@ -95,3 +96,47 @@ def test_scaled_product_row_and_column_results(plan):
     plan.gemm_scaled(*scaled(5, 256), *scaled(1, 256), out=torch.zeros(5, 80)[:, 16:17])
     plan.gemm_scaled(*scaled(1, 256), *scaled(1, 256), out=torch.zeros(5, 80)[:1, 16:17])
     assert [(c["M"], c["N"], c["ldc"]) for c in plan.lib.calls] == [(1, 61, 64), (1, 61, 64), (5, 1, 80), (1, 1, 8)]
+
+
+def record(argument):
+    """The bwgemm_scaled_t that the library would read: the argument is its address, or its bytes."""
+    if isinstance(argument, bytes):
+        return binding.Scaled.from_buffer_copy(argument)
+    return binding.Scaled.from_address(argument)
+
+
+def test_scaled_product_describes_its_own_operands(plan):
+    a, b = scaled(3, 300), (torch.zeros(40, 304, dtype=torch.uint8).view(torch.float8_e5m2)[:, :300], torch.ones(3, 1))
+    plan.gemm_scaled(*a, *b, out_dtype=torch.float32)
+    call, = plan.lib.calls
+    A, B = record(call["A"]), record(call["B"])
+    assert (A.values, A.ld, A.scales, A.ld_scales, A.type, A.block) == (a[0].data_ptr(), 300, a[1].data_ptr(), 3, 0, 0)
+    assert (B.values, B.ld, B.scales, B.ld_scales, B.type, B.block) == (b[0].data_ptr(), 304, b[1].data_ptr(), 1, 1, 1)
+
+
+def test_scaled_products_of_two_threads_keep_their_operands_apart(plan):
+    # ctypes lets other threads run during a call: while the first thread's product is in
+    # the library, a second thread starts and ends one of its own
+    first, second = (scaled(3, 256), scaled(40, 256)), (scaled(9, 512), scaled(70, 512))
+    inside, go = threading.Event(), threading.Event()
+    main = threading.get_ident()
+    seen = []
+
+    def before():
+        if threading.get_ident() != main:
+            inside.set()
+            assert go.wait(30)
+
+    def run():
+        plan.gemm_scaled(*first[0], *first[1])
+        call = plan.lib.calls[-1]
+        seen.append((call["M"], record(call["A"]).values, record(call["B"]).values))
+
+    plan.lib.before = before
+    t = threading.Thread(target=run)
+    t.start()
+    assert inside.wait(30)
+    plan.gemm_scaled(*second[0], *second[1])
+    go.set()
+    t.join(30)
+    assert seen == [(3, first[0][0].data_ptr(), first[1][0].data_ptr())]
