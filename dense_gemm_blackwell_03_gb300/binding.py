@@ -669,39 +669,45 @@ class Plan:
         return np.ctypeslib.as_array(buf)[:n].copy().reshape(ctas.value, slots.value)
 
 
+# (device, thread, stream) -> the default plan of the module's functions there.  A plan
+# serves one thread and one stream at a time: its launches share a workspace and a status
+# word.  Plans stay (a captured graph may hold their workspace); a thread that takes
+# over an ended one's identity takes its plans over too.
 _plans: dict = {}
 
 
-def gemm(A, B, out=None, stream=None):
-    """``A @ B.T`` with a cached default plan per device."""
-    dev = A.device.index if A.device.index is not None else 0
-    plan = _plans.get(dev)
-    if plan is None:
-        plan = _plans[dev] = Plan(dev)
-    return plan.gemm(A, B, out=out, stream=stream)
-
-
-def _default_plan(t) -> Plan:
-    """The cached default plan of a CUDA tensor's device."""
+def _default_plan(t, stream=None) -> Plan:
+    """The cached default plan of a CUDA tensor's device, for this thread and `stream`
+    (the current one if None)."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError("bwgemm takes CUDA tensors (it has no host path)")
-    plan = _plans.get(dev)
+    if stream is None:
+        handle = _torch()._C._cuda_getCurrentRawStream(dev)
+    else:
+        handle = stream.cuda_stream
+    key = (dev, threading.get_ident(), handle)
+    plan = _plans.get(key)
     if plan is None:
-        plan = _plans[dev] = Plan(dev)
+        plan = _plans[key] = Plan(dev)
     return plan
 
 
+def gemm(A, B, out=None, stream=None):
+    """``A @ B.T`` with a cached default plan per device, thread and stream."""
+    return _default_plan(A, stream).gemm(A, B, out=out, stream=stream)
+
+
 def quantize(X, blocks="row", transposed=False, pow2=False, dtype=None, stream=None):
-    """`Plan.quantize` with a cached default plan per device."""
-    return _default_plan(X).quantize(X, blocks, transposed, pow2, dtype, stream)
+    """`Plan.quantize` with a cached default plan per device, thread and stream."""
+    return _default_plan(X, stream).quantize(X, blocks, transposed, pow2, dtype, stream)
 
 
 def gemm_scaled(A, scale_a, B, scale_b, out=None, out_dtype=None, accumulate=False, stream=None):
-    """`Plan.gemm_scaled` with a cached default plan per device."""
-    return _default_plan(A).gemm_scaled(A, scale_a, B, scale_b, out, out_dtype, accumulate, stream)
+    """`Plan.gemm_scaled` with a cached default plan per device, thread and stream."""
+    return _default_plan(A, stream).gemm_scaled(A, scale_a, B, scale_b, out, out_dtype, accumulate, stream)
 
 
 def orthogonalize(G, out=None, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=1.0, stream=None):
-    """`Plan.orthogonalize` with a cached default plan per device."""
-    return _default_plan(G).orthogonalize(G, out, steps, coefficients, eps, scale, stream)
+    """`Plan.orthogonalize` with a cached default plan per device, thread and stream."""
+    return _default_plan(G, stream).orthogonalize(G, out, steps, coefficients, eps, scale, stream)

@@ -414,6 +414,38 @@ bwgemm_status_t grow(void*& buf, size_t& cap, size_t need)
 
 }  // namespace
 
+namespace {
+
+// While it lives, this thread may allocate although it is capturing a stream: a plan
+// made inside a capture (the first call on the capturing stream) is no part of the graph.
+struct AllocateInCapture {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    bool exchanged;
+    AllocateInCapture() : exchanged(cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess) {}
+    ~AllocateInCapture()
+    {
+        if (exchanged)
+            cudaThreadExchangeStreamCaptureMode(&mode);
+    }
+};
+
+// Zero two pieces of fresh device memory and wait for it, on a stream of its own: the
+// legacy stream cannot be used beside a capture.
+cudaError_t zero(void* a, size_t a_bytes, void* b, size_t b_bytes)
+{
+    cudaStream_t s = nullptr;
+    cudaError_t err = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+    if (err != cudaSuccess)
+        return err;
+    if ((err = cudaMemsetAsync(a, 0, a_bytes, s)) == cudaSuccess &&
+        (err = cudaMemsetAsync(b, 0, b_bytes, s)) == cudaSuccess)
+        err = cudaStreamSynchronize(s);
+    cudaStreamDestroy(s);
+    return err;
+}
+
+}  // namespace
+
 extern "C" {
 
 bwgemm_status_t bwgemm_create_plan(bwgemm_plan_t* out, int device,
@@ -450,6 +482,7 @@ bwgemm_status_t bwgemm_create_plan(bwgemm_plan_t* out, int device,
     DeviceGuard guard(device);
     if (!guard.ok)
         return BWGEMM_ERR_CUDA;
+    AllocateInCapture allocate;
     bwgemm_plan_s* plan = new (std::nothrow) bwgemm_plan_s();
     if (!plan)
         return BWGEMM_ERR_CUDA;
@@ -467,8 +500,7 @@ bwgemm_status_t bwgemm_create_plan(bwgemm_plan_t* out, int device,
     }
     if (cudaMalloc(&plan->d_status, 256) != cudaSuccess ||
         cudaMalloc(&plan->d_workspace, plan->workspace_bytes) != cudaSuccess ||
-        cudaMemset(plan->d_status, 0, 256) != cudaSuccess ||
-        cudaMemset(plan->d_workspace, 0, kCounterRegionBytes) != cudaSuccess) {
+        zero(plan->d_status, 256, plan->d_workspace, kCounterRegionBytes) != cudaSuccess) {
         cudaFree(plan->d_status);
         cudaFree(plan->d_workspace);
         delete plan;

@@ -185,6 +185,8 @@ void bwgemm_default_options(bwgemm_plan_options_t* opts);
  * capability 10.3 (sm_103) and returns BWGEMM_ERR_UNSUPPORTED otherwise --
  * there is no fallback path.  Allocates the plan's device status word and
  * split-K workspace.  `opts` may be NULL (defaults).  On failure *plan is NULL.
+ * May be called while this thread captures a stream; the plan is no part of the
+ * graph.
  */
 bwgemm_status_t bwgemm_create_plan(bwgemm_plan_t* plan, int device,
                                    const bwgemm_plan_options_t* opts);

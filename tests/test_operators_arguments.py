@@ -140,3 +140,62 @@ def test_scaled_products_of_two_threads_keep_their_operands_apart(plan):
     go.set()
     t.join(30)
     assert seen == [(3, first[0][0].data_ptr(), first[1][0].data_ptr())]
+
+
+# -------------------------------------------------------------- default plans
+class Handle:
+    """A CUDA tensor as far as the choice of a plan goes."""
+    device = torch.device("cuda:0")
+
+    def get_device(self):
+        return 0
+
+
+class Stream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+@pytest.fixture
+def plans(monkeypatch):
+    made = []
+
+    class Made:
+        def __init__(self, device):
+            self.device = device
+            made.append(self)
+
+        def gemm(self, *args, **kw):
+            return self
+
+        quantize = gemm_scaled = orthogonalize = gemm
+
+    monkeypatch.setattr(binding, "Plan", Made)
+    monkeypatch.setattr(binding, "_plans", {})
+    binding._torch()
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 7, raising=False)
+    return made
+
+
+CALLS = [lambda stream: binding.gemm(Handle(), None, stream=stream), lambda stream: binding.quantize(Handle(), stream=stream),
+         lambda stream: binding.gemm_scaled(Handle(), None, None, None, stream=stream),
+         lambda stream: binding.orthogonalize(Handle(), stream=stream)]
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_default_plans_are_of_one_stream_and_one_thread(plans, call):
+    # a plan's workspace and status serve one thread and one stream at a time
+    here = call(None)
+    assert call(None) is here and call(Stream(7)) is here
+    side = call(Stream(8))
+    assert side is not here and call(Stream(8)) is side
+    other = []
+    t = threading.Thread(target=lambda: other.extend((call(None), call(None))))
+    t.start()
+    t.join(30)
+    assert other[0] is other[1] and other[0] not in (here, side)
+    assert [p.device for p in plans] == [0, 0, 0]
+
+
+def test_the_calls_share_a_default_plan(plans):
+    assert len({id(call(None)) for call in CALLS}) == 1

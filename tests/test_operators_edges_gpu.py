@@ -2,6 +2,8 @@
 refused, and forms that only some sizes take.  Plain forms in 64 bits."""
 from __future__ import annotations
 
+import threading
+
 import pytest
 import torch
 
@@ -70,3 +72,70 @@ def test_linear_gradients_of_expanded_and_transposed_gradients(plan, outer, loss
     want = torch.autograd.grad(y, (x, w), dy.clone(memory_format=torch.contiguous_format), retain_graph=True)
     got = torch.autograd.grad(loss(y, v), (x, w))
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# -------------------------------------------------------------- default plans
+def split_product(seed):
+    """Operands whose product's tiles are cut along K (partial sums in the plan's workspace),
+    a matrix whose orthogonalisation is, and what a plan of their own gives for both."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    a, b = (torch.randn(n, 9000, generator=gen, device="cuda").to(torch.bfloat16) for n in (48, 300))
+    g = torch.randn(200, 9000, generator=gen, device="cuda").to(torch.bfloat16)
+    with binding.Plan(0) as p:
+        operands = p.quantize(a) + p.quantize(b, blocks="square")
+        want = (p.gemm_scaled(*operands, out_dtype=torch.float32), p.orthogonalize(g), p.gemm(a[:, :8000], b[:296, :8000]))
+        assert p.status() == 0
+    torch.cuda.synchronize()
+    return operands, g, (a[:, :8000], b[:296, :8000]), want
+
+
+def test_module_calls_on_two_streams_at_a_time(plan):
+    work = [split_product(s) for s in (1, 2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(40):
+        for (operands, g, ab, want), st in zip(work, streams):
+            got.append((binding.gemm_scaled(*operands, out_dtype=torch.float32, stream=st), binding.orthogonalize(g, stream=st),
+                        want))
+    torch.cuda.synchronize()
+    for c, x, want in got:
+        assert torch.equal(c, want[0]) and torch.equal(x, want[1])
+
+
+def test_module_calls_of_two_threads(plan):
+    work = [split_product(s) for s in (3, 4)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+
+    def run(i):
+        operands, g, ab, want = work[i]
+        with torch.cuda.stream(streams[i]):
+            for _ in range(40):
+                got[i].append((binding.gemm_scaled(*operands, out_dtype=torch.float32), binding.orthogonalize(g),
+                               binding.gemm(*ab)))
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 40
+        for outputs in got[i]:
+            assert all(torch.equal(o, w) for o, w in zip(outputs, work[i][3]))
+
+
+def test_the_first_module_call_of_a_stream_inside_a_capture(plan):
+    operands, g, ab, want = split_product(5)
+    binding.gemm_scaled(*operands)  # the library's kernels are loaded
+    fresh = torch.cuda.Stream()
+    assert (0, threading.get_ident(), fresh.cuda_stream) not in binding._plans
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=fresh):
+        got = (binding.gemm_scaled(*operands, out_dtype=torch.float32), binding.orthogonalize(g), binding.gemm(*ab))
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(got, want))
