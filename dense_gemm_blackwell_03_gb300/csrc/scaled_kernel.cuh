@@ -645,11 +645,11 @@ __global__ void __launch_bounds__(ScaledConfig<BN, SWAP, COLVEC>::kThreads, 1)
                         }
                     }
                 }
-                // relaxed: the slot's scales have been read into registers and used by
-                // now, in every lane
+                // released: every lane's reads of the slot come before the copies that
+                // the scales' warp starts into it once it sees the arrivals
                 __syncwarp();
                 if (lane == 0)
-                    ptx::mbar_arrive_relaxed(scale_empty);
+                    ptx::mbar_arrive(scale_empty);
             }
             if (!ok)
                 break;
