@@ -48,6 +48,7 @@ EXPORTED = [
     "bwgemm_plan_read_trace", "bwgemm_tune", "bwgemm_plan_tuned_count",
     "bwgemm_probe_tensor_rate", "bwgemm_noalloc_scratch", "bwgemm_bench_load_path",
     "bwgemm_quantize", "bwgemm_run_scaled", "bwgemm_orthogonalize", "bwgemm_orthogonalize_workspace",
+    "bwgemm_select_scaled", "bwgemm_select_orthogonalize",
 ]
 
 # layouts of bwgemm_bench_load_path
@@ -143,6 +144,20 @@ class Scaled(ctypes.Structure):
     ]
 
 
+class ScaledConfig(ctypes.Structure):
+    """``bwgemm_scaled_config_t``."""
+    _fields_ = [(name, ctypes.c_int32) for name in ("few_rows", "swap_ab", "tile_l", "tile_c", "column_scales", "dp_tiles",
+                                                    "sk_tiles", "workers")]
+    as_dict = Config.as_dict
+
+
+class OrthoConfig(ctypes.Structure):
+    """``bwgemm_ortho_config_t``."""
+    _fields_ = [("tile", ctypes.c_int32), ("splits", ctypes.c_int32), ("tiles", ctypes.c_int64),
+                ("workers", ctypes.c_int32)]
+    as_dict = Config.as_dict
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -231,6 +246,12 @@ def load_library(build_if_missing: bool = False):
         lib.bwgemm_orthogonalize.restype = st
         lib.bwgemm_orthogonalize_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(ctypes.c_uint64)]
         lib.bwgemm_orthogonalize_workspace.restype = st
+        lib.bwgemm_select_scaled.argtypes = [i32, i64, i64, i64, ci, ctypes.POINTER(PlanOptions),
+                                             ctypes.POINTER(ScaledConfig)]
+        lib.bwgemm_select_scaled.restype = st
+        lib.bwgemm_select_orthogonalize.argtypes = [i32, i32, i64, i64, i64, ci, i32, ctypes.POINTER(PlanOptions),
+                                                    ctypes.POINTER(OrthoConfig)]
+        lib.bwgemm_select_orthogonalize.restype = st
         _lib = lib
         return lib
 
@@ -333,6 +354,27 @@ def select_config(num_sms: int, M: int, N: int, K: int, dtype: int = BF16, max_p
     if rc != 0:
         raise BwgemmError(rc, "bwgemm_select_config")
     return cfg.as_dict()
+
+
+def select_scaled(num_sms: int, M: int, N: int, K: int, b_blocks: str = "square", **opts) -> dict:
+    """Host-only: how a plan would divide gemm_scaled's product (no GPU needed)."""
+    cfg = ScaledConfig()
+    rc = load_library().bwgemm_select_scaled(num_sms, M, N, K, BLOCK_SQUARE if b_blocks == "square" else BLOCK_ROW,
+                                             ctypes.byref(make_options(**opts)), ctypes.byref(cfg))
+    if rc != 0:
+        raise BwgemmError(rc, "bwgemm_select_scaled")
+    return cfg.as_dict()
+
+
+def select_orthogonalize(num_sms: int, batch: int, rows: int, cols: int, dtype: int = BF16, step: int = 0,
+                         max_pairs: int = 0, **opts) -> list:
+    """Host-only: how a plan would divide the products S, B and X of orthogonalize's `step`."""
+    cfg = (OrthoConfig * 3)()
+    rc = load_library().bwgemm_select_orthogonalize(num_sms, max_pairs, batch, rows, cols, dtype, step,
+                                                    ctypes.byref(make_options(**opts)), cfg)
+    if rc != 0:
+        raise BwgemmError(rc, "bwgemm_select_orthogonalize")
+    return [c.as_dict() for c in cfg]
 
 
 def probe_tensor_rate(device: int = 0):

@@ -11,6 +11,12 @@ using namespace bwgemm;
 
 namespace {
 
+// The workspace of a plan with these options (NULL = defaults).
+uint64_t workspace_of(const bwgemm_plan_options_t* opts)
+{
+    return opts && opts->workspace_bytes ? opts->workspace_bytes : 64ull << 20;
+}
+
 bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 int element_size(int dtype) { return dtype == BWGEMM_FP32 ? 4 : 2; }
@@ -297,6 +303,83 @@ bwgemm_status_t encode_result(CUtensorMap* map, int dtype, void* ptr, int64_t ro
                   CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
+// A step's three products.
+enum : int { kOrthoS = 0, kOrthoB = 1, kOrthoX = 2 };
+
+int ortho_first_terms(int dtype) { return dtype == BWGEMM_FP32 ? 2 : 1; }
+
+// The sizes of one of them: S = X X^T, B = a I + b S + c S S, X <- B X (X B upright).
+OrthoParams ortho_shape(int which, const OrthoLayout& l, int64_t batch, int64_t rows, int64_t cols, int step,
+                        int first_terms)
+{
+    OrthoParams p = {};
+    p.batch = int32_t(batch);
+    p.symmetric = which != kOrthoX;
+    p.rows = int32_t(p.symmetric ? l.m : rows);
+    p.cols = int32_t(p.symmetric ? l.m : cols);
+    p.steps_k = int32_t(blocks_of(which == kOrthoS ? l.n : l.m));
+    p.terms = 1;
+    if (which == kOrthoX) {
+        p.terms = step == 0 ? first_terms : (step < kTwoTermSteps ? 2 : 1);
+        p.low_side = step >= kTwoTermSteps ? 0 : l.wide ? 1 : 2;
+    }
+    return p;
+}
+
+struct OrthoPlan {
+    int cg;           // CTAs per tile: tiles of 128 on one, of 256 on a pair
+    int64_t tiles;    // of all matrices
+    int64_t workers;  // CTAs or pairs
+};
+
+// One product: square tiles of 256 on CTA pairs (1024 SM cycles per 128 of
+// K, bound by the MMAs) or of 128 on single CTAs (about 740, bound by the
+// copies of both operands), whichever takes fewer cycles in its waves; a
+// deep K of few tiles in slices (`sliceable`: S), whose join costs a kernel more and the
+// way of its bytes (us for the whole call, whole and in slices: 128 x 20000 335 and 93,
+// 1024 x 4096 185 and 163, 300 x 1000 88 and 85; 2048 x 8192, whole, 538 and 546).
+// Fills in p's division of the work; false where that would pass 32 bits.
+bool plan_ortho_product(OrthoParams* p, bool sliceable, int num_sms, int pairs, uint64_t workspace_bytes, OrthoPlan* out)
+{
+    int64_t tiles[3] = {}, best = 0;
+    int cg = 0;
+    for (int g = 1; g <= 2; ++g) {
+        const int64_t r = (p->rows + 128 * g - 1) / (128 * g), c = (p->cols + 128 * g - 1) / (128 * g);
+        tiles[g] = (p->symmetric ? r * (r + 1) / 2 : r * c) * p->batch;
+        const int64_t steps_all = int64_t(p->steps_k) * p->terms + (p->low_side ? g : 0);
+        const int64_t workers = g == 2 ? pairs : num_sms;
+        int64_t most = 1;
+        if (sliceable) {
+            const int64_t room = (int64_t(workspace_bytes) - int64_t(kCounterRegionBytes)) / (g * g * 128 * 128 * 4);
+            most = std::max<int64_t>(1, std::min(std::min(workers, room) / tiles[g], steps_all / 2));
+        }
+        for (int64_t splits = 1; splits <= most; ++splits) {
+            const int64_t cost = (tiles[g] * splits + workers - 1) / workers * ((steps_all + splits - 1) / splits) *
+                                     (g == 2 ? 1024 : 740) +
+                                 (splits > 1 ? 3000 + tiles[g] * splits * g * g * 65536 / 1250 : 0);
+            if (cg == 0 || cost < best) {
+                best = cost;
+                cg = g;
+                p->splits = int32_t(splits);
+            }
+        }
+    }
+    // of the join's CTAs some 2000 at most (24 tiles of 256 in three slices with
+    // eight warps a piece, five of them idle: 13 us a product more than with one)
+    for (p->join_share = 8;
+         p->join_share > 1 && (p->join_share > p->splits || tiles[cg] * cg * cg * 16 * p->join_share > 2048);)
+        p->join_share /= 2;
+    if (tiles[cg] * p->splits >= (1ll << 31))
+        return false;
+    p->num_r = int32_t((p->rows + 128 * cg - 1) / (128 * cg));
+    p->num_c = int32_t((p->cols + 128 * cg - 1) / (128 * cg));
+    p->tiles = int32_t(tiles[cg] / p->batch);
+    out->cg = cg;
+    out->tiles = tiles[cg];
+    out->workers = std::min<int64_t>(tiles[cg] * p->splits, cg == 2 ? pairs : num_sms);
+    return true;
+}
+
 bwgemm_status_t check_ortho(int64_t batch, int64_t rows, int64_t cols)
 {
     if (batch < 0 || rows < 0 || cols < 0)
@@ -482,6 +565,51 @@ bwgemm_status_t bwgemm_run_scaled(bwgemm_plan_t plan, const bwgemm_scaled_t* A, 
     return BWGEMM_OK;
 }
 
+bwgemm_status_t bwgemm_select_scaled(int32_t num_sms, int64_t M, int64_t N, int64_t K, bwgemm_block_t b_block,
+                                     const bwgemm_plan_options_t* opts, bwgemm_scaled_config_t* out)
+{
+    if (!out || num_sms < 1 || M < 1 || N < 1 || K < 1 || (b_block != BWGEMM_BLOCK_ROW && b_block != BWGEMM_BLOCK_SQUARE))
+        return BWGEMM_ERR_INVALID_ARG;
+    if (!extent_ok(M, K, K) || !extent_ok(N, K, K))
+        return BWGEMM_ERR_UNSUPPORTED;
+    *out = {};
+    if (takes_few_rows(M, N, K)) {
+        out->few_rows = 1;
+        return BWGEMM_OK;
+    }
+    const ScaledPlan s = plan_scaled(num_sms, M, N, K, b_block == BWGEMM_BLOCK_SQUARE, workspace_of(opts));
+    const ScaledVariant& v = kScaledVariants[s.variant];
+    out->swap_ab = v.swap;
+    out->tile_l = s.l_rows;
+    out->tile_c = v.bn;
+    out->column_scales = v.colvec;
+    out->dp_tiles = s.dp_tiles;
+    out->sk_tiles = s.sk_tiles;
+    out->workers = s.workers;
+    return BWGEMM_OK;
+}
+
+bwgemm_status_t bwgemm_select_orthogonalize(int32_t num_sms, int32_t max_pairs, int64_t batch, int64_t rows, int64_t cols,
+                                            bwgemm_dtype_t dtype, int32_t step, const bwgemm_plan_options_t* opts,
+                                            bwgemm_ortho_config_t out[3])
+{
+    if (!out || num_sms < 1 || max_pairs < 0 || batch < 1 || rows < 1 || cols < 1 || step < 0 || step >= kOrthoMaxSteps ||
+        (dtype != BWGEMM_BF16 && dtype != BWGEMM_FP16 && dtype != BWGEMM_FP32))
+        return BWGEMM_ERR_INVALID_ARG;
+    const bwgemm_status_t st = check_ortho(batch, rows, cols);
+    if (st != BWGEMM_OK)
+        return st;
+    const OrthoLayout l = ortho_layout(batch, rows, cols);
+    for (int which = kOrthoS; which <= kOrthoX; ++which) {
+        OrthoParams p = ortho_shape(which, l, batch, rows, cols, step, ortho_first_terms(dtype));
+        OrthoPlan s;
+        if (!plan_ortho_product(&p, which == kOrthoS, num_sms, max_pairs ? max_pairs : num_sms / 2, workspace_of(opts), &s))
+            return BWGEMM_ERR_UNSUPPORTED;
+        out[which] = {ortho_tile(s.cg), p.splits, s.tiles, int32_t(s.workers)};
+    }
+    return BWGEMM_OK;
+}
+
 bwgemm_status_t bwgemm_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, uint64_t* bytes)
 {
     if (!bytes)
@@ -527,7 +655,7 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
     const bool pdl = plan->opts.pdl_off == 0;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const int log2_scale = std::min(8, int(std::lround(0.5 * std::log2(double(l.m)))));
-    const int first_terms = dtype == BWGEMM_FP32 ? 2 : 1;
+    const int first_terms = ortho_first_terms(dtype);
 
     OrthoInput in = {};
     in.g = G;
@@ -576,56 +704,17 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
                       BWGEMM_OK)
         return st;
 
-    // One product: square tiles of 256 on CTA pairs (1024 SM cycles per 128 of
-    // K, bound by the MMAs) or of 128 on single CTAs (about 740, bound by the
-    // copies of both operands), whichever takes fewer cycles in its waves; a
-    // deep K of few tiles in slices, whose join costs a kernel more and the way of
-    // its bytes (us for the whole call, whole and in slices: 128 x 20000 335 and 93,
-    // 1024 x 4096 185 and 163, 300 x 1000 88 and 85; 2048 x 8192, whole, 538 and 546).
     const int pairs = plan->max_active[find_variant(2, 256, false, 1)];
-    OrthoParams p0 = {};
-    p0.batch = int32_t(batch);
-    p0.timeout_ns = plan->opts.timeout_ns ? plan->opts.timeout_ns : 4000000000ull;
-    p0.status = plan->d_status;
-    p0.stall_kblock = plan->opts.stall_kblock;
-    p0.partials = reinterpret_cast<float*>(plan->d_workspace + kCounterRegionBytes);
-    auto product = [&](int form, OrthoParams p, int64_t K, const CUtensorMap& a, const CUtensorMap& b,
+    auto product = [&](int form, OrthoParams p, bool sliceable, const CUtensorMap& a, const CUtensorMap& b,
                        const CUtensorMap& a2, const CUtensorMap& b2, const CUtensorMap& res, const CUtensorMap& res2) {
-        p.steps_k = int32_t((K + 127) / 128);
-        int64_t tiles[3] = {}, best = 0;
-        int cg = 0;
-        for (int g = 1; g <= 2; ++g) {
-            const int64_t r = (p.rows + 128 * g - 1) / (128 * g), c = (p.cols + 128 * g - 1) / (128 * g);
-            tiles[g] = (p.symmetric ? r * (r + 1) / 2 : r * c) * batch;
-            const int64_t steps_all = int64_t(p.steps_k) * p.terms + (p.low_side ? g : 0);
-            const int64_t workers = g == 2 ? pairs : plan->num_sms;
-            int64_t most = 1;
-            if (p.symmetric && !p.e) {
-                const int64_t room = (int64_t(plan->workspace_bytes) - int64_t(kCounterRegionBytes)) / (g * g * 128 * 128 * 4);
-                most = std::max<int64_t>(1, std::min(std::min(workers, room) / tiles[g], steps_all / 2));
-            }
-            for (int64_t splits = 1; splits <= most; ++splits) {
-                const int64_t cost = (tiles[g] * splits + workers - 1) / workers * ((steps_all + splits - 1) / splits) *
-                                         (g == 2 ? 1024 : 740) +
-                                     (splits > 1 ? 3000 + tiles[g] * splits * g * g * 65536 / 1250 : 0);
-                if (cg == 0 || cost < best) {
-                    best = cost;
-                    cg = g;
-                    p.splits = int32_t(splits);
-                }
-            }
-        }
-        // of the join's CTAs some 2000 at most (24 tiles of 256 in three slices with
-        // eight warps a piece, five of them idle: 13 us a product more than with one)
-        for (p.join_share = 8; p.join_share > 1 && (p.join_share > p.splits || tiles[cg] * cg * cg * 16 * p.join_share > 2048);)
-            p.join_share /= 2;
-        if (tiles[cg] * p.splits >= (1ll << 31))
+        p.timeout_ns = plan->opts.timeout_ns ? plan->opts.timeout_ns : 4000000000ull;
+        p.status = plan->d_status;
+        p.stall_kblock = plan->opts.stall_kblock;
+        p.partials = reinterpret_cast<float*>(plan->d_workspace + kCounterRegionBytes);
+        OrthoPlan sel;
+        if (!plan_ortho_product(&p, sliceable, plan->num_sms, pairs, plan->workspace_bytes, &sel))
             return BWGEMM_ERR_UNSUPPORTED;
-        p.num_r = int32_t((p.rows + 128 * cg - 1) / (128 * cg));
-        p.num_c = int32_t((p.cols + 128 * cg - 1) / (128 * cg));
-        p.tiles = int32_t(tiles[cg] / batch);
-        const int64_t workers = std::min<int64_t>(tiles[cg] * p.splits, cg == 2 ? pairs : plan->num_sms);
-        if (launch_ortho(form, cg, a, b, a2, b2, res, res2, p, int(workers * cg), s, pdl) != cudaSuccess)
+        if (launch_ortho(form, sel.cg, a, b, a2, b2, res, res2, p, int(sel.workers * sel.cg), s, pdl) != cudaSuccess)
             return BWGEMM_ERR_CUDA;
         plan->launches += p.splits > 1 ? 2 : 1;
         return BWGEMM_OK;
@@ -639,36 +728,30 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
         const float c = coefficients ? coefficients[3 * i + 2] : 2.0315f;
         const CUtensorMap& x = x_op[cur][0];
         // S = X X^T over the longer side
-        OrthoParams p = p0;
-        p.rows = p.cols = int32_t(l.m);
-        p.terms = 1;
-        p.symmetric = 1;
+        OrthoParams p = ortho_shape(kOrthoS, l, batch, rows, cols, i, first_terms);
         p.alpha = i == 0 ? 1.f : down * down;
         p.alpha_dev = i == 0 ? in.factors + batch : nullptr;
         p.store_cols = int32_t(l.lds);
         p.out = reinterpret_cast<uint16_t*>(ws + l.s);
         p.ldo = l.lds;
         p.stride_o = l.s_stride;
-        if ((st = product(l.wide ? kOrthoNT : kOrthoTN, p, l.n, x, x, x, x, s_res, s_turned)) != BWGEMM_OK)
+        if ((st = product(l.wide ? kOrthoNT : kOrthoTN, p, true, x, x, x, x, s_res, s_turned)) != BWGEMM_OK)
             return st;
         // B = a I + b S + c S S
+        p = ortho_shape(kOrthoB, l, batch, rows, cols, i, first_terms);
         p.alpha = c;
-        p.alpha_dev = nullptr;
+        p.store_cols = int32_t(l.lds);
         p.beta = b;
         p.diag = a;
         p.low = i < kTwoTermSteps;
         p.e = reinterpret_cast<const uint16_t*>(ws + l.s);
         p.lde = l.lds;
         p.stride_e = l.s_stride;
-        if ((st = product(kOrthoNT, p, l.m, s_op, s_op, s_op, s_op, b_res, b_turned)) != BWGEMM_OK)
+        if ((st = product(kOrthoNT, p, false, s_op, s_op, s_op, s_op, b_res, b_turned)) != BWGEMM_OK)
             return st;
         // X <- B X, or X B with X stored upright
         const bool last = i == steps - 1;
-        p = p0;
-        p.rows = int32_t(rows);
-        p.cols = int32_t(cols);
-        p.terms = i == 0 ? first_terms : (i < kTwoTermSteps ? 2 : 1);
-        p.low_side = i >= kTwoTermSteps ? 0 : l.wide ? 1 : 2;
+        p = ortho_shape(kOrthoX, l, batch, rows, cols, i, first_terms);
         p.alpha = last ? scale * (i == 0 ? 1.f : down) : (i == 0 ? 1.f / down : 1.f);
         p.alpha_dev = i == 0 ? in.factors : nullptr;
         p.store_cols = int32_t(last ? cols : l.ldx);
@@ -680,8 +763,8 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
         p.stride_o = batch > 1 ? stride_x : 0;
         const CUtensorMap &x2 = p.terms == 2 ? x_op[cur][1] : x, &res = last ? final_res : x_res[cur ^ 1][0],
                           &res2 = x_res[cur ^ 1][1];
-        st = l.wide ? product(kOrthoNN, p, l.m, b_op, x, b_op, x2, res, res2)
-                    : product(kOrthoNT, p, l.m, x, b_op, x2, b_op, res, res2);
+        st = l.wide ? product(kOrthoNN, p, false, b_op, x, b_op, x2, res, res2)
+                    : product(kOrthoNT, p, false, x, b_op, x2, b_op, res, res2);
         if (st != BWGEMM_OK)
             return st;
         cur ^= 1;

@@ -539,6 +539,38 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
 /* Host-only: the workspace bytes of bwgemm_orthogonalize for these sizes. */
 bwgemm_status_t bwgemm_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, uint64_t* bytes);
 
+/* How bwgemm_run_scaled divides a product (for inspection and tests). */
+typedef struct {
+    int32_t few_rows;      /* 1: the kernel for at most 16 rows of A (the rest is 0)     */
+    int32_t swap_ab;       /* 1: the weights' rows fill the MMA's 128-row side           */
+    int32_t tile_l;        /* rows per tile of that side's operand (A, or B if swapped)  */
+    int32_t tile_c;        /* and of the other's                                         */
+    int32_t column_scales; /* 1: the other side's scales are read per row, 0: per 128    */
+    int32_t dp_tiles;      /* tiles computed whole                                       */
+    int32_t sk_tiles;      /* tiles whose K blocks are spread over the workers           */
+    int32_t workers;       /* CTAs                                                       */
+} bwgemm_scaled_config_t;
+
+/* And bwgemm_orthogonalize one of its products. */
+typedef struct {
+    int32_t tile;    /* rows and columns per tile: 128 (a CTA) or 256 (a CTA pair) */
+    int32_t splits;  /* slices of K per tile (1 = whole)                           */
+    int64_t tiles;   /* of all matrices; of a symmetric product half of them       */
+    int32_t workers; /* CTAs or CTA pairs                                          */
+} bwgemm_ortho_config_t;
+
+/*
+ * Host-only: the division that a plan with `opts` (NULL = defaults) picks on a GPU
+ * of `num_sms` SMs holding `max_pairs` CTA pairs (0 = num_sms / 2); for the
+ * orthogonalisation of the step's (from 0) three products S, B and X.  b_block:
+ * how B carries its scales.
+ */
+bwgemm_status_t bwgemm_select_scaled(int32_t num_sms, int64_t M, int64_t N, int64_t K, bwgemm_block_t b_block,
+                                     const bwgemm_plan_options_t* opts, bwgemm_scaled_config_t* out);
+bwgemm_status_t bwgemm_select_orthogonalize(int32_t num_sms, int32_t max_pairs, int64_t batch, int64_t rows, int64_t cols,
+                                            bwgemm_dtype_t dtype, int32_t step, const bwgemm_plan_options_t* opts,
+                                            bwgemm_ortho_config_t out[3]);
+
 /* Static text for a status code ("unknown status" for anything else). */
 const char* bwgemm_status_string(bwgemm_status_t status);
 
