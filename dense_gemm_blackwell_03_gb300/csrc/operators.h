@@ -100,7 +100,7 @@ struct ScaledVariant {
 };
 constexpr ScaledVariant kScaledVariants[] = {
     {256, false, false}, {256, false, true}, {128, false, false}, {128, false, true},
-    {128, true, true},   {64, true, true},   {32, true, true},    {16, true, true},
+    {64, true, true},    {32, true, true},   {16, true, true},
 };
 constexpr int kNumScaledVariants = int(sizeof(kScaledVariants) / sizeof(kScaledVariants[0]));
 // K blocks per ring stage and TMA copy, and the ring: stages of kps * (l_rows +

@@ -484,30 +484,19 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64
             : "memory");
 }
 
-// The same for 8-bit floating point operands (each e4m3 or e5m2, named by
+// The one-CTA form for 8-bit floating point operands (each e4m3 or e5m2, named by
 // `idesc`): one instruction of shape M x N x 32.
-template <int CG>
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate)
 {
-    if constexpr (CG == 1)
-        asm volatile(
-            "{\n\t"
-            ".reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
-            "}" ::"r"(d_tmem),
-            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t"
-            ".reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
-            "}" ::"r"(d_tmem),
-            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-            : "memory");
+    asm volatile(
+        "{\n\t"
+        ".reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+        "}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // Arrive once on `bar` when every earlier tcgen05 async op of this thread completed.
@@ -759,7 +748,7 @@ __device__ __forceinline__ uint4 ld_global_cg_v4(const void* p)
     return v;
 }
 
-// Through L1 (data that several warps of the SM read), and past it (data read once).
+// Through L1 (data that several warps of the SM read).
 __device__ __forceinline__ uint4 ld_global_ca_v4(const void* p)
 {
     uint4 v;
@@ -774,16 +763,6 @@ __device__ __forceinline__ float ld_global_ca_f32(const float* p)
 {
     float v;
     asm volatile("ld.global.ca.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ uint4 ld_global_stream_v4(const void* p)
-{
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
-                 : "memory");
     return v;
 }
 

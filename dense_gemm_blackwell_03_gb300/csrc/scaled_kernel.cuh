@@ -42,7 +42,7 @@
 // waits for anybody.
 //
 // Swapped form (few rows of A): the weights fill the 128 lanes, A's rows are
-// the MMA's N (16 to 128), C leaves through plain stores (a warp's 32 lanes are
+// the MMA's N (16 to 64), C leaves through plain stores (a warp's 32 lanes are
 // 32 consecutive columns of C).  Tiles may hold fewer than 128 weight rows, so
 // that they fill the SMs without splitting K, and up to four K blocks share an
 // accumulator hand-over.  64 rows on 28672 x 8192 take 52 us (35.7 at the copy rate
@@ -71,7 +71,6 @@ struct ScaledConfig {
     static constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
     static constexpr bool kSplitRegs = BN >= 128;
     static constexpr int kRegsFirst = 56, kRegsEpi = 224;
-    static constexpr int kLoadCols = 64;  // columns per TMEM load: of one K block, or of several
     static constexpr int kLBlock = kRowsPerCta * kBlock;   // one K block of the lane side: 16 KiB
     static constexpr int kCBlock = BN * kBlock;
     // the ring: whole stages of the lane side, then of the column side; with
@@ -164,17 +163,6 @@ struct ScaledIter {
         return true;
     }
 };
-
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[N])
-{
-    if constexpr (N == 64)
-        ptx::tmem_ld_32x32b_x64(taddr, r);
-    else if constexpr (N == 32)
-        ptx::tmem_ld_32x32b_x32(taddr, r);
-    else
-        ptx::tmem_ld_32x32b_x16(taddr, r);
-}
 
 __device__ __forceinline__ void scaled_store_one(const ScaledParams& p, int64_t row, int64_t col, float v)
 {
@@ -443,7 +431,7 @@ __global__ void __launch_bounds__(ScaledConfig<BN, SWAP, COLVEC>::kThreads, 1)
                         const uint64_t cd = c_desc0 + uint64_t((s * Cfg::kCBytes + c * Cfg::kCBlock) >> 4);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            ptx::mma_f8<1>(tmem0 + uint32_t(b * Cfg::kBufCols + d * BN), ld + uint64_t(2 * kk),
+                            ptx::mma_f8(tmem0 + uint32_t(b * Cfg::kBufCols + d * BN), ld + uint64_t(2 * kk),
                                            cd + uint64_t(2 * kk), p.idesc, kk > 0 ? 1u : 0u);
                     };
                     if constexpr (Cfg::kIssuers == 2) {
@@ -609,12 +597,12 @@ __global__ void __launch_bounds__(ScaledConfig<BN, SWAP, COLVEC>::kThreads, 1)
                     const uint32_t empty = bar_acc_empty + 8 * b;
                     b = (b + 1) & (Cfg::kBufs - 1);
                     bphase ^= b == 0 ? 1u : 0u;
-                    constexpr int LD = Cfg::kLoadCols;
+                    constexpr int LD = 64;  // columns per TMEM load: of one K block, or of several
                     constexpr int TOTAL = Cfg::kJoin * COLS;  // columns this warp reads
 #pragma unroll
                     for (int i = 0; i < TOTAL; i += LD) {
                         uint32_t v[LD];
-                        tmem_load<LD>(taddr + uint32_t(i), v);
+                        ptx::tmem_ld_32x32b_x64(taddr + uint32_t(i), v);
                         ptx::tmem_ld_wait();
                         if (i + LD == TOTAL)
                             hand_back<1>(empty, lane);

@@ -45,16 +45,15 @@ cudaError_t launch_scaled(int idx, const CUtensorMap& l, const CUtensorMap& c, c
                           const CUtensorMap& c3, const CUtensorMap& out, const ScaledParams& p, int grid,
                           cudaStream_t stream, bool pdl)
 {
-    static_assert(kNumScaledVariants == 8, "one case per variant below, in the order of kScaledVariants");
+    static_assert(kNumScaledVariants == 7, "one case per variant below, in the order of kScaledVariants");
     switch (idx) {
     case 0: return launch_sc<256, false, false>(l, c, l3, c3, out, p, grid, stream, pdl);
     case 1: return launch_sc<256, false, true>(l, c, l3, c3, out, p, grid, stream, pdl);
     case 2: return launch_sc<128, false, false>(l, c, l3, c3, out, p, grid, stream, pdl);
     case 3: return launch_sc<128, false, true>(l, c, l3, c3, out, p, grid, stream, pdl);
-    case 4: return launch_sc<128, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
-    case 5: return launch_sc<64, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
-    case 6: return launch_sc<32, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
-    case 7: return launch_sc<16, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 4: return launch_sc<64, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 5: return launch_sc<32, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
+    case 6: return launch_sc<16, true, true>(l, c, l3, c3, out, p, grid, stream, pdl);
     default: return cudaErrorInvalidValue;
     }
 }

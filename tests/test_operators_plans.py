@@ -5,6 +5,7 @@ from __future__ import annotations
 import ctypes
 import os
 import random
+import re
 import shutil
 import subprocess
 
@@ -96,3 +97,21 @@ def test_ortho_plans_cover_their_products(workspace):
             if c["splits"] > 1:
                 assert c["tiles"] * c["splits"] * t * t * 4 <= (workspace or 64 << 20) - (1 << 20)
                 assert c["tiles"] <= 65535  # of the joining kernel's grid
+
+
+# a size of every compiled form of the scaled product, small ones
+FORMS = {(256, 0, 0): (7348, 389, 200, "square"), (256, 0, 1): (7431, 394, 200, "row"), (128, 0, 0): (4913, 179, 200, "square"),
+         (128, 0, 1): (5024, 184, 200, "row"), (64, 1, 1): (4987, 16, 200, "square"), (32, 1, 1): (17, 48, 200, "row"),
+         (16, 1, 1): (9, 18939, 553, "row")}
+
+
+def test_every_compiled_form_of_the_scaled_product_is_taken():
+    source = open(os.path.join(ROOT, "dense_gemm_blackwell_03_gb300", "csrc", "operators.h")).read()
+    table = re.search(r"kScaledVariants\[\] = \{(.*?)\};", source, re.S).group(1)
+    compiled = {(int(bn), int(swap == "true"), int(col == "true"))
+                for bn, swap, col in re.findall(r"\{(\d+), (true|false), (true|false)\}", table)}
+    taken = set()
+    for M, N, K, blocks in FORMS.values():
+        c = binding.select_scaled(SMS, M, N, K, blocks)
+        taken.add((c["tile_c"], c["swap_ab"], c["column_scales"]))
+    assert taken == compiled == set(FORMS)
