@@ -101,7 +101,8 @@ bwgemm_status_t check_operand(const bwgemm_scaled_t* x, int64_t rows, int64_t K)
     return BWGEMM_OK;
 }
 
-// The compiled form and the division of the work for one product.
+// The compiled form and the division of the work for one product; no workers where
+// every form has more tiles than are counted.
 struct ScaledPlan {
     int variant;
     int workers;
@@ -505,6 +506,8 @@ bwgemm_status_t bwgemm_run_scaled(bwgemm_plan_t plan, const bwgemm_scaled_t* A, 
 
     const ScaledPlan sel =
         plan_scaled(plan->num_sms, M, N, K, B->block == BWGEMM_BLOCK_SQUARE, plan->workspace_bytes);
+    if (sel.workers == 0)
+        return BWGEMM_ERR_UNSUPPORTED;
     const ScaledVariant& v = kScaledVariants[sel.variant];
     const bwgemm_scaled_t& L = v.swap ? *B : *A;
     const bwgemm_scaled_t& R = v.swap ? *A : *B;
@@ -578,6 +581,8 @@ bwgemm_status_t bwgemm_select_scaled(int32_t num_sms, int64_t M, int64_t N, int6
         return BWGEMM_OK;
     }
     const ScaledPlan s = plan_scaled(num_sms, M, N, K, b_block == BWGEMM_BLOCK_SQUARE, workspace_of(opts));
+    if (s.workers == 0)
+        return BWGEMM_ERR_UNSUPPORTED;
     const ScaledVariant& v = kScaledVariants[s.variant];
     out->swap_ab = v.swap;
     out->tile_l = s.l_rows;

@@ -115,3 +115,8 @@ def test_every_compiled_form_of_the_scaled_product_is_taken():
         c = binding.select_scaled(SMS, M, N, K, blocks)
         taken.add((c["tile_c"], c["swap_ab"], c["column_scales"]))
     assert taken == compiled == set(FORMS)
+
+
+def test_more_tiles_than_a_launch_counts_are_unsupported(lib):
+    c = binding.ScaledConfig()
+    assert lib.bwgemm_select_scaled(SMS, (1 << 31) - 1, (1 << 31) - 1, 128, 0, None, ctypes.byref(c)) == UNSUP
