@@ -17,6 +17,13 @@ uint64_t workspace_of(const bwgemm_plan_options_t* opts)
     return opts && opts->workspace_bytes ? opts->workspace_bytes : 64ull << 20;
 }
 
+// Of `workers` of `ctas` CTAs each, those that the options' cap on a persistent grid
+// leaves (NULL = no cap).
+int capped(int workers, int ctas, const bwgemm_plan_options_t* opts)
+{
+    return opts && opts->max_ctas > 0 ? std::min(workers, opts->max_ctas / ctas) : workers;
+}
+
 bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 int element_size(int dtype) { return dtype == BWGEMM_FP32 ? 4 : 2; }
@@ -340,15 +347,15 @@ struct OrthoPlan {
 // way of its bytes (us for the whole call, whole and in slices: 128 x 20000 335 and 93,
 // 1024 x 4096 185 and 163, 300 x 1000 88 and 85; 2048 x 8192, whole, 538 and 546).
 // Fills in p's division of the work; false where that would pass 32 bits.
-bool plan_ortho_product(OrthoParams* p, bool sliceable, int num_sms, int pairs, uint64_t workspace_bytes, OrthoPlan* out)
+bool plan_ortho_product(OrthoParams* p, bool sliceable, int singles, int pairs, uint64_t workspace_bytes, OrthoPlan* out)
 {
     int64_t tiles[3] = {}, best = 0;
     int cg = 0;
-    for (int g = 1; g <= 2; ++g) {
+    for (int g = 1; g <= (pairs > 0 ? 2 : 1); ++g) {
         const int64_t r = (p->rows + 128 * g - 1) / (128 * g), c = (p->cols + 128 * g - 1) / (128 * g);
         tiles[g] = (p->symmetric ? r * (r + 1) / 2 : r * c) * p->batch;
         const int64_t steps_all = int64_t(p->steps_k) * p->terms + (p->low_side ? g : 0);
-        const int64_t workers = g == 2 ? pairs : num_sms;
+        const int64_t workers = g == 2 ? pairs : singles;
         int64_t most = 1;
         if (sliceable) {
             const int64_t room = (int64_t(workspace_bytes) - int64_t(kCounterRegionBytes)) / (g * g * 128 * 128 * 4);
@@ -377,7 +384,7 @@ bool plan_ortho_product(OrthoParams* p, bool sliceable, int num_sms, int pairs, 
     p->tiles = int32_t(tiles[cg] / p->batch);
     out->cg = cg;
     out->tiles = tiles[cg];
-    out->workers = std::min<int64_t>(tiles[cg] * p->splits, cg == 2 ? pairs : num_sms);
+    out->workers = std::min<int64_t>(tiles[cg] * p->splits, cg == 2 ? pairs : singles);
     return true;
 }
 
@@ -505,7 +512,7 @@ bwgemm_status_t bwgemm_run_scaled(bwgemm_plan_t plan, const bwgemm_scaled_t* A, 
     }
 
     const ScaledPlan sel =
-        plan_scaled(plan->num_sms, M, N, K, B->block == BWGEMM_BLOCK_SQUARE, plan->workspace_bytes);
+        plan_scaled(capped(plan->num_sms, 1, &plan->opts), M, N, K, B->block == BWGEMM_BLOCK_SQUARE, plan->workspace_bytes);
     if (sel.workers == 0)
         return BWGEMM_ERR_UNSUPPORTED;
     const ScaledVariant& v = kScaledVariants[sel.variant];
@@ -580,7 +587,8 @@ bwgemm_status_t bwgemm_select_scaled(int32_t num_sms, int64_t M, int64_t N, int6
         out->few_rows = 1;
         return BWGEMM_OK;
     }
-    const ScaledPlan s = plan_scaled(num_sms, M, N, K, b_block == BWGEMM_BLOCK_SQUARE, workspace_of(opts));
+    const ScaledPlan s =
+        plan_scaled(capped(num_sms, 1, opts), M, N, K, b_block == BWGEMM_BLOCK_SQUARE, workspace_of(opts));
     if (s.workers == 0)
         return BWGEMM_ERR_UNSUPPORTED;
     const ScaledVariant& v = kScaledVariants[s.variant];
@@ -608,7 +616,8 @@ bwgemm_status_t bwgemm_select_orthogonalize(int32_t num_sms, int32_t max_pairs, 
     for (int which = kOrthoS; which <= kOrthoX; ++which) {
         OrthoParams p = ortho_shape(which, l, batch, rows, cols, step, ortho_first_terms(dtype));
         OrthoPlan s;
-        if (!plan_ortho_product(&p, which == kOrthoS, num_sms, max_pairs ? max_pairs : num_sms / 2, workspace_of(opts), &s))
+        if (!plan_ortho_product(&p, which == kOrthoS, capped(num_sms, 1, opts),
+                                capped(max_pairs ? max_pairs : num_sms / 2, 2, opts), workspace_of(opts), &s))
             return BWGEMM_ERR_UNSUPPORTED;
         out[which] = {ortho_tile(s.cg), p.splits, s.tiles, int32_t(s.workers)};
     }
@@ -709,7 +718,8 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
                       BWGEMM_OK)
         return st;
 
-    const int pairs = plan->max_active[find_variant(2, 256, false, 1)];
+    const int singles = capped(plan->num_sms, 1, &plan->opts);
+    const int pairs = capped(plan->max_active[find_variant(2, 256, false, 1)], 2, &plan->opts);
     auto product = [&](int form, OrthoParams p, bool sliceable, const CUtensorMap& a, const CUtensorMap& b,
                        const CUtensorMap& a2, const CUtensorMap& b2, const CUtensorMap& res, const CUtensorMap& res2) {
         p.timeout_ns = plan->opts.timeout_ns ? plan->opts.timeout_ns : 4000000000ull;
@@ -717,7 +727,7 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
         p.stall_kblock = plan->opts.stall_kblock;
         p.partials = reinterpret_cast<float*>(plan->d_workspace + kCounterRegionBytes);
         OrthoPlan sel;
-        if (!plan_ortho_product(&p, sliceable, plan->num_sms, pairs, plan->workspace_bytes, &sel))
+        if (!plan_ortho_product(&p, sliceable, singles, pairs, plan->workspace_bytes, &sel))
             return BWGEMM_ERR_UNSUPPORTED;
         if (launch_ortho(form, sel.cg, a, b, a2, b2, res, res2, p, int(sel.workers * sel.cg), s, pdl) != cudaSuccess)
             return BWGEMM_ERR_CUDA;

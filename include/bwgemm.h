@@ -89,7 +89,9 @@ typedef struct {
                                  N = 256 and N = tile_n - 256, into one accumulator)    */
     int32_t split_k;          /* 0 = auto, 1 = off, s >= 2: s K-slices per tile         */
     int32_t raster_group;     /* 0 = auto; m-blocks walked before stepping along N      */
-    int32_t max_ctas;         /* 0 = fill the GPU; else cap on the persistent grid      */
+    int32_t max_ctas;         /* 0 = fill the GPU; else cap on the persistent grids (the
+                                 quantiser, the product for few rows and the
+                                 orthogonalisation's input and joining kernels have none) */
     int32_t stall_kblock;     /* test hook, keep -1: the producer of CTA 0 never fills
                                  this k-block of its first unit, so a bounded wait runs
                                  out and the call reports BWGEMM_ERR_TIMEOUT            */

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from dense_gemm_blackwell_03_gb300 import binding
+from operators_ref import T, off, operand, orthogonalized, product
 
 pytestmark = pytest.mark.gpu
 
@@ -54,6 +55,19 @@ def test_scaled_product_refuses_a_strided_row_as_result(plan, dtype, K):
     assert (held == 5).all() and (wide == 5).all()
     plan.gemm_scaled(*operands, out=wide[:, 32:])  # in place: 32 elements and nothing else
     assert (wide[:, :32] == 5).all() and torch.equal(wide[:, 32:], plan.gemm_scaled(*operands, out_dtype=dtype))
+
+
+# -------------------------------------------------- a cap on the persistent grids
+@pytest.mark.parametrize("cap", [1, 2, 7])
+def test_few_ctas_give_the_same_results(cap):
+    a, sa, av = operand(300, 900, seed=cap)
+    b, sb, bv = operand(200, 900, square=True, seed=cap + 1)
+    g = torch.randn(3, 200, 700, device="cuda").to(torch.bfloat16)
+    with binding.Plan(0, max_ctas=cap) as p:
+        exact, bound = product(av, bv, "fp32")
+        assert ((p.gemm_scaled(a, sa, b, sb, out_dtype=T["fp32"]) - exact).abs() <= bound).all()
+        assert off(p.orthogonalize(g), orthogonalized(g)) <= 4.1e-3
+        assert p.status() == 0
 
 
 # ----------------------------------------------------------- a linear layer

@@ -120,3 +120,15 @@ def test_every_compiled_form_of_the_scaled_product_is_taken():
 def test_more_tiles_than_a_launch_counts_are_unsupported(lib):
     c = binding.ScaledConfig()
     assert lib.bwgemm_select_scaled(SMS, (1 << 31) - 1, (1 << 31) - 1, 128, 0, None, ctypes.byref(c)) == UNSUP
+
+
+@pytest.mark.parametrize("cap", [1, 2, 3, 40, 151, 1000])
+def test_the_cap_on_the_persistent_grid_holds(cap):
+    rng = random.Random(cap)
+    for _ in range(300):
+        M, N, K = sizes(rng, 17, 20000), sizes(rng, 64, 60000), sizes(rng, 128, 30000)
+        c = binding.select_scaled(SMS, M, N, K, rng.choice(["row", "square"]), max_ctas=cap)
+        assert 1 <= c["workers"] <= min(cap, SMS)
+        for p in binding.select_orthogonalize(SMS, rng.choice([1, 20]), *rng.sample([64, 500, 1024, 4096, 9000], 2),
+                                              step=rng.randrange(5), max_ctas=cap):
+            assert 1 <= p["workers"] * p["tile"] // 128 <= min(cap, SMS)
