@@ -14,7 +14,7 @@ COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 def operand(rows, K, square=False, kind="e4m3", seed=0):
     """(values in padded rows, scales, what they stand for in fp64), all on the GPU."""
     gen = torch.Generator(device="cuda").manual_seed(seed)
-    v = (20 * torch.randn(rows, K, generator=gen, device="cuda")).to(F8[kind])
+    v = (4 * torch.randn(rows, K, generator=gen, device="cuda")).to(F8[kind])
     wide = torch.zeros(rows, -(-K // 16) * 16, dtype=torch.uint8, device="cuda")
     wide[:, :K] = v.view(torch.uint8)
     s = torch.exp2(10 * torch.rand(-(-K // 128), -(-rows // 128) if square else rows, generator=gen, device="cuda") - 9)
