@@ -7,7 +7,8 @@ a scale per 128 elements of K, and its gradients from the same two operators:
     input gradient      dX = dY W       dY by rows,  W^T from the same pass
     weight gradient     dW = dY^T X     dY^T and X^T along the tokens, fp32 out
 
-Each tensor is read once by ``quantize``, which writes both directions.
+Each tensor is read once by ``quantize``, which writes both directions (the columns
+only where a gradient reads them).
 ``OrthogonalMomentum`` updates the weights with ``orthogonalize`` of their
 momentum.  ``python -m dense_gemm_blackwell_03_gb300.linear_training`` fits a
 small two-layer network to a teacher and prints the loss.
@@ -23,25 +24,28 @@ from . import binding
 
 class _ScaledLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight):
-        xq, xs, xtq, xts = binding.quantize(x, transposed=True)
-        wq, ws, wtq, wts = binding.quantize(weight, blocks="square", transposed=True)
-        ctx.save_for_backward(xtq, xts, wtq, wts)
+    def forward(ctx, x, weight, of_x, of_weight):
+        xq, xs, *xt = binding.quantize(x, transposed=of_weight)
+        wq, ws, *wt = binding.quantize(weight, blocks="square", transposed=of_x)
+        ctx.save_for_backward(*xt, *wt)
         ctx.weight_dtype = weight.dtype
         return binding.gemm_scaled(xq, xs, wq, ws, out_dtype=x.dtype)
 
     @staticmethod
     @torch.autograd.function.once_differentiable  # computed outside the graph: a second derivative raises
     def backward(ctx, dy):
-        xtq, xts, wtq, wts = ctx.saved_tensors
+        of_x, of_weight = ctx.needs_input_grad[:2]
         # quantize reads rows on 16-byte boundaries; autograd may hand in any layout
-        dyq, dys, dytq, dyts = binding.quantize(_aligned_rows(dy), transposed=True)
+        dyq, dys, *dyt = binding.quantize(_aligned_rows(dy), transposed=of_weight)
         dx = dw = None
-        if ctx.needs_input_grad[0]:
+        saved = list(ctx.saved_tensors)
+        if of_weight:
+            xtq, xts = saved[:2]
+            dw = binding.gemm_scaled(*dyt, xtq, xts, out_dtype=torch.float32).to(ctx.weight_dtype)
+        if of_x:
+            wtq, wts = saved[-2:]
             dx = binding.gemm_scaled(dyq, dys, wtq, wts, out_dtype=dy.dtype)
-        if ctx.needs_input_grad[1]:
-            dw = binding.gemm_scaled(dytq, dyts, xtq, xts, out_dtype=torch.float32).to(ctx.weight_dtype)
-        return dx, dw
+        return dx, dw, None, None
 
 
 def _aligned_rows(t):
@@ -59,7 +63,8 @@ def _aligned_rows(t):
 def scaled_linear(x, weight):
     """``x @ weight.T`` of CUDA matrices x (tokens x K) and weight (N x K), computed in 8 bits;
     differentiable in both, once."""
-    return _ScaledLinear.apply(_aligned_rows(x), _aligned_rows(weight))
+    grad = torch.is_grad_enabled()
+    return _ScaledLinear.apply(_aligned_rows(x), _aligned_rows(weight), grad and x.requires_grad, grad and weight.requires_grad)
 
 
 class OrthogonalMomentum:

@@ -80,3 +80,38 @@ def test_a_second_derivative_raises(plain):
     gx, = torch.autograd.grad((y ** 3).sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="twice"):
         gx.square().sum().backward()
+
+
+# ------------------------------------- each direction is quantised only where it is read
+@pytest.mark.parametrize("of_x,of_w", [(True, True), (True, False), (False, True), (False, False)])
+def test_only_the_directions_that_gradients_read(plain, of_x, of_w):
+    x, w = leaves(12, 16, 24)
+    x.requires_grad_(of_x)
+    w.requires_grad_(of_w)
+    y = linear_training.scaled_linear(x, w)
+    # the weight's gradient reads x's columns, x's gradient the weight's
+    assert plain.quantized == [("row", of_w), ("square", of_x)]
+    if of_x or of_w:
+        plain.quantized.clear()
+        y.sum().backward()
+        assert plain.quantized == [("row", of_w)]
+        for t, want in ((x, of_x), (w, of_w)):
+            assert (t.grad is not None) == want
+
+
+def test_no_direction_for_gradients_without_a_graph(plain):
+    x, w = leaves(12, 16, 24)
+    with torch.no_grad():
+        y = linear_training.scaled_linear(x, w)
+    assert not y.requires_grad and plain.quantized == [("row", False), ("square", False)]
+
+
+def test_a_gradient_of_one_operand_alone(plain):
+    x, w = leaves(12, 16, 24)
+    both = torch.autograd.grad(linear_training.scaled_linear(x, w).square().sum(), (x, w))
+    for i, t in enumerate((x, w)):
+        for of in (True, False):
+            (w if t is x else x).requires_grad_(of)
+            got, = torch.autograd.grad(linear_training.scaled_linear(x, w).square().sum(), t)
+            assert torch.equal(got, both[i])
+            (w if t is x else x).requires_grad_(True)
