@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kInThreads) ortho_convert_kernel(const OrthoIn
         e = min(max(p.log2_scale - ilogbf(norm), -120), 120);
     const float up = ldexpf(1.f, e);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        const float f = ldexpf(1.f / norm, -e);
+        const float f = norm == 0.f ? 0.f : ldexpf(1.f / norm, -e);  // zeros (eps = 0): not 0 / 0
         p.factors[mat] = f;
         p.factors[p.batch + mat] = f * f;
     }

@@ -40,6 +40,16 @@ def test_orthogonalize_refuses_rows_closer_than_their_length(plan, shape):
     assert (room == 1).all() and (expanded == 1).all()
 
 
+@pytest.mark.parametrize("shape", [(140, 200), (3, 64, 64), (2000, 16)])
+@pytest.mark.parametrize("eps", [0.0, 1e-7])
+def test_orthogonalize_zeros_give_zeros_with_any_eps(plan, shape, eps):
+    g = torch.zeros(shape, device="cuda")
+    assert (plan.orthogonalize(g, eps=eps) == 0).all()
+    g.view(-1)[5] = float("nan")
+    x = plan.orthogonalize(g, eps=eps)
+    assert torch.isnan(x[0] if x.dim() == 3 else x).all() and (x.dim() == 2 or (x[1:] == 0).all())
+
+
 # ------------------------------------------------------------ scaled product
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("K", [256, 0])
