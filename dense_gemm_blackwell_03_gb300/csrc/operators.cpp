@@ -276,7 +276,7 @@ OrthoLayout ortho_layout(int64_t batch, int64_t rows, int64_t cols)
     l.s = take(uint64_t(batch) * l.s_stride * 2);
     l.b = take(uint64_t(batch) * l.s_stride * 2 * 2);  // B and its low part
     l.sums = take(uint64_t(batch) * l.parts * 4);
-    l.factors = take(uint64_t(batch) * 2 * 4);
+    l.factors = take(uint64_t(batch) * 2 * 4 * kOrthoMaxSteps);
     l.total = at;
     return l;
 }
@@ -683,6 +683,11 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
     in.vectors = aligned(G, 16) && ldg % per_vector == 0 && in.stride_g % per_vector == 0;
     in.eps = eps;
     in.log2_scale = log2_scale;
+    in.steps = steps;
+    for (int i = 0; i < steps; ++i) {
+        const float a = std::fabs(coefficients ? coefficients[3 * i] : 3.4445f);
+        in.growth[i] = a > 0.f && a < 1e30f ? int8_t(std::ceil(std::log2(a))) : 0;
+    }
     in.sums = reinterpret_cast<float*>(ws + l.sums);
     in.parts = l.parts;
     in.hi = reinterpret_cast<uint16_t*>(ws + l.hi[0]);
@@ -745,7 +750,7 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
         // S = X X^T over the longer side
         OrthoParams p = ortho_shape(kOrthoS, l, batch, rows, cols, i, first_terms);
         p.alpha = i == 0 ? 1.f : down * down;
-        p.alpha_dev = i == 0 ? in.factors + batch : nullptr;
+        p.alpha_dev = in.factors + 2 * i * batch;
         p.store_cols = int32_t(l.lds);
         p.out = reinterpret_cast<uint16_t*>(ws + l.s);
         p.ldo = l.lds;
@@ -768,7 +773,7 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
         const bool last = i == steps - 1;
         p = ortho_shape(kOrthoX, l, batch, rows, cols, i, first_terms);
         p.alpha = last ? scale * (i == 0 ? 1.f : down) : (i == 0 ? 1.f / down : 1.f);
-        p.alpha_dev = i == 0 ? in.factors : nullptr;
+        p.alpha_dev = in.factors + (2 * i + 1) * batch;
         p.store_cols = int32_t(last ? cols : l.ldx);
         p.low = !last && i + 1 < kTwoTermSteps;
         p.out_bf16 = last && out == BWGEMM_BF16;

@@ -189,12 +189,14 @@ struct OrthoInput {
     int32_t vectors;             // 1: rows start on 16-byte boundaries
     float eps;
     int32_t log2_scale;          // X is stored times 2^log2_scale
+    int32_t steps;
+    int8_t growth[64];           // per step, powers of two that a small X grows by: ceil(log2 |a|)
     float* sums;                 // [batch][parts]
     int32_t parts;               // blocks per matrix of the first kernel
     uint16_t* hi;                // fp16, `ld` apart, `stride` per matrix; columns up to ld are zeroed
     uint16_t* lo;                // what fp16 lost (null: nothing is)
     int64_t ld, stride;
-    float* factors;              // [2][batch]: stored -> true X, and its square
+    float* factors;              // [step][2][batch]: further factors of S and of the next X
 };
 cudaError_t launch_ortho_input(const OrthoInput& p, cudaStream_t stream, bool pdl);
 

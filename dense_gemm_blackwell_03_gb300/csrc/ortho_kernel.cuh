@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
             const int row0 = x.r * TILE + int(rank) * 128 + 32 * q;
             const int col0 = x.c * TILE + (e >> 2) * Cfg::kCols;
             const int row = row0 + lane;
-            const float alpha = p.alpha_dev ? p.alpha * ptx::ld_global_cg_f32(p.alpha_dev + x.matrix) : p.alpha;
+            const float factor = p.alpha_dev ? ptx::ld_global_cg_f32(p.alpha_dev + x.matrix) : 1.f;  // on its way until the sums are there
             const bool mirror = p.symmetric && x.r != x.c;
             // The CTA's last tile: once its sums are there, the ring has been read and
             // takes the result's boxes, so that none waits for the one before it to leave.
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
             // schedulers with the issuing ones, and a 256-wide tile is 128 columns a
             // thread), so what only some products need is tested once per 64
             // columns, and fp32 values go in pairs.
-            const uint64_t alpha2 = ptx::pack_f32x2(__float_as_uint(alpha), __float_as_uint(alpha));
+            uint64_t alpha2 = 0;
             const uint64_t beta2 = ptx::pack_f32x2(__float_as_uint(p.beta), __float_as_uint(p.beta));
             // E's 64 columns, loaded before the sums are waited for, later ones a
             // piece ahead: four rows of 128 bytes at a time (eight lanes each), turned
@@ -488,6 +488,8 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
             if (!ok)
                 break;
             ptx::tc_fence_after_sync();
+            const float alpha = p.alpha * factor;
+            alpha2 = ptx::pack_f32x2(__float_as_uint(alpha), __float_as_uint(alpha));
             const uint32_t taddr = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(b * TILE + (e >> 2) * Cfg::kCols);
             if (p.splits == 1) {
 #pragma unroll 1
@@ -587,6 +589,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ortho_join_kernel(const Ortho
     const bool mirror = x.r != x.c;
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
+    const float factor = p.alpha_dev ? ptx::ld_global_cg_f32(p.alpha_dev + x.matrix) : 1.f;
     const float* at = p.partials + (size_t(t) * CG + rank) * (128 * TILE) + e * (32 * Cfg::kCols) + c * 32 + i * 128 + 4 * lane;
     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
     if ((row0 < p.rows && col < p.store_cols) || (mirror && col < p.rows && row0 < p.store_cols)) {
@@ -611,7 +614,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ortho_join_kernel(const Ortho
         f.z += g.z;
         f.w += g.w;
     }
-    const float alpha = p.alpha_dev ? p.alpha * ptx::ld_global_cg_f32(p.alpha_dev + x.matrix) : p.alpha;
+    const float alpha = p.alpha * factor;
     const uint32_t lo = pack2(__float_as_uint(f.x * alpha), __float_as_uint(f.y * alpha), 1);
     const uint32_t hi = pack2(__float_as_uint(f.z * alpha), __float_as_uint(f.w * alpha), 1);
     uint16_t* const out = p.out + x.matrix * p.stride_o;

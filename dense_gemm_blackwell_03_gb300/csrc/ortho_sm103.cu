@@ -162,10 +162,16 @@ __global__ void __launch_bounds__(kInThreads) ortho_sums_kernel(const OrthoInput
         p.sums[int64_t(blockIdx.y) * p.parts + blockIdx.x] = sum;
 }
 
-// X is stored as G times a power of two near 2^log2_scale / (|G| + eps): exact
-// for bf16 and fp16 input (but for elements below fp16's range, 2^-24 and less
-// of the largest), with elements around 2^log2_scale / sqrt(rows cols), clear
-// of fp16's subnormals.  The rest of the factor is applied to fp32 sums.
+// X is stored as G times a power of two near 2^log2_scale / |G|: exact for bf16 and
+// fp16 input (but for elements below fp16's range, 2^-24 and less of the largest),
+// with elements around 2^log2_scale / sqrt(rows cols), clear of fp16's subnormals.
+// The rest of the factor is applied to fp32 sums.
+//
+// Where |G| is far below eps, X is small and stays so for some steps: every step is then
+// X <- a X, but for terms of X^3.  Stored times 2^log2_scale alone it would sink into
+// fp16's subnormals (|G| = 1e-12, eps = 1e-7: 4 to 7 % off), so it is stored times a
+// further 2^t: t0 = floor(log2((|G| + eps) / |G|)), and each step takes ceil(log2 |a|) off t
+// until none is left, so that the stored X never grows by it.  t = 0 for |G| > eps.
 template <typename T>
 __global__ void __launch_bounds__(kInThreads) ortho_convert_kernel(const OrthoInput p)
 {
@@ -179,15 +185,24 @@ __global__ void __launch_bounds__(kInThreads) ortho_convert_kernel(const OrthoIn
     float sum = 0.f;
     for (int i = threadIdx.x; i < p.parts; i += kInThreads)
         sum += ptx::ld_global_cg_f32(p.sums + mat * p.parts + i);
-    const float norm = sqrtf(block_sum(sum, shared)) + p.eps;
-    int e = 0;
-    if (norm > 0.f && norm <= 3.0e38f)
-        e = min(max(p.log2_scale - ilogbf(norm), -120), 120);
+    const float size = sqrtf(block_sum(sum, shared)), norm = size + p.eps;
+    int e = 0, t = 0;
+    if (size > 0.f && size <= 3.0e38f) {
+        e = min(max(p.log2_scale - ilogbf(size), -120), 120);
+        t = min(ilogbf(norm / size), 100);
+    }
     const float up = ldexpf(1.f, e);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (blockIdx.x == 0 && int(threadIdx.x) < p.steps) {  // a thread per step
+        const int step = threadIdx.x;
+        auto less = [&](int i) { return t > 0 ? max(t - p.growth[i], 0) : 0; };
+        for (int i = 0; i < step; ++i)
+            t = less(i);
         const float f = norm == 0.f ? 0.f : ldexpf(1.f / norm, -e);  // zeros (eps = 0): not 0 / 0
-        p.factors[mat] = f;
-        p.factors[p.batch + mat] = f * f;
+        // the step's stored X to the true one, less 2^log2_scale after the first step
+        const float down = step == 0 ? f : ldexpf(1.f, -t);
+        float* const to = p.factors + int64_t(2 * step) * p.batch + mat;
+        to[0] = down * down;
+        to[p.batch] = step + 1 < p.steps ? ldexpf(down, less(step)) : down;
     }
     each_piece(p, g, [&](const Eight<T>& x, int row, int c) {
         uint32_t h[4], l[4];

@@ -524,10 +524,12 @@ bwgemm_status_t bwgemm_run_scaled(bwgemm_plan_t plan, const bwgemm_scaled_t* A, 
  *       holding nothing of use before or after
  *
  * Products take fp16 operands -- X and the polynomial's diagonal in two terms
- * where one would cost accuracy -- and sum in fp32; the norm is summed in fp32.
- * The relative error before the result's rounding is about 1e-3 for the default
- * steps (1.7e-3 where all singular values are close).  A matrix of
- * zeros gives zeros; one holding a NaN or an infinity gives NaNs.
+ * where one would cost accuracy -- and sum in fp32.  The relative error before the
+ * result's rounding is about 1e-3 for the default steps (1.7e-3 where all singular
+ * values are close), for |G|_F far below eps too.  The norm's squares are summed in
+ * fp32: a norm above 1.8e19 gives NaNs, one below about 1e-19 counts as smaller
+ * than it is.  A matrix of zeros gives zeros; one holding a NaN or an infinity gives
+ * NaNs.
  * Asynchronous: 2 + 3 steps launches, one more per step where S is cut into
  * slices of K (in the plan's workspace); no allocation, capturable; errors as
  * for bwgemm_run.

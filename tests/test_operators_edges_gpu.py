@@ -50,6 +50,34 @@ def test_orthogonalize_zeros_give_zeros_with_any_eps(plan, shape, eps):
     assert torch.isnan(x[0] if x.dim() == 3 else x).all() and (x.dim() == 2 or (x[1:] == 0).all())
 
 
+# Tolerance: as in test_ortho_forms_gpu, 3.1e-3; where X stays small, the only operation
+# is X <- a X.
+TINY = 3.1e-3
+
+
+@pytest.mark.parametrize("power", [-7, -8, -9, -10, -11, -12, -13, -15, -17])
+@pytest.mark.parametrize("shape,dtype", [((300, 1000), "fp32"), ((64, 4096), "bf16"), ((700, 90), "fp32"), ((1, 40), "bf16")])
+def test_orthogonalize_matrices_far_below_eps(plan, power, shape, dtype):
+    # |G| = 10^power, eps = 1e-7: the result is small too, and right to the same relative error
+    g = torch.randn(shape, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda", dtype=torch.float64)
+    g = (g / g.norm() * 10.0 ** power).to(T[dtype])
+    assert off(plan.orthogonalize(g), orthogonalized(g)) <= TINY
+
+
+@pytest.mark.parametrize("table", [[(3.4445, -4.775, 2.0315)], [(0.3, -0.1, 0.2), (5.0, -4.0, 1.0)], [(2.0, -1.5, 0.5)] * 12,
+                                   [(-2.5, 1.0, 0.0), (0.01, 1.0, 1.0), (60.0, 0.0, 0.0)]])
+def test_orthogonalize_small_matrices_with_other_coefficients(plan, table):
+    g = torch.randn(3, 150, 260, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda", dtype=torch.float64)
+    g = g / g.norm(dim=(1, 2), keepdim=True) * torch.tensor([1e-3, 1e-9, 1e-12], device="cuda")[:, None, None]
+    g = g.float()
+    want = g.double() / (g.double().norm(dim=(1, 2), keepdim=True) + 1e-5)
+    for a, b, c in table:
+        s = want @ want.mT
+        want = a * want + (b * s + c * (s @ s)) @ want
+    x = plan.orthogonalize(g, steps=len(table), coefficients=table, eps=1e-5, scale=0.5)
+    assert off(x, 0.5 * want) <= TINY
+
+
 # ------------------------------------------------------------ scaled product
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("K", [256, 0])
