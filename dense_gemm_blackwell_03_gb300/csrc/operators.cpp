@@ -47,11 +47,12 @@ bwgemm_status_t check_resident(std::initializer_list<const void*> ptrs, int devi
     return BWGEMM_OK;
 }
 
-// Elements between the first and one past the last of `rows` rows of `cols`.
+// Whether sizes and strides fit the kernels: rows, columns and K within a tile, at most
+// 256 past its first, are counted in 32 bits; products with strides stay far inside 64.
 bool extent_ok(int64_t rows, int64_t cols, int64_t ld)
 {
-    // products of sizes and strides stay far inside 64 bits
-    return rows < (1ll << 31) && cols < (1ll << 31) && ld < (1ll << 40);
+    constexpr int64_t kMost = (1ll << 31) - 256;
+    return rows <= kMost && cols <= kMost && ld < (1ll << 40);
 }
 
 bwgemm_status_t encode(CUtensorMap* map, CUtensorMapDataType type, uint32_t rank, const void* ptr, const cuuint64_t* dims,

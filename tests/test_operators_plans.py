@@ -132,3 +132,13 @@ def test_the_cap_on_the_persistent_grid_holds(cap):
         for p in binding.select_orthogonalize(SMS, rng.choice([1, 20]), *rng.sample([64, 500, 1024, 4096, 9000], 2),
                                               step=rng.randrange(5), max_ctas=cap):
             assert 1 <= p["workers"] * p["tile"] // 128 <= min(cap, SMS)
+
+
+@pytest.mark.parametrize("size", [(1 << 31) - 1, (1 << 31) - 100, (1 << 31) - 255])
+def test_sizes_whose_last_tile_would_pass_32_bits_are_unsupported(lib, size):
+    # the kernels count rows and columns of a tile, up to 256 past its first, in 32 bits
+    c = binding.ScaledConfig()
+    for sizes_ in ((1, size, 16), (size, 64, 16), (64, 64, size)):
+        assert lib.bwgemm_select_scaled(SMS, *sizes_, 0, None, ctypes.byref(c)) == UNSUP
+    for sizes_ in ((1, (1 << 31) - 256, 16), ((1 << 31) - 256, 64, 16), (64, 64, (1 << 31) - 256)):
+        assert lib.bwgemm_select_scaled(SMS, *sizes_, 0, None, ctypes.byref(c)) == 0
