@@ -408,7 +408,8 @@ def check_args(A_ptr, B_ptr, C_ptr, M, N, K, lda, ldb, ldc, dtype=BF16) -> int:
 
 
 class Plan:
-    """A bwgemm plan on one CUDA device (see ``bwgemm_create_plan``)."""
+    """A bwgemm plan on one CUDA device (see ``bwgemm_create_plan``), for one thread and one
+    stream at a time: its launches share a workspace and a status word."""
 
     def __init__(self, device: int | None = None, **opts):
         import torch
@@ -610,7 +611,8 @@ class Plan:
         """``bwgemm_orthogonalize``: the Newton-Schulz iteration on a CUDA matrix, or a
         stack of them (3-D), in bf16, fp16 or fp32.  `coefficients`: one triple
         (a, b, c) for every step, or one per step.  Returns `scale` times the
-        result in bf16, or in `out` (bf16 or fp16, G's shape)."""
+        result in bf16, or in `out` (bf16 or fp16, G's shape).  Operands are fp16, sums
+        fp32: about 1e-3 off before the result's own rounding, whichever type it has."""
         torch = _torch()
         if stream is not None:
             with torch.cuda.stream(stream):

@@ -132,10 +132,11 @@ double block_us(const ScaledVariant& v, int l_rows)
 // fitted in microseconds to M = 1, 8, 9 and 16 on 18 shapes.  Few rows: the bytes,
 // the K blocks that a warp takes one after another, and the CTAs; tiles: the K
 // blocks of a tile, split over CTAs where they are many, or the bytes.  Measured,
-// few rows against tiles: 1 x 1024 x 1024 1.7 and 6.9, 1 x 4096 x 4096 4.9 and 11.2,
-// 8 x 8192 x 8192 18.6 and 18.1, 1 x 16384 x 8192 30.0 and 24.0, 1 x 128 x 28672
-// 9.0 and 28.8, 1 x 28672 x 1024 10.3 and 7.9; 16 x 4096 x 8192 15.7 and 20.1,
-// 16 x 8192 x 4096 12.8 and 11.7.
+// few rows against tiles, weights from HBM: 1 x 1024 x 1024 1.5 and 5.9, 1 x 4096 x 4096
+// 6.3 and 10.6, 1 x 8192 x 8192 16.7 and 19.0, 8 x 8192 x 8192 18.9 and 17.7 (from L2 12.9
+// and 16.4), 1 x 16384 x 8192 30.2 and 23.3, 1 x 128 x 28672 16.5 and 29.7, 1 x 28672 x
+// 1024 11.3 and 9.0; 16 x 4096 x 4096 10.3 and 10.7, 16 x 4096 x 8192 16.6 and 20.1,
+// 16 x 8192 x 4096 14.5 and 12.1.
 bool takes_few_rows(int64_t M, int64_t N, int64_t K)
 {
     if (M > kScaledFewRows)

@@ -14,11 +14,12 @@
 // and the transposed scales.
 //
 // One read of x serves both outputs: it is bound by HBM traffic.  Measured, of the
-// 6690 GB/s of a plain copy: rows only 6030 (8192 x 8192 bf16, 33.8 us), both
-// directions 5100 (53 us), square blocks in both 6200 (28672 x 8192, 152 us); one
-// row of 8192 takes 2.3 us.  (Loads marked evict-first: 56 and 159 us.)  A CTA takes a
-// 128 x 128 tile, so that it holds whole blocks in both directions: a thread
-// has 8 columns of 8 consecutive rows in registers (16 lanes cover a row of the
+// 6690 GB/s of a plain copy: rows only 6100 (8192 x 8192 bf16, 33.3 us), both
+// directions 5100 (53 us), square blocks in both 6200 (28672 x 8192, 152 us); from
+// fp32, 8192 x 8192, rows only 6120 (55.1 us), both directions 5700 (71.4), square blocks
+// in both 6270 (64.3); one row of 8192 takes 2.2 us.  (Loads marked evict-first: 56 and
+// 159 us.)  A CTA takes a 128 x 128 tile, so that it holds whole blocks in both
+// directions: a thread has 8 columns of 8 consecutive rows in registers (16 lanes cover a row of the
 // tile: 16-byte loads, 8-byte stores, whole 128-byte lines), row maxima are
 // reduced in half a warp, column maxima across the warps through shared memory,
 // and the transposed tile goes through shared memory so that its rows leave as

@@ -12,11 +12,12 @@
 // consume a block.  The block's fresh accumulator is weighted with both scales and
 // added to the running sums.
 //
-// Measured at one row: 1024 x 1024 1.7 us (tiles: 6.9), 4096 x 4096 4.9 (11.2),
-// 8192 x 8192 16.7 (18.8), 4 TB/s; 128 x 28672 9.0 (28.8).  Neither deeper rings nor
-// more or fewer CTAs per SM help, and a persistent form that copies ahead into the
-// next rows is slower (19.1) by the instructions it adds: a warp's own way through a
-// block bounds it.  Larger products are left to the tiles.
+// Measured at one row, us with other weights in every call, so that they come from HBM
+// (with the same weights, from L2): 1024 x 1024 1.5 (1.7; tiles 5.9), 4096 x 4096 6.3
+// (4.9; tiles 10.6), 8192 x 8192 16.7 (12.2; tiles 19.0), 4 TB/s, 128 x 28672 16.5 (8.9;
+// tiles 29.7).  Neither deeper rings nor more or fewer CTAs per SM help, and a persistent
+// form that copies ahead into the next rows is slower (19.1) by the instructions it adds: a
+// warp's own way through a block bounds it.  Larger products are left to the tiles.
 //
 // A CTA takes 8 weight rows -- many small CTAs, so that the last ones do not run
 // alone (16 rows: 18.4 us) -- and its eight warps take the K blocks in turn, kRing

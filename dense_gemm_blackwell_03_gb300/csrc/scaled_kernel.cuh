@@ -15,10 +15,10 @@
 // multiplication each), and the path of a block through the epilogue -- barrier,
 // two TMEM loads, additions, hand-back, each waiting for the one before -- about
 // 1050; the two TMEM buffers let that overlap only with the next block's MMAs.
-// 8192 x 28672 x 8192 runs at 2.2 PFLOP/s, with a scale per column 8192^3 at 1.57;
-// the same kernel without the additions at 2.5.  Tried and slower: CTA pairs (half
-// the copies, but every hand-back crosses the pair; 2.1), 192 columns with twelve
-// epilogue warps of 64 (1.9), 128 columns (1.7), TMEM loads of 32 columns.
+// 8192 x 28672 x 8192 takes 1833 to 1875 us (2.1 PFLOP/s), with a scale per column
+// 8192^3 696 (1.58).  Of its rate then, without the additions 1.14.  Tried and slower:
+// CTA pairs (half the copies, but every hand-back crosses the pair; 0.95), 192 columns
+// with twelve epilogue warps of 64 (0.86), 128 columns (0.77), TMEM loads of 32 columns.
 // On few rows of A it is bound by HBM: see the swapped form.
 //
 //   warp 0      TMA producer: a ring of stages of several K blocks, one 3-D copy
@@ -45,10 +45,10 @@
 // the MMA's N (16 to 64), C leaves through plain stores (a warp's 32 lanes are
 // 32 consecutive columns of C).  Tiles may hold fewer than 128 weight rows, so
 // that they fill the SMs without splitting K, and up to four K blocks share an
-// accumulator hand-over.  64 rows on 28672 x 8192 take 52 us (35.7 at the copy rate
-// of HBM), 16 rows 37; on 64 rows HBM is busy 48 % of the time, the rest is the
-// way of a K block through barriers and epilogue.  A few rows on smaller weights are taken by
-// scaled_few_sm103.cu.
+// accumulator hand-over.  64 rows on 28672 x 8192 take 53 us (35.7 at the copy rate
+// of HBM), 16 rows 38; on 64 rows HBM is busy 48 % of the time, the rest is the
+// way of a K block through barriers and epilogue.  A few rows on smaller weights are
+// taken by scaled_few_sm103.cu.
 #pragma once
 
 #include "operators.h"
@@ -580,8 +580,8 @@ __global__ void __launch_bounds__(ScaledConfig<BN, SWAP, COLVEC>::kThreads, 1)
                     sphase ^= 1u;
                 }
                 // unrolled, but with a scale per column: twice the code, which then
-                // misses the instruction cache (8192^3: 721 us unrolled, 701 rolled;
-                // 8192 x 28672 x 8192 with a scale per block: 1759 and 1881)
+                // misses the instruction cache (8192^3: 722 us unrolled, 697 rolled;
+                // 8192 x 28672 x 8192 with a scale per block: 1858 and 1962)
                 constexpr int kUnroll = COLVEC && !SWAP ? 1 : Cfg::kGroup;
 #pragma unroll kUnroll
                 for (int g = 0; g < Cfg::kGroup; g += Cfg::kJoin) {
