@@ -191,3 +191,32 @@ def test_the_first_module_call_of_a_stream_inside_a_capture(plan):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(got, want))
+
+
+@pytest.mark.parametrize("warm", [False, True])
+def test_a_training_step_of_a_linear_layer_inside_a_capture(plan, warm):
+    # forward here, backward on autograd's thread: both make their plans while this thread captures
+    from dense_gemm_blackwell_03_gb300.linear_training import scaled_linear
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x, w = (torch.randn(*s, generator=gen, device="cuda").to(torch.bfloat16).requires_grad_() for s in ((48, 9000), (300, 9000)))
+
+    def step():  # (detached: a graph that lives on keeps its leaves on the stream of its forward pass)
+        y = scaled_linear(x, w)
+        return [t.detach() for t in (y, *torch.autograd.grad(y.float().square().sum(), (x, w)))]
+
+    stream = torch.cuda.Stream()
+    want = step()
+    torch.cuda.synchronize()
+    if warm:
+        with torch.cuda.stream(stream):
+            step()
+        torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        got = step()
+    for t in got:
+        t.zero_()
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
