@@ -688,7 +688,7 @@ bwgemm_status_t bwgemm_orthogonalize(bwgemm_plan_t plan, const void* G, bwgemm_d
     in.steps = steps;
     for (int i = 0; i < steps; ++i) {
         const float a = std::fabs(coefficients ? coefficients[3 * i] : 3.4445f);
-        in.growth[i] = a > 0.f && a < 1e30f ? int8_t(std::ceil(std::log2(a))) : 0;
+        in.growth[i] = a > 0.f && a < 1e30f ? int8_t(std::max(std::ceil(std::log2(a)), -100.f)) : 0;
     }
     in.sums = reinterpret_cast<float*>(ws + l.sums);
     in.parts = l.parts;

@@ -510,15 +510,16 @@ bwgemm_status_t bwgemm_run_scaled(bwgemm_plan_t plan, const bwgemm_scaled_t* A, 
  * (X^T X and X (...) when there are more rows than columns -- the same result),
  * which drives all singular values towards one; the result is `scale` * X.
  *
- *   G : batch x rows x cols, bf16, fp16 or fp32 (`dtype`), row stride ldg and
- *       matrix stride stride_g in elements (any; rows on 16-byte boundaries are
- *       read in vectors).  Read only.
+ *   G : batch x rows x cols, bf16, fp16 or fp32 (`dtype`), row stride ldg >= cols
+ *       and matrix stride stride_g >= (rows - 1) ldg + cols in elements (rows on
+ *       16-byte boundaries are read in vectors).  Read only.
  *   X : the result, bf16 or fp16 (`out`), strides ldx and stride_x (rows on
  *       16-byte boundaries and cols a multiple of 8 are stored by TMA).  May be
  *       G itself only if the types and strides are the same.
  *   steps : 1..64
  *   coefficients : host array of `steps` triples (a, b, c), read before the
- *       call returns; NULL = (3.4445, -4.7750, 2.0315) in every step
+ *       call returns; NULL = (3.4445, -4.7750, 2.0315) in every step.  The
+ *       polynomial is held in fp16: its largest value has to lie between 1e-4 and 6e4
  *   eps >= 0; workspace: device memory, 256-byte aligned, of at least
  *       bwgemm_orthogonalize_workspace() bytes (else BWGEMM_ERR_WORKSPACE),
  *       holding nothing of use before or after
