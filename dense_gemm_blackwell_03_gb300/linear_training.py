@@ -81,6 +81,8 @@ class OrthogonalMomentum:
     @torch.no_grad()
     def step(self):
         for w, m in zip(self.weights, self.momentum):
+            if w.grad is None:  # not part of this step's loss
+                continue
             g = w.grad.float()
             m.mul_(self.beta).add_(g)
             rows, cols = w.shape

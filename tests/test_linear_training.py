@@ -115,3 +115,12 @@ def test_a_gradient_of_one_operand_alone(plain):
             got, = torch.autograd.grad(linear_training.scaled_linear(x, w).square().sum(), t)
             assert torch.equal(got, both[i])
             (w if t is x else x).requires_grad_(True)
+
+
+def test_weights_without_a_gradient_stay(plain):
+    plain.orthogonalize = lambda g, steps, scale: scale * g
+    a, b = torch.ones(4, 8, requires_grad=True), torch.ones(4, 8, requires_grad=True)
+    opt = linear_training.OrthogonalMomentum([a, b], lr=0.5, beta=0.0)
+    a.sum().backward()
+    opt.step()
+    assert (a == 0.5).all() and (b == 1).all() and a.grad is None and (opt.momentum[1] == 0).all()
