@@ -8,8 +8,8 @@ it raises if the library is missing rather than computing anything on the host.
 """
 import importlib
 
-__all__ = ["BF16", "FP16", "BwgemmError", "Plan", "PlanOptions", "gemm", "gemm_scaled", "orthogonalize", "quantize",
-           "library_path", "load_library", "select_config", "check_args"]
+__all__ = ["BF16", "FP16", "BwgemmError", "Plan", "PlanOptions", "gated_linear", "gated_linear_backward", "gemm",
+           "gemm_int8", "gemm_scaled", "orthogonalize", "quantize", "quantize_int8", "library_path", "load_library", "select_config", "check_args"]
 
 
 def __getattr__(name):

@@ -23,6 +23,11 @@ BLOCK = 128
 BLOCK_ROW = 0
 BLOCK_SQUARE = 1
 
+SILU = 0
+GELU = 1
+GELU_TANH = 2
+ACTIVATIONS = {"silu": SILU, "gelu": GELU, "gelu_tanh": GELU_TANH}
+
 SCHEDULE_AUTO = 0
 SCHEDULE_TILES = 1
 SCHEDULE_STREAM_K = 2
@@ -48,7 +53,9 @@ EXPORTED = [
     "bwgemm_plan_read_trace", "bwgemm_tune", "bwgemm_plan_tuned_count",
     "bwgemm_probe_tensor_rate", "bwgemm_noalloc_scratch", "bwgemm_bench_load_path",
     "bwgemm_quantize", "bwgemm_run_scaled", "bwgemm_orthogonalize", "bwgemm_orthogonalize_workspace",
-    "bwgemm_select_scaled", "bwgemm_select_orthogonalize",
+    "bwgemm_select_scaled", "bwgemm_select_orthogonalize", "bwgemm_gated", "bwgemm_gated_backward",
+    "bwgemm_gated_backward_workspace", "bwgemm_quantize_integer", "bwgemm_run_integer", "bwgemm_run_integer_workspace",
+    "bwgemm_select_gated", "bwgemm_select_integer", "bwgemm_select_gated_backward",
 ]
 
 # layouts of bwgemm_bench_load_path
@@ -158,6 +165,17 @@ class OrthoConfig(ctypes.Structure):
     as_dict = Config.as_dict
 
 
+class Matrix(ctypes.Structure):
+    """``bwgemm_matrix_t``: a 16-bit matrix."""
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64)]
+
+
+class LanesConfig(ctypes.Structure):
+    """``bwgemm_lanes_config_t``."""
+    _fields_ = [(name, ctypes.c_int32) for name in ("lanes", "tile_w", "tile_x", "dp_tiles", "sk_tiles", "workers")]
+    as_dict = Config.as_dict
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -252,6 +270,23 @@ def load_library(build_if_missing: bool = False):
         lib.bwgemm_select_orthogonalize.argtypes = [i32, i32, i64, i64, i64, ci, i32, ctypes.POINTER(PlanOptions),
                                                     ctypes.POINTER(OrthoConfig)]
         lib.bwgemm_select_orthogonalize.restype = st
+        # bwgemm_matrix_t as addresses or packed bytes
+        lib.bwgemm_gated.argtypes = [vp] * 7 + [i64, i64, i64, ci, ci, vp]
+        lib.bwgemm_gated.restype = st
+        lib.bwgemm_gated_backward.argtypes = [vp] * 10 + [i64, i64, i64, ci, ci, vp, ctypes.c_uint64, vp]
+        lib.bwgemm_gated_backward.restype = st
+        lib.bwgemm_gated_backward_workspace.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_uint64)]
+        lib.bwgemm_gated_backward_workspace.restype = st
+        lib.bwgemm_quantize_integer.argtypes = [vp, vp, ci, i64, i64, i64, vp, i64, vp, vp]
+        lib.bwgemm_quantize_integer.restype = st
+        lib.bwgemm_run_integer.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, ci, vp, ctypes.c_uint64, vp]
+        lib.bwgemm_run_integer.restype = st
+        lib.bwgemm_run_integer_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(ctypes.c_uint64)]
+        lib.bwgemm_run_integer_workspace.restype = st
+        for name, config in (("gated", LanesConfig), ("integer", LanesConfig), ("gated_backward", OrthoConfig)):
+            f = getattr(lib, f"bwgemm_select_{name}")
+            f.argtypes = [i32, i32, i64, i64, i64, ctypes.POINTER(PlanOptions), ctypes.POINTER(config)]
+            f.restype = st
         _lib = lib
         return lib
 
@@ -343,6 +378,57 @@ def _pack_scaled(values, scales, name: str):
     return record, rows, K
 
 
+# bwgemm_matrix_t as a packed record
+_MATRIX = struct.Struct("@Pq")
+assert _MATRIX.size == ctypes.sizeof(Matrix)
+
+
+def _pack_matrix(t, name: str, rows: int, cols: int, dtype, device: int):
+    """The bytes of a bwgemm_matrix_t of the rows x cols CUDA tensor `t`.  Strides are passed as
+    they are: rows closer than their length are refused by the library."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the plan on cuda:{device}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be {rows} x {cols}, got {tuple(t.shape)}")
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{name} must be row-major (unit stride along the last dim)")
+    if rows <= 1:
+        ld = (cols + 7) & -8  # a single row has no next one
+    return _MATRIX.pack(t.data_ptr(), ld)
+
+
+def _int8_operand(t, scale, name: str, device: int):
+    """(rows, K, bytes between rows) of the 8-bit integers `t` with a scale per row."""
+    torch = _torch_mod
+    if t.dtype is not torch.int8:
+        raise TypeError(f"{name} must be int8, got {t.dtype}")
+    if scale.dtype is not torch.float32:
+        raise TypeError(f"the scales of {name} must be float32, got {scale.dtype}")
+    if t.get_device() != device or scale.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, its scales on {scale.device}, the plan on cuda:{device}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, K = t.shape
+    if scale.dim() != 1 or scale.shape[0] != rows:
+        raise ValueError(f"{name} has {rows} rows, its scales have the shape {tuple(scale.shape)}")
+    ld, unit = t.stride()
+    if (unit != 1 and K > 1) or (rows > 1 and scale.stride(0) != 1):
+        raise ValueError(f"{name} and its scales need unit stride along the last dim")
+    if rows <= 1:
+        ld = (K + 15) & -16  # a single row has no next one
+    return rows, K, ld
+
+
+def _activation_code(activation) -> int:
+    code = ACTIVATIONS.get(activation)
+    if code is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    return code
+
+
 def select_config(num_sms: int, M: int, N: int, K: int, dtype: int = BF16, max_pairs: int = 0,
                   max_quads: int = 0, **opts) -> dict:
     """Host-only: the configuration a plan would choose (no GPU needed)."""
@@ -374,6 +460,33 @@ def select_orthogonalize(num_sms: int, batch: int, rows: int, cols: int, dtype: 
                                                     ctypes.byref(make_options(**opts)), cfg)
     if rc != 0:
         raise BwgemmError(rc, "bwgemm_select_orthogonalize")
+    return [c.as_dict() for c in cfg]
+
+
+def _select_lanes(name, num_sms, M, N, K, max_pairs, opts) -> dict:
+    cfg = LanesConfig()
+    rc = getattr(load_library(), name)(num_sms, max_pairs, M, N, K, ctypes.byref(make_options(**opts)), ctypes.byref(cfg))
+    if rc != 0:
+        raise BwgemmError(rc, name)
+    return cfg.as_dict()
+
+
+def select_gated(num_sms: int, M: int, N: int, K: int, max_pairs: int = 0, **opts) -> dict:
+    """Host-only: how a plan would divide gated_linear's product (no GPU needed)."""
+    return _select_lanes("bwgemm_select_gated", num_sms, M, N, K, max_pairs, opts)
+
+
+def select_int8(num_sms: int, M: int, N: int, K: int, max_pairs: int = 0, **opts) -> dict:
+    """Host-only: how a plan would divide gemm_int8's product."""
+    return _select_lanes("bwgemm_select_integer", num_sms, M, N, K, max_pairs, opts)
+
+
+def select_gated_backward(num_sms: int, M: int, N: int, K: int, max_pairs: int = 0, **opts) -> list:
+    """Host-only: how a plan would divide the products dX and dW of gated_linear_backward."""
+    cfg = (OrthoConfig * 2)()
+    rc = load_library().bwgemm_select_gated_backward(num_sms, max_pairs, M, N, K, ctypes.byref(make_options(**opts)), cfg)
+    if rc != 0:
+        raise BwgemmError(rc, "bwgemm_select_gated_backward")
     return [c.as_dict() for c in cfg]
 
 
@@ -657,6 +770,149 @@ class Plan:
             raise BwgemmError(rc, "bwgemm_orthogonalize")
         return out
 
+    def gated_linear(self, x, w_gate, w_up, activation: str = "silu", keep: bool = False, stream=None):
+        """``bwgemm_gated``: ``act(x @ w_gate.T) * (x @ w_up.T)`` of CUDA tensors x (M x K), w_gate
+        and w_up (N x K), all bf16 or all fp16.  `activation`: "silu", "gelu" or "gelu_tanh".
+
+        Returns the M x N result, and with `keep` ``(result, gate, up)`` with the two projections
+        that `gated_linear_backward` reads.  Rows of the results are padded to 16 bytes."""
+        torch = _torch()
+        if stream is not None:  # results come from that stream's memory, free there and then
+            with torch.cuda.stream(stream):
+                return self.gated_linear(x, w_gate, w_up, activation, keep)
+        dt = _dtype_code(x)
+        act = _activation_code(activation)
+        dev, dtype = self.device, x.dtype
+        if x.dim() != 2 or w_gate.dim() != 2:
+            raise ValueError("x and the weights must be 2-D")
+        M, K = x.shape
+        N = w_gate.shape[0]
+        xm = _pack_matrix(x, "x", M, K, dtype, dev)
+        gm = _pack_matrix(w_gate, "w_gate", N, K, dtype, dev)
+        um = _pack_matrix(w_up, "w_up", N, K, dtype, dev)
+        ld = (N + 7) & -8
+        outs = [_padded_empty(M, N, dtype, x.device, 8) for _ in range(3 if keep else 1)]
+        records = [_MATRIX.pack(t.data_ptr(), ld) for t in outs] + [None] * (3 - len(outs))
+        rc = self.lib.bwgemm_gated(self.handle, xm, gm, um, *records, M, N, K, dt, act,
+                                   torch._C._cuda_getCurrentRawStream(dev))
+        if rc != 0:
+            raise BwgemmError(rc, "bwgemm_gated")
+        return tuple(outs) if keep else outs[0]
+
+    def gated_linear_backward(self, dh, gate, up, x, w_gate, w_up, activation: str = "silu", input_grad: bool = True,
+                              weight_grads: bool = True, stream=None):
+        """``bwgemm_gated_backward``: ``(dx, dw_gate, dw_up)`` from the gradient `dh` of gated_linear's
+        result and the `gate` and `up` that it kept; None for what is not asked for (`x` is read for
+        the weights' gradients alone, `w_gate` and `w_up` for the input's: else None will do)."""
+        torch = _torch()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.gated_linear_backward(dh, gate, up, x, w_gate, w_up, activation, input_grad, weight_grads)
+        dt = _dtype_code(dh)
+        act = _activation_code(activation)
+        dev, dtype = self.device, dh.dtype
+        if not input_grad and not weight_grads:
+            return None, None, None
+        wide = x if weight_grads else w_gate
+        if dh.dim() != 2 or wide.dim() != 2:
+            raise ValueError("dh, x and the weights must be 2-D")
+        M, N = dh.shape
+        K = wide.shape[1]
+        records = [_pack_matrix(t, name, M, N, dtype, dev) for t, name in ((dh, "dh"), (gate, "gate"), (up, "up"))]
+        records.append(_pack_matrix(x, "x", M, K, dtype, dev) if weight_grads else None)
+        for t, name in ((w_gate, "w_gate"), (w_up, "w_up")):
+            records.append(_pack_matrix(t, name, N, K, dtype, dev) if input_grad else None)
+        ld = (K + 7) & -8
+        dx = _padded_empty(M, K, dtype, dh.device, 8) if input_grad else None
+        dwg, dwu = (_padded_empty(N, K, dtype, dh.device, 8) if weight_grads else None for _ in range(2))
+        records += [None if t is None else _MATRIX.pack(t.data_ptr(), ld) for t in (dx, dwg, dwu)]
+        need = ctypes.c_uint64()
+        rc = self.lib.bwgemm_gated_backward_workspace(M, N, ctypes.byref(need))
+        if rc != 0:
+            raise BwgemmError(rc, "bwgemm_gated_backward_workspace")
+        ws = torch.empty(need.value, dtype=torch.uint8, device=dh.device)
+        rc = self.lib.bwgemm_gated_backward(self.handle, *records, M, N, K, dt, act, ws.data_ptr(), need.value,
+                                            torch._C._cuda_getCurrentRawStream(dev))
+        if rc != 0:
+            raise BwgemmError(rc, "bwgemm_gated_backward")
+        return dx, dwg, dwu
+
+    def quantize_int8(self, x, stream=None):
+        """``bwgemm_quantize_integer``: the rows of a 2-D CUDA tensor (bf16, fp16 or fp32; tokens, or a
+        weight's output channels) as 8-bit integers with one fp32 scale each: ``(q, scales)``.
+        q's rows are padded to 16 bytes."""
+        torch = _torch()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.quantize_int8(x)
+        dt = _all_dtype_codes.get(x.dtype)
+        if dt is None:
+            raise TypeError(f"quantize_int8 takes bfloat16, float16 or float32 tensors, got {x.dtype}")
+        if x.get_device() != self.device:
+            self._check_tensor("x", x)
+        if x.dim() != 2:
+            raise ValueError("x must be 2-D")
+        rows, cols = x.shape
+        ldx, unit = x.stride()
+        if unit != 1 and cols > 1:
+            raise ValueError("x must be row-major (unit stride along the last dim)")
+        if rows <= 1:
+            ldx = (cols + 7) & -8  # a single row has no next one
+        q = _padded_empty(rows, cols, torch.int8, x.device, 16)
+        scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+        if cols == 0:
+            scales.fill_(2.0 ** -100 / 127)  # rows without a value: as rows of zeros
+        rc = self.lib.bwgemm_quantize_integer(self.handle, x.data_ptr(), dt, rows, cols, ldx, q.data_ptr(), (cols + 15) & -16,
+                                           scales.data_ptr(), torch._C._cuda_getCurrentRawStream(self.device))
+        if rc != 0:
+            raise BwgemmError(rc, "bwgemm_quantize_integer")
+        return q, scales
+
+    def gemm_int8(self, A, scale_a, B, scale_b, out=None, out_dtype=None, stream=None):
+        """``bwgemm_run_integer``: ``out = scale_a[:, None] * scale_b * (A @ B.T)`` of int8 CUDA tensors A
+        (M x K) and B (N x K) with a scale per row, as `quantize_int8` returns them.  `out_dtype`:
+        bf16 (default), fp16 or fp32."""
+        torch = _torch()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.gemm_int8(A, scale_a, B, scale_b, out, out_dtype)
+        dev = self.device
+        M, K, lda = _int8_operand(A, scale_a, "A", dev)
+        N, Kb, ldb = _int8_operand(B, scale_b, "B", dev)
+        if Kb != K:
+            raise ValueError(f"K mismatch: A is {tuple(A.shape)}, B is {tuple(B.shape)}")
+        if out is None:
+            if out_dtype is None:
+                out_dtype = torch.bfloat16
+            dt = _all_dtype_codes.get(out_dtype)
+            if dt is None:
+                raise TypeError(f"gemm_int8 writes bfloat16, float16 or float32, got {out_dtype}")
+            ldc = (N + 7) & -8
+            out = _padded_empty(M, N, out_dtype, A.device, 8)
+        else:
+            self._check_tensor("out", out)
+            if tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
+                raise ValueError("out must be an M x N CUDA tensor of out_dtype")
+            dt = _all_dtype_codes.get(out.dtype)
+            if dt is None:
+                raise TypeError(f"gemm_int8 writes bfloat16, float16 or float32, got {out.dtype}")
+            ldc, unit = out.stride()  # as it is: rows closer than their length are refused
+            if unit != 1 and N > 1:
+                raise ValueError("out must be row-major (unit stride along the last dim)")
+            if M <= 1:
+                ldc = (N + 7) & -8  # a single row has no next one
+        need = ctypes.c_uint64()
+        rc = self.lib.bwgemm_run_integer_workspace(M, N, K, ctypes.byref(need))
+        if rc != 0:
+            raise BwgemmError(rc, "bwgemm_run_integer_workspace")
+        ws = torch.empty(need.value, dtype=torch.uint8, device=A.device) if need.value else None
+        rc = self.lib.bwgemm_run_integer(self.handle, A.data_ptr(), scale_a.data_ptr(), B.data_ptr(), scale_b.data_ptr(),
+                                      out.data_ptr(), M, N, K, lda, ldb, ldc, dt, ws.data_ptr() if ws is not None else None,
+                                      need.value, torch._C._cuda_getCurrentRawStream(dev))
+        if rc != 0:
+            raise BwgemmError(rc, "bwgemm_run_integer")
+        return out
+
     def status(self, stream=None) -> int:
         """``bwgemm_get_status``: synchronises the stream, returns and clears the status."""
         return int(self.lib.bwgemm_get_status(self.handle, self._stream_handle(stream)))
@@ -755,3 +1011,24 @@ def gemm_scaled(A, scale_a, B, scale_b, out=None, out_dtype=None, accumulate=Fal
 def orthogonalize(G, out=None, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=1.0, stream=None):
     """`Plan.orthogonalize` with a cached default plan per device, thread and stream."""
     return _default_plan(G, stream).orthogonalize(G, out, steps, coefficients, eps, scale, stream)
+
+
+def gated_linear(x, w_gate, w_up, activation="silu", keep=False, stream=None):
+    """`Plan.gated_linear` with a cached default plan per device, thread and stream."""
+    return _default_plan(x, stream).gated_linear(x, w_gate, w_up, activation, keep, stream)
+
+
+def gated_linear_backward(dh, gate, up, x, w_gate, w_up, activation="silu", input_grad=True, weight_grads=True, stream=None):
+    """`Plan.gated_linear_backward` with a cached default plan per device, thread and stream."""
+    return _default_plan(dh, stream).gated_linear_backward(dh, gate, up, x, w_gate, w_up, activation, input_grad,
+                                                           weight_grads, stream)
+
+
+def quantize_int8(x, stream=None):
+    """`Plan.quantize_int8` with a cached default plan per device, thread and stream."""
+    return _default_plan(x, stream).quantize_int8(x, stream)
+
+
+def gemm_int8(A, scale_a, B, scale_b, out=None, out_dtype=None, stream=None):
+    """`Plan.gemm_int8` with a cached default plan per device, thread and stream."""
+    return _default_plan(A, stream).gemm_int8(A, scale_a, B, scale_b, out, out_dtype, stream)

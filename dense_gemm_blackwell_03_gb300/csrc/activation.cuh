@@ -1,0 +1,56 @@
+// activation.cuh -- the gated layer's activations and their slopes, in fp32.
+//
+// silu(g) = g s(g) and gelu_tanh(g) = g (1 + tanh z) / 2 = g s(2 z) with the logistic
+// function s(t) = 1 / (1 + exp(-t)) and z = sqrt(2 / pi) (g + 0.044715 g^3); gelu(g) = g Phi(g).
+// exp and the quotient are CUDA's fast ones, good to a few 2^-23 -- results are rounded
+// to 2^-9 or 2^-12 after them.
+#pragma once
+
+#include <cstdint>
+
+#include "../../include/bwgemm.h"
+
+namespace bwgemm {
+
+// s(t); 0 and 1 at the ends: exp(-t) past fp32 is inf, and 1 / inf = 0.
+__device__ __forceinline__ float logistic(float t)
+{
+    return __fdividef(1.f, 1.f + __expf(-t));
+}
+
+constexpr float kGeluC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kGeluC3 = 0.044715f;
+
+__device__ __forceinline__ float activate(float g, int activation)
+{
+    if (activation == BWGEMM_SILU)
+        return g * logistic(g);
+    if (activation == BWGEMM_GELU)
+        return g * normcdff(g);
+    return g * logistic(kGeluC * fmaf(kGeluC3 * g * g, g, g));
+}
+
+// The activation and its derivative.
+__device__ __forceinline__ void activate_slope(float g, int activation, float& value, float& slope)
+{
+    if (activation == BWGEMM_GELU) {
+        const float cdf = normcdff(g);
+        value = g * cdf;
+        slope = fmaf(g, 0.3989422804014327f * __expf(-0.5f * g * g), cdf);
+        return;
+    }
+    // g s(t): slope s + g s (1 - s) t', with t' = 1 or the cubic's; 1 - s(t) = s(-t) without
+    // cancellation
+    float t = g, gdt = g;
+    if (activation == BWGEMM_GELU_TANH) {
+        // past 30 the slope is 0 or 1, and the cubic's is kept from infinity times zero
+        const float c = g > 30.f ? 30.f : g < -30.f ? -30.f : g;
+        t = kGeluC * fmaf(kGeluC3 * c * c, c, c);
+        gdt = kGeluC * c * fmaf(3.f * kGeluC3 * c, c, 1.f);
+    }
+    const float s = logistic(t);
+    value = g * s;
+    slope = fmaf(gdt * s, logistic(-t), s);
+}
+
+}  // namespace bwgemm

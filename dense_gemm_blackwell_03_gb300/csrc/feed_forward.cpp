@@ -1,0 +1,693 @@
+// feed_forward.cpp -- argument checks, tensor maps and work division of the gated
+// feed-forward layer and of the 8-bit integer product.
+#include <cstring>
+
+#include "feed_forward.h"
+#include "operators_host.h"
+
+using namespace bwgemm;
+
+namespace {
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+uint64_t limit_ns(bwgemm_plan_t plan) { return plan->opts.timeout_ns ? plan->opts.timeout_ns : 4000000000ull; }
+
+// Whether the pointer is there (an absent matrix, or one without data, is none).
+bool present(const bwgemm_matrix_t* x) { return x && x->data; }
+
+bwgemm_status_t check_matrix(const bwgemm_matrix_t* x, int64_t rows, int64_t cols)
+{
+    if (!present(x) || x->ld < cols)
+        return BWGEMM_ERR_INVALID_ARG;
+    if (!extent_ok(rows, cols, x->ld))
+        return BWGEMM_ERR_UNSUPPORTED;
+    if (!aligned(x->data, 16) || x->ld % 8 != 0)
+        return BWGEMM_ERR_ALIGNMENT;
+    return BWGEMM_OK;
+}
+
+CUtensorMapDataType type16(int dtype)
+{
+    return dtype == BWGEMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
+// A 16-bit operand in boxes of 64 elements x box_rows, and in boxes of two whole
+// 64-element chunks (the same map again where its rows hold no two).
+bwgemm_status_t encode_operand16(CUtensorMap* map, CUtensorMap* map3, const void* data, int64_t ld, int dtype, int64_t rows,
+                                 int64_t cols, uint32_t box_rows)
+{
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
+    const cuuint32_t box[2] = {64, box_rows};
+    const bwgemm_status_t st = encode(map, type16(dtype), 2, data, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    if (st != BWGEMM_OK)
+        return st;
+    *map3 = *map;
+    const int64_t chunks = cols / 64;
+    if (chunks < 2)
+        return BWGEMM_OK;
+    const cuuint64_t dims3[3] = {64, cuuint64_t(rows), cuuint64_t(chunks)};
+    const cuuint64_t strides3[2] = {cuuint64_t(ld) * 2, 128};
+    const cuuint32_t box3[3] = {64, box_rows, 2};
+    return encode(map3, type16(dtype), 3, data, dims3, strides3, box3, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+bwgemm_status_t encode_result16(CUtensorMap* map, const bwgemm_matrix_t& x, int dtype, int64_t rows, int64_t cols)
+{
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(x.ld) * 2};
+    const cuuint32_t box[2] = {64, 32};
+    return encode(map, type16(dtype), 2, x.data, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE);
+}
+
+// ------------------------------------------------ work with the weights in the lanes
+struct LanesPlan {
+    int variant;      // of kLanesVariants
+    int workers;      // CTAs or pairs; 0: none
+    int l_rows, num_l, num_c, dp_tiles, sk_tiles, sk_iters, raster;
+    double us;
+};
+
+// Microseconds of 128 of K of a tile on its CTA or pair: the bytes' way into shared
+// memory (150 GB/s and SM), or the MMAs (M = 64 runs at half the rate of M = 128).
+double lanes_step_us(const LanesVariant& v, int l_rows)
+{
+    if (v.mode == kLanesGated)
+        return std::max((2.0 * l_rows + v.bn) * 256.0 / 150e3, 0.0043 * v.bn);
+    if (v.cg == 2)
+        return 0.56;
+    return std::max(0.14, (l_rows * 128.0 + v.bn * 256.0) / 150e3);
+}
+
+LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N, int64_t K,
+                     const bwgemm_plan_options_t* opts, uint64_t workspace_bytes)
+{
+    const int64_t kb = blocks_of(K);
+    const double weights = double(N) * double(K) * (mode == kLanesGated ? 4 : 1);
+    LanesPlan best = {};
+    for (int i = 0; i < kNumLanesVariants; ++i) {
+        const LanesVariant& v = kLanesVariants[i];
+        if (v.mode != mode)
+            continue;
+        const int W = v.cg == 2 ? capped(max_pairs, 2, opts) : capped(num_sms, 1, opts);
+        if (W < 1)
+            continue;
+        const int most = v.mode == kLanesGated ? 64 : 128 * v.cg;  // weight rows per tile
+        const int64_t nc = (M + v.bn - 1) / v.bn;
+        for (int low = 0; low <= (v.cg == 1 ? 1 : 0); ++low) {
+            LanesPlan s = {};
+            s.variant = i;
+            s.l_rows = most;
+            if (low) {  // tiles as high as makes them fill whole waves
+                const int64_t waves = ((N + most - 1) / most * nc + W - 1) / W;
+                const int64_t blocks = std::max<int64_t>(waves * W / nc, 1);
+                s.l_rows = int(std::min<int64_t>(most, round_up((N + blocks - 1) / blocks, 8)));
+            }
+            const int64_t nl = (N + s.l_rows - 1) / s.l_rows, tiles = nl * nc;
+            if (tiles > (1ll << 30))
+                continue;
+            s.num_l = int(nl);
+            s.num_c = int(nc);
+            // whole tiles, or whole tiles for the full waves and the rest in K steps over all
+            // workers, at least four a piece
+            const int64_t full = tiles / W * W, rest = tiles - full;
+            const uint64_t slot_bytes = uint64_t(lanes_partial_floats(mode, v.bn)) * 4 * v.cg;
+            const bool room = kCounterRegionBytes + uint64_t(W) * 2 * slot_bytes <= workspace_bytes &&
+                              uint64_t(rest) * v.cg * lanes_epi_warps(v.bn) * 4 <= kCounterRegionBytes;
+            for (int spread = 0; spread <= (rest > 0 && room && rest * kb < (1ll << 30) ? 1 : 0); ++spread) {
+                s.workers = int(std::min<int64_t>(tiles, W));
+                s.dp_tiles = int(tiles);
+                s.sk_tiles = s.sk_iters = 0;
+                if (spread) {
+                    s.dp_tiles = int(full);
+                    s.sk_tiles = int(rest);
+                    s.sk_iters = int(rest * kb);
+                    s.workers = full == 0 ? std::max(std::min(W, s.sk_iters / 4), 1) : W;
+                }
+                const double us = lanes_step_us(v, s.l_rows);
+                double t = double((s.dp_tiles + s.workers - 1) / s.workers) * double(kb) * us;
+                if (spread) {
+                    // a piece's partial tile out, the fence and the counter, and the pieces of
+                    // a tile in again by one CTA
+                    const double pieces = double(s.workers) / double(rest);
+                    t += double((s.sk_iters + s.workers - 1) / s.workers) * us;
+                    t += 4.0 + (1.0 + pieces) * double(slot_bytes) / v.cg / 200e3;
+                }
+                // the weights once from HBM, and again from L2 or HBM for every block of rows
+                t = std::max(t, weights / 6.5e6) + 0.1 * t;
+                if (best.workers == 0 || t < best.us) {
+                    s.us = t;
+                    best = s;
+                }
+            }
+        }
+    }
+    best.raster = best.num_c <= 2 ? std::max(best.num_l, 1) : std::min(8, best.num_l);
+    return best;
+}
+
+// ------------------------------------------------------------- tiles of products
+struct PairPlan {
+    int cg;
+    int64_t tiles;    // of all results
+    int64_t workers;  // CTAs or pairs; 0: none
+};
+
+// One gradient product: tiles of 256 on CTA pairs (1024 SM cycles per 128 of K, bound by
+// the MMAs) or of 128 on single CTAs (about 740, bound by the copies of both operands),
+// whichever takes fewer cycles in its waves; a deep K of few tiles in slices, whose join
+// costs a kernel more and the way of its bytes.  Fills in p's division of the work.
+PairPlan plan_pair(PairParams* p, int singles, int pairs, uint64_t workspace_bytes)
+{
+    PairPlan out = {};
+    int64_t tiles[3] = {}, best = 0;
+    const int64_t steps = int64_t(p->steps_k) * p->terms;
+    for (int g = 1; g <= 2; ++g) {
+        const int64_t workers = g == 2 ? pairs : singles;
+        if (workers < 1)
+            continue;
+        const int64_t r = (p->rows + 128 * g - 1) / (128 * g), c = (p->cols + 128 * g - 1) / (128 * g);
+        tiles[g] = r * c * p->results;
+        const int64_t room = (int64_t(workspace_bytes) - int64_t(kCounterRegionBytes)) / (g * g * 128 * 128 * 4);
+        const int64_t most = std::max<int64_t>(1, std::min(std::min(workers, room) / tiles[g], steps / 2));
+        for (int64_t splits = 1; splits <= most; ++splits) {
+            const int64_t cost = (tiles[g] * splits + workers - 1) / workers * ((steps + splits - 1) / splits) *
+                                     (g == 2 ? 1024 : 740) +
+                                 (splits > 1 ? 3000 + tiles[g] * splits * g * g * 65536 / 1250 : 0);
+            if (out.cg == 0 || cost < best) {
+                best = cost;
+                out.cg = g;
+                p->splits = int32_t(splits);
+            }
+        }
+    }
+    if (out.cg == 0 || tiles[out.cg] >= (1ll << 31))
+        return PairPlan{};
+    const int cg = out.cg;
+    for (p->join_share = 8;
+         p->join_share > 1 && (p->join_share > p->splits || tiles[cg] * cg * cg * 16 * p->join_share > 2048);)
+        p->join_share /= 2;
+    p->num_r = int32_t((p->rows + 128 * cg - 1) / (128 * cg));
+    p->num_c = int32_t((p->cols + 128 * cg - 1) / (128 * cg));
+    out.tiles = tiles[cg];
+    out.workers = std::min<int64_t>(tiles[cg] * p->splits, cg == 2 ? pairs : singles);
+    return out;
+}
+
+PairParams input_gradient_shape(int64_t M, int64_t N, int64_t K)
+{
+    PairParams p = {};
+    p.rows = int32_t(M);
+    p.cols = int32_t(K);
+    p.steps_k = int32_t(blocks_of(N));
+    p.terms = 2;
+    p.results = 1;
+    return p;
+}
+
+PairParams weight_gradient_shape(int64_t M, int64_t N, int64_t K)
+{
+    PairParams p = {};
+    p.rows = int32_t(N);
+    p.cols = int32_t(K);
+    p.steps_k = int32_t(blocks_of(M));
+    p.terms = 1;
+    p.results = 2;
+    return p;
+}
+
+// The gated layer's forward product in tiles of 256 rows of X x 128 of each weight on
+// CTA pairs.
+struct GatedPlan {
+    bool lanes;
+    LanesPlan l;
+    int64_t num_r, num_c;
+    int workers;
+};
+
+GatedPlan plan_gated(int num_sms, int max_pairs, int64_t M, int64_t N, int64_t K, const bwgemm_plan_options_t* opts,
+                     uint64_t workspace_bytes)
+{
+    GatedPlan g = {};
+    g.l = plan_lanes(kLanesGated, num_sms, max_pairs, M, N, K, opts, workspace_bytes);
+    g.num_r = (M + 255) / 256;
+    g.num_c = (N + 127) / 128;
+    const int pairs = capped(max_pairs, 2, opts);
+    g.lanes = true;
+    if (pairs < 1 || g.num_r * g.num_c >= (1ll << 31))
+        return g;
+    g.workers = int(std::min<int64_t>(g.num_r * g.num_c, pairs));
+    const double waves = double((g.num_r * g.num_c + pairs - 1) / pairs);
+    const double us = std::max(waves * double(blocks_of(K)) * 0.56 + 2.0, double(N) * double(K) * 4 / 6.5e6);
+    g.lanes = g.l.workers > 0 && g.l.us < us;
+    return g;
+}
+
+int pairs_of(bwgemm_plan_t plan) { return plan->max_active[find_variant(2, 256, false, 1)]; }
+
+bool dtype16(bwgemm_dtype_t dtype) { return dtype == BWGEMM_BF16 || dtype == BWGEMM_FP16; }
+
+bool known(bwgemm_activation_t a) { return a == BWGEMM_SILU || a == BWGEMM_GELU || a == BWGEMM_GELU_TANH; }
+
+bool fits(int64_t n) { return n <= (1ll << 31) - 256; }
+
+void take_lanes(LanesParams* p, const LanesPlan& s, bwgemm_plan_t plan, int64_t M, int64_t N, int64_t K)
+{
+    p->lrows = int32_t(N);
+    p->crows = int32_t(M);
+    p->K = int32_t(K);
+    p->num_kb = int32_t(blocks_of(K));
+    p->l_rows = s.l_rows / kLanesVariants[s.variant].cg;
+    p->num_l = s.num_l;
+    p->num_c = s.num_c;
+    p->raster_group = std::max(1, std::min(s.raster, s.num_l));
+    p->dp_tiles = s.dp_tiles;
+    p->sk_tiles = s.sk_tiles;
+    p->sk_iters = s.sk_iters;
+    p->timeout_ns = limit_ns(plan);
+    p->status = plan->d_status;
+    p->counters = reinterpret_cast<uint32_t*>(plan->d_workspace);
+    p->partials = reinterpret_cast<float*>(plan->d_workspace + kCounterRegionBytes);
+    p->stall_kblock = plan->opts.stall_kblock;
+}
+
+bwgemm_status_t zero(void* data, int64_t ld, int64_t rows, int64_t cols, int size, cudaStream_t s)
+{
+    if (rows == 0 || cols == 0)
+        return BWGEMM_OK;
+    return cudaMemset2DAsync(data, size_t(ld) * size, 0, size_t(cols) * size, size_t(rows), s) == cudaSuccess
+               ? BWGEMM_OK
+               : BWGEMM_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+bwgemm_status_t bwgemm_gated(bwgemm_plan_t plan, const bwgemm_matrix_t* X, const bwgemm_matrix_t* Wg,
+                             const bwgemm_matrix_t* Wu, const bwgemm_matrix_t* H, const bwgemm_matrix_t* G,
+                             const bwgemm_matrix_t* U, int64_t M, int64_t N, int64_t K, bwgemm_dtype_t dtype,
+                             bwgemm_activation_t activation, void* stream)
+{
+    if (!plan || M < 0 || N < 0 || K < 0 || !dtype16(dtype) || !known(activation) || present(G) != present(U))
+        return BWGEMM_ERR_INVALID_ARG;
+    if (!fits(M) || !fits(N) || !fits(K))
+        return BWGEMM_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0)
+        return BWGEMM_OK;
+    bwgemm_status_t st;
+    const bool keep = present(G);
+    const bwgemm_matrix_t* out[3] = {H, keep ? G : nullptr, keep ? U : nullptr};
+    for (int i = 0; i < (keep ? 3 : 1); ++i)
+        if ((st = check_matrix(out[i], M, N)) != BWGEMM_OK)
+            return st;
+    if (K > 0 && ((st = check_matrix(X, M, K)) != BWGEMM_OK || (st = check_matrix(Wg, N, K)) != BWGEMM_OK ||
+                  (st = check_matrix(Wu, N, K)) != BWGEMM_OK))
+        return st;
+    DeviceGuard guard(plan->device);
+    if (!guard.ok)
+        return BWGEMM_ERR_CUDA;
+    if ((st = check_resident({H->data, keep ? G->data : nullptr, keep ? U->data : nullptr, K ? X->data : nullptr,
+                              K ? Wg->data : nullptr, K ? Wu->data : nullptr}, plan->device)) != BWGEMM_OK)
+        return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (K == 0) {  // empty sums: act(0) * 0
+        for (int i = 0; i < (keep ? 3 : 1); ++i)
+            if ((st = zero(out[i]->data, out[i]->ld, M, N, 2, s)) != BWGEMM_OK)
+                return st;
+        return BWGEMM_OK;
+    }
+    const bool pdl = plan->opts.pdl_off == 0;
+    const GatedPlan sel = plan_gated(plan->num_sms, pairs_of(plan), M, N, K, &plan->opts, plan->workspace_bytes);
+    if (sel.lanes) {
+        if (sel.l.workers == 0)
+            return BWGEMM_ERR_UNSUPPORTED;
+        const LanesVariant& v = kLanesVariants[sel.l.variant];
+        LanesParams p = {};
+        take_lanes(&p, sel.l, plan, M, N, K);
+        p.l_chunks = p.c_chunks = int32_t(K / 64);
+        p.dtype = p.out_type = dtype;
+        p.activation = activation;
+        for (int i = 0; i < (keep ? 3 : 1); ++i) {
+            p.out[i] = out[i]->data;
+            p.ldo[i] = out[i]->ld;
+        }
+        LanesMaps maps;
+        if ((st = encode_operand16(&maps.w, &maps.w3, Wg->data, Wg->ld, dtype, N, K, uint32_t(p.l_rows))) != BWGEMM_OK ||
+            (st = encode_operand16(&maps.w2, &maps.w23, Wu->data, Wu->ld, dtype, N, K, uint32_t(p.l_rows))) != BWGEMM_OK ||
+            (st = encode_operand16(&maps.x, &maps.x3, X->data, X->ld, dtype, M, K, uint32_t(v.bn))) != BWGEMM_OK)
+            return st;
+        if (launch_lanes(sel.l.variant, maps, p, sel.l.workers, s, pdl) != cudaSuccess)
+            return BWGEMM_ERR_CUDA;
+        plan->launches += 1;
+        return BWGEMM_OK;
+    }
+    PairParams p = {};
+    p.rows = int32_t(M);
+    p.cols = int32_t(N);
+    p.steps_k = int32_t(blocks_of(K));
+    p.terms = p.results = p.splits = p.join_share = 1;
+    p.chunks_a = p.chunks_b = int32_t(K / 64);
+    p.num_r = int32_t(sel.num_r);
+    p.num_c = int32_t(sel.num_c);
+    p.dtype = dtype;
+    p.activation = activation;
+    p.timeout_ns = limit_ns(plan);
+    p.status = plan->d_status;
+    p.stall_kblock = plan->opts.stall_kblock;
+    PairMaps maps;
+    if ((st = encode_operand16(&maps.a[0], &maps.a3[0], X->data, X->ld, dtype, M, K, 128)) != BWGEMM_OK ||
+        (st = encode_operand16(&maps.b[0], &maps.b3[0], Wg->data, Wg->ld, dtype, N, K, 128)) != BWGEMM_OK ||
+        (st = encode_operand16(&maps.b[1], &maps.b3[1], Wu->data, Wu->ld, dtype, N, K, 128)) != BWGEMM_OK)
+        return st;
+    maps.a[1] = maps.a[0];
+    maps.a3[1] = maps.a3[0];
+    for (int i = 0; i < 3; ++i) {
+        if (!out[i]) {
+            maps.out[i] = maps.out[0];
+            continue;
+        }
+        if ((st = encode_result16(&maps.out[i], *out[i], dtype, M, N)) != BWGEMM_OK)
+            return st;
+        p.out[i] = static_cast<uint16_t*>(out[i]->data);
+        p.ldo[i] = out[i]->ld;
+    }
+    if (launch_pair(kPairGated, 2, maps, p, 2 * sel.workers, s, pdl) != cudaSuccess)
+        return BWGEMM_ERR_CUDA;
+    plan->launches += 1;
+    return BWGEMM_OK;
+}
+
+bwgemm_status_t bwgemm_gated_backward_workspace(int64_t M, int64_t N, uint64_t* bytes)
+{
+    if (!bytes)
+        return BWGEMM_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (M < 0 || N < 0)
+        return BWGEMM_ERR_INVALID_ARG;
+    if (!fits(M) || !fits(N))
+        return BWGEMM_ERR_UNSUPPORTED;
+    *bytes = 2 * uint64_t(round_up(M * round_up(N, 8) * 2, 256));
+    return BWGEMM_OK;
+}
+
+bwgemm_status_t bwgemm_gated_backward(bwgemm_plan_t plan, const bwgemm_matrix_t* dH, const bwgemm_matrix_t* G,
+                                      const bwgemm_matrix_t* U, const bwgemm_matrix_t* X, const bwgemm_matrix_t* Wg,
+                                      const bwgemm_matrix_t* Wu, const bwgemm_matrix_t* dX, const bwgemm_matrix_t* dWg,
+                                      const bwgemm_matrix_t* dWu, int64_t M, int64_t N, int64_t K, bwgemm_dtype_t dtype,
+                                      bwgemm_activation_t activation, void* workspace, uint64_t workspace_bytes,
+                                      void* stream)
+{
+    if (!plan || M < 0 || N < 0 || K < 0 || !dtype16(dtype) || !known(activation))
+        return BWGEMM_ERR_INVALID_ARG;
+    if (!fits(M) || !fits(N) || !fits(K))
+        return BWGEMM_ERR_UNSUPPORTED;
+    // results without elements need no memory
+    const bool of_x = present(dX) && M > 0 && K > 0, of_w = (present(dWg) || present(dWu)) && N > 0 && K > 0;
+    if (!of_x && !of_w)
+        return BWGEMM_OK;
+    bwgemm_status_t st;
+    if (of_x && (st = check_matrix(dX, M, K)) != BWGEMM_OK)
+        return st;
+    if (of_w && ((st = check_matrix(dWg, N, K)) != BWGEMM_OK || (st = check_matrix(dWu, N, K)) != BWGEMM_OK))
+        return st;
+    const bool sums = M > 0 && N > 0;  // else empty ones
+    uint64_t need = 0;
+    if (sums) {
+        for (const bwgemm_matrix_t* x : {dH, G, U})
+            if ((st = check_matrix(x, M, N)) != BWGEMM_OK)
+                return st;
+        if (of_x && ((st = check_matrix(Wg, N, K)) != BWGEMM_OK || (st = check_matrix(Wu, N, K)) != BWGEMM_OK))
+            return st;
+        if (of_w && (st = check_matrix(X, M, K)) != BWGEMM_OK)
+            return st;
+        bwgemm_gated_backward_workspace(M, N, &need);
+        if (!workspace)
+            return BWGEMM_ERR_INVALID_ARG;
+        if (!aligned(workspace, 256))
+            return BWGEMM_ERR_ALIGNMENT;
+        if (workspace_bytes < need)
+            return BWGEMM_ERR_WORKSPACE;
+    }
+    DeviceGuard guard(plan->device);
+    if (!guard.ok)
+        return BWGEMM_ERR_CUDA;
+    auto at = [](bool read, const bwgemm_matrix_t* x) { return read ? x->data : nullptr; };
+    if ((st = check_resident({at(of_x, dX), at(of_w, dWg), at(of_w, dWu), at(sums, dH), at(sums, G), at(sums, U),
+                              at(sums && of_w, X), at(sums && of_x, Wg), at(sums && of_x, Wu), sums ? workspace : nullptr},
+                             plan->device)) != BWGEMM_OK)
+        return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!sums) {
+        if (of_x && (st = zero(dX->data, dX->ld, M, K, 2, s)) != BWGEMM_OK)
+            return st;
+        if (of_w && ((st = zero(dWg->data, dWg->ld, N, K, 2, s)) != BWGEMM_OK ||
+                     (st = zero(dWu->data, dWu->ld, N, K, 2, s)) != BWGEMM_OK))
+            return st;
+        return BWGEMM_OK;
+    }
+    const bool pdl = plan->opts.pdl_off == 0;
+    const int64_t ldd = round_up(N, 8);
+    uint16_t* const d[2] = {static_cast<uint16_t*>(workspace),
+                            reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + need / 2)};
+    // both divisions before the first launch: a size without one launches nothing
+    PairParams px = input_gradient_shape(M, N, K), pw = weight_gradient_shape(M, N, K);
+    const int singles = capped(plan->num_sms, 1, &plan->opts), pairs = capped(pairs_of(plan), 2, &plan->opts);
+    const PairPlan sx = plan_pair(&px, singles, pairs, plan->workspace_bytes);
+    const PairPlan sw = plan_pair(&pw, singles, pairs, plan->workspace_bytes);
+    if ((of_x && sx.workers == 0) || (of_w && sw.workers == 0))
+        return BWGEMM_ERR_UNSUPPORTED;
+
+    GateGradParams gg = {};
+    gg.dh = static_cast<const uint16_t*>(dH->data);
+    gg.g = static_cast<const uint16_t*>(G->data);
+    gg.u = static_cast<const uint16_t*>(U->data);
+    gg.lddh = dH->ld;
+    gg.ldg = G->ld;
+    gg.ldu = U->ld;
+    gg.dg = d[0];
+    gg.du = d[1];
+    gg.ldd = ldd;
+    gg.rows = M;
+    gg.cols = N;
+    gg.dtype = dtype;
+    gg.activation = activation;
+    PairMaps mx, mw;
+    // dG and dU: rows of tokens, K-major in the first product, stored K x rows in the second
+    CUtensorMap dm[2], dm3[2];
+    for (int i = 0; i < 2; ++i)
+        if ((st = encode_operand16(&dm[i], &dm3[i], d[i], ldd, dtype, M, N, 128)) != BWGEMM_OK)
+            return st;
+    for (PairParams* p : {&px, &pw}) {
+        p->chunks_a = int32_t(N / 64);
+        p->chunks_b = int32_t(K / 64);
+        p->dtype = dtype;
+        p->partials = reinterpret_cast<float*>(plan->d_workspace + kCounterRegionBytes);
+        p->timeout_ns = limit_ns(plan);
+        p->status = plan->d_status;
+        p->stall_kblock = plan->opts.stall_kblock;
+    }
+    if (of_x) {
+        for (int i = 0; i < 2; ++i) {
+            const bwgemm_matrix_t& w = *(i ? Wu : Wg);
+            mx.a[i] = dm[i];
+            mx.a3[i] = dm3[i];
+            if ((st = encode_operand16(&mx.b[i], &mx.b3[i], w.data, w.ld, dtype, N, K, 128)) != BWGEMM_OK)
+                return st;
+        }
+        if ((st = encode_result16(&mx.out[0], *dX, dtype, M, K)) != BWGEMM_OK)
+            return st;
+        mx.out[1] = mx.out[2] = mx.out[0];
+        px.out[0] = static_cast<uint16_t*>(dX->data);
+        px.ldo[0] = dX->ld;
+    }
+    if (of_w) {
+        for (int i = 0; i < 2; ++i) {
+            const bwgemm_matrix_t& w = *(i ? dWu : dWg);
+            mw.a[i] = dm[i];
+            mw.a3[i] = dm3[i];
+            if ((st = encode_operand16(&mw.b[i], &mw.b3[i], X->data, X->ld, dtype, M, K, 128)) != BWGEMM_OK ||
+                (st = encode_result16(&mw.out[i], w, dtype, N, K)) != BWGEMM_OK)
+                return st;
+            pw.out[i] = static_cast<uint16_t*>(w.data);
+            pw.ldo[i] = w.ld;
+        }
+        mw.out[2] = mw.out[0];
+    }
+    if (launch_gate_grad(gg, s, pdl) != cudaSuccess)
+        return BWGEMM_ERR_CUDA;
+    plan->launches += 1;
+    if (of_x) {
+        if (launch_pair(kPairInput, sx.cg, mx, px, int(sx.workers) * sx.cg, s, pdl) != cudaSuccess)
+            return BWGEMM_ERR_CUDA;
+        plan->launches += px.splits > 1 ? 2 : 1;
+    }
+    if (of_w) {
+        if (launch_pair(kPairWeight, sw.cg, mw, pw, int(sw.workers) * sw.cg, s, pdl) != cudaSuccess)
+            return BWGEMM_ERR_CUDA;
+        plan->launches += pw.splits > 1 ? 2 : 1;
+    }
+    return BWGEMM_OK;
+}
+
+bwgemm_status_t bwgemm_quantize_integer(bwgemm_plan_t plan, const void* X, bwgemm_dtype_t dtype, int64_t rows,
+                                     int64_t cols, int64_t ldx, int8_t* q, int64_t ldq, float* scales, void* stream)
+{
+    if (!plan || (!dtype16(dtype) && dtype != BWGEMM_FP32) || rows < 0 || cols < 0)
+        return BWGEMM_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0)
+        return BWGEMM_OK;
+    if (!X || !q || !scales || ldx < cols || ldq < cols)
+        return BWGEMM_ERR_INVALID_ARG;
+    if (!extent_ok(rows, cols, ldx) || !extent_ok(rows, cols, ldq))
+        return BWGEMM_ERR_UNSUPPORTED;
+    if (!aligned(X, 16) || ldx * element_size(dtype) % 16 != 0 || !aligned(q, 16) || ldq % 16 != 0 || !aligned(scales, 4))
+        return BWGEMM_ERR_ALIGNMENT;
+    DeviceGuard guard(plan->device);
+    if (!guard.ok)
+        return BWGEMM_ERR_CUDA;
+    const bwgemm_status_t st = check_resident({X, q, scales}, plan->device);
+    if (st != BWGEMM_OK)
+        return st;
+    const RowsInt8Params p = {X, ldx, rows, cols, q, ldq, scales};
+    if (launch_quantize_int8(dtype, p, static_cast<cudaStream_t>(stream), plan->opts.pdl_off == 0) != cudaSuccess)
+        return BWGEMM_ERR_CUDA;
+    plan->launches += 1;
+    return BWGEMM_OK;
+}
+
+bwgemm_status_t bwgemm_run_integer_workspace(int64_t M, int64_t N, int64_t K, uint64_t* bytes)
+{
+    if (!bytes)
+        return BWGEMM_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (M < 0 || N < 0 || K < 0)
+        return BWGEMM_ERR_INVALID_ARG;
+    if (!fits(M) || !fits(N) || !fits(K))
+        return BWGEMM_ERR_UNSUPPORTED;
+    if (M > 0 && N > 0 && K > 0)
+        *bytes = uint64_t(round_up(M * round_up(K, 128) * 2, 256));  // A as fp16
+    return BWGEMM_OK;
+}
+
+bwgemm_status_t bwgemm_run_integer(bwgemm_plan_t plan, const int8_t* A, const float* scale_a, const int8_t* B,
+                                const float* scale_b, void* C, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
+                                int64_t ldc, bwgemm_dtype_t out, void* workspace, uint64_t workspace_bytes, void* stream)
+{
+    if (!plan || M < 0 || N < 0 || K < 0 || (!dtype16(out) && out != BWGEMM_FP32))
+        return BWGEMM_ERR_INVALID_ARG;
+    uint64_t need = 0;
+    bwgemm_status_t st = bwgemm_run_integer_workspace(M, N, K, &need);
+    if (st != BWGEMM_OK || M == 0 || N == 0)
+        return st;
+    const int es = element_size(out);
+    if (!C || ldc < N || (K > 0 && (!A || !B || !scale_a || !scale_b || lda < K || ldb < K)) || (need > 0 && !workspace))
+        return BWGEMM_ERR_INVALID_ARG;
+    if (!extent_ok(M, N, ldc) || (K > 0 && (!extent_ok(M, K, lda) || !extent_ok(N, K, ldb))))
+        return BWGEMM_ERR_UNSUPPORTED;
+    if (!aligned(C, 16) || ldc * es % 16 != 0 ||
+        (K > 0 && (!aligned(A, 16) || lda % 16 != 0 || !aligned(B, 16) || ldb % 16 != 0 || !aligned(scale_a, 4) ||
+                   !aligned(scale_b, 4) || !aligned(workspace, 256))))
+        return BWGEMM_ERR_ALIGNMENT;
+    if (workspace_bytes < need)
+        return BWGEMM_ERR_WORKSPACE;
+    DeviceGuard guard(plan->device);
+    if (!guard.ok)
+        return BWGEMM_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (K == 0) {
+        if ((st = check_resident({C}, plan->device)) != BWGEMM_OK)
+            return st;
+        return zero(C, ldc, M, N, es, s);
+    }
+    if ((st = check_resident({A, scale_a, B, scale_b, C, workspace}, plan->device)) != BWGEMM_OK)
+        return st;
+    const bool pdl = plan->opts.pdl_off == 0;
+    const LanesPlan sel = plan_lanes(kLanesInt8, plan->num_sms, pairs_of(plan), M, N, K, &plan->opts, plan->workspace_bytes);
+    if (sel.workers == 0)
+        return BWGEMM_ERR_UNSUPPORTED;
+    const LanesVariant& v = kLanesVariants[sel.variant];
+    const int64_t ldy = round_up(K, 128);
+    LanesParams p = {};
+    take_lanes(&p, sel, plan, M, N, K);
+    p.c_chunks = int32_t(ldy / 64);
+    p.ls = scale_b;
+    p.cs = scale_a;
+    p.dtype = BWGEMM_FP16;
+    p.out_type = out;
+    p.out[0] = C;
+    p.ldo[0] = ldc;
+    LanesMaps maps;
+    const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(N)};
+    const cuuint64_t strides[1] = {cuuint64_t(ldb)};
+    const cuuint32_t box[2] = {128, uint32_t(p.l_rows)};
+    if ((st = encode(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, B, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B)) != BWGEMM_OK ||
+        (st = encode_operand16(&maps.x, &maps.x3, workspace, ldy, BWGEMM_FP16, M, ldy, uint32_t(v.bn / v.cg))) != BWGEMM_OK)
+        return st;
+    maps.w2 = maps.w3 = maps.w23 = maps.w;
+    const WidenParams wp = {A, lda, int32_t(M), int32_t(K), static_cast<uint16_t*>(workspace), ldy};
+    if (launch_widen(wp, s, pdl) != cudaSuccess)
+        return BWGEMM_ERR_CUDA;
+    plan->launches += 1;
+    if (launch_lanes(sel.variant, maps, p, sel.workers * v.cg, s, pdl) != cudaSuccess)
+        return BWGEMM_ERR_CUDA;
+    plan->launches += 1;
+    return BWGEMM_OK;
+}
+
+bwgemm_status_t bwgemm_select_gated(int32_t num_sms, int32_t max_pairs, int64_t M, int64_t N, int64_t K,
+                                    const bwgemm_plan_options_t* opts, bwgemm_lanes_config_t* out)
+{
+    if (!out || num_sms < 1 || max_pairs < 0 || M < 1 || N < 1 || K < 1)
+        return BWGEMM_ERR_INVALID_ARG;
+    if (!fits(M) || !fits(N) || !fits(K))
+        return BWGEMM_ERR_UNSUPPORTED;
+    const GatedPlan g = plan_gated(num_sms, max_pairs ? max_pairs : num_sms / 2, M, N, K, opts, workspace_of(opts));
+    if (g.lanes && g.l.workers == 0)
+        return BWGEMM_ERR_UNSUPPORTED;
+    if (g.lanes)
+        *out = {1, g.l.l_rows, kLanesVariants[g.l.variant].bn, g.l.dp_tiles, g.l.sk_tiles, g.l.workers};
+    else
+        *out = {0, 128, 256, int32_t(g.num_r * g.num_c), 0, g.workers};
+    return BWGEMM_OK;
+}
+
+bwgemm_status_t bwgemm_select_integer(int32_t num_sms, int32_t max_pairs, int64_t M, int64_t N, int64_t K,
+                                   const bwgemm_plan_options_t* opts, bwgemm_lanes_config_t* out)
+{
+    if (!out || num_sms < 1 || max_pairs < 0 || M < 1 || N < 1 || K < 1)
+        return BWGEMM_ERR_INVALID_ARG;
+    if (!fits(M) || !fits(N) || !fits(K))
+        return BWGEMM_ERR_UNSUPPORTED;
+    const LanesPlan s =
+        plan_lanes(kLanesInt8, num_sms, max_pairs ? max_pairs : num_sms / 2, M, N, K, opts, workspace_of(opts));
+    if (s.workers == 0)
+        return BWGEMM_ERR_UNSUPPORTED;
+    *out = {1, s.l_rows, kLanesVariants[s.variant].bn, s.dp_tiles, s.sk_tiles, s.workers};
+    return BWGEMM_OK;
+}
+
+bwgemm_status_t bwgemm_select_gated_backward(int32_t num_sms, int32_t max_pairs, int64_t M, int64_t N, int64_t K,
+                                             const bwgemm_plan_options_t* opts, bwgemm_ortho_config_t out[2])
+{
+    if (!out || num_sms < 1 || max_pairs < 0 || M < 1 || N < 1 || K < 1)
+        return BWGEMM_ERR_INVALID_ARG;
+    if (!fits(M) || !fits(N) || !fits(K))
+        return BWGEMM_ERR_UNSUPPORTED;
+    for (int i = 0; i < 2; ++i) {
+        PairParams p = i ? weight_gradient_shape(M, N, K) : input_gradient_shape(M, N, K);
+        const PairPlan s = plan_pair(&p, capped(num_sms, 1, opts), capped(max_pairs ? max_pairs : num_sms / 2, 2, opts),
+                                     workspace_of(opts));
+        if (s.workers == 0)
+            return BWGEMM_ERR_UNSUPPORTED;
+        out[i] = {pair_tile(s.cg), p.splits, s.tiles, int32_t(s.workers)};
+    }
+    return BWGEMM_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,131 @@
+// gated_sm103.cu -- the gated feed-forward layer's large products (pair_kernel.cuh), and
+// the gradients of its two projections.
+#include "pair_kernel.cuh"
+
+namespace bwgemm {
+namespace {
+
+template <int CG, int FORM>
+cudaError_t launch_form(const PairMaps& maps, const PairParams& p, int grid, cudaStream_t stream, bool pdl)
+{
+    using Cfg = OrthoConfig<CG>;
+    auto kernel = pair_kernel<CG, FORM>;
+    if (grid % CG != 0)
+        return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_smem(kernel, Cfg::kSmemBytes, allowed);
+    if (err != cudaSuccess)
+        return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid), 1, 1);
+    cfg.blockDim = dim3(Cfg::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (CG == 2) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = 2;
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    err = cudaLaunchKernelEx(&cfg, kernel, maps, p);
+    if (err != cudaSuccess || p.splits == 1)
+        return err;
+    cudaLaunchConfig_t join = {};
+    join.gridDim = dim3(unsigned(CG * 8 * Cfg::kCols / 4 / kJoinWarps * p.join_share),
+                        unsigned(p.num_r * p.num_c * p.results), 1);
+    join.blockDim = dim3(32 * kJoinWarps, 1, 1);
+    join.stream = stream;
+    join.attrs = pdl ? attr + n - 1 : nullptr;  // the dependency's
+    join.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&join, pair_join_kernel<CG>, p);
+}
+
+// dU = dH act(G), dG = dH U act'(G): three reads and two writes of rows x cols, eight
+// values a thread.  Bound by HBM.
+constexpr int kGradThreads = 256;
+
+__device__ __forceinline__ float2 unpack16(uint32_t w, int dtype)
+{
+    return dtype == BWGEMM_BF16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w))
+                                : __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+__global__ void __launch_bounds__(kGradThreads) gate_grad_kernel(const GateGradParams p)
+{
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    const int64_t per_row = (p.cols + 7) / 8, pieces = per_row * p.rows;
+    const int64_t step = int64_t(gridDim.x) * kGradThreads;
+#pragma unroll 1
+    for (int64_t i = int64_t(blockIdx.x) * kGradThreads + threadIdx.x; i < pieces; i += step) {
+        const int64_t row = i / per_row, col = (i - row * per_row) * 8;
+        uint4 dh, g, u, dg, du;
+        if (col + 8 <= p.cols) {
+            dh = ptx::ld_global_cg_v4(p.dh + row * p.lddh + col);
+            g = ptx::ld_global_cg_v4(p.g + row * p.ldg + col);
+            u = ptx::ld_global_cg_v4(p.u + row * p.ldu + col);
+        } else {  // nothing is read past a row's end
+            dh = g = u = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int k = 0; k < 7; ++k)
+                if (col + k < p.cols) {
+                    reinterpret_cast<uint16_t*>(&dh)[k] = p.dh[row * p.lddh + col + k];
+                    reinterpret_cast<uint16_t*>(&g)[k] = p.g[row * p.ldg + col + k];
+                    reinterpret_cast<uint16_t*>(&u)[k] = p.u[row * p.ldu + col + k];
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 fh = unpack16((&dh.x)[k], p.dtype), fg = unpack16((&g.x)[k], p.dtype), fu = unpack16((&u.x)[k], p.dtype);
+            float2 value, slope;
+            activate_slope(fg.x, p.activation, value.x, slope.x);
+            activate_slope(fg.y, p.activation, value.y, slope.y);
+            (&dg.x)[k] = pack2(__float_as_uint(fh.x * fu.x * slope.x), __float_as_uint(fh.y * fu.y * slope.y), p.dtype);
+            (&du.x)[k] = pack2(__float_as_uint(fh.x * value.x), __float_as_uint(fh.y * value.y), p.dtype);
+        }
+        // the workspace's rows are whole pieces: what lies past the end is not read as a value
+        *reinterpret_cast<uint4*>(p.dg + row * p.ldd + col) = dg;
+        *reinterpret_cast<uint4*>(p.du + row * p.ldd + col) = du;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_pair(int form, int cg, const PairMaps& maps, const PairParams& p, int grid, cudaStream_t stream, bool pdl)
+{
+    switch (form * 2 + (cg - 1)) {
+    case kPairGated * 2 + 1: return launch_form<2, kPairGated>(maps, p, grid, stream, pdl);
+    case kPairInput * 2: return launch_form<1, kPairInput>(maps, p, grid, stream, pdl);
+    case kPairInput * 2 + 1: return launch_form<2, kPairInput>(maps, p, grid, stream, pdl);
+    case kPairWeight * 2: return launch_form<1, kPairWeight>(maps, p, grid, stream, pdl);
+    case kPairWeight * 2 + 1: return launch_form<2, kPairWeight>(maps, p, grid, stream, pdl);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_gate_grad(const GateGradParams& p, cudaStream_t stream, bool pdl)
+{
+    const int64_t pieces = (p.cols + 7) / 8 * p.rows;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>((pieces + kGradThreads - 1) / kGradThreads, 1 << 20)), 1, 1);
+    cfg.blockDim = dim3(kGradThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, gate_grad_kernel, p);
+}
+
+}  // namespace bwgemm

@@ -1,0 +1,251 @@
+// int8_sm103.cu -- rows to 8-bit integers with a scale each, and 8-bit integers to the
+// fp16 operand of their product.
+//
+// quantize_int8: a = max(max |x|, 2^-100) of the row, scale = a / 127, q = 127 x / a rounded
+// to the nearest integer, ties to the even one.  The quotient is decided exactly: x times
+// the fp32 reciprocal is within 8e-6 of it, so only a value within 1e-4 of the middle of two
+// integers is in doubt, and for that the two sides of the comparison, 254 |x| and (2 L + 1) a,
+// are formed in fp64, where both are exact (8 and 24 bits).
+//
+// Bound by HBM: a row is read once, held in registers between the maximum and the
+// rounding (up to 8 pieces of 16 bytes a thread; what a longer row has beyond that is
+// read again, from L2), by a warp, 128 or 512 threads according to its length.
+#include <type_traits>
+
+#include "feed_forward.h"
+#include "lanes_kernel.cuh"
+
+namespace bwgemm {
+namespace {
+
+constexpr float kMagic = 12582912.f;  // 1.5 2^23: a sum with it holds the rounded integer in its low bits
+constexpr int kHeld = 8;              // pieces a thread holds
+
+template <typename T>
+struct Piece {
+    static constexpr int kN = 16 / sizeof(T);  // elements of 16 bytes
+    uint4 w;
+
+    __device__ __forceinline__ void load(const T* row, int64_t c, int64_t cols)
+    {
+        if (c + kN <= cols) {
+            w = ptx::ld_global_cg_v4(row + c);
+        } else {  // nothing is read past the row's end
+            w = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int i = 0; i < kN - 1; ++i)
+                if (c + i < cols)
+                    reinterpret_cast<T*>(&w)[i] = row[c + i];
+        }
+    }
+    // the bits of the largest magnitude as fp32 (integers compare like magnitudes, NaN
+    // above infinity)
+    __device__ __forceinline__ uint32_t top() const
+    {
+        if constexpr (std::is_same<T, float>::value) {
+            const uint32_t m = 0x7FFFFFFFu;
+            return max(max(w.x & m, w.y & m), max(w.z & m, w.w & m));
+        } else {
+            // both halves of a word at once
+            using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+            const T2* v = reinterpret_cast<const T2*>(&w);
+            const T2 a = __hmax2_nan(__hmax2_nan(__habs2(v[0]), __habs2(v[1])), __hmax2_nan(__habs2(v[2]), __habs2(v[3])));
+            return max(__float_as_uint(fabsf(__low2float(a))), __float_as_uint(fabsf(__high2float(a))));
+        }
+    }
+    __device__ __forceinline__ float operator[](int i) const
+    {
+        const uint32_t h = (&w.x)[std::is_same<T, float>::value ? i : i / 2];
+        if constexpr (std::is_same<T, float>::value)
+            return __uint_as_float(h);
+        else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+            return __uint_as_float(i & 1 ? h & 0xFFFF0000u : h << 16);
+        else
+            return __half2float(__ushort_as_half(uint16_t(i & 1 ? h >> 16 : h)));
+    }
+};
+
+// 127 x / a rounded exactly, where fp32 leaves it open.
+static __device__ __noinline__ int round_exactly(float x, float a, float near)
+{
+    const float low = floorf(fabsf(near));
+    const double left = 254.0 * double(fabsf(x)), right = double(2.f * low + 1.f) * double(a);
+    const int l = int(low);
+    const int r = left > right || (left == right && (l & 1)) ? l + 1 : l;
+    return x < 0.f ? -r : r;
+}
+
+// One row by TR threads of the block; ROWS rows per block.
+template <typename T, int TR, int ROWS>
+__global__ void __launch_bounds__(TR* ROWS) quantize_rows_kernel(const RowsInt8Params p)
+{
+    using P = Piece<T>;
+    __shared__ uint32_t tops[TR > 32 ? TR / 32 : 1];
+    const int t = TR == 32 ? int(threadIdx.x & 31) : int(threadIdx.x);
+    const int64_t row = int64_t(blockIdx.x) * ROWS + (TR == 32 ? threadIdx.x >> 5 : 0);
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    if (TR == 32 && row >= p.rows)
+        return;
+    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+    P held[kHeld];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int64_t c = int64_t(i * TR + t) * P::kN;
+        held[i].w = make_uint4(0u, 0u, 0u, 0u);
+        if (c < p.cols)
+            held[i].load(x, c, p.cols);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        top = max(top, held[i].top());
+#pragma unroll 4
+    for (int64_t c = int64_t(kHeld * TR + t) * P::kN; c < p.cols; c += TR * P::kN) {
+        P v;
+        v.load(x, c, p.cols);
+        top = max(top, v.top());
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if constexpr (TR > 32) {
+        if ((t & 31) == 0)
+            tops[t >> 5] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < TR / 32; ++i)
+            top = max(top, tops[i]);
+    }
+    const bool finite = top < 0x7F800000u;
+    const float a = fmaxf(__uint_as_float(top), kSmallestAmax);
+    const float up = finite ? 127.f / a : 0.f;
+    if (t == 0)
+        p.scales[row] = finite ? a / 127.f : __uint_as_float(0x7FC00000u);
+    int8_t* q = p.q + row * p.ldq;
+    auto put = [&](const P& v, int64_t c) {
+        uint32_t bits[P::kN];
+        float worst = 0.f;
+#pragma unroll
+        for (int i = 0; i < P::kN; ++i) {
+            const float f = fmaf(v[i], up, kMagic);
+            worst = fmaxf(worst, fabsf(fmaf(v[i], up, -(f - kMagic))));
+            bits[i] = __float_as_uint(f);
+        }
+        if (worst > 0.4999f) {
+#pragma unroll
+            for (int i = 0; i < P::kN; ++i) {
+                const float near = v[i] * up;
+                if (fabsf(near - rintf(near)) > 0.4999f)
+                    bits[i] = uint32_t(round_exactly(v[i], a, near));
+            }
+        }
+        uint32_t w[P::kN / 4];
+#pragma unroll
+        for (int i = 0; i < P::kN / 4; ++i)
+            w[i] = finite ? __byte_perm(__byte_perm(bits[4 * i], bits[4 * i + 1], 0x0040),
+                                        __byte_perm(bits[4 * i + 2], bits[4 * i + 3], 0x0040), 0x5410)
+                          : 0u;
+        if (c + P::kN <= p.cols) {
+            if constexpr (P::kN == 8)
+                *reinterpret_cast<uint2*>(q + c) = make_uint2(w[0], w[1]);
+            else
+                *reinterpret_cast<uint32_t*>(q + c) = w[0];
+        } else {
+#pragma unroll
+            for (int i = 0; i < P::kN - 1; ++i)
+                if (c + i < p.cols)
+                    q[c + i] = int8_t(w[i / 4] >> (8 * (i % 4)));
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int64_t c = int64_t(i * TR + t) * P::kN;
+        if (c < p.cols)
+            put(held[i], c);
+    }
+#pragma unroll 1
+    for (int64_t c = int64_t(kHeld * TR + t) * P::kN; c < p.cols; c += TR * P::kN) {
+        P v;
+        v.load(x, c, p.cols);
+        put(v, c);
+    }
+}
+
+template <typename Kernel, typename Params>
+cudaError_t launch_plain(Kernel kernel, unsigned grid, unsigned threads, const Params& p, cudaStream_t stream, bool pdl)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <typename T>
+cudaError_t launch_rows(const RowsInt8Params& p, cudaStream_t stream, bool pdl)
+{
+    const int64_t pieces = (p.cols + Piece<T>::kN - 1) / Piece<T>::kN;
+    if (pieces <= 32 * 4)
+        return launch_plain(quantize_rows_kernel<T, 32, 4>, unsigned((p.rows + 3) / 4), 128, p, stream, pdl);
+    if (pieces <= 128 * kHeld)
+        return launch_plain(quantize_rows_kernel<T, 128, 1>, unsigned(p.rows), 128, p, stream, pdl);
+    return launch_plain(quantize_rows_kernel<T, 512, 1>, unsigned(p.rows), 512, p, stream, pdl);
+}
+
+// Sixteen values a thread; the pad to whole stages of 128 is zeros.
+constexpr int kWidenThreads = 256;
+
+__global__ void __launch_bounds__(kWidenThreads) widen_kernel(const WidenParams p)
+{
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    const int64_t per_row = p.ldy / 16, pieces = per_row * p.rows;
+#pragma unroll 1
+    for (int64_t i = int64_t(blockIdx.x) * kWidenThreads + threadIdx.x; i < pieces; i += int64_t(gridDim.x) * kWidenThreads) {
+        const int64_t row = i / per_row;
+        const int c = int(i - row * per_row) * 16;
+        const int8_t* x = p.x + row * p.ldx + c;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (c + 16 <= p.cols) {
+            v = ptx::ld_global_cg_v4(x);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 15; ++k)
+                if (c + k < p.cols)
+                    reinterpret_cast<int8_t*>(&v)[k] = x[k];
+        }
+        uint4 a, b;
+        widen4(v.x, a.x, a.y);
+        widen4(v.y, a.z, a.w);
+        widen4(v.z, b.x, b.y);
+        widen4(v.w, b.z, b.w);
+        uint4* y = reinterpret_cast<uint4*>(p.y + row * p.ldy + c);
+        y[0] = a;
+        y[1] = b;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_int8(int dtype, const RowsInt8Params& p, cudaStream_t stream, bool pdl)
+{
+    switch (dtype) {
+    case BWGEMM_BF16: return launch_rows<__nv_bfloat16>(p, stream, pdl);
+    case BWGEMM_FP16: return launch_rows<__half>(p, stream, pdl);
+    case BWGEMM_FP32: return launch_rows<float>(p, stream, pdl);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_widen(const WidenParams& p, cudaStream_t stream, bool pdl)
+{
+    const int64_t pieces = p.ldy / 16 * p.rows;
+    const unsigned grid = unsigned(std::min<int64_t>((pieces + kWidenThreads - 1) / kWidenThreads, 1 << 20));
+    return launch_plain(widen_kernel, grid, kWidenThreads, p, stream, pdl);
+}
+
+}  // namespace bwgemm

@@ -1,0 +1,572 @@
+// lanes_kernel.cuh -- products whose weights fill the rows of the MMA: the gated layer
+// on few rows of X, and the product of 8-bit integers at any size.
+//
+//   kLanesGated   H[m, n] = act(G) * U,  G = X Wg^T, U = X Wu^T      bf16 or fp16
+//   kLanesInt8    C[m, n] = sx[m] * sw[n] * sum_k X[m, k] * W[n, k]  8-bit integers
+//
+// The accumulator holds the result transposed: a TMEM lane per weight row, a column per
+// row of X (16 to 256), so that one to a few hundred tokens cost no more tensor time than
+// they need, and a warp's lanes are consecutive columns of the result.
+//
+// Gated: tiles of 64 rows of each weight, two MMAs of M = 64 into columns of the same
+// lanes -- a thread has both G and U of its outputs.
+//
+// 8-bit integers: the tensor cores of sm_103a have none, but an fp16 holds every 8-bit
+// integer exactly, their products are exact in fp32 and so are sums up to 2^24 (longer
+// ones round as fp32 does).  So the weights travel as bytes -- HBM, L2 and shared memory --
+// and become fp16 on the last stretch: four warps take a row each into registers, widen
+// it (xor 0x80 makes u = x + 128, a byte permutation 0x6400 | u = 1024 + u, one
+// subtraction 1024 + u - 1152 = x, all exact) and store it to TMEM, from where the MMA
+// reads its A operand.  X, the smaller or at least the shared operand, is widened before
+// (launch_widen) and comes through shared memory as fp16.
+//
+//   warp 0      TMA producer: a ring of stages of 128 of K
+//   warp 1      TMEM allocator and MMA issuer (in the even CTA of a pair)
+//   warps 4..   kLanesInt8: groups of four converting warps, a TMEM lane quarter each; two
+//               groups take turns, so that one's waits overlap the other's work
+//   then        epilogue: four warps, eight from 128 columns on
+//
+// Work: whole tiles, and the last, partial wave spread over all workers in K steps; the
+// warp that completes a tile's K adds the pieces in worker order (as in the block-scaled
+// product).  Tiles may hold fewer weight rows than the MMA has, so that they fill the SMs.
+#pragma once
+
+#include "activation.cuh"
+#include "feed_forward.h"
+#include "scaled_kernel.cuh"
+
+namespace bwgemm {
+
+constexpr int kLanesK = 128;  // of K per stage
+
+template <int MODE, int CG, int BN>
+struct LanesConfig {
+    static constexpr bool kGated = MODE == kLanesGated;
+    static_assert(CG == 1 || (!kGated && BN == 256), "pairs: 8-bit integers, 256 rows of X");
+    static constexpr int kLRows = kGated ? 64 : 128;          // weight rows per CTA and matrix
+    static constexpr int kXRows = BN / CG;                    // rows of X this CTA copies
+    static constexpr int kLBytes = kGated ? 2 * 64 * kLanesK * 2 : 128 * kLanesK;
+    static constexpr int kXBytes = kXRows * kLanesK * 2;
+    static constexpr int kRingBytes = 222 * 1024;
+    // an even number for the 8-bit integers: each group of converting warps then meets every
+    // phase of its stages' barriers
+    static constexpr int kFit = kRingBytes / (kLBytes + kXBytes);
+    static constexpr int kStages = kGated ? kFit : kFit > 10 ? 10 : kFit / 2 * 2;
+    static constexpr int kConvWarps = kGated ? 0 : CG == 2 ? 4 : 8;
+    static constexpr int kConvGroups = kConvWarps / 4;
+    static constexpr int kEpiWarps = lanes_epi_warps(BN);
+    static constexpr int kFirstEpi = 4 + kConvWarps;
+    static constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+    static constexpr int kCols = BN / (kEpiWarps / 4);        // columns per epilogue warp
+    static constexpr int kPiece = kCols < 32 ? kCols : 32;    // of which it reads this many at a time
+    static constexpr int kAccCols = kGated ? 2 * BN : BN;
+    static constexpr int kBufs = !kGated && BN == 256 ? 1 : 2;
+    static constexpr int kASlots = 4;                         // stages of widened weights in TMEM
+    static constexpr int kACol0 = 256, kASlotCols = kLanesK / 2;
+    static constexpr int kTmemCols = kGated ? kBufs * kAccCols : 512;
+    static_assert(kGated || kBufs * kAccCols <= kACol0, "TMEM");
+    static_assert(kTmemCols >= 32 && kTmemCols <= 512, "TMEM");
+    static constexpr size_t kPartialFloats = lanes_partial_floats(MODE, BN);
+    static constexpr int kOffL = 0;
+    static constexpr int kOffX = kStages * kLBytes;
+    static constexpr int kOffScale = kOffX + kStages * kXBytes;  // a warp's 32 scales of X
+    static constexpr int kOffBar = kOffScale + kEpiWarps * 128;
+    // full, wfull, empty, afull, aempty, acc_full, acc_empty, drain
+    static constexpr int kNumBars = 3 * kStages + 2 * kASlots + 2 * kBufs + 1;
+    static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars;
+    static constexpr int kOffAbort = kOffTmemSlot + 4;
+    static constexpr int kSmemBytes = kOffAbort + 4 + 1024;
+    static_assert(kLBytes % 1024 == 0 && kXBytes % 1024 == 0, "swizzle atoms need 1 KiB alignment");
+    static_assert(kSmemBytes <= 227 * 1024, "exceeds the 227 KiB shared memory of one CTA");
+};
+
+// Four 8-bit integers as two pairs of fp16.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi)
+{
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+__device__ __forceinline__ uint16_t round16(float v, int dtype)
+{
+    return dtype == BWGEMM_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+
+template <int MODE, int CG, int BN>
+__global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
+    lanes_kernel(const __grid_constant__ LanesMaps maps, const LanesParams p)
+{
+    using Cfg = LanesConfig<MODE, CG, BN>;
+    constexpr bool GATED = Cfg::kGated;
+    constexpr int STAGES = Cfg::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;
+    const int worker = int(blockIdx.x) / CG;
+    const int workers = int(gridDim.x) / CG;
+    const int l_rows = p.l_rows;  // of this CTA
+    const uint32_t sL = base + Cfg::kOffL;
+    const uint32_t sX = base + Cfg::kOffX;
+    const uint32_t bar_full = base + Cfg::kOffBar;              // X (gated: all) has landed
+    const uint32_t bar_wfull = bar_full + 8 * STAGES;           // 8-bit weights have landed
+    const uint32_t bar_empty = bar_wfull + 8 * STAGES;
+    const uint32_t bar_afull = bar_empty + 8 * STAGES;          // widened weights are in TMEM
+    const uint32_t bar_aempty = bar_afull + 8 * Cfg::kASlots;
+    const uint32_t bar_acc_full = bar_aempty + 8 * Cfg::kASlots;
+    const uint32_t bar_acc_empty = bar_acc_full + 8 * Cfg::kBufs;
+    const uint32_t bar_drain = bar_acc_empty + 8 * Cfg::kBufs;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffTmemSlot);
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffAbort);
+
+    if (threadIdx.x == 64) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(bar_full + 8 * s, 1);
+            ptx::mbar_init(bar_wfull + 8 * s, 1);
+            ptx::mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int a = 0; a < Cfg::kASlots; ++a) {
+            ptx::mbar_init(bar_afull + 8 * a, CG * 4);
+            ptx::mbar_init(bar_aempty + 8 * a, 1);
+        }
+        for (int b = 0; b < Cfg::kBufs; ++b) {
+            ptx::mbar_init(bar_acc_full + 8 * b, 1);
+            ptx::mbar_init(bar_acc_empty + 8 * b, CG * Cfg::kEpiWarps);
+        }
+        ptx::mbar_init(bar_drain, 1);
+        *abort_flag = 0u;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tensormap(&maps.w);
+        ptx::prefetch_tensormap(&maps.x3);
+        if (GATED) {
+            ptx::prefetch_tensormap(&maps.w3);
+            ptx::prefetch_tensormap(&maps.w23);
+        }
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc<CG>(ptx::smem_addr(tmem_slot), Cfg::kTmemCols);
+        ptx::tmem_relinquish<CG>();
+    }
+    ptx::tc_fence_before_sync();
+    if constexpr (CG == 2)
+        ptx::cluster_sync();
+    else
+        __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    ptx::launch_dependents();
+    uint32_t armed_mask = 0, armed_parity = 0, warmed_mask = 0, warmed_parity = 0;
+
+    ScaledIter iter;
+    ScaledSegment seg;
+    iter.init(p, worker, workers);
+
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        const uint32_t leader_full = CG == 2 ? ptx::map_to_cta(bar_full, 0) : bar_full;
+        int s = 0, n = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        while (ok && iter.next(p, seg)) {
+            const int l_row = (seg.l_blk * CG + int(rank)) * l_rows;
+            const int x_row = seg.c_blk * BN + int(rank) * Cfg::kXRows;
+#pragma unroll 1
+            for (int kb = seg.kb0; kb < seg.kb1; ++kb, ++n) {
+                ok = __all_sync(0xffffffffu,
+                                pipe_wait(bar_empty + 8 * s, phase ^ 1u, p, abort_flag, kStatusProducerTimeout));
+                if (!ok)
+                    break;
+                // test hook: the producer of CTA 0 never fills this stage of the launch
+                const bool stall = p.stall_kblock >= 0 && blockIdx.x == 0 && p.stall_kblock == n;
+                if (!stall) {
+                    if (rank == 0) {
+                        armed_mask |= 1u << s;
+                        armed_parity = (armed_parity & ~(1u << s)) | (phase << s);
+                    }
+                    warmed_mask |= 1u << s;
+                    warmed_parity = (warmed_parity & ~(1u << s)) | (phase << s);
+                }
+                if (!stall && ptx::elect_one()) {
+                    const uint32_t fb = leader_full + 8 * s;
+                    const uint32_t dL = sL + uint32_t(s * Cfg::kLBytes), dX = sX + uint32_t(s * Cfg::kXBytes);
+                    const int k = kb * kLanesK;
+                    if (rank == 0)
+                        ptx::mbar_arrive_expect_tx(fb, uint32_t(CG * Cfg::kXBytes + (GATED ? 4 * l_rows * 128 : 0)));
+                    if (n == 0)  // all before it overlaps the kernel before
+                        ptx::grid_dependency_wait();
+                    if constexpr (GATED) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t d = dL + uint32_t(i * 16384);
+                            if (2 * kb + 2 <= p.l_chunks) {
+                                ptx::tma_load_3d(d, i ? &maps.w23 : &maps.w3, fb, 0, l_row, 2 * kb);
+                            } else {
+                                ptx::tma_load_2d(d, i ? &maps.w2 : &maps.w, fb, k, l_row);
+                                ptx::tma_load_2d(d + uint32_t(l_rows * 128), i ? &maps.w2 : &maps.w, fb, k + 64, l_row);
+                            }
+                        }
+                    } else {
+                        ptx::mbar_arrive_expect_tx(bar_wfull + 8 * s, uint32_t(l_rows * 128));
+                        ptx::tma_load_2d(dL, &maps.w, bar_wfull + 8 * s, k, l_row);
+                    }
+                    if (2 * kb + 2 <= p.c_chunks) {
+                        if constexpr (CG == 2)
+                            ptx::tma_load_3d_pair(dX, &maps.x3, fb, 0, x_row, 2 * kb);
+                        else
+                            ptx::tma_load_3d(dX, &maps.x3, fb, 0, x_row, 2 * kb);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t d = dX + uint32_t(i * Cfg::kXRows * 128);
+                            if constexpr (CG == 2)
+                                ptx::tma_load_2d_pair(d, &maps.x, fb, k + 64 * i, x_row);
+                            else
+                                ptx::tma_load_2d(d, &maps.x, fb, k + 64 * i, x_row);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (++s == STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1 && rank == 0) {
+        // ---------------------------------------------------------- MMA issue
+        const uint64_t l_desc0 = make_sdesc_sw128(sL);
+        const uint64_t x_desc0 = make_sdesc_sw128(sX);
+        const uint32_t idesc = make_idesc(GATED ? p.dtype : int(BWGEMM_FP16), CG * Cfg::kLRows, BN);
+        const uint32_t tmem0 = __shfl_sync(0xffffffffu, tmem_base, 0);
+        int s = 0, b = 0, a = 0;
+        uint32_t phase = 0, bphase = 0, aphase = 0;
+        bool ok = true;
+        while (ok && iter.next(p, seg)) {
+            ok = __all_sync(0xffffffffu,
+                            pipe_wait(bar_acc_empty + 8 * b, bphase ^ 1u, p, abort_flag, kStatusMmaTimeout));
+#pragma unroll 1
+            for (int kb = seg.kb0; ok && kb < seg.kb1; ++kb) {
+                ok = __all_sync(0xffffffffu, pipe_wait(bar_full + 8 * s, phase, p, abort_flag, kStatusMmaTimeout));
+                if constexpr (!GATED)
+                    if (ok)
+                        ok = __all_sync(0xffffffffu, pipe_wait(bar_afull + 8 * a, aphase, p, abort_flag, kStatusMmaTimeout));
+                if (!ok)
+                    break;
+                ptx::tc_fence_after_sync();
+                if (ptx::elect_one()) {
+                    const uint64_t xd = x_desc0 + uint64_t((s * Cfg::kXBytes) >> 4);
+                    const uint32_t d = tmem0 + uint32_t(b * Cfg::kAccCols);
+                    const uint32_t more = kb > seg.kb0 ? 1u : 0u;
+#pragma unroll
+                    for (int kk = 0; kk < kLanesK / 16; ++kk) {
+                        const uint64_t xk = xd + uint64_t(((kk >> 2) * Cfg::kXRows * 128 + (kk & 3) * 32) >> 4);
+                        if constexpr (GATED) {
+                            const uint64_t lk = l_desc0 + uint64_t((s * Cfg::kLBytes + (kk >> 2) * l_rows * 128 + (kk & 3) * 32) >> 4);
+                            ptx::mma_f16<1>(d, lk, xk, idesc, kk > 0 ? 1u : more);
+                            ptx::mma_f16<1>(d + BN, lk + uint64_t(16384 >> 4), xk, idesc, kk > 0 ? 1u : more);
+                        } else {
+                            ptx::mma_f16_tmem<CG>(d, tmem0 + uint32_t(Cfg::kACol0 + a * Cfg::kASlotCols + 8 * kk), xk, idesc,
+                                                  kk > 0 ? 1u : more);
+                        }
+                    }
+                    if constexpr (CG == 2) {
+                        ptx::mma_commit_pair(bar_empty + 8 * s, 0x3);
+                        ptx::mma_commit_pair(bar_aempty + 8 * a, 0x3);
+                        if (kb == seg.kb1 - 1)
+                            ptx::mma_commit_pair(bar_acc_full + 8 * b, 0x3);
+                    } else {
+                        ptx::mma_commit(bar_empty + 8 * s);
+                        if constexpr (!GATED)
+                            ptx::mma_commit(bar_aempty + 8 * a);
+                        if (kb == seg.kb1 - 1)
+                            ptx::mma_commit(bar_acc_full + 8 * b);
+                    }
+                }
+                __syncwarp();
+                if (++s == STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+                if (++a == Cfg::kASlots) {
+                    a = 0;
+                    aphase ^= 1u;
+                }
+            }
+            if (++b == Cfg::kBufs) {
+                b = 0;
+                bphase ^= 1u;
+            }
+        }
+    } else if (!GATED && warp >= 4 && warp < Cfg::kFirstEpi) {
+        // ------------------------------------------------- 8-bit weights to fp16
+        const int group = (warp - 4) >> 2, q = warp & 3;
+        const int row = 32 * q + lane;
+        const uint32_t leader_afull = CG == 2 ? ptx::map_to_cta(bar_afull, 0) : bar_afull;
+        const uint32_t src0 = sL + uint32_t(row * 128);
+        const uint32_t dst0 = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(Cfg::kACol0);
+        int s = 0, a = 0, turn = 0;
+        uint32_t phase = 0, aphase = 0;
+        bool ok = true;
+        while (ok && iter.next(p, seg)) {
+#pragma unroll 1
+            for (int kb = seg.kb0; kb < seg.kb1; ++kb) {
+                if (turn == group) {
+                    ok = __all_sync(0xffffffffu,
+                                    pipe_wait(bar_wfull + 8 * s, phase, p, abort_flag, kStatusMmaTimeout) &&
+                                        pipe_wait(bar_aempty + 8 * a, aphase ^ 1u, p, abort_flag, kStatusMmaTimeout));
+                    if (!ok)
+                        break;
+                    ptx::tc_fence_after_sync();
+                    const uint32_t src = src0 + uint32_t(s * Cfg::kLBytes);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t r[32];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t w[4];
+                            ptx::ld_shared_v4(src + (uint32_t((4 * half + c) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                widen4(w[i], r[8 * c + 2 * i], r[8 * c + 2 * i + 1]);
+                        }
+                        ptx::tmem_st_32x32b_x32(dst0 + uint32_t(a * Cfg::kASlotCols + 32 * half), r);
+                    }
+                    ptx::tmem_st_wait();
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CG == 2)
+                            ptx::mbar_arrive_cluster_relaxed(leader_afull + 8 * a);
+                        else
+                            ptx::mbar_arrive(bar_afull + 8 * a);
+                    }
+                }
+                turn = turn + 1 == Cfg::kConvGroups ? 0 : turn + 1;
+                if (++s == STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+                if (++a == Cfg::kASlots) {
+                    a = 0;
+                    aphase ^= 1u;
+                }
+            }
+        }
+    } else if (warp >= Cfg::kFirstEpi) {
+        // ------------------------------------------------------------ epilogue
+        ptx::grid_dependency_wait();
+        constexpr int P = Cfg::kPiece;
+        constexpr int MATS = GATED ? 2 : 1;
+        const int e = warp - Cfg::kFirstEpi;
+        const int q = warp & 3;
+        const int col = (e >> 2) * Cfg::kCols;  // its first column of the tile
+        // M = 64: row 16 q + i of the weights in lane i of quarter q, lanes 16 to 31 unused
+        const int row = GATED ? 16 * q + lane : 32 * q + lane;
+        const bool in_tile = row < l_rows && (!GATED || lane < 16);
+        const uint32_t scale_buf = base + uint32_t(Cfg::kOffScale + e * 128);
+        int b = 0;
+        uint32_t bphase = 0;
+        bool ok = true;
+        while (ok && iter.next(p, seg)) {
+            const int n = (seg.l_blk * CG + int(rank)) * l_rows + row;  // column of the result
+            const int m0 = seg.c_blk * BN + col;                        // its row of column 0
+            const bool live = in_tile && n < p.lrows;
+            const float ls = !GATED && live ? p.ls[n] : 0.f;
+            // P columns of finished sums (gated: of G, then of U) from column c of the warp's on
+            auto finish = [&](int c, const float(&v)[MATS][P]) {
+                const int m = m0 + c, count = p.crows - m;
+                if constexpr (GATED) {
+                    if (!live)
+                        return;
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        if (j >= count)
+                            break;
+                        const float g = v[0][j], u = v[MATS - 1][j];
+                        static_cast<uint16_t*>(p.out[0])[int64_t(m + j) * p.ldo[0] + n] =
+                            round16(activate(g, p.activation) * u, p.dtype);
+                        if (p.out[1] != nullptr) {
+                            static_cast<uint16_t*>(p.out[1])[int64_t(m + j) * p.ldo[1] + n] = round16(g, p.dtype);
+                            static_cast<uint16_t*>(p.out[2])[int64_t(m + j) * p.ldo[2] + n] = round16(u, p.dtype);
+                        }
+                    }
+                } else {
+                    if (count <= 0)
+                        return;
+                    __syncwarp();
+                    const float cs = lane < count && lane < P ? p.cs[m + lane] : 0.f;
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(scale_buf + 4 * lane), "f"(cs) : "memory");
+                    __syncwarp();
+                    if (!live)
+                        return;
+                    // (the sum times its token's scale) times its channel's: neither product
+                    // leaves fp32's range where the result does not
+                    if (p.out_type == BWGEMM_FP32) {
+                        float* dst = static_cast<float*>(p.out[0]) + int64_t(m) * p.ldo[0] + n;
+#pragma unroll
+                        for (int j = 0; j < P; j += 4) {
+                            const float4 f = ptx::ld_shared_f32x4(scale_buf + 4 * j);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (j + k < count)
+                                    dst[(j + k) * p.ldo[0]] = v[0][j + k] * (&f.x)[k] * ls;
+                        }
+                    } else {
+                        uint16_t* dst = static_cast<uint16_t*>(p.out[0]) + int64_t(m) * p.ldo[0] + n;
+#pragma unroll
+                        for (int j = 0; j < P; j += 4) {
+                            const float4 f = ptx::ld_shared_f32x4(scale_buf + 4 * j);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (j + k < count)
+                                    dst[(j + k) * p.ldo[0]] = round16(v[0][j + k] * (&f.x)[k] * ls, p.out_type);
+                        }
+                    }
+                }
+            };
+            ok = __all_sync(0xffffffffu,
+                            pipe_wait(bar_acc_full + 8 * b, bphase, p, abort_flag, kStatusEpilogueTimeout));
+            if (!ok)
+                break;
+            ptx::tc_fence_after_sync();
+            const uint32_t taddr = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(b * Cfg::kAccCols + col);
+            const uint32_t empty = bar_acc_empty + 8 * b;
+            if (++b == Cfg::kBufs) {
+                b = 0;
+                bphase ^= 1u;
+            }
+            constexpr size_t kStride = Cfg::kPartialFloats;
+            constexpr size_t kWarpFloats = size_t(MATS) * 32 * Cfg::kCols;
+            const size_t mine = size_t(e) * kWarpFloats + 4 * lane;
+            float* const part = p.partials + ((size_t(worker) * 2 + seg.slot) * CG + rank) * kStride + mine;
+#pragma unroll 1
+            for (int c = 0; c < Cfg::kCols; c += P) {
+                uint32_t v[MATS][P];
+#pragma unroll
+                for (int i = 0; i < MATS; ++i) {
+                    if constexpr (P == 16)
+                        ptx::tmem_ld_32x32b_x16(taddr + uint32_t(i * BN + c), v[i]);
+                    else
+                        ptx::tmem_ld_32x32b_x32(taddr + uint32_t(i * BN + c), v[i]);
+                }
+                ptx::tmem_ld_wait();
+                if (c + P >= Cfg::kCols)
+                    hand_back<CG>(empty, lane);
+                if (seg.whole) {
+                    float f[MATS][P];
+#pragma unroll
+                    for (int i = 0; i < MATS; ++i)
+#pragma unroll
+                        for (int j = 0; j < P; ++j)
+                            f[i][j] = __uint_as_float(v[i][j]);
+                    finish(c, f);
+                } else {
+                    // a piece of a tile: its sums to global memory
+#pragma unroll
+                    for (int i = 0; i < MATS; ++i)
+#pragma unroll
+                        for (int j = 0; j < P; j += 4)
+                            ptx::st_global_cg_v4(part + size_t(i) * 32 * Cfg::kCols + size_t(c + j) * 32,
+                                                 make_uint4(v[i][j], v[i][j + 1], v[i][j + 2], v[i][j + 3]));
+                }
+            }
+            if (seg.whole)
+                continue;
+            // whoever brings the tile's last K step adds all pieces in worker order
+            __threadfence();
+            __syncwarp();
+            const int st = seg.tile - p.dp_tiles;
+            uint32_t* counter = p.counters + (size_t(st) * CG + rank) * Cfg::kEpiWarps + e;
+            uint32_t before = 0;
+            if (lane == 0)
+                before = ptx::atom_add_acq_rel_gpu(counter, uint32_t(seg.kb1 - seg.kb0));
+            before = __shfl_sync(0xffffffffu, before, 0);
+            if (before + uint32_t(seg.kb1 - seg.kb0) != uint32_t(p.num_kb))
+                continue;
+            if (lane == 0)
+                *counter = 0u;  // ready for the next call
+            __threadfence();
+            const long long first = (long long)st * p.num_kb;
+            const int w0 = int(((first + 1) * workers - 1) / p.sk_iters);
+            const int w1 = int(((first + p.num_kb) * workers - 1) / p.sk_iters);
+#pragma unroll 1
+            for (int c = 0; c < Cfg::kCols; c += P) {
+                float f[MATS][P];
+#pragma unroll
+                for (int i = 0; i < MATS; ++i)
+#pragma unroll
+                    for (int j = 0; j < P; ++j)
+                        f[i][j] = 0.f;
+#pragma unroll 1
+                for (int w = w0; w <= w1; ++w) {
+                    const int wslot = ScaledIter::begin(p, w, workers) / p.num_kb == st ? 0 : 1;
+                    const float* src = p.partials + ((size_t(w) * 2 + wslot) * CG + rank) * kStride + mine + size_t(c) * 32;
+#pragma unroll
+                    for (int i = 0; i < MATS; ++i)
+#pragma unroll
+                        for (int j = 0; j < P; j += 4) {
+                            const uint4 x = ptx::ld_global_cg_v4(src + size_t(i) * 32 * Cfg::kCols + size_t(j) * 32);
+                            f[i][j] += __uint_as_float(x.x);
+                            f[i][j + 1] += __uint_as_float(x.y);
+                            f[i][j + 2] += __uint_as_float(x.z);
+                            f[i][j + 3] += __uint_as_float(x.w);
+                        }
+                }
+                finish(c, f);
+            }
+        }
+        __syncwarp();
+    }
+
+    // --------------------------------------------------------------- teardown
+    // After an abort, drain the MMAs and the loads this CTA armed (bounded) and
+    // settle before TMEM and shared memory are released.
+    __syncwarp();
+    __syncthreads();
+    if (*abort_flag) {
+        if (warp == 1 && rank == 0) {
+            if (ptx::elect_one()) {
+                if constexpr (CG == 2)
+                    ptx::mma_commit_pair(bar_drain, 0x1);
+                else
+                    ptx::mma_commit(bar_drain);
+            }
+            __syncwarp();
+            drain_wait(bar_drain, 0u, kDrainNs);
+        }
+        if (warp == 0) {
+#pragma unroll 1
+            for (int s = 0; s < STAGES; ++s) {
+                if ((armed_mask >> s) & 1u)
+                    drain_wait(bar_full + 8 * s, (armed_parity >> s) & 1u, kDrainNs);
+                if (!GATED && ((warmed_mask >> s) & 1u))
+                    drain_wait(bar_wfull + 8 * s, (warmed_parity >> s) & 1u, kDrainNs);
+            }
+            if (lane == 0)
+                settle(kSettleNs);
+        }
+        __syncwarp();
+        __syncthreads();
+    }
+    ptx::tc_fence_before_sync();
+    if constexpr (CG == 2)
+        ptx::cluster_sync();
+    else
+        __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc<CG>(tmem_base, Cfg::kTmemCols);
+    }
+}
+
+}  // namespace bwgemm

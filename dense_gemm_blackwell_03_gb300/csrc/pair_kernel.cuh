@@ -1,0 +1,453 @@
+// pair_kernel.cuh -- the large products of the gated feed-forward layer on 16-bit
+// operands (bf16 or fp16) with fp32 sums:
+//
+//   kPairGated    G = X Wg^T, U = X Wu^T, H = act(G) * U     forward, in one pass
+//   kPairInput    dX = dG Wg + dU Wu                          input gradient
+//   kPairWeight   dWg = dG^T X,  dWu = dU^T X                 weight gradients
+//
+// One persistent, warp-specialised tcgen05 kernel, tiles of 256 x 256 on CTA pairs (or
+// 128 x 128 on single CTAs for the gradients of small layers).  tcgen05 reads either
+// major order, so no operand is transposed in memory: dX reads the weights as they are
+// stored (columns of a row are outputs), dW both operands.
+//
+// Gated: the pair's MMA takes 256 rows of B, half of them from either CTA's shared
+// memory.  The even CTA brings 128 rows of Wg, the odd one the same rows of Wu, so
+// each accumulator row holds G in its first 128 columns and U in the last: every
+// epilogue thread has both values of its outputs, and X's tile is read once for both.
+//
+// Input gradient: one accumulator over both products (the K loop runs over dG, Wg, then
+// over dU, Wu).  Weight gradient: both results' tiles are one list of work, so that X is
+// in L2 for both.  Few tiles and a deep K: slices of K, whose fp32 sums a second kernel
+// adds in order.
+//
+// What bounds it: the MMAs, 1024 cycles per 128 of K of a 256 x 256 tile; the epilogue
+// of a tile (other TMEM buffer) overlaps the next tile's.  Each stage of the ring holds
+// 128 of K of both operands (64 KiB per CTA), one 32 KiB copy each where the box lies
+// in whole 64-element chunks, two of 16 KiB at a row's end (TMA fills zeros past it).
+#pragma once
+
+#include "activation.cuh"
+#include "feed_forward.h"
+#include "ortho_kernel.cuh"
+
+namespace bwgemm {
+
+struct PairTile {
+    int r, c, result;
+    int slice, k0, k1;
+};
+
+__device__ __forceinline__ PairTile pair_tile_at(const PairParams& p, int t)
+{
+    PairTile x;
+    const int i = t / p.splits;
+    const int steps = p.steps_k * p.terms;
+    x.slice = t - i * p.splits;
+    x.k0 = int(int64_t(x.slice) * steps / p.splits);
+    x.k1 = int(int64_t(x.slice + 1) * steps / p.splits);
+    // groups of 8 tile rows (of all results), walked down before stepping along the columns
+    const int rows = p.num_r * p.results;
+    const int per_group = 8 * p.num_c;
+    const int g = i / per_group;
+    const int height = min(rows - 8 * g, 8);
+    const int local = i - g * per_group;
+    const int r = 8 * g + local % height;
+    x.c = local / height;
+    x.result = r / p.num_r;
+    x.r = r - x.result * p.num_r;
+    return x;
+}
+
+// A box of 128 rows x 128 elements of an operand: whole chunks in one copy, else chunk by
+// chunk (zeros past the row's end, and past the last row).
+template <int CG>
+__device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* m, const CUtensorMap* m3, int chunks, uint32_t bar,
+                                          int row, int col)
+{
+    if (col / 64 + 2 <= chunks) {
+        if constexpr (CG == 2)
+            ptx::tma_load_3d_pair(dst, m3, bar, 0, row, col / 64);
+        else
+            ptx::tma_load_3d(dst, m3, bar, 0, row, col / 64);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if constexpr (CG == 2)
+                ptx::tma_load_2d_pair(dst + uint32_t(i * 16384), m, bar, col + 64 * i, row);
+            else
+                ptx::tma_load_2d(dst + uint32_t(i * 16384), m, bar, col + 64 * i, row);
+    }
+}
+
+template <int CG, int FORM>
+__global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
+    pair_kernel(const __grid_constant__ PairMaps maps, const PairParams p)
+{
+    using Cfg = OrthoConfig<CG>;
+    static_assert(FORM != kPairGated || CG == 2, "gate and up rows come from the two CTAs");
+    constexpr bool A_MN = FORM == kPairWeight, B_MN = FORM != kPairGated;
+    constexpr int STAGES = Cfg::kStages;
+    constexpr int TILE = Cfg::kTile;
+    constexpr int COLS = FORM == kPairGated ? TILE / 2 : TILE;  // result columns of a tile
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;
+    const int worker = int(blockIdx.x) / CG;
+    const int workers = int(gridDim.x) / CG;
+    const int total = p.num_r * p.num_c * p.results * p.splits;  // a unit is a tile, or a slice of its K
+    const uint32_t sA = base + Cfg::kOffA;
+    const uint32_t sB = base + Cfg::kOffB;
+    const uint32_t bar_full = base + Cfg::kOffBar;
+    const uint32_t bar_empty = bar_full + 8 * STAGES;
+    const uint32_t bar_acc_full = bar_empty + 8 * STAGES;
+    const uint32_t bar_acc_empty = bar_acc_full + 16;
+    const uint32_t bar_drain = bar_acc_empty + 16;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffTmemSlot);
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffAbort);
+
+    if (threadIdx.x == 64) {
+        for (int s = 0; s < STAGES; ++s) {
+            ptx::mbar_init(bar_full + 8 * s, 1);
+            ptx::mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(bar_acc_full + 8 * b, 1);
+            ptx::mbar_init(bar_acc_empty + 8 * b, CG * Cfg::kEpiWarps);
+        }
+        ptx::mbar_init(bar_drain, 1);
+        *abort_flag = 0u;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tensormap(&maps.a[0]);
+        ptx::prefetch_tensormap(&maps.a3[0]);
+        ptx::prefetch_tensormap(&maps.b[0]);
+        ptx::prefetch_tensormap(&maps.b3[0]);
+        ptx::prefetch_tensormap(&maps.out[0]);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc<CG>(ptx::smem_addr(tmem_slot), Cfg::kTmemCols);
+        ptx::tmem_relinquish<CG>();
+    }
+    ptx::tc_fence_before_sync();
+    if constexpr (CG == 2)
+        ptx::cluster_sync();
+    else
+        __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    ptx::launch_dependents();
+    uint32_t armed_mask = 0, armed_parity = 0;
+
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        const uint32_t leader_full = CG == 2 ? ptx::map_to_cta(bar_full, 0) : bar_full;
+        int s = 0, n = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int t = worker; ok && t < total; t += workers) {
+            const PairTile x = pair_tile_at(p, t);
+            const int a0 = x.r * TILE + int(rank) * 128;
+            const int b0 = FORM == kPairGated ? x.c * COLS : x.c * TILE + int(rank) * 128;
+#pragma unroll 1
+            for (int i = x.k0; i < x.k1; ++i, ++n) {
+                ok = __all_sync(0xffffffffu,
+                                pipe_wait(bar_empty + 8 * s, phase ^ 1u, p, abort_flag, kStatusProducerTimeout));
+                if (!ok)
+                    break;
+                const bool stall = p.stall_kblock >= 0 && blockIdx.x == 0 && p.stall_kblock == n;
+                if (!stall && rank == 0) {
+                    armed_mask |= 1u << s;
+                    armed_parity = (armed_parity & ~(1u << s)) | (phase << s);
+                }
+                if (!stall && ptx::elect_one()) {
+                    const int term = FORM == kPairInput && i >= p.steps_k ? 1 : 0;
+                    const int k = (i - term * p.steps_k) * kOrthoK;
+                    const int za = FORM == kPairWeight ? x.result : term;
+                    const int zb = FORM == kPairGated ? int(rank) : FORM == kPairInput ? term : 0;
+                    const uint32_t fb = leader_full + 8 * s;
+                    const uint32_t dA = sA + uint32_t(s * Cfg::kOperandBytes), dB = sB + uint32_t(s * Cfg::kOperandBytes);
+                    if (rank == 0)
+                        ptx::mbar_arrive_expect_tx(fb, uint32_t(CG * 2 * Cfg::kOperandBytes));
+                    if (n == 0)  // all before it overlaps the kernel before
+                        ptx::grid_dependency_wait();
+                    pair_load<CG>(dA, &maps.a[za], &maps.a3[za], p.chunks_a, fb, A_MN ? k : a0, A_MN ? a0 : k);
+                    pair_load<CG>(dB, &maps.b[zb], &maps.b3[zb], p.chunks_b, fb, B_MN ? k : b0, B_MN ? b0 : k);
+                }
+                __syncwarp();
+                if (++s == STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1 && rank == 0) {
+        // ---------------------------------------------------------- MMA issue
+        const uint64_t a_desc0 = A_MN ? make_sdesc_mn(sA) : make_sdesc_sw128(sA);
+        const uint64_t b_desc0 = B_MN ? make_sdesc_mn(sB) : make_sdesc_sw128(sB);
+        const uint32_t idesc = make_idesc(p.dtype, 128 * CG, TILE) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+        const uint32_t tmem0 = __shfl_sync(0xffffffffu, tmem_base, 0);
+        int s = 0, b = 0;
+        uint32_t phase = 0, bphase = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int t = worker; ok && t < total; t += workers) {
+            const PairTile x = pair_tile_at(p, t);
+            ok = __all_sync(0xffffffffu,
+                            pipe_wait(bar_acc_empty + 8 * b, bphase ^ 1u, p, abort_flag, kStatusMmaTimeout));
+#pragma unroll 1
+            for (int i = x.k0; ok && i < x.k1; ++i) {
+                ok = __all_sync(0xffffffffu, pipe_wait(bar_full + 8 * s, phase, p, abort_flag, kStatusMmaTimeout));
+                if (!ok)
+                    break;
+                ptx::tc_fence_after_sync();
+                if (ptx::elect_one()) {
+                    const uint64_t ad = a_desc0 + uint64_t((s * Cfg::kOperandBytes) >> 4);
+                    const uint64_t bd = b_desc0 + uint64_t((s * Cfg::kOperandBytes) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < kOrthoK / 16; ++kk) {
+                        // K-major: two chunks of 64 k, 32 bytes per MMA; MN-major: 128 k in rows of 128 bytes
+                        const uint32_t k_major = uint32_t((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                        const uint32_t mn_major = uint32_t(kk * 2048) >> 4;
+                        ptx::mma_f16<CG>(tmem0 + uint32_t(b * TILE), ad + (A_MN ? mn_major : k_major),
+                                         bd + (B_MN ? mn_major : k_major), idesc, (i > x.k0 || kk > 0) ? 1u : 0u);
+                    }
+                    if constexpr (CG == 2) {
+                        ptx::mma_commit_pair(bar_empty + 8 * s, 0x3);
+                        if (i == x.k1 - 1)
+                            ptx::mma_commit_pair(bar_acc_full + 8 * b, 0x3);
+                    } else {
+                        ptx::mma_commit(bar_empty + 8 * s);
+                        if (i == x.k1 - 1)
+                            ptx::mma_commit(bar_acc_full + 8 * b);
+                    }
+                }
+                __syncwarp();
+                if (++s == STAGES) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (++b == 2) {
+                b = 0;
+                bphase ^= 1u;
+            }
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------------------ epilogue
+        ptx::grid_dependency_wait();
+        const int e = warp - 2;
+        const int q = warp & 3;
+        const uint32_t sb = base + uint32_t(Cfg::kOffStore + e * Cfg::kStoreBytes);
+        int b = 0;
+        uint32_t bphase = 0;
+        bool ok = true;
+        // 64 columns of this lane's row, packed, to columns col.. of rows row0.. of result z
+        auto put = [&](const uint32_t(&w)[32], int z, int row0, int col) {
+            if (row0 >= p.rows || col >= p.cols)
+                return;
+            if ((p.cols & 7) != 0 && col + 64 > p.cols) {
+                // a TMA store clips a row's end only in whole 16-byte pieces
+                if (row0 + lane < p.rows) {
+                    uint16_t* dst = p.out[z] + int64_t(row0 + lane) * p.ldo[z] + col;
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        if (col + i < p.cols)
+                            dst[i] = uint16_t((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xFFFFu));
+                }
+                return;
+            }
+            if (lane == 0)
+                ptx::bulk_wait_group_read<0>();  // the store before has read the staging block
+            __syncwarp();
+            ortho_stage(w, sb, lane);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                ptx::tma_store_2d(&maps.out[z], sb, col, row0);
+                ptx::bulk_commit_group();
+            }
+        };
+#pragma unroll 1
+        for (int t = worker; ok && t < total; t += workers) {
+            const PairTile x = pair_tile_at(p, t);
+            const int row0 = x.r * TILE + int(rank) * 128 + 32 * q;
+            ok = __all_sync(0xffffffffu,
+                            pipe_wait(bar_acc_full + 8 * b, bphase, p, abort_flag, kStatusEpilogueTimeout));
+            if (!ok)
+                break;
+            ptx::tc_fence_after_sync();
+            const uint32_t taddr = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(b * TILE);
+            if constexpr (FORM == kPairGated) {
+                const int c0 = (e >> 2) * 64;  // this warp's 64 columns of the tile's 128
+                uint32_t h[32], gw[32], uw[32];
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    uint32_t g[32], u[32];
+                    ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c0 + c), g);
+                    ptx::tmem_ld_32x32b_x32(taddr + uint32_t(COLS + c0 + c), u);
+                    ptx::tmem_ld_wait();
+                    if (c == 32)
+                        hand_back<CG>(bar_acc_empty + 8 * b, lane);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float v[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            v[k] = activate(__uint_as_float(g[2 * i + k]), p.activation) * __uint_as_float(u[2 * i + k]);
+                        h[c / 2 + i] = pack2(__float_as_uint(v[0]), __float_as_uint(v[1]), p.dtype);
+                        gw[c / 2 + i] = pack2(g[2 * i], g[2 * i + 1], p.dtype);
+                        uw[c / 2 + i] = pack2(u[2 * i], u[2 * i + 1], p.dtype);
+                    }
+                }
+                const int col = x.c * COLS + c0;
+                put(h, 0, row0, col);
+                if (p.out[1] != nullptr) {
+                    put(gw, 1, row0, col);
+                    put(uw, 2, row0, col);
+                }
+            } else {
+                const int c0 = (e >> 2) * Cfg::kCols;
+                if (p.splits == 1) {
+#pragma unroll 1
+                    for (int c = 0; c < Cfg::kCols; c += 64) {
+                        uint32_t v[64], w[32];
+                        ptx::tmem_ld_32x32b_x64(taddr + uint32_t(c0 + c), v);
+                        ptx::tmem_ld_wait();
+                        if (c + 64 >= Cfg::kCols)
+                            hand_back<CG>(bar_acc_empty + 8 * b, lane);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            w[i] = pack2(v[2 * i], v[2 * i + 1], p.dtype);
+                        put(w, x.result, row0, x.c * TILE + c0 + c);
+                    }
+                } else {
+                    // a slice of K: its sums to global memory, where pair_join_kernel adds
+                    // them; lanes next to each other, so a warp's store is 512 bytes
+                    float* const part = p.partials + (size_t(t) * CG + rank) * (128 * TILE) + e * (32 * Cfg::kCols) + 4 * lane;
+#pragma unroll 1
+                    for (int c = 0; c < Cfg::kCols; c += 32) {
+                        uint32_t v[32];
+                        ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c0 + c), v);
+                        ptx::tmem_ld_wait();
+                        if (c + 32 >= Cfg::kCols)
+                            hand_back<CG>(bar_acc_empty + 8 * b, lane);
+                        if (row0 < p.rows && x.c * TILE + c0 + c < p.cols) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                ptx::st_global_cg_v4(part + c * 32 + i * 128,
+                                                     make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                        }
+                    }
+                }
+            }
+            if (++b == 2) {
+                b = 0;
+                bphase ^= 1u;
+            }
+        }
+        if (lane == 0)
+            ptx::bulk_wait_group_all();
+        __syncwarp();
+    }
+
+    // --------------------------------------------------------------- teardown
+    // as in the other kernels: after an abort, drain MMAs and loads (bounded)
+    // before TMEM and shared memory are released
+    __syncwarp();
+    __syncthreads();
+    if (*abort_flag) {
+        if (warp == 1 && rank == 0) {
+            if (ptx::elect_one()) {
+                if constexpr (CG == 2)
+                    ptx::mma_commit_pair(bar_drain, 0x1);
+                else
+                    ptx::mma_commit(bar_drain);
+            }
+            __syncwarp();
+            drain_wait(bar_drain, 0u, kDrainNs);
+        }
+        if (warp == 0) {
+#pragma unroll 1
+            for (int s = 0; s < STAGES; ++s)
+                if ((armed_mask >> s) & 1u)
+                    drain_wait(bar_full + 8 * s, (armed_parity >> s) & 1u, kDrainNs);
+            if (lane == 0)
+                settle(kSettleNs);
+        }
+        __syncwarp();
+        __syncthreads();
+    }
+    ptx::tc_fence_before_sync();
+    if constexpr (CG == 2)
+        ptx::cluster_sync();
+    if (warp == 1) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc<CG>(tmem_base, Cfg::kTmemCols);
+    }
+}
+
+// Adds the slices of the tiles.  A warp takes 32 rows x 4 columns of a tile (512 bytes
+// of a slice) and every join_share-th slice; the sums of that many warps meet in shared
+// memory, in order.
+template <int CG>
+__global__ void __launch_bounds__(32 * kJoinWarps) pair_join_kernel(const PairParams p)
+{
+    using Cfg = OrthoConfig<CG>;
+    constexpr int TILE = Cfg::kTile, CHUNKS = Cfg::kCols / 32;
+    __shared__ float4 sums[kJoinWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int share = p.join_share, first = warp % share;
+    const int piece = int(blockIdx.x) * (kJoinWarps / share) + warp / share;
+    const int i = piece % 8, c = piece / 8 % CHUNKS * 32, e = piece / (8 * CHUNKS) % 8, rank = piece / (64 * CHUNKS);
+    const int t = int(blockIdx.y) * p.splits;
+    const PairTile x = pair_tile_at(p, t);
+    const int row0 = x.r * TILE + rank * 128 + 32 * ((e + 2) & 3), row = row0 + lane;
+    const int col = x.c * TILE + (e >> 2) * Cfg::kCols + c + 4 * i;
+    ptx::grid_dependency_wait();
+    ptx::launch_dependents();
+    const float* at = p.partials + (size_t(t) * CG + rank) * (128 * TILE) + e * (32 * Cfg::kCols) + c * 32 + i * 128 + 4 * lane;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row0 < p.rows && col < p.cols) {
+#pragma unroll 8
+        for (int k = first; k < p.splits; k += share) {
+            const uint4 v = ptx::ld_global_cg_v4(at + size_t(k) * (CG * 128 * TILE));
+            f.x += __uint_as_float(v.x);
+            f.y += __uint_as_float(v.y);
+            f.z += __uint_as_float(v.z);
+            f.w += __uint_as_float(v.w);
+        }
+    }
+    sums[warp][lane] = f;
+    __syncthreads();
+    if (first != 0)
+        return;
+#pragma unroll 1
+    for (int k = 1; k < share; ++k) {
+        const float4 g = sums[warp + k][lane];
+        f.x += g.x;
+        f.y += g.y;
+        f.z += g.z;
+        f.w += g.w;
+    }
+    if (row >= p.rows)
+        return;
+    const uint32_t lo = pack2(__float_as_uint(f.x), __float_as_uint(f.y), p.dtype);
+    const uint32_t hi = pack2(__float_as_uint(f.z), __float_as_uint(f.w), p.dtype);
+    uint16_t* const out = p.out[x.result] + row * p.ldo[x.result] + col;
+    if (col + 4 <= p.cols) {
+        *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            if (col + k < p.cols)
+                out[k] = uint16_t((k < 2 ? lo : hi) >> (k & 1 ? 16 : 0));
+    }
+}
+
+}  // namespace bwgemm

@@ -121,19 +121,22 @@ struct ScaledIter {
     int it, it_begin, it_end;
     int t, step;
 
-    static __device__ __forceinline__ int begin(const ScaledParams& p, int worker, int workers)
+    template <typename Params>
+    static __device__ __forceinline__ int begin(const Params& p, int worker, int workers)
     {
         const long long prod = (long long)worker * p.sk_iters;
         return prod < (1ll << 32) ? int(unsigned(prod) / unsigned(workers)) : int(prod / workers);
     }
-    __device__ __forceinline__ void init(const ScaledParams& p, int worker, int workers)
+    template <typename Params>
+    __device__ __forceinline__ void init(const Params& p, int worker, int workers)
     {
         it_begin = it = begin(p, worker, workers);
         it_end = begin(p, worker + 1, workers);
         t = worker;
         step = workers;
     }
-    __device__ __forceinline__ bool next(const ScaledParams& p, ScaledSegment& s)
+    template <typename Params>
+    __device__ __forceinline__ bool next(const Params& p, ScaledSegment& s)
     {
         if (it < it_end) {
             const int tile = it / p.num_kb;

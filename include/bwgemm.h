@@ -576,6 +576,125 @@ bwgemm_status_t bwgemm_select_orthogonalize(int32_t num_sms, int32_t max_pairs, 
                                             bwgemm_dtype_t dtype, int32_t step, const bwgemm_plan_options_t* opts,
                                             bwgemm_ortho_config_t out[3]);
 
+/* ------------------------------------------------------------------------
+ * The gated feed-forward layer of a language model in 16 bits, forward and
+ * backward, and matrices of 8-bit integers for serving its products.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+    BWGEMM_SILU = 0,     /* g / (1 + exp(-g))                                          */
+    BWGEMM_GELU = 1,     /* g Phi(g), Phi the normal distribution                      */
+    BWGEMM_GELU_TANH = 2 /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2            */
+} bwgemm_activation_t;
+
+/* A matrix of 16-bit elements: 16-byte aligned, rows `ld` elements apart (a multiple of 8). */
+typedef struct {
+    void* data;
+    int64_t ld;
+} bwgemm_matrix_t;
+
+/*
+ * H = act(G) * U elementwise, with G = X Wg^T and U = X Wu^T: both projections, the
+ * activation and the product in one pass over X and both weights.
+ *
+ *   X : M x K;  Wg, Wu : N x K (may be halves of one matrix);  H : M x N
+ *   G, U : M x N, what the backward pass needs, or both NULL (data NULL counts as NULL)
+ *
+ * All bf16 or all fp16 (`dtype`).  Sums, activation and product are fp32, each result
+ * is rounded once.  Results must not overlap the operands or one another.  K == 0: empty
+ * sums.  Device memory, empty sizes, asynchrony (one launch), capture, workspace and status
+ * after a timeout are as for bwgemm_run; sums are in a fixed order for a shape.
+ */
+bwgemm_status_t bwgemm_gated(bwgemm_plan_t plan, const bwgemm_matrix_t* X, const bwgemm_matrix_t* Wg,
+                             const bwgemm_matrix_t* Wu, const bwgemm_matrix_t* H, const bwgemm_matrix_t* G,
+                             const bwgemm_matrix_t* U, int64_t M, int64_t N, int64_t K, bwgemm_dtype_t dtype,
+                             bwgemm_activation_t activation, void* stream);
+
+/*
+ * Its gradients, from dH (M x N) and the G and U that bwgemm_gated kept:
+ *
+ *   dU = dH act(G), dG = dH U act'(G);   dX = dG Wg + dU Wu;   dWg = dG^T X, dWu = dU^T X
+ *
+ *   dX : M x K, or NULL: not wanted;  dWg, dWu : N x K, or both NULL
+ *   (Wg and Wu are read only for dX, X only for dWg and dWu: NULL where not read)
+ *   workspace : device memory, 256-byte aligned, of at least
+ *       bwgemm_gated_backward_workspace() bytes (else BWGEMM_ERR_WORKSPACE), holding
+ *       nothing of use before or after
+ *
+ * dG and dU are rounded to `dtype`, as operands of the products that follow; sums are fp32.
+ * M == 0 gives dWg = dWu = 0, N == 0 gives dX = 0.  Two or three launches, one more where a
+ * product is cut into slices of K (in the plan's workspace); the rest as for bwgemm_gated.
+ */
+bwgemm_status_t bwgemm_gated_backward(bwgemm_plan_t plan, const bwgemm_matrix_t* dH, const bwgemm_matrix_t* G,
+                                      const bwgemm_matrix_t* U, const bwgemm_matrix_t* X, const bwgemm_matrix_t* Wg,
+                                      const bwgemm_matrix_t* Wu, const bwgemm_matrix_t* dX, const bwgemm_matrix_t* dWg,
+                                      const bwgemm_matrix_t* dWu, int64_t M, int64_t N, int64_t K, bwgemm_dtype_t dtype,
+                                      bwgemm_activation_t activation, void* workspace, uint64_t workspace_bytes,
+                                      void* stream);
+
+/* Host-only: the workspace bytes of bwgemm_gated_backward for these sizes. */
+bwgemm_status_t bwgemm_gated_backward_workspace(int64_t M, int64_t N, uint64_t* bytes);
+
+/*
+ * Quantise the rows of X (rows x cols, bf16, fp16 or fp32, row stride ldx elements) to
+ * 8-bit integers: tokens of an activation, output channels of a weight.  For a row with
+ * largest magnitude a >= 2^-100 (smaller ones count as 2^-100): scale = a / 127 in fp32,
+ * value = 127 x / a rounded to the nearest integer, ties to even -- of the exact quotient, not
+ * of its fp32 value.  A row holding a NaN or an infinity gets the scale NaN and zeros.
+ *
+ * X and q 16-byte aligned; ldx a multiple of 16 bytes, ldq (bytes between rows) of 16;
+ * scales one per row, 4-byte aligned.  Device memory as for bwgemm_run.  Asynchronous, one
+ * launch (none for an empty X), no allocation, capturable.
+ */
+bwgemm_status_t bwgemm_quantize_integer(bwgemm_plan_t plan, const void* X, bwgemm_dtype_t dtype, int64_t rows,
+                                     int64_t cols, int64_t ldx, int8_t* q, int64_t ldq, float* scales, void* stream);
+
+/*
+ * C[m, n] = scale_a[m] * scale_b[n] * sum_k A[m, k] * B[n, k] of 8-bit integers (-128..127),
+ * A of M rows, B of N rows, both K wide, rows lda and ldb bytes apart, with an fp32 scale per
+ * row each (a token, an output channel).
+ *
+ *   A, B : 16-byte aligned, lda and ldb multiples of 16;  scales 4-byte aligned
+ *   C : M x N bf16, fp16 or fp32 (`out`), row stride ldc elements, 16-byte aligned, ldc a
+ *       multiple of 16 bytes
+ *   workspace : device memory, 256-byte aligned, of at least bwgemm_run_integer_workspace()
+ *       bytes (else BWGEMM_ERR_WORKSPACE; NULL where that is 0), holding nothing of use
+ *       before or after
+ *
+ * Sums are fp32: exact as long as none passes 2^24 in magnitude (K <= 1024 for any operands),
+ * beyond that rounded as fp32 sums are.  The sum is multiplied with scale_a, then with
+ * scale_b.  Everything else -- device memory, empty sizes (K == 0: C = 0), asynchrony, capture,
+ * status after a timeout, the plan's workspace -- is as for bwgemm_run; sums are in a fixed
+ * order for a shape.
+ */
+bwgemm_status_t bwgemm_run_integer(bwgemm_plan_t plan, const int8_t* A, const float* scale_a, const int8_t* B,
+                                const float* scale_b, void* C, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
+                                int64_t ldc, bwgemm_dtype_t out, void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* Host-only: the workspace bytes of bwgemm_run_integer for these sizes. */
+bwgemm_status_t bwgemm_run_integer_workspace(int64_t M, int64_t N, int64_t K, uint64_t* bytes);
+
+/* How bwgemm_gated and bwgemm_run_integer divide a product (for inspection and tests). */
+typedef struct {
+    int32_t lanes;    /* 1: the weights' rows fill the MMA's rows; 0: X's (bwgemm_gated)  */
+    int32_t tile_w;   /* weight rows per tile (bwgemm_gated: of each weight)              */
+    int32_t tile_x;   /* rows of X per tile                                               */
+    int32_t dp_tiles; /* tiles computed whole                                             */
+    int32_t sk_tiles; /* tiles whose K is spread over the workers                         */
+    int32_t workers;  /* CTAs, or CTA pairs (lanes == 0, or tile_x == 256)                */
+} bwgemm_lanes_config_t;
+
+/*
+ * Host-only: the division that a plan with `opts` (NULL = defaults) picks on a GPU of
+ * `num_sms` SMs holding `max_pairs` CTA pairs (0 = num_sms / 2); for the backward pass of its
+ * two products dX (out[0]) and dWg, dWu (out[1], tiles of both), whose `splits` are slices of K.
+ */
+bwgemm_status_t bwgemm_select_gated(int32_t num_sms, int32_t max_pairs, int64_t M, int64_t N, int64_t K,
+                                    const bwgemm_plan_options_t* opts, bwgemm_lanes_config_t* out);
+bwgemm_status_t bwgemm_select_integer(int32_t num_sms, int32_t max_pairs, int64_t M, int64_t N, int64_t K,
+                                   const bwgemm_plan_options_t* opts, bwgemm_lanes_config_t* out);
+bwgemm_status_t bwgemm_select_gated_backward(int32_t num_sms, int32_t max_pairs, int64_t M, int64_t N, int64_t K,
+                                             const bwgemm_plan_options_t* opts, bwgemm_ortho_config_t out[2]);
+
 /* Static text for a status code ("unknown status" for anything else). */
 const char* bwgemm_status_string(bwgemm_status_t status);
 
