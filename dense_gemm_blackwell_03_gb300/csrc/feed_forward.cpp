@@ -247,6 +247,14 @@ GatedPlan plan_gated(int num_sms, int max_pairs, int64_t M, int64_t N, int64_t K
     return g;
 }
 
+// Whether the kernel for few rows takes the product.
+bool takes_few_rows(int mode, int64_t M, int64_t N, int64_t K)
+{
+    if (M > kFewMost || (mode == kLanesInt8 && K > kFewIntegerK))
+        return false;
+    return true;
+}
+
 int pairs_of(bwgemm_plan_t plan) { return plan->max_active[find_variant(2, 256, false, 1)]; }
 
 bool dtype16(bwgemm_dtype_t dtype) { return dtype == BWGEMM_BF16 || dtype == BWGEMM_FP16; }
@@ -322,6 +330,28 @@ bwgemm_status_t bwgemm_gated(bwgemm_plan_t plan, const bwgemm_matrix_t* X, const
         return BWGEMM_OK;
     }
     const bool pdl = plan->opts.pdl_off == 0;
+    if (takes_few_rows(kLanesGated, M, N, K)) {
+        FewRowsParams p = {};
+        p.w[0] = static_cast<const uint8_t*>(Wg->data);
+        p.w[1] = static_cast<const uint8_t*>(Wu->data);
+        p.ldw[0] = 2 * Wg->ld;
+        p.ldw[1] = 2 * Wu->ld;
+        p.x = static_cast<const uint8_t*>(X->data);
+        p.ldx = 2 * X->ld;
+        p.row_bytes = 2 * K;
+        p.M = int32_t(M);
+        p.N = int32_t(N);
+        p.out_type = dtype;
+        p.activation = activation;
+        for (int i = 0; i < (keep ? 3 : 1); ++i) {
+            p.out[i] = out[i]->data;
+            p.ldo[i] = out[i]->ld;
+        }
+        if (launch_few_rows(dtype == BWGEMM_BF16 ? kFewBf16 : kFewFp16, p, s, pdl) != cudaSuccess)
+            return BWGEMM_ERR_CUDA;
+        plan->launches += 1;
+        return BWGEMM_OK;
+    }
     const GatedPlan sel = plan_gated(plan->num_sms, pairs_of(plan), M, N, K, &plan->opts, plan->workspace_bytes);
     if (sel.lanes) {
         if (sel.l.workers == 0)
@@ -569,7 +599,7 @@ bwgemm_status_t bwgemm_run_integer_workspace(int64_t M, int64_t N, int64_t K, ui
         return BWGEMM_ERR_INVALID_ARG;
     if (!fits(M) || !fits(N) || !fits(K))
         return BWGEMM_ERR_UNSUPPORTED;
-    if (M > 0 && N > 0 && K > 0)
+    if (M > 0 && N > 0 && K > 0 && !takes_few_rows(kLanesInt8, M, N, K))
         *bytes = uint64_t(round_up(M * round_up(K, 128) * 2, 256));  // A as fp16
     return BWGEMM_OK;
 }
@@ -591,7 +621,7 @@ bwgemm_status_t bwgemm_run_integer(bwgemm_plan_t plan, const int8_t* A, const fl
         return BWGEMM_ERR_UNSUPPORTED;
     if (!aligned(C, 16) || ldc * es % 16 != 0 ||
         (K > 0 && (!aligned(A, 16) || lda % 16 != 0 || !aligned(B, 16) || ldb % 16 != 0 || !aligned(scale_a, 4) ||
-                   !aligned(scale_b, 4) || !aligned(workspace, 256))))
+                   !aligned(scale_b, 4) || (need > 0 && !aligned(workspace, 256)))))
         return BWGEMM_ERR_ALIGNMENT;
     if (workspace_bytes < need)
         return BWGEMM_ERR_WORKSPACE;
@@ -604,9 +634,28 @@ bwgemm_status_t bwgemm_run_integer(bwgemm_plan_t plan, const int8_t* A, const fl
             return st;
         return zero(C, ldc, M, N, es, s);
     }
-    if ((st = check_resident({A, scale_a, B, scale_b, C, workspace}, plan->device)) != BWGEMM_OK)
+    if ((st = check_resident({A, scale_a, B, scale_b, C, need ? workspace : nullptr}, plan->device)) != BWGEMM_OK)
         return st;
     const bool pdl = plan->opts.pdl_off == 0;
+    if (takes_few_rows(kLanesInt8, M, N, K)) {
+        FewRowsParams p = {};
+        p.w[0] = reinterpret_cast<const uint8_t*>(B);
+        p.ldw[0] = ldb;
+        p.x = reinterpret_cast<const uint8_t*>(A);
+        p.ldx = lda;
+        p.row_bytes = K;
+        p.M = int32_t(M);
+        p.N = int32_t(N);
+        p.ls = scale_b;
+        p.cs = scale_a;
+        p.out_type = out;
+        p.out[0] = C;
+        p.ldo[0] = ldc;
+        if (launch_few_rows(kFewInt8, p, s, pdl) != cudaSuccess)
+            return BWGEMM_ERR_CUDA;
+        plan->launches += 1;
+        return BWGEMM_OK;
+    }
     const LanesPlan sel = plan_lanes(kLanesInt8, plan->num_sms, pairs_of(plan), M, N, K, &plan->opts, plan->workspace_bytes);
     if (sel.workers == 0)
         return BWGEMM_ERR_UNSUPPORTED;
@@ -647,6 +696,10 @@ bwgemm_status_t bwgemm_select_gated(int32_t num_sms, int32_t max_pairs, int64_t 
         return BWGEMM_ERR_INVALID_ARG;
     if (!fits(M) || !fits(N) || !fits(K))
         return BWGEMM_ERR_UNSUPPORTED;
+    if (takes_few_rows(kLanesGated, M, N, K)) {
+        *out = {2, 8, int32_t(M > 8 ? 16 : 8), 0, 0, 0};
+        return BWGEMM_OK;
+    }
     const GatedPlan g = plan_gated(num_sms, max_pairs ? max_pairs : num_sms / 2, M, N, K, opts, workspace_of(opts));
     if (g.lanes && g.l.workers == 0)
         return BWGEMM_ERR_UNSUPPORTED;
@@ -664,6 +717,10 @@ bwgemm_status_t bwgemm_select_integer(int32_t num_sms, int32_t max_pairs, int64_
         return BWGEMM_ERR_INVALID_ARG;
     if (!fits(M) || !fits(N) || !fits(K))
         return BWGEMM_ERR_UNSUPPORTED;
+    if (takes_few_rows(kLanesInt8, M, N, K)) {
+        *out = {2, 16, int32_t(M > 8 ? 16 : 8), 0, 0, 0};
+        return BWGEMM_OK;
+    }
     const LanesPlan s =
         plan_lanes(kLanesInt8, num_sms, max_pairs ? max_pairs : num_sms / 2, M, N, K, opts, workspace_of(opts));
     if (s.workers == 0)

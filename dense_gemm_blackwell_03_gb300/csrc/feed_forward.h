@@ -107,6 +107,26 @@ constexpr int lanes_epi_warps(int bn) { return bn >= 128 ? 8 : 4; }
 // fp32 sums of a CTA's partial tile.
 constexpr int lanes_partial_floats(int mode, int bn) { return mode == kLanesGated ? 2 * 128 * bn : 128 * bn; }
 
+// ------------------------------------------------ at most 16 rows of X
+enum : int { kFewInt8 = 0, kFewBf16 = 1, kFewFp16 = 2 };
+
+struct FewRowsParams {
+    const uint8_t* w[2];         // 8-bit weights, or Wg and Wu; rows ldw bytes apart
+    int64_t ldw[2];
+    const uint8_t* x;
+    int64_t ldx;
+    int64_t row_bytes;           // K in bytes
+    int32_t M, N;
+    const float* ls;             // kFewInt8: a scale per weight row,
+    const float* cs;             // and per row of X
+    int32_t out_type, activation;
+    void* out[3];                // as in LanesParams
+    int64_t ldo[3];
+};
+constexpr int kFewMost = 16;
+constexpr int64_t kFewIntegerK = 131071;  // 2^14 each, sums in 32 bits
+cudaError_t launch_few_rows(int kind, const FewRowsParams& p, cudaStream_t stream, bool pdl);
+
 // ------------------------------------------------------- 8-bit integers
 struct RowsInt8Params {
     const void* x;               // rows x cols, ldx elements apart

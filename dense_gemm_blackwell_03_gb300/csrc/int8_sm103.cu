@@ -2,14 +2,22 @@
 // fp16 operand of their product.
 //
 // quantize_int8: a = max(max |x|, 2^-100) of the row, scale = a / 127, q = 127 x / a rounded
-// to the nearest integer, ties to the even one.  The quotient is decided exactly: x times
-// the fp32 reciprocal is within 8e-6 of it, so only a value within 1e-4 of the middle of two
-// integers is in doubt, and for that the two sides of the comparison, 254 |x| and (2 L + 1) a,
-// are formed in fp64, where both are exact (8 and 24 bits).
+// to the nearest integer, ties to the even one, of the exact quotient.  x times fl(127 / a)
+// is within 127 * 2^-24 < 2^-17 of it, so it is right but for values that close to the middle
+// of two integers:
+//
+// * bf16: x and a are integers X, A < 2^8 times powers of two, and where x / a lies in
+//   [2^-j-1, 2^-j + 1) the quotient's distance from a middle is a multiple of 2^-j / A: 0 or, as
+//   no middle lies below j = 8, more than 2^-16.  One fma that adds 384 rounds it to a multiple of 2^-15:
+//   to the middle itself from within 2^-17, never to it from beyond 2^-16; ties then go to
+//   the even integer by themselves.
+// * fp16: 127 x and r a are exact in fp32 and so is the rest e = 127 x - r a (a multiple of
+//   x's last place, at most a / 2 or so: 20 bits); 2 |e| against a decides.
+// * fp32: 254 |x| against (2 L + 1) a, both as the sum of two fp32 values.
 //
 // Bound by HBM: a row is read once, held in registers between the maximum and the
 // rounding (up to 8 pieces of 16 bytes a thread; what a longer row has beyond that is
-// read again, from L2), by a warp, 128 or 512 threads according to its length.
+// read again, from L2), by a warp, 128, 256 or 512 threads according to its length.
 #include <type_traits>
 
 #include "feed_forward.h"
@@ -19,7 +27,7 @@ namespace bwgemm {
 namespace {
 
 constexpr float kMagic = 12582912.f;  // 1.5 2^23: a sum with it holds the rounded integer in its low bits
-constexpr int kHeld = 8;              // pieces a thread holds
+constexpr float kSnap = 384.f;        // a sum with it is a multiple of 2^-15
 
 template <typename T>
 struct Piece {
@@ -65,18 +73,23 @@ struct Piece {
     }
 };
 
-// 127 x / a rounded exactly, where fp32 leaves it open.
+// 127 x / a rounded exactly, where fp32 leaves open on which side of the middle of two
+// integers `near` lies (|x|, a below 2^118).
 static __device__ __noinline__ int round_exactly(float x, float a, float near)
 {
-    const float low = floorf(fabsf(near));
-    const double left = 254.0 * double(fabsf(x)), right = double(2.f * low + 1.f) * double(a);
+    const float y = fabsf(x), low = floorf(fabsf(near)), odd = 2.f * low + 1.f;
+    const float p = 254.f * y, p2 = fmaf(254.f, y, -p);  // p + p2 = 254 |x|
+    const float q = odd * a, q2 = fmaf(odd, a, -q);
+    const float d = (p - q) + (p2 - q2);  // p and q are close: each difference is exact
     const int l = int(low);
-    const int r = left > right || (left == right && (l & 1)) ? l + 1 : l;
+    const int r = d > 0.f || (d == 0.f && (l & 1)) ? l + 1 : l;
     return x < 0.f ? -r : r;
 }
 
-// One row by TR threads of the block; ROWS rows per block.
-template <typename T, int TR, int ROWS>
+__device__ __forceinline__ uint64_t twice(float v) { return ptx::pack_f32x2(__float_as_uint(v), __float_as_uint(v)); }
+
+// One row by TR threads of the block, kHeld pieces each in registers; ROWS rows per block.
+template <typename T, int TR, int ROWS, int kHeld>
 __global__ void __launch_bounds__(TR* ROWS) quantize_rows_kernel(const RowsInt8Params p)
 {
     using P = Piece<T>;
@@ -117,25 +130,68 @@ __global__ void __launch_bounds__(TR* ROWS) quantize_rows_kernel(const RowsInt8P
     }
     const bool finite = top < 0x7F800000u;
     const float a = fmaxf(__uint_as_float(top), kSmallestAmax);
-    const float up = finite ? 127.f / a : 0.f;
+    // x and a times a power of two, exact, that keeps 254 x in range
+    const float down = a > 1.f ? 0.0009765625f : 1.f;
+    const float as = a * down, half = 0.5f * as;
+    const float inv = finite ? 1.f / as : 0.f, times = 127.f * down, up = finite ? 127.f / a : 0.f;
+    const bool tie_exact = (__float_as_uint(a) & 0x7FFFFFu) == 0u;
     if (t == 0)
         p.scales[row] = finite ? a / 127.f : __uint_as_float(0x7FC00000u);
     int8_t* q = p.q + row * p.ldq;
     auto put = [&](const P& v, int64_t c) {
         uint32_t bits[P::kN];
         float worst = 0.f;
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
 #pragma unroll
-        for (int i = 0; i < P::kN; ++i) {
-            const float f = fmaf(v[i], up, kMagic);
-            worst = fmaxf(worst, fabsf(fmaf(v[i], up, -(f - kMagic))));
-            bits[i] = __float_as_uint(f);
-        }
-        if (worst > 0.4999f) {
+            for (int i = 0; i < P::kN; i += 2) {
+                const uint64_t x2 = ptx::pack_f32x2(__float_as_uint(v[i]), __float_as_uint(v[i + 1]));
+                float lo, hi;
+                ptx::unpack_f32x2(ptx::fma_f32x2(ptx::fma_f32x2(x2, twice(up), twice(kSnap)), twice(1.f), twice(kMagic - kSnap)),
+                                  lo, hi);
+                bits[i] = __float_as_uint(lo);
+                bits[i + 1] = __float_as_uint(hi);
+            }
+        } else if constexpr (std::is_same<T, __half>::value) {
 #pragma unroll
-            for (int i = 0; i < P::kN; ++i) {
-                const float near = v[i] * up;
-                if (fabsf(near - rintf(near)) > 0.4999f)
-                    bits[i] = uint32_t(round_exactly(v[i], a, near));
+            for (int i = 0; i < P::kN; i += 2) {
+                const uint64_t x2 = ptx::pack_f32x2(__float_as_uint(v[i]), __float_as_uint(v[i + 1]));
+                const uint64_t y = ptx::mul_f32x2(x2, twice(times)), f = ptx::fma_f32x2(y, twice(inv), twice(kMagic));
+                const uint64_t e = ptx::fma_f32x2(ptx::fma_f32x2(f, twice(-1.f), twice(kMagic)), twice(as), y);
+                float lo, hi;
+                ptx::unpack_f32x2(e, lo, hi);
+                worst = fmaxf(worst, fmaxf(fabsf(lo), fabsf(hi)));
+                ptx::unpack_f32x2(f, lo, hi);
+                bits[i] = __float_as_uint(lo);
+                bits[i + 1] = __float_as_uint(hi);
+            }
+            if (worst >= half && !tie_exact) {
+#pragma unroll
+                for (int i = 0; i < P::kN; ++i) {
+                    const float e = fmaf(kMagic - __uint_as_float(bits[i]), as, v[i] * times);
+                    if (fabsf(e) > half || (fabsf(e) == half && (bits[i] & 1u)))
+                        bits[i] += e > 0.f ? 1u : 0xFFFFFFFFu;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < P::kN; i += 2) {
+                const uint64_t x2 = ptx::pack_f32x2(__float_as_uint(v[i]), __float_as_uint(v[i + 1]));
+                const uint64_t f = ptx::fma_f32x2(x2, twice(up), twice(kMagic));
+                const uint64_t d = ptx::fma_f32x2(x2, twice(up), ptx::fma_f32x2(f, twice(-1.f), twice(kMagic)));
+                float lo, hi;
+                ptx::unpack_f32x2(d, lo, hi);
+                worst = fmaxf(worst, fmaxf(fabsf(lo), fabsf(hi)));
+                ptx::unpack_f32x2(f, lo, hi);
+                bits[i] = __float_as_uint(lo);
+                bits[i + 1] = __float_as_uint(hi);
+            }
+            if (worst > 0.4999f) {
+#pragma unroll
+                for (int i = 0; i < P::kN; ++i) {
+                    const float near = v[i] * up;
+                    if (fabsf(near - rintf(near)) > 0.4999f)
+                        bits[i] = uint32_t(round_exactly(v[i] * down, as, near));
+                }
             }
         }
         uint32_t w[P::kN / 4];
@@ -190,10 +246,12 @@ cudaError_t launch_rows(const RowsInt8Params& p, cudaStream_t stream, bool pdl)
 {
     const int64_t pieces = (p.cols + Piece<T>::kN - 1) / Piece<T>::kN;
     if (pieces <= 32 * 4)
-        return launch_plain(quantize_rows_kernel<T, 32, 4>, unsigned((p.rows + 3) / 4), 128, p, stream, pdl);
-    if (pieces <= 128 * kHeld)
-        return launch_plain(quantize_rows_kernel<T, 128, 1>, unsigned(p.rows), 128, p, stream, pdl);
-    return launch_plain(quantize_rows_kernel<T, 512, 1>, unsigned(p.rows), 512, p, stream, pdl);
+        return launch_plain(quantize_rows_kernel<T, 32, 4, 4>, unsigned((p.rows + 3) / 4), 128, p, stream, pdl);
+    if (pieces <= 128 * 8)
+        return launch_plain(quantize_rows_kernel<T, 128, 1, 8>, unsigned(p.rows), 128, p, stream, pdl);
+    if (pieces <= 256 * 8)
+        return launch_plain(quantize_rows_kernel<T, 256, 1, 8>, unsigned(p.rows), 256, p, stream, pdl);
+    return launch_plain(quantize_rows_kernel<T, 512, 1, 8>, unsigned(p.rows), 512, p, stream, pdl);
 }
 
 // Sixteen values a thread; the pad to whole stages of 128 is zeros.

@@ -73,6 +73,20 @@ def test_rows_to_int8_between_two_integers(plan, dtype):
     assert torch.equal(q, want) and torch.equal(s, scale.float())
 
 
+@pytest.mark.parametrize("dtype,bits", [("bf16", 8), ("fp16", 11)])
+def test_rows_to_int8_every_quotient(plan, dtype, bits):
+    # every significand against every other as the row's largest, down to quotients below 1/2
+    # (fp16: each 7th row, which meets all remainders)
+    sig = torch.arange(2 ** (bits - 1), 2 ** bits, device="cuda").double()
+    tops = sig if bits == 8 else sig[::7]
+    x = torch.cat([sig * 2.0 ** -j for j in range(1, 10)] + [-sig * 2.0 ** -1])
+    rows = torch.cat([tops[:, None], x.expand(len(tops), -1)], 1).to(T[dtype])
+    wide = ref.padded(rows, 8)
+    q, s = plan.quantize_int8(wide)
+    want, scale = ref.rows_int8(wide)
+    assert torch.equal(q, want) and torch.equal(s, scale.float())
+
+
 def test_rows_to_int8_special_rows(plan):
     x = torch.randn(8, 3000, device="cuda")
     x[1] = 0
