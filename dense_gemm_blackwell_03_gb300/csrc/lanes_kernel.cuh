@@ -20,11 +20,17 @@
 // reads its A operand.  X, the smaller or at least the shared operand, is widened before
 // (launch_widen) and comes through shared memory as fp16.
 //
-//   warp 0      TMA producer: a ring of stages of 128 of K
+//   warp 0      TMA producer: a ring of stages of 128 of K of the weights (gated: and of X)
 //   warp 1      TMEM allocator and MMA issuer (in the even CTA of a pair)
+//   warp 2      kLanesInt8: TMA producer of X's ring
 //   warps 4..   kLanesInt8: groups of four converting warps, a TMEM lane quarter each; two
 //               groups take turns, so that one's waits overlap the other's work
 //   then        epilogue: four warps, eight from 128 columns on
+//
+// The integers' two rings: what bounds few rows of X is how many bytes of weights are on
+// their way, so those get most of the shared memory, and a stage is free as soon as it is
+// in registers.  They do not depend on the kernel that widens X, which lets this one start
+// only when all before it is done: their copies run while it works.
 //
 // Work: whole tiles, and the last, partial wave spread over all workers in K steps; the
 // warp that completes a tile's K adds the pieces in worker order (as in the block-scaled
@@ -47,13 +53,20 @@ struct LanesConfig {
     static constexpr int kXRows = BN / CG;                    // rows of X this CTA copies
     static constexpr int kLBytes = kGated ? 2 * 64 * kLanesK * 2 : 128 * kLanesK;
     static constexpr int kXBytes = kXRows * kLanesK * 2;
+    // The rings (gated: one, of both operands).  A step is what one barrier round trip between
+    // producers and MMA warp covers: kStep stages of the weights, each widened by a group of
+    // converting warps into its part of a TMEM slot, with X's part in shared memory.  The MMA warp's
+    // way through a step is some 600 cycles beside its MMAs, hence two stages where tiles are
+    // narrow (64 x 28672 x 8192: 49 us with one).  A stage past the end of K is passed on
+    // empty, so that each group meets every phase of its barriers.
     static constexpr int kRingBytes = 222 * 1024;
-    // an even number for the 8-bit integers: each group of converting warps then meets every
-    // phase of its stages' barriers
-    static constexpr int kFit = kRingBytes / (kLBytes + kXBytes);
-    static constexpr int kStages = kGated ? kFit : kFit > 10 ? 10 : kFit / 2 * 2;
-    static constexpr int kConvWarps = kGated ? 0 : CG == 2 ? 4 : 8;
-    static constexpr int kConvGroups = kConvWarps / 4;
+    static constexpr int kStep = !kGated && BN <= 64 ? 2 : 1;
+    static constexpr int kXStep = kStep * kXBytes;
+    static constexpr int kXStages = kGated ? kRingBytes / (kLBytes + kXBytes) : BN == 64 ? 2 : 3;
+    static constexpr int kConvGroups = kGated ? 0 : kStep;
+    static constexpr int kFit = (kRingBytes - kXStages * kXStep) / kLBytes;
+    static constexpr int kLStages = kGated ? kXStages : (kFit > 10 ? 10 : kFit) / kStep * kStep;
+    static constexpr int kConvWarps = 4 * kConvGroups;
     static constexpr int kEpiWarps = lanes_epi_warps(BN);
     static constexpr int kFirstEpi = 4 + kConvWarps;
     static constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
@@ -61,18 +74,18 @@ struct LanesConfig {
     static constexpr int kPiece = kCols < 32 ? kCols : 32;    // of which it reads this many at a time
     static constexpr int kAccCols = kGated ? 2 * BN : BN;
     static constexpr int kBufs = !kGated && BN == 256 ? 1 : 2;
-    static constexpr int kASlots = 4;                         // stages of widened weights in TMEM
-    static constexpr int kACol0 = 256, kASlotCols = kLanesK / 2;
+    static constexpr int kACol0 = kBufs * kAccCols;           // widened weights in TMEM
+    static constexpr int kACols = kLanesK / 2, kASlotCols = kStep * kACols;
     static constexpr int kTmemCols = kGated ? kBufs * kAccCols : 512;
-    static_assert(kGated || kBufs * kAccCols <= kACol0, "TMEM");
+    static_assert(kGated || kACol0 + kXStages * kASlotCols <= 512, "TMEM");
     static_assert(kTmemCols >= 32 && kTmemCols <= 512, "TMEM");
     static constexpr size_t kPartialFloats = lanes_partial_floats(MODE, BN);
     static constexpr int kOffL = 0;
-    static constexpr int kOffX = kStages * kLBytes;
-    static constexpr int kOffScale = kOffX + kStages * kXBytes;  // a warp's 32 scales of X
+    static constexpr int kOffX = kLStages * kLBytes;
+    static constexpr int kOffScale = kOffX + kXStages * kXStep;  // a warp's 32 scales of X
     static constexpr int kOffBar = kOffScale + kEpiWarps * 128;
-    // full, wfull, empty, afull, aempty, acc_full, acc_empty, drain
-    static constexpr int kNumBars = 3 * kStages + 2 * kASlots + 2 * kBufs + 1;
+    // full, empty, wfull, wempty, acc_full, acc_empty, drain
+    static constexpr int kNumBars = 2 * kXStages + 2 * kLStages + 2 * kBufs + 1;
     static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars;
     static constexpr int kOffAbort = kOffTmemSlot + 4;
     static constexpr int kSmemBytes = kOffAbort + 4 + 1024;
@@ -103,7 +116,7 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
 {
     using Cfg = LanesConfig<MODE, CG, BN>;
     constexpr bool GATED = Cfg::kGated;
-    constexpr int STAGES = Cfg::kStages;
+    constexpr int XS = Cfg::kXStages, LS = Cfg::kLStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -116,26 +129,24 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
     const int l_rows = p.l_rows;  // of this CTA
     const uint32_t sL = base + Cfg::kOffL;
     const uint32_t sX = base + Cfg::kOffX;
-    const uint32_t bar_full = base + Cfg::kOffBar;              // X (gated: all) has landed
-    const uint32_t bar_wfull = bar_full + 8 * STAGES;           // 8-bit weights have landed
-    const uint32_t bar_empty = bar_wfull + 8 * STAGES;
-    const uint32_t bar_afull = bar_empty + 8 * STAGES;          // widened weights are in TMEM
-    const uint32_t bar_aempty = bar_afull + 8 * Cfg::kASlots;
-    const uint32_t bar_acc_full = bar_aempty + 8 * Cfg::kASlots;
+    const uint32_t bar_full = base + Cfg::kOffBar;              // X has landed, the weights (widened) are there
+    const uint32_t bar_empty = bar_full + 8 * XS;
+    const uint32_t bar_wfull = bar_empty + 8 * XS;              // 8-bit weights have landed
+    const uint32_t bar_wempty = bar_wfull + 8 * LS;
+    const uint32_t bar_acc_full = bar_wempty + 8 * LS;
     const uint32_t bar_acc_empty = bar_acc_full + 8 * Cfg::kBufs;
     const uint32_t bar_drain = bar_acc_empty + 8 * Cfg::kBufs;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffTmemSlot);
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffAbort);
 
     if (threadIdx.x == 64) {
-        for (int s = 0; s < STAGES; ++s) {
-            ptx::mbar_init(bar_full + 8 * s, 1);
-            ptx::mbar_init(bar_wfull + 8 * s, 1);
+        for (int s = 0; s < XS; ++s) {
+            ptx::mbar_init(bar_full + 8 * s, GATED ? 1 : 1 + CG * Cfg::kConvWarps);  // a producer, and the converting warps
             ptx::mbar_init(bar_empty + 8 * s, 1);
         }
-        for (int a = 0; a < Cfg::kASlots; ++a) {
-            ptx::mbar_init(bar_afull + 8 * a, CG * 4);
-            ptx::mbar_init(bar_aempty + 8 * a, 1);
+        for (int s = 0; s < LS; ++s) {
+            ptx::mbar_init(bar_wfull + 8 * s, 1);
+            ptx::mbar_init(bar_wempty + 8 * s, 4);
         }
         for (int b = 0; b < Cfg::kBufs; ++b) {
             ptx::mbar_init(bar_acc_full + 8 * b, 1);
@@ -165,46 +176,54 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
     ptx::tc_fence_after_sync();
     const uint32_t tmem_base = *tmem_slot;
     ptx::launch_dependents();
-    uint32_t armed_mask = 0, armed_parity = 0, warmed_mask = 0, warmed_parity = 0;
+    uint32_t armed_mask = 0, armed_parity = 0;  // of this warp's ring
 
     ScaledIter iter;
     ScaledSegment seg;
     iter.init(p, worker, workers);
 
+    auto arm = [&](int s, uint32_t phase) {
+        armed_mask |= 1u << s;
+        armed_parity = (armed_parity & ~(1u << s)) | (phase << s);
+    };
+    // X's rows of a stage
+    auto load_x = [&](uint32_t d, uint32_t bar, int row, int kb) {
+        if (2 * kb + 2 <= p.c_chunks) {
+            if constexpr (CG == 2)
+                ptx::tma_load_3d_pair(d, &maps.x3, bar, 0, row, 2 * kb);
+            else
+                ptx::tma_load_3d(d, &maps.x3, bar, 0, row, 2 * kb);
+        } else {
+            ptx::tma_load_2d(d, &maps.x, bar, kb * kLanesK, row);
+            ptx::tma_load_2d(d + uint32_t(Cfg::kXRows * 128), &maps.x, bar, kb * kLanesK + 64, row);
+        }
+    };
+
     if (warp == 0) {
-        // ------------------------------------------------------ TMA producer
-        const uint32_t leader_full = CG == 2 ? ptx::map_to_cta(bar_full, 0) : bar_full;
+        // -------------------------------------- TMA producer of the weights (gated: of all)
         int s = 0, n = 0;
         uint32_t phase = 0;
         bool ok = true;
         while (ok && iter.next(p, seg)) {
             const int l_row = (seg.l_blk * CG + int(rank)) * l_rows;
-            const int x_row = seg.c_blk * BN + int(rank) * Cfg::kXRows;
+            const int kb1 = seg.kb0 + (seg.kb1 - seg.kb0 + Cfg::kStep - 1) / Cfg::kStep * Cfg::kStep;
 #pragma unroll 1
-            for (int kb = seg.kb0; kb < seg.kb1; ++kb, ++n) {
-                ok = __all_sync(0xffffffffu,
-                                pipe_wait(bar_empty + 8 * s, phase ^ 1u, p, abort_flag, kStatusProducerTimeout));
+            for (int kb = seg.kb0; kb < kb1; ++kb, ++n) {
+                ok = warp_wait((GATED ? bar_empty : bar_wempty) + 8 * s, phase ^ 1u, p, abort_flag, kStatusProducerTimeout);
                 if (!ok)
                     break;
                 // test hook: the producer of CTA 0 never fills this stage of the launch
                 const bool stall = p.stall_kblock >= 0 && blockIdx.x == 0 && p.stall_kblock == n;
-                if (!stall) {
-                    if (rank == 0) {
-                        armed_mask |= 1u << s;
-                        armed_parity = (armed_parity & ~(1u << s)) | (phase << s);
-                    }
-                    warmed_mask |= 1u << s;
-                    warmed_parity = (warmed_parity & ~(1u << s)) | (phase << s);
-                }
+                if (!stall)
+                    arm(s, phase);
                 if (!stall && ptx::elect_one()) {
-                    const uint32_t fb = leader_full + 8 * s;
-                    const uint32_t dL = sL + uint32_t(s * Cfg::kLBytes), dX = sX + uint32_t(s * Cfg::kXBytes);
+                    const uint32_t dL = sL + uint32_t(s * Cfg::kLBytes);
                     const int k = kb * kLanesK;
-                    if (rank == 0)
-                        ptx::mbar_arrive_expect_tx(fb, uint32_t(CG * Cfg::kXBytes + (GATED ? 4 * l_rows * 128 : 0)));
-                    if (n == 0)  // all before it overlaps the kernel before
-                        ptx::grid_dependency_wait();
                     if constexpr (GATED) {
+                        const uint32_t fb = bar_full + 8 * s;
+                        ptx::mbar_arrive_expect_tx(fb, uint32_t(Cfg::kXBytes + 4 * l_rows * 128));
+                        if (n == 0)  // all before it overlaps the kernel before
+                            ptx::grid_dependency_wait();
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const uint32_t d = dL + uint32_t(i * 16384);
@@ -215,28 +234,48 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
                                 ptx::tma_load_2d(d + uint32_t(l_rows * 128), i ? &maps.w2 : &maps.w, fb, k + 64, l_row);
                             }
                         }
+                        load_x(sX + uint32_t(s * Cfg::kXBytes), fb, seg.c_blk * BN, kb);
                     } else {
-                        ptx::mbar_arrive_expect_tx(bar_wfull + 8 * s, uint32_t(l_rows * 128));
-                        ptx::tma_load_2d(dL, &maps.w, bar_wfull + 8 * s, k, l_row);
-                    }
-                    if (2 * kb + 2 <= p.c_chunks) {
-                        if constexpr (CG == 2)
-                            ptx::tma_load_3d_pair(dX, &maps.x3, fb, 0, x_row, 2 * kb);
-                        else
-                            ptx::tma_load_3d(dX, &maps.x3, fb, 0, x_row, 2 * kb);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t d = dX + uint32_t(i * Cfg::kXRows * 128);
-                            if constexpr (CG == 2)
-                                ptx::tma_load_2d_pair(d, &maps.x, fb, k + 64 * i, x_row);
-                            else
-                                ptx::tma_load_2d(d, &maps.x, fb, k + 64 * i, x_row);
+                        if (kb < seg.kb1) {
+                            ptx::mbar_arrive_expect_tx(bar_wfull + 8 * s, uint32_t(l_rows * 128));
+                            ptx::tma_load_2d(dL, &maps.w, bar_wfull + 8 * s, k, l_row);
+                        } else {
+                            ptx::mbar_arrive(bar_wfull + 8 * s);
                         }
                     }
                 }
                 __syncwarp();
-                if (++s == STAGES) {
+                if (++s == LS) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (!GATED && warp == 2) {
+        // ------------------------------------------------------ TMA producer of X
+        const uint32_t leader_full = CG == 2 ? ptx::map_to_cta(bar_full, 0) : bar_full;
+        ptx::grid_dependency_wait();  // what X is widened by
+        int s = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        while (ok && iter.next(p, seg)) {
+            const int x_row = seg.c_blk * BN + int(rank) * Cfg::kXRows;
+#pragma unroll 1
+            for (int kb = seg.kb0; kb < seg.kb1; kb += Cfg::kStep) {
+                ok = warp_wait(bar_empty + 8 * s, phase ^ 1u, p, abort_flag, kStatusProducerTimeout);
+                if (!ok)
+                    break;
+                if (rank == 0)
+                    arm(s, phase);
+                if (ptx::elect_one()) {
+                    const int count = min(Cfg::kStep, seg.kb1 - kb);
+                    if (rank == 0)
+                        ptx::mbar_arrive_expect_tx(bar_full + 8 * s, uint32_t(CG * count * Cfg::kXBytes));
+                    for (int i = 0; i < count; ++i)
+                        load_x(sX + uint32_t(s * Cfg::kXStep + i * Cfg::kXBytes), leader_full + 8 * s, x_row, kb + i);
+                }
+                __syncwarp();
+                if (++s == XS) {
                     s = 0;
                     phase ^= 1u;
                 }
@@ -248,58 +287,55 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
         const uint64_t x_desc0 = make_sdesc_sw128(sX);
         const uint32_t idesc = make_idesc(GATED ? p.dtype : int(BWGEMM_FP16), CG * Cfg::kLRows, BN);
         const uint32_t tmem0 = __shfl_sync(0xffffffffu, tmem_base, 0);
-        int s = 0, b = 0, a = 0;
-        uint32_t phase = 0, bphase = 0, aphase = 0;
+        int s = 0, b = 0;
+        uint32_t phase = 0, bphase = 0;
         bool ok = true;
         while (ok && iter.next(p, seg)) {
-            ok = __all_sync(0xffffffffu,
-                            pipe_wait(bar_acc_empty + 8 * b, bphase ^ 1u, p, abort_flag, kStatusMmaTimeout));
+            ok = warp_wait(bar_acc_empty + 8 * b, bphase ^ 1u, p, abort_flag, kStatusMmaTimeout);
 #pragma unroll 1
-            for (int kb = seg.kb0; ok && kb < seg.kb1; ++kb) {
-                ok = __all_sync(0xffffffffu, pipe_wait(bar_full + 8 * s, phase, p, abort_flag, kStatusMmaTimeout));
-                if constexpr (!GATED)
-                    if (ok)
-                        ok = __all_sync(0xffffffffu, pipe_wait(bar_afull + 8 * a, aphase, p, abort_flag, kStatusMmaTimeout));
+            for (int kb = seg.kb0; ok && kb < seg.kb1; kb += Cfg::kStep) {
+                ok = warp_wait(bar_full + 8 * s, phase, p, abort_flag, kStatusMmaTimeout);
                 if (!ok)
                     break;
                 ptx::tc_fence_after_sync();
                 if (ptx::elect_one()) {
-                    const uint64_t xd = x_desc0 + uint64_t((s * Cfg::kXBytes) >> 4);
+                    const uint64_t xd = x_desc0 + uint64_t((s * Cfg::kXStep) >> 4);
                     const uint32_t d = tmem0 + uint32_t(b * Cfg::kAccCols);
                     const uint32_t more = kb > seg.kb0 ? 1u : 0u;
 #pragma unroll
-                    for (int kk = 0; kk < kLanesK / 16; ++kk) {
-                        const uint64_t xk = xd + uint64_t(((kk >> 2) * Cfg::kXRows * 128 + (kk & 3) * 32) >> 4);
-                        if constexpr (GATED) {
-                            const uint64_t lk = l_desc0 + uint64_t((s * Cfg::kLBytes + (kk >> 2) * l_rows * 128 + (kk & 3) * 32) >> 4);
-                            ptx::mma_f16<1>(d, lk, xk, idesc, kk > 0 ? 1u : more);
-                            ptx::mma_f16<1>(d + BN, lk + uint64_t(16384 >> 4), xk, idesc, kk > 0 ? 1u : more);
-                        } else {
-                            ptx::mma_f16_tmem<CG>(d, tmem0 + uint32_t(Cfg::kACol0 + a * Cfg::kASlotCols + 8 * kk), xk, idesc,
-                                                  kk > 0 ? 1u : more);
+                    for (int i = 0; i < Cfg::kStep; ++i) {
+                        if (i > 0 && kb + i >= seg.kb1)
+                            break;
+#pragma unroll
+                        for (int kk = 0; kk < kLanesK / 16; ++kk) {
+                            const uint64_t xk =
+                                xd + uint64_t((i * Cfg::kXBytes + (kk >> 2) * Cfg::kXRows * 128 + (kk & 3) * 32) >> 4);
+                            const uint32_t on = i > 0 || kk > 0 ? 1u : more;
+                            if constexpr (GATED) {
+                                const uint64_t lk =
+                                    l_desc0 + uint64_t((s * Cfg::kLBytes + (kk >> 2) * l_rows * 128 + (kk & 3) * 32) >> 4);
+                                ptx::mma_f16<1>(d, lk, xk, idesc, on);
+                                ptx::mma_f16<1>(d + BN, lk + uint64_t(16384 >> 4), xk, idesc, on);
+                            } else {
+                                const uint32_t at = uint32_t(Cfg::kACol0 + s * Cfg::kASlotCols + i * Cfg::kACols + 8 * kk);
+                                ptx::mma_f16_tmem<CG>(d, tmem0 + at, xk, idesc, on);
+                            }
                         }
                     }
                     if constexpr (CG == 2) {
                         ptx::mma_commit_pair(bar_empty + 8 * s, 0x3);
-                        ptx::mma_commit_pair(bar_aempty + 8 * a, 0x3);
-                        if (kb == seg.kb1 - 1)
+                        if (kb + Cfg::kStep >= seg.kb1)
                             ptx::mma_commit_pair(bar_acc_full + 8 * b, 0x3);
                     } else {
                         ptx::mma_commit(bar_empty + 8 * s);
-                        if constexpr (!GATED)
-                            ptx::mma_commit(bar_aempty + 8 * a);
-                        if (kb == seg.kb1 - 1)
+                        if (kb + Cfg::kStep >= seg.kb1)
                             ptx::mma_commit(bar_acc_full + 8 * b);
                     }
                 }
                 __syncwarp();
-                if (++s == STAGES) {
+                if (++s == XS) {
                     s = 0;
                     phase ^= 1u;
-                }
-                if (++a == Cfg::kASlots) {
-                    a = 0;
-                    aphase ^= 1u;
                 }
             }
             if (++b == Cfg::kBufs) {
@@ -311,52 +347,56 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
         // ------------------------------------------------- 8-bit weights to fp16
         const int group = (warp - 4) >> 2, q = warp & 3;
         const int row = 32 * q + lane;
-        const uint32_t leader_afull = CG == 2 ? ptx::map_to_cta(bar_afull, 0) : bar_afull;
+        const uint32_t leader_full = CG == 2 ? ptx::map_to_cta(bar_full, 0) : bar_full;
         const uint32_t src0 = sL + uint32_t(row * 128);
         const uint32_t dst0 = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(Cfg::kACol0);
-        int s = 0, a = 0, turn = 0;
+        int s = group, a = 0;
         uint32_t phase = 0, aphase = 0;
         bool ok = true;
         while (ok && iter.next(p, seg)) {
 #pragma unroll 1
-            for (int kb = seg.kb0; kb < seg.kb1; ++kb) {
-                if (turn == group) {
-                    ok = __all_sync(0xffffffffu,
-                                    pipe_wait(bar_wfull + 8 * s, phase, p, abort_flag, kStatusMmaTimeout) &&
-                                        pipe_wait(bar_aempty + 8 * a, aphase ^ 1u, p, abort_flag, kStatusMmaTimeout));
-                    if (!ok)
-                        break;
-                    ptx::tc_fence_after_sync();
-                    const uint32_t src = src0 + uint32_t(s * Cfg::kLBytes);
+            for (int kb = seg.kb0; kb < seg.kb1; kb += Cfg::kStep) {
+                ok = warp_wait(bar_wfull + 8 * s, phase, p, abort_flag, kStatusMmaTimeout);
+                if (!ok)
+                    break;
+                const uint32_t src = src0 + uint32_t(s * Cfg::kLBytes);
+                uint32_t w[8][4];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t r[32];
+                for (int c = 0; c < 8; ++c)
+                    ptx::ld_shared_v4(src + (uint32_t(c ^ (row & 7)) << 4), w[c][0], w[c][1], w[c][2], w[c][3]);
+                ok = warp_wait(bar_empty + 8 * a, aphase ^ 1u, p, abort_flag, kStatusMmaTimeout);
+                if (!ok)
+                    break;
+                ptx::tc_fence_after_sync();
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t w[4];
-                            ptx::ld_shared_v4(src + (uint32_t((4 * half + c) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t r[32];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                widen4(w[i], r[8 * c + 2 * i], r[8 * c + 2 * i + 1]);
-                        }
-                        ptx::tmem_st_32x32b_x32(dst0 + uint32_t(a * Cfg::kASlotCols + 32 * half), r);
+                    for (int i = 0; i < 16; ++i)
+                        widen4(w[4 * half + i / 4][i % 4], r[2 * i], r[2 * i + 1]);
+                    if (half == 0) {  // the stage is in registers
+                        __syncwarp();
+                        if (lane == 0)
+                            ptx::mbar_arrive(bar_wempty + 8 * s);
                     }
-                    ptx::tmem_st_wait();
-                    ptx::tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (CG == 2)
-                            ptx::mbar_arrive_cluster_relaxed(leader_afull + 8 * a);
-                        else
-                            ptx::mbar_arrive(bar_afull + 8 * a);
-                    }
+                    if (kb + group < seg.kb1)
+                        ptx::tmem_st_32x32b_x32(dst0 + uint32_t(a * Cfg::kASlotCols + group * Cfg::kACols + 32 * half), r);
                 }
-                turn = turn + 1 == Cfg::kConvGroups ? 0 : turn + 1;
-                if (++s == STAGES) {
-                    s = 0;
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 2)
+                        ptx::mbar_arrive_cluster_relaxed(leader_full + 8 * a);
+                    else
+                        ptx::mbar_arrive(bar_full + 8 * a);
+                }
+                s += Cfg::kStep;
+                if (s >= LS) {
+                    s -= LS;
                     phase ^= 1u;
                 }
-                if (++a == Cfg::kASlots) {
+                if (++a == XS) {
                     a = 0;
                     aphase ^= 1u;
                 }
@@ -434,8 +474,7 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
                     }
                 }
             };
-            ok = __all_sync(0xffffffffu,
-                            pipe_wait(bar_acc_full + 8 * b, bphase, p, abort_flag, kStatusEpilogueTimeout));
+            ok = warp_wait(bar_acc_full + 8 * b, bphase, p, abort_flag, kStatusEpilogueTimeout);
             if (!ok)
                 break;
             ptx::tc_fence_after_sync();
@@ -544,14 +583,12 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
             __syncwarp();
             drain_wait(bar_drain, 0u, kDrainNs);
         }
-        if (warp == 0) {
+        if (warp == 0 || (!GATED && warp == 2)) {
+            const uint32_t bar = GATED || warp == 2 ? bar_full : bar_wfull;
 #pragma unroll 1
-            for (int s = 0; s < STAGES; ++s) {
+            for (int s = 0; s < (GATED || warp == 2 ? XS : LS); ++s)
                 if ((armed_mask >> s) & 1u)
-                    drain_wait(bar_full + 8 * s, (armed_parity >> s) & 1u, kDrainNs);
-                if (!GATED && ((warmed_mask >> s) & 1u))
-                    drain_wait(bar_wfull + 8 * s, (warmed_parity >> s) & 1u, kDrainNs);
-            }
+                    drain_wait(bar + 8 * s, (armed_parity >> s) & 1u, kDrainNs);
             if (lane == 0)
                 settle(kSettleNs);
         }

