@@ -8,6 +8,7 @@ cannot be loaded the calls raise; there is no host-side fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 import threading
@@ -383,36 +384,36 @@ _MATRIX = struct.Struct("@Pq")
 assert _MATRIX.size == ctypes.sizeof(Matrix)
 
 
-def _pack_matrix(t, name: str, rows: int, cols: int, dtype, device: int):
-    """The bytes of a bwgemm_matrix_t of the rows x cols CUDA tensor `t`.  Strides are passed as
-    they are: rows closer than their length are refused by the library."""
+def _pack_matrix(t, name: str, shape: tuple, dtype, device: int):
+    """The bytes of a bwgemm_matrix_t of the CUDA tensor `t`, which must have this shape, type and
+    device.  Strides are passed as they are: rows closer than their length are refused by the
+    library."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, the plan on cuda:{device}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError(f"{name} must be {rows} x {cols}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {shape[0]} x {shape[1]}, got {tuple(t.shape)}")
     ld, unit = t.stride()
-    if unit != 1 and cols > 1:
+    if unit != 1 and shape[1] > 1:
         raise ValueError(f"{name} must be row-major (unit stride along the last dim)")
-    if rows <= 1:
-        ld = (cols + 7) & -8  # a single row has no next one
+    if shape[0] <= 1:
+        ld = (shape[1] + 7) & -8  # a single row has no next one
     return _MATRIX.pack(t.data_ptr(), ld)
 
 
 def _int8_operand(t, scale, name: str, device: int):
     """(rows, K, bytes between rows) of the 8-bit integers `t` with a scale per row."""
-    torch = _torch_mod
-    if t.dtype is not torch.int8:
+    if t.dtype is not _torch_mod.int8:
         raise TypeError(f"{name} must be int8, got {t.dtype}")
-    if scale.dtype is not torch.float32:
+    if scale.dtype is not _torch_mod.float32:
         raise TypeError(f"the scales of {name} must be float32, got {scale.dtype}")
     if t.get_device() != device or scale.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, its scales on {scale.device}, the plan on cuda:{device}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, K = t.shape
-    if scale.dim() != 1 or scale.shape[0] != rows:
+    if scale.shape != (rows,):
         raise ValueError(f"{name} has {rows} rows, its scales have the shape {tuple(scale.shape)}")
     ld, unit = t.stride()
     if (unit != 1 and K > 1) or (rows > 1 and scale.stride(0) != 1):
@@ -420,6 +421,16 @@ def _int8_operand(t, scale, name: str, device: int):
     if rows <= 1:
         ld = (K + 15) & -16  # a single row has no next one
     return rows, K, ld
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(name: str, *sizes) -> int:
+    """What the library's workspace query `name` answers for these sizes."""
+    need = ctypes.c_uint64()
+    rc = getattr(load_library(), name)(*sizes, ctypes.byref(need))
+    if rc != 0:
+        raise BwgemmError(rc, name)
+    return need.value
 
 
 def _activation_code(activation) -> int:
@@ -787,17 +798,19 @@ class Plan:
             raise ValueError("x and the weights must be 2-D")
         M, K = x.shape
         N = w_gate.shape[0]
-        xm = _pack_matrix(x, "x", M, K, dtype, dev)
-        gm = _pack_matrix(w_gate, "w_gate", N, K, dtype, dev)
-        um = _pack_matrix(w_up, "w_up", N, K, dtype, dev)
-        ld = (N + 7) & -8
-        outs = [_padded_empty(M, N, dtype, x.device, 8) for _ in range(3 if keep else 1)]
-        records = [_MATRIX.pack(t.data_ptr(), ld) for t in outs] + [None] * (3 - len(outs))
-        rc = self.lib.bwgemm_gated(self.handle, xm, gm, um, *records, M, N, K, dt, act,
+        weight = (N, K)
+        xm = _pack_matrix(x, "x", (M, K), dtype, dev)
+        gm = _pack_matrix(w_gate, "w_gate", weight, dtype, dev)
+        um = _pack_matrix(w_up, "w_up", weight, dtype, dev)
+        ld, device = (N + 7) & -8, x.device
+        out = _padded_empty(M, N, dtype, device, 8)
+        kept = (_padded_empty(M, N, dtype, device, 8), _padded_empty(M, N, dtype, device, 8)) if keep else ()
+        records = [_MATRIX.pack(t.data_ptr(), ld) for t in kept] or (None, None)
+        rc = self.lib.bwgemm_gated(self.handle, xm, gm, um, _MATRIX.pack(out.data_ptr(), ld), *records, M, N, K, dt, act,
                                    torch._C._cuda_getCurrentRawStream(dev))
         if rc != 0:
             raise BwgemmError(rc, "bwgemm_gated")
-        return tuple(outs) if keep else outs[0]
+        return (out, *kept) if keep else out
 
     def gated_linear_backward(self, dh, gate, up, x, w_gate, w_up, activation: str = "silu", input_grad: bool = True,
                               weight_grads: bool = True, stream=None):
@@ -818,20 +831,19 @@ class Plan:
             raise ValueError("dh, x and the weights must be 2-D")
         M, N = dh.shape
         K = wide.shape[1]
-        records = [_pack_matrix(t, name, M, N, dtype, dev) for t, name in ((dh, "dh"), (gate, "gate"), (up, "up"))]
-        records.append(_pack_matrix(x, "x", M, K, dtype, dev) if weight_grads else None)
+        kept, weight, device = (M, N), (N, K), dh.device
+        records = [_pack_matrix(t, name, kept, dtype, dev) for t, name in ((dh, "dh"), (gate, "gate"), (up, "up"))]
+        records.append(_pack_matrix(x, "x", (M, K), dtype, dev) if weight_grads else None)
         for t, name in ((w_gate, "w_gate"), (w_up, "w_up")):
-            records.append(_pack_matrix(t, name, N, K, dtype, dev) if input_grad else None)
+            records.append(_pack_matrix(t, name, weight, dtype, dev) if input_grad else None)
         ld = (K + 7) & -8
-        dx = _padded_empty(M, K, dtype, dh.device, 8) if input_grad else None
-        dwg, dwu = (_padded_empty(N, K, dtype, dh.device, 8) if weight_grads else None for _ in range(2))
+        dx = _padded_empty(M, K, dtype, device, 8) if input_grad else None
+        dwg = _padded_empty(N, K, dtype, device, 8) if weight_grads else None
+        dwu = _padded_empty(N, K, dtype, device, 8) if weight_grads else None
         records += [None if t is None else _MATRIX.pack(t.data_ptr(), ld) for t in (dx, dwg, dwu)]
-        need = ctypes.c_uint64()
-        rc = self.lib.bwgemm_gated_backward_workspace(M, N, ctypes.byref(need))
-        if rc != 0:
-            raise BwgemmError(rc, "bwgemm_gated_backward_workspace")
-        ws = torch.empty(need.value, dtype=torch.uint8, device=dh.device)
-        rc = self.lib.bwgemm_gated_backward(self.handle, *records, M, N, K, dt, act, ws.data_ptr(), need.value,
+        need = _workspace_bytes("bwgemm_gated_backward_workspace", M, N)
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        rc = self.lib.bwgemm_gated_backward(self.handle, *records, M, N, K, dt, act, ws.data_ptr(), need,
                                             torch._C._cuda_getCurrentRawStream(dev))
         if rc != 0:
             raise BwgemmError(rc, "bwgemm_gated_backward")
@@ -901,14 +913,11 @@ class Plan:
                 raise ValueError("out must be row-major (unit stride along the last dim)")
             if M <= 1:
                 ldc = (N + 7) & -8  # a single row has no next one
-        need = ctypes.c_uint64()
-        rc = self.lib.bwgemm_run_integer_workspace(M, N, K, ctypes.byref(need))
-        if rc != 0:
-            raise BwgemmError(rc, "bwgemm_run_integer_workspace")
-        ws = torch.empty(need.value, dtype=torch.uint8, device=A.device) if need.value else None
+        need = _workspace_bytes("bwgemm_run_integer_workspace", M, N, K)
+        ws = torch.empty(need, dtype=torch.uint8, device=A.device) if need else None
         rc = self.lib.bwgemm_run_integer(self.handle, A.data_ptr(), scale_a.data_ptr(), B.data_ptr(), scale_b.data_ptr(),
-                                      out.data_ptr(), M, N, K, lda, ldb, ldc, dt, ws.data_ptr() if ws is not None else None,
-                                      need.value, torch._C._cuda_getCurrentRawStream(dev))
+                                         out.data_ptr(), M, N, K, lda, ldb, ldc, dt, ws.data_ptr() if need else None, need,
+                                         torch._C._cuda_getCurrentRawStream(dev))
         if rc != 0:
             raise BwgemmError(rc, "bwgemm_run_integer")
         return out

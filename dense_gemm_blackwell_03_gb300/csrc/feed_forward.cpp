@@ -1,6 +1,6 @@
 // feed_forward.cpp -- argument checks, tensor maps and work division of the gated
 // feed-forward layer and of the 8-bit integer product.
-#include <cstring>
+#include <cmath>
 
 #include "feed_forward.h"
 #include "operators_host.h"
@@ -32,27 +32,33 @@ CUtensorMapDataType type16(int dtype)
     return dtype == BWGEMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
-// A 16-bit operand in boxes of 64 elements x box_rows, and in boxes of two whole
-// 64-element chunks (the same map again where its rows hold no two).
+// A 16-bit operand in boxes of two whole 64-element chunks x box_rows (map3), and of one
+// (map), which is read at the end of rows that are no multiple of 128.  A map that no copy
+// uses is a copy of the other.
 bwgemm_status_t encode_operand16(CUtensorMap* map, CUtensorMap* map3, const void* data, int64_t ld, int dtype, int64_t rows,
                                  int64_t cols, uint32_t box_rows)
 {
+    const int64_t chunks = cols / 64;
+    if (chunks >= 2) {
+        const cuuint64_t dims3[3] = {64, cuuint64_t(rows), cuuint64_t(chunks)};
+        const cuuint64_t strides3[2] = {cuuint64_t(ld) * 2, 128};
+        const cuuint32_t box3[3] = {64, box_rows, 2};
+        const bwgemm_status_t st = encode(map3, type16(dtype), 3, data, dims3, strides3, box3, CU_TENSOR_MAP_SWIZZLE_128B,
+                                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+        if (st != BWGEMM_OK)
+            return st;
+        *map = *map3;
+        if (cols % 128 == 0)
+            return BWGEMM_OK;
+    }
     const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
     const cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
     const cuuint32_t box[2] = {64, box_rows};
     const bwgemm_status_t st = encode(map, type16(dtype), 2, data, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
                                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-    if (st != BWGEMM_OK)
-        return st;
-    *map3 = *map;
-    const int64_t chunks = cols / 64;
     if (chunks < 2)
-        return BWGEMM_OK;
-    const cuuint64_t dims3[3] = {64, cuuint64_t(rows), cuuint64_t(chunks)};
-    const cuuint64_t strides3[2] = {cuuint64_t(ld) * 2, 128};
-    const cuuint32_t box3[3] = {64, box_rows, 2};
-    return encode(map3, type16(dtype), 3, data, dims3, strides3, box3, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+        *map3 = *map;
+    return st;
 }
 
 bwgemm_status_t encode_result16(CUtensorMap* map, const bwgemm_matrix_t& x, int dtype, int64_t rows, int64_t cols)
@@ -72,15 +78,13 @@ struct LanesPlan {
     double us;
 };
 
-// Microseconds of 128 of K of a tile on its CTA or pair: the bytes' way into shared
-// memory (150 GB/s and SM), or the MMAs (M = 64 runs at half the rate of M = 128).
-double lanes_step_us(const LanesVariant& v, int l_rows)
+// Microseconds of 128 of K of a tile on its CTA or pair, weights at hand: the way of a step
+// through its barriers, the MMAs, and the widening.  Fitted to 4 to 333 rows on eight shapes.
+double lanes_step_us(const LanesVariant& v)
 {
     if (v.mode == kLanesGated)
-        return std::max((2.0 * l_rows + v.bn) * 256.0 / 150e3, 0.0043 * v.bn);
-    if (v.cg == 2)
-        return 0.56;
-    return std::max(0.14, (l_rows * 128.0 + v.bn * 256.0) / 150e3);
+        return v.bn == 128 ? 0.83 : v.bn == 64 ? 0.54 : v.bn == 32 ? 0.42 : 0.36;
+    return v.cg == 2 ? 0.57 : v.bn == 128 ? 0.46 : v.bn == 64 ? 0.37 : 0.25;
 }
 
 LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N, int64_t K,
@@ -98,7 +102,7 @@ LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N,
             continue;
         const int most = v.mode == kLanesGated ? 64 : 128 * v.cg;  // weight rows per tile
         const int64_t nc = (M + v.bn - 1) / v.bn;
-        for (int low = 0; low <= (v.cg == 1 ? 1 : 0); ++low) {
+        for (int low = v.cg == 1 ? 1 : 0; low >= 0; --low) {
             LanesPlan s = {};
             s.variant = i;
             s.l_rows = most;
@@ -118,7 +122,8 @@ LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N,
             const uint64_t slot_bytes = uint64_t(lanes_partial_floats(mode, v.bn)) * 4 * v.cg;
             const bool room = kCounterRegionBytes + uint64_t(W) * 2 * slot_bytes <= workspace_bytes &&
                               uint64_t(rest) * v.cg * lanes_epi_warps(v.bn) * 4 <= kCounterRegionBytes;
-            for (int spread = 0; spread <= (rest > 0 && room && rest * kb < (1ll << 30) ? 1 : 0); ++spread) {
+            // (spread: over all workers, or, where there is no full wave, over 8, 4 or 2 a tile)
+            for (int spread = 0; spread <= (rest > 0 && room && rest * kb < (1ll << 30) ? (full == 0 ? 4 : 1) : 0); ++spread) {
                 s.workers = int(std::min<int64_t>(tiles, W));
                 s.dp_tiles = int(tiles);
                 s.sk_tiles = s.sk_iters = 0;
@@ -127,18 +132,22 @@ LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N,
                     s.sk_tiles = int(rest);
                     s.sk_iters = int(rest * kb);
                     s.workers = full == 0 ? std::max(std::min(W, s.sk_iters / 4), 1) : W;
+                    if (spread > 1)
+                        s.workers = int(std::min<int64_t>(s.workers, rest << (5 - spread)));
                 }
-                const double us = lanes_step_us(v, s.l_rows);
+                const double us = lanes_step_us(v);
                 double t = double((s.dp_tiles + s.workers - 1) / s.workers) * double(kb) * us;
-                if (spread) {
-                    // a piece's partial tile out, the fence and the counter, and the pieces of
-                    // a tile in again by one CTA
-                    const double pieces = double(s.workers) / double(rest);
+                if (spread)
                     t += double((s.sk_iters + s.workers - 1) / s.workers) * us;
-                    t += 4.0 + (1.0 + pieces) * double(slot_bytes) / v.cg / 200e3;
-                }
-                // the weights once from HBM, and again from L2 or HBM for every block of rows
+                // the weights once from HBM; bound by that, the form with the least work of its own
                 t = std::max(t, weights / 6.5e6) + 0.1 * t;
+                if (spread) {
+                    // a piece's partial tile out, the fence, the counter, and the pieces of a tile
+                    // in again by the warps that come last, a few at a time
+                    const int cols = v.bn / (lanes_epi_warps(v.bn) / 4), width = std::min(cols, 32);
+                    const int pieces = int((s.workers + rest - 1) / rest) + 1;
+                    t += 7.0 + 0.8 * (cols / width) * std::ceil(double(pieces) / lanes_flight(mode, width));
+                }
                 if (best.workers == 0 || t < best.us) {
                     s.us = t;
                     best = s;
@@ -241,18 +250,37 @@ GatedPlan plan_gated(int num_sms, int max_pairs, int64_t M, int64_t N, int64_t K
     if (pairs < 1 || g.num_r * g.num_c >= (1ll << 31))
         return g;
     g.workers = int(std::min<int64_t>(g.num_r * g.num_c, pairs));
-    const double waves = double((g.num_r * g.num_c + pairs - 1) / pairs);
-    const double us = std::max(waves * double(blocks_of(K)) * 0.56 + 2.0, double(N) * double(K) * 4 / 6.5e6);
+    // measured, lanes against pairs: 64 x 28672 x 8192 149 and 158 us, 128 x 28672 x 8192 165 and 159,
+    // 64 x 10240 x 8192 71 and 93, 100 x 10240 x 8192 113 and 93, 200 x 4096 x 4096 33 and 24,
+    // 333 x 1000 x 5005 27 and 29
+    const double waves = double((g.num_r * g.num_c + pairs - 1) / pairs), t = waves * double(blocks_of(K)) * 0.6;
+    const double us = std::max(t, double(N) * double(K) * 4 / 6.5e6) + 0.1 * t;
     g.lanes = g.l.workers > 0 && g.l.us < us;
     return g;
 }
 
-// Whether the kernel for few rows takes the product.
+// Whether the kernel for few rows takes the product.  Measured in us, it against tiles: integers
+// 8 x 28672 x 8192 44 and 46, 16 x 28672 x 8192 59 and 46, 12 x 8192 x 8192 23.2 and 20.4, 16 x 4096 x
+// 4096 8.3 and 14.7; gated 1 x 10240 x 8192 51.7 and 56.5, 2 55.3 and 56.5, 4 62 and 57, 8 x 8192 x
+// 8192 45.0 and 42.9, 16 x 4096 x 4096 15.1 and 16.6.
 bool takes_few_rows(int mode, int64_t M, int64_t N, int64_t K)
 {
-    if (M > kFewMost || (mode == kLanesInt8 && K > kFewIntegerK))
+    if (M > kFewMost)
         return false;
-    return true;
+    const double weights = double(N) * double(K);
+    if (mode == kLanesInt8)
+        return K <= kFewIntegerK && (M <= 8 || weights <= 48e6);
+    return M <= 2 || weights <= 32e6;
+}
+
+// Its warps per CTA: eight, so that many CTAs share an SM; more where there are too few of
+// them and K is deep (us with 8, 16 and 32 warps, one row: integers 512 x 28672 23.5, 14.3, 10.8,
+// 2048 x 4096 5.2, 4.4, 4.5, 1024 x 1024 1.8, 2.0, 2.3, 8192 x 8192 14.4, 16.8, 20.5; gated
+// 512 x 8192 12.3, 7.5, 6.3, 4096 x 4096 12.7, 14.2, 17.5).
+int few_warps(int kind, int64_t N, int64_t row_bytes)
+{
+    const int64_t ctas = (N + few_rows(kind) - 1) / few_rows(kind), blocks = row_bytes / 128;
+    return ctas <= 64 && blocks >= 64 ? 32 : ctas <= 256 && blocks >= 32 ? 16 : 8;
 }
 
 int pairs_of(bwgemm_plan_t plan) { return plan->max_active[find_variant(2, 256, false, 1)]; }
@@ -347,7 +375,7 @@ bwgemm_status_t bwgemm_gated(bwgemm_plan_t plan, const bwgemm_matrix_t* X, const
             p.out[i] = out[i]->data;
             p.ldo[i] = out[i]->ld;
         }
-        if (launch_few_rows(dtype == BWGEMM_BF16 ? kFewBf16 : kFewFp16, p, s, pdl) != cudaSuccess)
+        if (launch_few_rows(dtype == BWGEMM_BF16 ? kFewBf16 : kFewFp16, few_warps(kFewBf16, N, p.row_bytes), p, s, pdl) != cudaSuccess)
             return BWGEMM_ERR_CUDA;
         plan->launches += 1;
         return BWGEMM_OK;
@@ -456,12 +484,10 @@ bwgemm_status_t bwgemm_gated_backward(bwgemm_plan_t plan, const bwgemm_matrix_t*
         if (of_w && (st = check_matrix(X, M, K)) != BWGEMM_OK)
             return st;
         bwgemm_gated_backward_workspace(M, N, &need);
-        if (!workspace)
-            return BWGEMM_ERR_INVALID_ARG;
+        if (workspace_bytes < need || !workspace)
+            return BWGEMM_ERR_WORKSPACE;
         if (!aligned(workspace, 256))
             return BWGEMM_ERR_ALIGNMENT;
-        if (workspace_bytes < need)
-            return BWGEMM_ERR_WORKSPACE;
     }
     DeviceGuard guard(plan->device);
     if (!guard.ok)
@@ -540,13 +566,16 @@ bwgemm_status_t bwgemm_gated_backward(bwgemm_plan_t plan, const bwgemm_matrix_t*
             const bwgemm_matrix_t& w = *(i ? dWu : dWg);
             mw.a[i] = dm[i];
             mw.a3[i] = dm3[i];
-            if ((st = encode_operand16(&mw.b[i], &mw.b3[i], X->data, X->ld, dtype, M, K, 128)) != BWGEMM_OK ||
-                (st = encode_result16(&mw.out[i], w, dtype, N, K)) != BWGEMM_OK)
+            if ((st = encode_result16(&mw.out[i], w, dtype, N, K)) != BWGEMM_OK)
                 return st;
             pw.out[i] = static_cast<uint16_t*>(w.data);
             pw.ldo[i] = w.ld;
         }
         mw.out[2] = mw.out[0];
+        if ((st = encode_operand16(&mw.b[0], &mw.b3[0], X->data, X->ld, dtype, M, K, 128)) != BWGEMM_OK)
+            return st;
+        mw.b[1] = mw.b[0];
+        mw.b3[1] = mw.b3[0];
     }
     if (launch_gate_grad(gg, s, pdl) != cudaSuccess)
         return BWGEMM_ERR_CUDA;
@@ -615,7 +644,7 @@ bwgemm_status_t bwgemm_run_integer(bwgemm_plan_t plan, const int8_t* A, const fl
     if (st != BWGEMM_OK || M == 0 || N == 0)
         return st;
     const int es = element_size(out);
-    if (!C || ldc < N || (K > 0 && (!A || !B || !scale_a || !scale_b || lda < K || ldb < K)) || (need > 0 && !workspace))
+    if (!C || ldc < N || (K > 0 && (!A || !B || !scale_a || !scale_b || lda < K || ldb < K)))
         return BWGEMM_ERR_INVALID_ARG;
     if (!extent_ok(M, N, ldc) || (K > 0 && (!extent_ok(M, K, lda) || !extent_ok(N, K, ldb))))
         return BWGEMM_ERR_UNSUPPORTED;
@@ -623,7 +652,7 @@ bwgemm_status_t bwgemm_run_integer(bwgemm_plan_t plan, const int8_t* A, const fl
         (K > 0 && (!aligned(A, 16) || lda % 16 != 0 || !aligned(B, 16) || ldb % 16 != 0 || !aligned(scale_a, 4) ||
                    !aligned(scale_b, 4) || (need > 0 && !aligned(workspace, 256)))))
         return BWGEMM_ERR_ALIGNMENT;
-    if (workspace_bytes < need)
+    if (workspace_bytes < need || (need > 0 && !workspace))
         return BWGEMM_ERR_WORKSPACE;
     DeviceGuard guard(plan->device);
     if (!guard.ok)
@@ -651,7 +680,7 @@ bwgemm_status_t bwgemm_run_integer(bwgemm_plan_t plan, const int8_t* A, const fl
         p.out_type = out;
         p.out[0] = C;
         p.ldo[0] = ldc;
-        if (launch_few_rows(kFewInt8, p, s, pdl) != cudaSuccess)
+        if (launch_few_rows(kFewInt8, few_warps(kFewInt8, N, p.row_bytes), p, s, pdl) != cudaSuccess)
             return BWGEMM_ERR_CUDA;
         plan->launches += 1;
         return BWGEMM_OK;

@@ -19,11 +19,8 @@
 namespace bwgemm {
 namespace {
 
-constexpr int kFewWarps = 8;
-constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kFewRing = 3;
 constexpr int kFewBlock = 2048;  // 16 rows of 128 bytes
-constexpr int kFewSmem = kFewWarps * kFewRing * kFewBlock;
 
 // 16 bytes of a row at byte k, zeros from byte `len` on, where nothing is read.
 __device__ __forceinline__ uint4 load_ragged(const uint8_t* row, int64_t k, int64_t len)
@@ -66,11 +63,11 @@ __device__ __forceinline__ uint16_t round_to(float v, int dtype)
 }
 
 // NT: groups of 8 rows of X (1 or 2).
-template <int KIND, int NT>
-__global__ void __launch_bounds__(kFewThreads, 4) few_rows_kernel(const FewRowsParams p)
+template <int KIND, int NT, int kFewWarps>
+__global__ void __launch_bounds__(32 * kFewWarps, 32 / kFewWarps) few_rows_kernel(const FewRowsParams p)
 {
     constexpr bool INT8 = KIND == kFewInt8;
-    constexpr int ROWS = INT8 ? 16 : 8;  // columns of the result per CTA
+    constexpr int ROWS = few_rows(KIND);
     extern __shared__ __align__(16) uint8_t few_smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, q = lane & 3;
@@ -190,35 +187,50 @@ __global__ void __launch_bounds__(kFewThreads, 4) few_rows_kernel(const FewRowsP
     }
 }
 
-template <int KIND, int NT>
+template <int KIND, int NT, int WARPS>
 cudaError_t launch_one(const FewRowsParams& p, cudaStream_t stream, bool pdl)
 {
-    constexpr int ROWS = KIND == kFewInt8 ? 16 : 8;
+    constexpr int kRows = few_rows(KIND), kSmem = WARPS * kFewRing * kFewBlock;
+    auto kernel = few_rows_kernel<KIND, NT, WARPS>;
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_smem(kernel, kSmem, allowed);
+    if (err != cudaSuccess)
+        return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned((p.N + ROWS - 1) / ROWS), 1, 1);
-    cfg.blockDim = dim3(kFewThreads, 1, 1);
-    cfg.dynamicSmemBytes = kFewSmem;
+    cfg.gridDim = dim3(unsigned((p.N + kRows - 1) / kRows), 1, 1);
+    cfg.blockDim = dim3(32 * WARPS, 1, 1);
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    static_assert(kFewSmem <= 48 * 1024, "more would have to be allowed first");
-    return cudaLaunchKernelEx(&cfg, few_rows_kernel<KIND, NT>, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int KIND, int NT>
+cudaError_t launch_warps(int warps, const FewRowsParams& p, cudaStream_t stream, bool pdl)
+{
+    switch (warps) {
+    case 8: return launch_one<KIND, NT, 8>(p, stream, pdl);
+    case 16: return launch_one<KIND, NT, 16>(p, stream, pdl);
+    case 32: return launch_one<KIND, NT, 32>(p, stream, pdl);
+    default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_few_rows(int kind, const FewRowsParams& p, cudaStream_t stream, bool pdl)
+cudaError_t launch_few_rows(int kind, int warps, const FewRowsParams& p, cudaStream_t stream, bool pdl)
 {
     switch (2 * kind + (p.M > 8)) {
-    case 2 * kFewInt8: return launch_one<kFewInt8, 1>(p, stream, pdl);
-    case 2 * kFewInt8 + 1: return launch_one<kFewInt8, 2>(p, stream, pdl);
-    case 2 * kFewBf16: return launch_one<kFewBf16, 1>(p, stream, pdl);
-    case 2 * kFewBf16 + 1: return launch_one<kFewBf16, 2>(p, stream, pdl);
-    case 2 * kFewFp16: return launch_one<kFewFp16, 1>(p, stream, pdl);
-    case 2 * kFewFp16 + 1: return launch_one<kFewFp16, 2>(p, stream, pdl);
+    case 2 * kFewInt8: return launch_warps<kFewInt8, 1>(warps, p, stream, pdl);
+    case 2 * kFewInt8 + 1: return launch_warps<kFewInt8, 2>(warps, p, stream, pdl);
+    case 2 * kFewBf16: return launch_warps<kFewBf16, 1>(warps, p, stream, pdl);
+    case 2 * kFewBf16 + 1: return launch_warps<kFewBf16, 2>(warps, p, stream, pdl);
+    case 2 * kFewFp16: return launch_warps<kFewFp16, 1>(warps, p, stream, pdl);
+    case 2 * kFewFp16 + 1: return launch_warps<kFewFp16, 2>(warps, p, stream, pdl);
     default: return cudaErrorInvalidValue;
     }
 }

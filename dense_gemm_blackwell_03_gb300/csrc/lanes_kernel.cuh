@@ -62,7 +62,7 @@ struct LanesConfig {
     static constexpr int kRingBytes = 222 * 1024;
     static constexpr int kStep = !kGated && BN <= 64 ? 2 : 1;
     static constexpr int kXStep = kStep * kXBytes;
-    static constexpr int kXStages = kGated ? kRingBytes / (kLBytes + kXBytes) : BN == 64 ? 2 : 3;
+    static constexpr int kXStages = kGated ? kRingBytes / (kLBytes + kXBytes) : 3;
     static constexpr int kConvGroups = kGated ? 0 : kStep;
     static constexpr int kFit = (kRingBytes - kXStages * kXStep) / kLBytes;
     static constexpr int kLStages = kGated ? kXStages : (kFit > 10 ? 10 : kFit) / kStep * kStep;
@@ -546,20 +546,33 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < P; ++j)
                         f[i][j] = 0.f;
+                // pieces on their way at once, added in order
+                constexpr int FLIGHT = lanes_flight(MODE, P);
 #pragma unroll 1
-                for (int w = w0; w <= w1; ++w) {
-                    const int wslot = ScaledIter::begin(p, w, workers) / p.num_kb == st ? 0 : 1;
-                    const float* src = p.partials + ((size_t(w) * 2 + wslot) * CG + rank) * kStride + mine + size_t(c) * 32;
+                for (int w = w0; w <= w1; w += FLIGHT) {
+                    uint4 x[FLIGHT][MATS][P / 4];
 #pragma unroll
-                    for (int i = 0; i < MATS; ++i)
+                    for (int k = 0; k < FLIGHT; ++k) {
+                        if (w + k > w1)
+                            break;
+                        const int wslot = ScaledIter::begin(p, w + k, workers) / p.num_kb == st ? 0 : 1;
+                        const float* src = p.partials + ((size_t(w + k) * 2 + wslot) * CG + rank) * kStride + mine + size_t(c) * 32;
 #pragma unroll
-                        for (int j = 0; j < P; j += 4) {
-                            const uint4 x = ptx::ld_global_cg_v4(src + size_t(i) * 32 * Cfg::kCols + size_t(j) * 32);
-                            f[i][j] += __uint_as_float(x.x);
-                            f[i][j + 1] += __uint_as_float(x.y);
-                            f[i][j + 2] += __uint_as_float(x.z);
-                            f[i][j + 3] += __uint_as_float(x.w);
-                        }
+                        for (int i = 0; i < MATS; ++i)
+#pragma unroll
+                            for (int j = 0; j < P; j += 4)
+                                x[k][i][j / 4] = ptx::ld_global_cg_v4(src + size_t(i) * 32 * Cfg::kCols + size_t(j) * 32);
+                    }
+#pragma unroll
+                    for (int k = 0; k < FLIGHT; ++k) {
+                        if (w + k > w1)
+                            break;
+#pragma unroll
+                        for (int i = 0; i < MATS; ++i)
+#pragma unroll
+                            for (int j = 0; j < P; ++j)
+                                f[i][j] += __uint_as_float((&x[k][i][j / 4].x)[j % 4]);
+                    }
                 }
                 finish(c, f);
             }
