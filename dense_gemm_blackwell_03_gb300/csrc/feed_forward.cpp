@@ -160,73 +160,87 @@ LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N,
 }
 
 // ------------------------------------------------------------- tiles of products
+// The gradients' products.  No workers where there is no division.
 struct PairPlan {
+    PairProduct prod[2];
     int cg;
-    int64_t tiles;    // of all results
-    int64_t workers;  // CTAs or pairs; 0: none
+    int workers;  // CTAs or pairs
 };
 
-// One gradient product: tiles of 256 on CTA pairs (1024 SM cycles per 128 of K, bound by
-// the MMAs) or of 128 on single CTAs (about 740, bound by the copies of both operands),
-// whichever takes fewer cycles in its waves; a deep K of few tiles in slices, whose join
-// costs a kernel more and the way of its bytes.  Fills in p's division of the work.
-PairPlan plan_pair(PairParams* p, int singles, int pairs, uint64_t workspace_bytes)
+// The longest worker's cycles when `workers` take the units of both products in turn.
+int64_t pair_cycles(const PairProduct (&d)[2], int64_t workers, int64_t step)
 {
-    PairPlan out = {};
-    int64_t tiles[3] = {}, best = 0;
-    const int64_t steps = int64_t(p->steps_k) * p->terms;
+    int64_t most = 0;
+    const int64_t first = d[0].units % workers;
+    // the workers that the last of dX's, and of the weights', units end at, and the ones after
+    for (int64_t w : {int64_t(0), first, (first + d[1].units) % workers, workers - 1}) {
+        int64_t cycles = 0;
+        for (int i = 0; i < 2; ++i) {
+            if (d[i].units == 0)
+                continue;
+            const int64_t before = i == 0 ? 0 : d[0].units;  // units t = before.. with t % workers == w
+            auto upto = [&](int64_t t) { return t / workers + (t % workers > w ? 1 : 0); };
+            cycles += (upto(before + d[i].units) - upto(before)) * ((d[i].steps + d[i].splits - 1) / d[i].splits * step + 500);
+        }
+        most = std::max(most, cycles);
+    }
+    return most;
+}
+
+// Tiles of 256 on CTA pairs (1024 SM cycles per 128 of K, bound by the MMAs) or of 128 on
+// single CTAs (about 740, bound by the copies of both operands), whichever take fewer
+// cycles; few tiles and a deep K in slices, whose join costs a kernel more and the way of
+// its bytes.
+PairPlan plan_backward(int64_t M, int64_t N, int64_t K, bool of_x, bool of_w, int singles, int pairs,
+                       uint64_t workspace_bytes)
+{
+    PairPlan best = {};
+    int64_t best_cycles = 0;
     for (int g = 1; g <= 2; ++g) {
-        const int64_t workers = g == 2 ? pairs : singles;
+        const int64_t workers = g == 2 ? pairs : singles, tile = 128 * g;
         if (workers < 1)
             continue;
-        const int64_t r = (p->rows + 128 * g - 1) / (128 * g), c = (p->cols + 128 * g - 1) / (128 * g);
-        tiles[g] = r * c * p->results;
-        const int64_t room = (int64_t(workspace_bytes) - int64_t(kCounterRegionBytes)) / (g * g * 128 * 128 * 4);
-        const int64_t most = std::max<int64_t>(1, std::min(std::min(workers, room) / tiles[g], steps / 2));
-        for (int64_t splits = 1; splits <= most; ++splits) {
-            const int64_t cost = (tiles[g] * splits + workers - 1) / workers * ((steps + splits - 1) / splits) *
-                                     (g == 2 ? 1024 : 740) +
-                                 (splits > 1 ? 3000 + tiles[g] * splits * g * g * 65536 / 1250 : 0);
-            if (out.cg == 0 || cost < best) {
-                best = cost;
-                out.cg = g;
-                p->splits = int32_t(splits);
+        PairPlan s = {};
+        s.cg = g;
+        PairProduct &x = s.prod[0], &w = s.prod[1];
+        x = {int32_t(M), int32_t(K), int32_t(2 * blocks_of(N)), 1, int32_t((M + tile - 1) / tile), int32_t((K + tile - 1) / tile),
+             1, 0, 1};
+        w = {int32_t(N), int32_t(K), int32_t(blocks_of(M)), 2, int32_t((N + tile - 1) / tile), x.num_c, 1, 0, 1};
+        const int64_t tiles[2] = {of_x ? int64_t(x.num_r) * x.num_c : 0, of_w ? 2 * int64_t(w.num_r) * w.num_c : 0};
+        if (tiles[0] + tiles[1] >= (1ll << 31))
+            continue;
+        const int64_t room = (int64_t(workspace_bytes) - int64_t(kCounterRegionBytes)) / (tile * tile * 4);
+        auto slices = [&](int i, int64_t splits) {  // whether product i may be cut so
+            return splits == 1 || (tiles[i] * splits <= std::min(2 * workers, room) && s.prod[i].steps >= 2 * splits);
+        };
+        for (int64_t sx = 1; slices(0, sx); sx = sx < 4 ? sx + 1 : sx * 3 / 2)
+            for (int64_t sw = 1; slices(1, sw); sw = sw < 4 ? sw + 1 : sw * 3 / 2) {
+                x.splits = int32_t(sx);
+                w.splits = int32_t(sw);
+                x.units = int32_t(tiles[0] * sx);
+                w.units = int32_t(tiles[1] * sw);
+                // partial sums lie by unit, of both products where either has slices
+                if ((sx > 1 || sw > 1) && int64_t(sw > 1 ? x.units + w.units : x.units) > room)
+                    continue;
+                int64_t cycles = pair_cycles(s.prod, workers, g == 2 ? 1024 : 740);
+                for (int i = 0; i < 2; ++i)
+                    if (s.prod[i].splits > 1)
+                        cycles += 3000 + s.prod[i].units * tile * tile * 4 / 1250;
+                if (best.workers == 0 || cycles < best_cycles) {
+                    best_cycles = cycles;
+                    s.workers = int(std::min<int64_t>(x.units + w.units, workers));
+                    best = s;
+                }
+                if (tiles[1] == 0)
+                    break;
             }
-        }
     }
-    if (out.cg == 0 || tiles[out.cg] >= (1ll << 31))
-        return PairPlan{};
-    const int cg = out.cg;
-    for (p->join_share = 8;
-         p->join_share > 1 && (p->join_share > p->splits || tiles[cg] * cg * cg * 16 * p->join_share > 2048);)
-        p->join_share /= 2;
-    p->num_r = int32_t((p->rows + 128 * cg - 1) / (128 * cg));
-    p->num_c = int32_t((p->cols + 128 * cg - 1) / (128 * cg));
-    out.tiles = tiles[cg];
-    out.workers = std::min<int64_t>(tiles[cg] * p->splits, cg == 2 ? pairs : singles);
-    return out;
-}
-
-PairParams input_gradient_shape(int64_t M, int64_t N, int64_t K)
-{
-    PairParams p = {};
-    p.rows = int32_t(M);
-    p.cols = int32_t(K);
-    p.steps_k = int32_t(blocks_of(N));
-    p.terms = 2;
-    p.results = 1;
-    return p;
-}
-
-PairParams weight_gradient_shape(int64_t M, int64_t N, int64_t K)
-{
-    PairParams p = {};
-    p.rows = int32_t(N);
-    p.cols = int32_t(K);
-    p.steps_k = int32_t(blocks_of(M));
-    p.terms = 1;
-    p.results = 2;
-    return p;
+    for (PairProduct& d : best.prod)
+        if (d.units > 0)
+            for (d.join_share = 8; d.join_share > 1 && (d.join_share > d.splits ||
+                                                        d.units / d.splits * best.cg * best.cg * 16 * d.join_share > 2048);)
+                d.join_share /= 2;
+    return best;
 }
 
 // The gated layer's forward product in tiles of 256 rows of X x 128 of each weight on
@@ -405,13 +419,10 @@ bwgemm_status_t bwgemm_gated(bwgemm_plan_t plan, const bwgemm_matrix_t* X, const
         return BWGEMM_OK;
     }
     PairParams p = {};
-    p.rows = int32_t(M);
-    p.cols = int32_t(N);
-    p.steps_k = int32_t(blocks_of(K));
-    p.terms = p.results = p.splits = p.join_share = 1;
+    p.prod[0] = {int32_t(M), int32_t(N), int32_t(blocks_of(K)), 1, int32_t(sel.num_r), int32_t(sel.num_c), 1,
+                 int32_t(sel.num_r * sel.num_c), 1};
+    p.steps_k = p.prod[0].steps;
     p.chunks_a = p.chunks_b = int32_t(K / 64);
-    p.num_r = int32_t(sel.num_r);
-    p.num_c = int32_t(sel.num_c);
     p.dtype = dtype;
     p.activation = activation;
     p.timeout_ns = limit_ns(plan);
@@ -424,6 +435,8 @@ bwgemm_status_t bwgemm_gated(bwgemm_plan_t plan, const bwgemm_matrix_t* X, const
         return st;
     maps.a[1] = maps.a[0];
     maps.a3[1] = maps.a3[0];
+    maps.b[2] = maps.b[1];
+    maps.b3[2] = maps.b3[1];
     for (int i = 0; i < 3; ++i) {
         if (!out[i]) {
             maps.out[i] = maps.out[0];
@@ -510,12 +523,10 @@ bwgemm_status_t bwgemm_gated_backward(bwgemm_plan_t plan, const bwgemm_matrix_t*
     const int64_t ldd = round_up(N, 8);
     uint16_t* const d[2] = {static_cast<uint16_t*>(workspace),
                             reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + need / 2)};
-    // both divisions before the first launch: a size without one launches nothing
-    PairParams px = input_gradient_shape(M, N, K), pw = weight_gradient_shape(M, N, K);
-    const int singles = capped(plan->num_sms, 1, &plan->opts), pairs = capped(pairs_of(plan), 2, &plan->opts);
-    const PairPlan sx = plan_pair(&px, singles, pairs, plan->workspace_bytes);
-    const PairPlan sw = plan_pair(&pw, singles, pairs, plan->workspace_bytes);
-    if ((of_x && sx.workers == 0) || (of_w && sw.workers == 0))
+    // the division before the first launch: a size without one launches nothing
+    const PairPlan sel = plan_backward(M, N, K, of_x, of_w, capped(plan->num_sms, 1, &plan->opts),
+                                       capped(pairs_of(plan), 2, &plan->opts), plan->workspace_bytes);
+    if (sel.workers == 0)
         return BWGEMM_ERR_UNSUPPORTED;
 
     GateGradParams gg = {};
@@ -532,64 +543,44 @@ bwgemm_status_t bwgemm_gated_backward(bwgemm_plan_t plan, const bwgemm_matrix_t*
     gg.cols = N;
     gg.dtype = dtype;
     gg.activation = activation;
-    PairMaps mx, mw;
-    // dG and dU: rows of tokens, K-major in the first product, stored K x rows in the second
-    CUtensorMap dm[2], dm3[2];
+    PairParams p = {};
+    p.prod[0] = sel.prod[0];
+    p.prod[1] = sel.prod[1];
+    p.steps_k = int32_t(blocks_of(N));
+    p.chunks_a = int32_t(N / 64);
+    p.chunks_b = int32_t(K / 64);
+    p.dtype = dtype;
+    p.partials = reinterpret_cast<float*>(plan->d_workspace + kCounterRegionBytes);
+    p.timeout_ns = limit_ns(plan);
+    p.status = plan->d_status;
+    p.stall_kblock = plan->opts.stall_kblock;
+    // dG and dU: rows of tokens, K-major for dX, stored K x rows for the weights
+    PairMaps maps;
     for (int i = 0; i < 2; ++i)
-        if ((st = encode_operand16(&dm[i], &dm3[i], d[i], ldd, dtype, M, N, 128)) != BWGEMM_OK)
+        if ((st = encode_operand16(&maps.a[i], &maps.a3[i], d[i], ldd, dtype, M, N, 128)) != BWGEMM_OK)
             return st;
-    for (PairParams* p : {&px, &pw}) {
-        p->chunks_a = int32_t(N / 64);
-        p->chunks_b = int32_t(K / 64);
-        p->dtype = dtype;
-        p->partials = reinterpret_cast<float*>(plan->d_workspace + kCounterRegionBytes);
-        p->timeout_ns = limit_ns(plan);
-        p->status = plan->d_status;
-        p->stall_kblock = plan->opts.stall_kblock;
-    }
-    if (of_x) {
-        for (int i = 0; i < 2; ++i) {
-            const bwgemm_matrix_t& w = *(i ? Wu : Wg);
-            mx.a[i] = dm[i];
-            mx.a3[i] = dm3[i];
-            if ((st = encode_operand16(&mx.b[i], &mx.b3[i], w.data, w.ld, dtype, N, K, 128)) != BWGEMM_OK)
-                return st;
-        }
-        if ((st = encode_result16(&mx.out[0], *dX, dtype, M, K)) != BWGEMM_OK)
+    const bwgemm_matrix_t* const b[3] = {of_x ? Wg : nullptr, of_x ? Wu : nullptr, of_w ? X : nullptr};
+    const bwgemm_matrix_t* const out[3] = {of_x ? dX : nullptr, of_w ? dWg : nullptr, of_w ? dWu : nullptr};
+    for (int i = 0; i < 3; ++i) {
+        maps.b[i] = maps.b3[i] = maps.out[i] = maps.a[0];  // where there is none, none is read
+        if (b[i] && (st = encode_operand16(&maps.b[i], &maps.b3[i], b[i]->data, b[i]->ld, dtype, i < 2 ? N : M, K, 128)) !=
+                        BWGEMM_OK)
             return st;
-        mx.out[1] = mx.out[2] = mx.out[0];
-        px.out[0] = static_cast<uint16_t*>(dX->data);
-        px.ldo[0] = dX->ld;
-    }
-    if (of_w) {
-        for (int i = 0; i < 2; ++i) {
-            const bwgemm_matrix_t& w = *(i ? dWu : dWg);
-            mw.a[i] = dm[i];
-            mw.a3[i] = dm3[i];
-            if ((st = encode_result16(&mw.out[i], w, dtype, N, K)) != BWGEMM_OK)
-                return st;
-            pw.out[i] = static_cast<uint16_t*>(w.data);
-            pw.ldo[i] = w.ld;
-        }
-        mw.out[2] = mw.out[0];
-        if ((st = encode_operand16(&mw.b[0], &mw.b3[0], X->data, X->ld, dtype, M, K, 128)) != BWGEMM_OK)
+        if (!out[i])
+            continue;
+        if ((st = encode_result16(&maps.out[i], *out[i], dtype, i ? N : M, K)) != BWGEMM_OK)
             return st;
-        mw.b[1] = mw.b[0];
-        mw.b3[1] = mw.b3[0];
+        p.out[i] = static_cast<uint16_t*>(out[i]->data);
+        p.ldo[i] = out[i]->ld;
     }
     if (launch_gate_grad(gg, s, pdl) != cudaSuccess)
         return BWGEMM_ERR_CUDA;
     plan->launches += 1;
-    if (of_x) {
-        if (launch_pair(kPairInput, sx.cg, mx, px, int(sx.workers) * sx.cg, s, pdl) != cudaSuccess)
-            return BWGEMM_ERR_CUDA;
-        plan->launches += px.splits > 1 ? 2 : 1;
-    }
-    if (of_w) {
-        if (launch_pair(kPairWeight, sw.cg, mw, pw, int(sw.workers) * sw.cg, s, pdl) != cudaSuccess)
-            return BWGEMM_ERR_CUDA;
-        plan->launches += pw.splits > 1 ? 2 : 1;
-    }
+    if (launch_pair(kPairBackward, sel.cg, maps, p, sel.workers * sel.cg, s, pdl) != cudaSuccess)
+        return BWGEMM_ERR_CUDA;
+    plan->launches += 1;
+    for (const PairProduct& q : sel.prod)
+        plan->launches += q.units > 0 && q.splits > 1 ? 1 : 0;
     return BWGEMM_OK;
 }
 
@@ -765,14 +756,12 @@ bwgemm_status_t bwgemm_select_gated_backward(int32_t num_sms, int32_t max_pairs,
         return BWGEMM_ERR_INVALID_ARG;
     if (!fits(M) || !fits(N) || !fits(K))
         return BWGEMM_ERR_UNSUPPORTED;
-    for (int i = 0; i < 2; ++i) {
-        PairParams p = i ? weight_gradient_shape(M, N, K) : input_gradient_shape(M, N, K);
-        const PairPlan s = plan_pair(&p, capped(num_sms, 1, opts), capped(max_pairs ? max_pairs : num_sms / 2, 2, opts),
-                                     workspace_of(opts));
-        if (s.workers == 0)
-            return BWGEMM_ERR_UNSUPPORTED;
-        out[i] = {pair_tile(s.cg), p.splits, s.tiles, int32_t(s.workers)};
-    }
+    const PairPlan s = plan_backward(M, N, K, true, true, capped(num_sms, 1, opts),
+                                     capped(max_pairs ? max_pairs : num_sms / 2, 2, opts), workspace_of(opts));
+    if (s.workers == 0)
+        return BWGEMM_ERR_UNSUPPORTED;
+    for (int i = 0; i < 2; ++i)
+        out[i] = {pair_tile(s.cg), s.prod[i].splits, s.prod[i].units / s.prod[i].splits, s.workers};
     return BWGEMM_OK;
 }
 

@@ -8,34 +8,41 @@
 namespace bwgemm {
 
 // ------------------------------------------- products in square tiles
-// What a product of the gated layer computes from 16-bit operands; `a` and `b`
-// are the sides whose rows (columns, where stored transposed) are D's rows and columns.
+// What a launch computes from 16-bit operands; `a` and `b` are the sides whose rows
+// (columns, where stored transposed) are D's rows and columns.
 enum : int {
-    kPairGated = 0,  // H = act(X Wg^T) * (X Wu^T):  a = X, b = Wg and Wu
-    kPairInput = 1,  // dX = dG Wg + dU Wu:          a = dG then dU, b = Wg then Wu, stored K x columns
-    kPairWeight = 2  // dWg = dG^T X, dWu = dU^T X:  a = dG or dU, b = X, both stored K x rows
+    kPairGated = 0,    // H = act(X Wg^T) * (X Wu^T):  a = X, b = Wg and Wu
+    kPairBackward = 1  // dX = dG Wg + dU Wu:          a = dG then dU, b = Wg then Wu, stored K x columns
+                       // dWg = dG^T X, dWu = dU^T X:  a = dG or dU, b = X, both stored K x rows
 };
 
 // An operand in boxes of 64 elements x 128 rows, and in boxes of two whole 64-element
 // chunks of those rows.
 struct PairMaps {
-    CUtensorMap a[2], a3[2], b[2], b3[2];
-    CUtensorMap out[3];          // 64 columns x 32 rows
+    CUtensorMap a[2], a3[2];     // X | dG, dU
+    CUtensorMap b[3], b3[3];     // Wg, Wu | Wg, Wu, X
+    CUtensorMap out[3];          // H, G, U | dX, dWg, dWu in boxes of 64 columns x 32 rows
+};
+
+// One of a launch's products: H | dX, and dWg with dWu.
+struct PairProduct {
+    int32_t rows, cols;          // of one result
+    int32_t steps;               // of 128 of K, of all terms
+    int32_t results;             // results stacked along the tile rows (dWg, dWu: 2)
+    int32_t num_r, num_c;        // tiles of one result
+    int32_t splits;              // slices of K per tile (1: whole)
+    int32_t units;               // tiles, or slices of them: 0 where it is not wanted
+    int32_t join_share;          // warps that add the slices of one piece: 1, 2, 4 or 8
 };
 
 struct PairParams {
-    int32_t rows, cols;          // of one result
-    int32_t steps_k;             // ceil(K / 128), of one term
-    int32_t terms;               // products summed (kPairInput: 2)
-    int32_t results;             // results stacked along the tile rows (kPairWeight: 2)
+    PairProduct prod[2];
+    int32_t steps_k;             // of one term of dX: ceil(N / 128)
     int32_t chunks_a, chunks_b;  // whole 64-element chunks of the operands' rows (0: no a3 / b3)
-    int32_t num_r, num_c;        // tiles of one result
-    int32_t splits;              // slices of K per tile (1: whole)
-    int32_t join_share;          // warps that add the slices of one piece: 1, 2, 4 or 8
-    float* partials;             // the slices' fp32 sums
+    float* partials;             // the slices' fp32 sums, by unit
     int32_t dtype;
     int32_t activation;          // kPairGated
-    uint16_t* out[3];            // results; kPairGated: H, G, U (G null: not kept)
+    uint16_t* out[3];            // results; kPairGated: G and U null where they are not kept
     int64_t ldo[3];
     uint64_t timeout_ns;
     uint32_t* status;
@@ -43,6 +50,7 @@ struct PairParams {
 };
 
 constexpr int pair_tile(int cg) { return 128 * cg; }
+// The products, then for those in slices the kernel that adds them.
 cudaError_t launch_pair(int form, int cg, const PairMaps& maps, const PairParams& p, int grid, cudaStream_t stream, bool pdl);
 
 // ------------------------------------------------ gradients of G and U

@@ -38,16 +38,19 @@ cudaError_t launch_form(const PairMaps& maps, const PairParams& p, int grid, cud
     cfg.attrs = attr;
     cfg.numAttrs = n;
     err = cudaLaunchKernelEx(&cfg, kernel, maps, p);
-    if (err != cudaSuccess || p.splits == 1)
-        return err;
-    cudaLaunchConfig_t join = {};
-    join.gridDim = dim3(unsigned(CG * 8 * Cfg::kCols / 4 / kJoinWarps * p.join_share),
-                        unsigned(p.num_r * p.num_c * p.results), 1);
-    join.blockDim = dim3(32 * kJoinWarps, 1, 1);
-    join.stream = stream;
-    join.attrs = pdl ? attr + n - 1 : nullptr;  // the dependency's
-    join.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&join, pair_join_kernel<CG>, p);
+    for (int which = 0; which < 2 && err == cudaSuccess; ++which) {
+        const PairProduct& d = p.prod[which];
+        if (d.units == 0 || d.splits == 1)
+            continue;
+        cudaLaunchConfig_t join = {};
+        join.gridDim = dim3(unsigned(CG * 8 * Cfg::kCols / 4 / kJoinWarps * d.join_share), unsigned(d.units / d.splits), 1);
+        join.blockDim = dim3(32 * kJoinWarps, 1, 1);
+        join.stream = stream;
+        join.attrs = pdl ? attr + n - 1 : nullptr;  // the dependency's
+        join.numAttrs = pdl ? 1 : 0;
+        err = cudaLaunchKernelEx(&join, pair_join_kernel<CG>, p, which);
+    }
+    return err;
 }
 
 // dU = dH act(G), dG = dH U act'(G): three reads and two writes of rows x cols, eight
@@ -105,10 +108,8 @@ cudaError_t launch_pair(int form, int cg, const PairMaps& maps, const PairParams
 {
     switch (form * 2 + (cg - 1)) {
     case kPairGated * 2 + 1: return launch_form<2, kPairGated>(maps, p, grid, stream, pdl);
-    case kPairInput * 2: return launch_form<1, kPairInput>(maps, p, grid, stream, pdl);
-    case kPairInput * 2 + 1: return launch_form<2, kPairInput>(maps, p, grid, stream, pdl);
-    case kPairWeight * 2: return launch_form<1, kPairWeight>(maps, p, grid, stream, pdl);
-    case kPairWeight * 2 + 1: return launch_form<2, kPairWeight>(maps, p, grid, stream, pdl);
+    case kPairBackward * 2: return launch_form<1, kPairBackward>(maps, p, grid, stream, pdl);
+    case kPairBackward * 2 + 1: return launch_form<2, kPairBackward>(maps, p, grid, stream, pdl);
     default: return cudaErrorInvalidValue;
     }
 }

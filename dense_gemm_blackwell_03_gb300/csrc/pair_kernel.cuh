@@ -1,9 +1,9 @@
 // pair_kernel.cuh -- the large products of the gated feed-forward layer on 16-bit
 // operands (bf16 or fp16) with fp32 sums:
 //
-//   kPairGated    G = X Wg^T, U = X Wu^T, H = act(G) * U     forward, in one pass
-//   kPairInput    dX = dG Wg + dU Wu                          input gradient
-//   kPairWeight   dWg = dG^T X,  dWu = dU^T X                 weight gradients
+//   kPairGated      G = X Wg^T, U = X Wu^T, H = act(G) * U     forward, in one pass
+//   kPairBackward   dX = dG Wg + dU Wu                          input gradient, and
+//                   dWg = dG^T X,  dWu = dU^T X                 weight gradients, in one launch
 //
 // One persistent, warp-specialised tcgen05 kernel, tiles of 256 x 256 on CTA pairs (or
 // 128 x 128 on single CTAs for the gradients of small layers).  tcgen05 reads either
@@ -15,10 +15,10 @@
 // each accumulator row holds G in its first 128 columns and U in the last: every
 // epilogue thread has both values of its outputs, and X's tile is read once for both.
 //
-// Input gradient: one accumulator over both products (the K loop runs over dG, Wg, then
-// over dU, Wu).  Weight gradient: both results' tiles are one list of work, so that X is
-// in L2 for both.  Few tiles and a deep K: slices of K, whose fp32 sums a second kernel
-// adds in order.
+// Backward: all tiles are one list of work, dX's first (its K is 2 N deep) and the weights'
+// after them, so that no wave is left partly filled between the two.  dX sums both products
+// in one accumulator (the K loop runs over dG, Wg, then over dU, Wu).  Few tiles and a deep
+// K: slices of K, whose fp32 sums a second kernel adds in order.
 //
 // What bounds it: the MMAs, 1024 cycles per 128 of K of a 256 x 256 tile; the epilogue
 // of a tile (other TMEM buffer) overlaps the next tile's.  Each stage of the ring holds
@@ -33,28 +33,29 @@
 namespace bwgemm {
 
 struct PairTile {
-    int r, c, result;
-    int slice, k0, k1;
+    int which, r, c, result;  // of product `which`
+    int k0, k1;
 };
 
 __device__ __forceinline__ PairTile pair_tile_at(const PairParams& p, int t)
 {
     PairTile x;
-    const int i = t / p.splits;
-    const int steps = p.steps_k * p.terms;
-    x.slice = t - i * p.splits;
-    x.k0 = int(int64_t(x.slice) * steps / p.splits);
-    x.k1 = int(int64_t(x.slice + 1) * steps / p.splits);
+    x.which = t >= p.prod[0].units ? 1 : 0;
+    const PairProduct& d = p.prod[x.which];
+    t -= x.which ? p.prod[0].units : 0;
+    const int i = t / d.splits, slice = t - i * d.splits;
+    x.k0 = int(int64_t(slice) * d.steps / d.splits);
+    x.k1 = int(int64_t(slice + 1) * d.steps / d.splits);
     // groups of 8 tile rows (of all results), walked down before stepping along the columns
-    const int rows = p.num_r * p.results;
-    const int per_group = 8 * p.num_c;
+    const int rows = d.num_r * d.results;
+    const int per_group = 8 * d.num_c;
     const int g = i / per_group;
     const int height = min(rows - 8 * g, 8);
     const int local = i - g * per_group;
     const int r = 8 * g + local % height;
     x.c = local / height;
-    x.result = r / p.num_r;
-    x.r = r - x.result * p.num_r;
+    x.result = r / d.num_r;
+    x.r = r - x.result * d.num_r;
     return x;
 }
 
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
 {
     using Cfg = OrthoConfig<CG>;
     static_assert(FORM != kPairGated || CG == 2, "gate and up rows come from the two CTAs");
-    constexpr bool A_MN = FORM == kPairWeight, B_MN = FORM != kPairGated;
+    constexpr bool B_MN = FORM == kPairBackward;
     constexpr int STAGES = Cfg::kStages;
     constexpr int TILE = Cfg::kTile;
     constexpr int COLS = FORM == kPairGated ? TILE / 2 : TILE;  // result columns of a tile
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
     const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0u;
     const int worker = int(blockIdx.x) / CG;
     const int workers = int(gridDim.x) / CG;
-    const int total = p.num_r * p.num_c * p.results * p.splits;  // a unit is a tile, or a slice of its K
+    const int total = p.prod[0].units + (FORM == kPairBackward ? p.prod[1].units : 0);
     const uint32_t sA = base + Cfg::kOffA;
     const uint32_t sB = base + Cfg::kOffB;
     const uint32_t bar_full = base + Cfg::kOffBar;
@@ -165,17 +166,18 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                     armed_parity = (armed_parity & ~(1u << s)) | (phase << s);
                 }
                 if (!stall && ptx::elect_one()) {
-                    const int term = FORM == kPairInput && i >= p.steps_k ? 1 : 0;
+                    const bool of_w = FORM == kPairBackward && x.which == 1;  // a stored K x rows
+                    const int term = FORM == kPairBackward && !of_w && i >= p.steps_k ? 1 : 0;
                     const int k = (i - term * p.steps_k) * kOrthoK;
-                    const int za = FORM == kPairWeight ? x.result : term;
-                    const int zb = FORM == kPairGated ? int(rank) : FORM == kPairInput ? term : 0;
+                    const int za = of_w ? x.result : term;
+                    const int zb = FORM == kPairGated ? int(rank) : of_w ? 2 : term;
                     const uint32_t fb = leader_full + 8 * s;
                     const uint32_t dA = sA + uint32_t(s * Cfg::kOperandBytes), dB = sB + uint32_t(s * Cfg::kOperandBytes);
                     if (rank == 0)
                         ptx::mbar_arrive_expect_tx(fb, uint32_t(CG * 2 * Cfg::kOperandBytes));
                     if (n == 0)  // all before it overlaps the kernel before
                         ptx::grid_dependency_wait();
-                    pair_load<CG>(dA, &maps.a[za], &maps.a3[za], p.chunks_a, fb, A_MN ? k : a0, A_MN ? a0 : k);
+                    pair_load<CG>(dA, &maps.a[za], &maps.a3[za], p.chunks_a, fb, of_w ? k : a0, of_w ? a0 : k);
                     pair_load<CG>(dB, &maps.b[zb], &maps.b3[zb], p.chunks_b, fb, B_MN ? k : b0, B_MN ? b0 : k);
                 }
                 __syncwarp();
@@ -187,9 +189,9 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
         }
     } else if (warp == 1 && rank == 0) {
         // ---------------------------------------------------------- MMA issue
-        const uint64_t a_desc0 = A_MN ? make_sdesc_mn(sA) : make_sdesc_sw128(sA);
+        const uint64_t a_k0 = make_sdesc_sw128(sA), a_mn0 = make_sdesc_mn(sA);
         const uint64_t b_desc0 = B_MN ? make_sdesc_mn(sB) : make_sdesc_sw128(sB);
-        const uint32_t idesc = make_idesc(p.dtype, 128 * CG, TILE) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+        const uint32_t idesc0 = make_idesc(p.dtype, 128 * CG, TILE) | (B_MN ? 1u << 16 : 0u);
         const uint32_t tmem0 = __shfl_sync(0xffffffffu, tmem_base, 0);
         int s = 0, b = 0;
         uint32_t phase = 0, bphase = 0;
@@ -205,16 +207,22 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                     break;
                 ptx::tc_fence_after_sync();
                 if (ptx::elect_one()) {
-                    const uint64_t ad = a_desc0 + uint64_t((s * Cfg::kOperandBytes) >> 4);
                     const uint64_t bd = b_desc0 + uint64_t((s * Cfg::kOperandBytes) >> 4);
+                    auto issue = [&](uint64_t ad, bool a_mn, uint32_t idesc) {
 #pragma unroll
-                    for (int kk = 0; kk < kOrthoK / 16; ++kk) {
-                        // K-major: two chunks of 64 k, 32 bytes per MMA; MN-major: 128 k in rows of 128 bytes
-                        const uint32_t k_major = uint32_t((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                        const uint32_t mn_major = uint32_t(kk * 2048) >> 4;
-                        ptx::mma_f16<CG>(tmem0 + uint32_t(b * TILE), ad + (A_MN ? mn_major : k_major),
-                                         bd + (B_MN ? mn_major : k_major), idesc, (i > x.k0 || kk > 0) ? 1u : 0u);
-                    }
+                        for (int kk = 0; kk < kOrthoK / 16; ++kk) {
+                            // K-major: two chunks of 64 k, 32 bytes per MMA; MN-major: 128 k in rows of 128 bytes
+                            const uint32_t k_major = uint32_t((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                            const uint32_t mn_major = uint32_t(kk * 2048) >> 4;
+                            ptx::mma_f16<CG>(tmem0 + uint32_t(b * TILE), ad + (a_mn ? mn_major : k_major),
+                                             bd + (B_MN ? mn_major : k_major), idesc, (i > x.k0 || kk > 0) ? 1u : 0u);
+                        }
+                    };
+                    const uint64_t stage = uint64_t((s * Cfg::kOperandBytes) >> 4);
+                    if (FORM == kPairBackward && x.which == 1)
+                        issue(a_mn0 + stage, true, idesc0 | 1u << 15);
+                    else
+                        issue(a_k0 + stage, false, idesc0);
                     if constexpr (CG == 2) {
                         ptx::mma_commit_pair(bar_empty + 8 * s, 0x3);
                         if (i == x.k1 - 1)
@@ -246,16 +254,16 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
         uint32_t bphase = 0;
         bool ok = true;
         // 64 columns of this lane's row, packed, to columns col.. of rows row0.. of result z
-        auto put = [&](const uint32_t(&w)[32], int z, int row0, int col) {
-            if (row0 >= p.rows || col >= p.cols)
+        auto put = [&](const uint32_t (&w)[32], const PairProduct& d, int z, int row0, int col) {
+            if (row0 >= d.rows || col >= d.cols)
                 return;
-            if ((p.cols & 7) != 0 && col + 64 > p.cols) {
+            if ((d.cols & 7) != 0 && col + 64 > d.cols) {
                 // a TMA store clips a row's end only in whole 16-byte pieces
-                if (row0 + lane < p.rows) {
+                if (row0 + lane < d.rows) {
                     uint16_t* dst = p.out[z] + int64_t(row0 + lane) * p.ldo[z] + col;
 #pragma unroll
                     for (int i = 0; i < 64; ++i)
-                        if (col + i < p.cols)
+                        if (col + i < d.cols)
                             dst[i] = uint16_t((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xFFFFu));
                 }
                 return;
@@ -274,6 +282,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
 #pragma unroll 1
         for (int t = worker; ok && t < total; t += workers) {
             const PairTile x = pair_tile_at(p, t);
+            const PairProduct& d = p.prod[x.which];
             const int row0 = x.r * TILE + int(rank) * 128 + 32 * q;
             ok = warp_wait(bar_acc_full + 8 * b, bphase, p, abort_flag, kStatusEpilogueTimeout);
             if (!ok)
@@ -303,14 +312,14 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                     }
                 }
                 const int col = x.c * COLS + c0;
-                put(h, 0, row0, col);
+                put(h, d, 0, row0, col);
                 if (p.out[1] != nullptr) {
-                    put(gw, 1, row0, col);
-                    put(uw, 2, row0, col);
+                    put(gw, d, 1, row0, col);
+                    put(uw, d, 2, row0, col);
                 }
             } else {
                 const int c0 = (e >> 2) * Cfg::kCols;
-                if (p.splits == 1) {
+                if (d.splits == 1) {
 #pragma unroll 1
                     for (int c = 0; c < Cfg::kCols; c += 64) {
                         uint32_t v[64], w[32];
@@ -321,7 +330,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             w[i] = pack2(v[2 * i], v[2 * i + 1], p.dtype);
-                        put(w, x.result, row0, x.c * TILE + c0 + c);
+                        put(w, d, x.which + x.result, row0, x.c * TILE + c0 + c);
                     }
                 } else {
                     // a slice of K: its sums to global memory, where pair_join_kernel adds
@@ -334,7 +343,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                         ptx::tmem_ld_wait();
                         if (c + 32 >= Cfg::kCols)
                             hand_back<CG>(bar_acc_empty + 8 * b, lane);
-                        if (row0 < p.rows && x.c * TILE + c0 + c < p.cols) {
+                        if (row0 < d.rows && x.c * TILE + c0 + c < d.cols) {
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
                                 ptx::st_global_cg_v4(part + c * 32 + i * 128,
@@ -393,16 +402,17 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
 // of a slice) and every join_share-th slice; the sums of that many warps meet in shared
 // memory, in order.
 template <int CG>
-__global__ void __launch_bounds__(32 * kJoinWarps) pair_join_kernel(const PairParams p)
+__global__ void __launch_bounds__(32 * kJoinWarps) pair_join_kernel(const PairParams p, int which)
 {
     using Cfg = OrthoConfig<CG>;
     constexpr int TILE = Cfg::kTile, CHUNKS = Cfg::kCols / 32;
     __shared__ float4 sums[kJoinWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int share = p.join_share, first = warp % share;
+    const PairProduct& d = p.prod[which];
+    const int share = d.join_share, first = warp % share;
     const int piece = int(blockIdx.x) * (kJoinWarps / share) + warp / share;
     const int i = piece % 8, c = piece / 8 % CHUNKS * 32, e = piece / (8 * CHUNKS) % 8, rank = piece / (64 * CHUNKS);
-    const int t = int(blockIdx.y) * p.splits;
+    const int t = (which ? p.prod[0].units : 0) + int(blockIdx.y) * d.splits;
     const PairTile x = pair_tile_at(p, t);
     const int row0 = x.r * TILE + rank * 128 + 32 * ((e + 2) & 3), row = row0 + lane;
     const int col = x.c * TILE + (e >> 2) * Cfg::kCols + c + 4 * i;
@@ -410,9 +420,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) pair_join_kernel(const PairPa
     ptx::launch_dependents();
     const float* at = p.partials + (size_t(t) * CG + rank) * (128 * TILE) + e * (32 * Cfg::kCols) + c * 32 + i * 128 + 4 * lane;
     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row0 < p.rows && col < p.cols) {
+    if (row0 < d.rows && col < d.cols) {
 #pragma unroll 8
-        for (int k = first; k < p.splits; k += share) {
+        for (int k = first; k < d.splits; k += share) {
             const uint4 v = ptx::ld_global_cg_v4(at + size_t(k) * (CG * 128 * TILE));
             f.x += __uint_as_float(v.x);
             f.y += __uint_as_float(v.y);
@@ -432,17 +442,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) pair_join_kernel(const PairPa
         f.z += g.z;
         f.w += g.w;
     }
-    if (row >= p.rows)
+    if (row >= d.rows || col >= d.cols)
         return;
     const uint32_t lo = pack2(__float_as_uint(f.x), __float_as_uint(f.y), p.dtype);
     const uint32_t hi = pack2(__float_as_uint(f.z), __float_as_uint(f.w), p.dtype);
-    uint16_t* const out = p.out[x.result] + row * p.ldo[x.result] + col;
-    if (col + 4 <= p.cols) {
+    const int z = which + x.result;
+    uint16_t* const out = p.out[z] + row * p.ldo[z] + col;
+    if (col + 4 <= d.cols) {
         *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
     } else {
 #pragma unroll
         for (int k = 0; k < 3; ++k)
-            if (col + k < p.cols)
+            if (col + k < d.cols)
                 out[k] = uint16_t((k < 2 ? lo : hi) >> (k & 1 ? 16 : 0));
     }
 }

@@ -621,8 +621,8 @@ bwgemm_status_t bwgemm_gated(bwgemm_plan_t plan, const bwgemm_matrix_t* X, const
  *       nothing of use before or after
  *
  * dG and dU are rounded to `dtype`, as operands of the products that follow; sums are fp32.
- * M == 0 gives dWg = dWu = 0, N == 0 gives dX = 0.  Two or three launches, one more where a
- * product is cut into slices of K (in the plan's workspace); the rest as for bwgemm_gated.
+ * M == 0 gives dWg = dWu = 0, N == 0 gives dX = 0.  Two launches, one more for each product
+ * that is cut into slices of K (in the plan's workspace); the rest as for bwgemm_gated.
  */
 bwgemm_status_t bwgemm_gated_backward(bwgemm_plan_t plan, const bwgemm_matrix_t* dH, const bwgemm_matrix_t* G,
                                       const bwgemm_matrix_t* U, const bwgemm_matrix_t* X, const bwgemm_matrix_t* Wg,
@@ -687,7 +687,8 @@ typedef struct {
 /*
  * Host-only: the division that a plan with `opts` (NULL = defaults) picks on a GPU of
  * `num_sms` SMs holding `max_pairs` CTA pairs (0 = num_sms / 2); for the backward pass of its
- * two products dX (out[0]) and dWg, dWu (out[1], tiles of both), whose `splits` are slices of K.
+ * two products dX (out[0]) and dWg, dWu (out[1], tiles of both), whose `splits` are slices of K
+ * and whose workers are the same.
  */
 bwgemm_status_t bwgemm_select_gated(int32_t num_sms, int32_t max_pairs, int64_t M, int64_t N, int64_t K,
                                     const bwgemm_plan_options_t* opts, bwgemm_lanes_config_t* out);
