@@ -305,6 +305,8 @@ bool known(bwgemm_activation_t a) { return a == BWGEMM_SILU || a == BWGEMM_GELU 
 
 bool fits(int64_t n) { return n <= (1ll << 31) - 256; }
 
+constexpr int64_t kMostElements = 1ll << 56;  // of a workspace's matrix: its bytes stay far inside 64 bits
+
 void take_lanes(LanesParams* p, const LanesPlan& s, bwgemm_plan_t plan, int64_t M, int64_t N, int64_t K)
 {
     p->lrows = int32_t(N);
@@ -460,7 +462,7 @@ bwgemm_status_t bwgemm_gated_backward_workspace(int64_t M, int64_t N, uint64_t* 
     *bytes = 0;
     if (M < 0 || N < 0)
         return BWGEMM_ERR_INVALID_ARG;
-    if (!fits(M) || !fits(N))
+    if (!fits(M) || !fits(N) || M > kMostElements / round_up(std::max<int64_t>(N, 1), 8))
         return BWGEMM_ERR_UNSUPPORTED;
     *bytes = 2 * uint64_t(round_up(M * round_up(N, 8) * 2, 256));
     return BWGEMM_OK;
@@ -496,7 +498,8 @@ bwgemm_status_t bwgemm_gated_backward(bwgemm_plan_t plan, const bwgemm_matrix_t*
             return st;
         if (of_w && (st = check_matrix(X, M, K)) != BWGEMM_OK)
             return st;
-        bwgemm_gated_backward_workspace(M, N, &need);
+        if ((st = bwgemm_gated_backward_workspace(M, N, &need)) != BWGEMM_OK)
+            return st;
         if (workspace_bytes < need || !workspace)
             return BWGEMM_ERR_WORKSPACE;
         if (!aligned(workspace, 256))
@@ -617,7 +620,7 @@ bwgemm_status_t bwgemm_run_integer_workspace(int64_t M, int64_t N, int64_t K, ui
     *bytes = 0;
     if (M < 0 || N < 0 || K < 0)
         return BWGEMM_ERR_INVALID_ARG;
-    if (!fits(M) || !fits(N) || !fits(K))
+    if (!fits(M) || !fits(N) || !fits(K) || M > kMostElements / round_up(std::max<int64_t>(K, 1), 128))
         return BWGEMM_ERR_UNSUPPORTED;
     if (M > 0 && N > 0 && K > 0 && !takes_few_rows(kLanesInt8, M, N, K))
         *bytes = uint64_t(round_up(M * round_up(K, 128) * 2, 256));  // A as fp16

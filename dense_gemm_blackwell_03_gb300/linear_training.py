@@ -9,9 +9,12 @@ a scale per 128 elements of K, and its gradients from the same two operators:
 
 Each tensor is read once by ``quantize``, which writes both directions (the columns
 only where a gradient reads them).
+``gated_linear(x, w_gate, w_up)`` is the gated layer ``act(x @ w_gate.T) * (x @ w_up.T)``
+in 16 bits, with its gradients by ``gated_linear_backward``.
 ``OrthogonalMomentum`` updates the weights with ``orthogonalize`` of their
 momentum.  ``python -m dense_gemm_blackwell_03_gb300.linear_training`` fits a
-small two-layer network to a teacher and prints the loss.
+small two-layer network to a teacher and prints the loss; with ``--gated`` its
+hidden layer is a gated one.
 """
 from __future__ import annotations
 
@@ -67,6 +70,32 @@ def scaled_linear(x, weight):
     return _ScaledLinear.apply(_aligned_rows(x), _aligned_rows(weight), grad and x.requires_grad, grad and weight.requires_grad)
 
 
+class _GatedLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, activation, keep):
+        if not keep:
+            return binding.gated_linear(x, w_gate, w_up, activation)
+        h, gate, up = binding.gated_linear(x, w_gate, w_up, activation, keep=True)
+        ctx.save_for_backward(gate, up, x, w_gate, w_up)
+        ctx.activation = activation
+        return h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable  # computed outside the graph: a second derivative raises
+    def backward(ctx, dh):
+        of_x, of_gate, of_up = ctx.needs_input_grad[:3]
+        dx, dwg, dwu = binding.gated_linear_backward(_aligned_rows(dh), *ctx.saved_tensors, ctx.activation, input_grad=of_x,
+                                                     weight_grads=of_gate or of_up)
+        return dx, dwg if of_gate else None, dwu if of_up else None, None, None
+
+
+def gated_linear(x, w_gate, w_up, activation="silu"):
+    """``act(x @ w_gate.T) * (x @ w_up.T)`` of CUDA matrices x (tokens x K), w_gate and w_up (N x K), all
+    bf16 or all fp16; differentiable in all three, once."""
+    keep = torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad)
+    return _GatedLinear.apply(_aligned_rows(x), _aligned_rows(w_gate), _aligned_rows(w_up), activation, keep)
+
+
 class OrthogonalMomentum:
     """Momentum whose update is its orthogonalised direction (Muon): per weight
 
@@ -92,8 +121,8 @@ class OrthogonalMomentum:
             w.grad = None
 
 
-def train(tokens=512, inner=256, hidden=640, outer=128, steps=60, seed=0, device="cuda:0"):
-    """Fit hidden(relu) and output layers to a random teacher; returns the losses."""
+def train(tokens=512, inner=256, hidden=640, outer=128, steps=60, seed=0, device="cuda:0", gated=False):
+    """Fit hidden(relu, or `gated` in bf16) and output layers to a random teacher; returns the losses."""
     gen = torch.Generator(device=device).manual_seed(seed)
 
     def draw(*shape):
@@ -102,11 +131,18 @@ def train(tokens=512, inner=256, hidden=640, outer=128, steps=60, seed=0, device
     teacher = draw(outer, inner) / inner ** 0.5
     w1 = (draw(hidden, inner) / inner ** 0.5).requires_grad_()
     w2 = (draw(outer, hidden) / hidden ** 0.5).requires_grad_()
-    opt = OrthogonalMomentum([w1, w2])
+    weights = [w1, w2]
+    if gated:
+        weights.append((draw(hidden, inner) / inner ** 0.5).requires_grad_())
+    opt = OrthogonalMomentum(weights)
     losses = []
     for _ in range(steps):
         x = draw(tokens, inner)
-        y = scaled_linear(torch.relu(scaled_linear(x, w1)), w2)
+        if gated:  # (the casts' gradients come back in the weights' fp32)
+            h = gated_linear(*(t.to(torch.bfloat16) for t in (x, weights[2], w1))).float()
+        else:
+            h = torch.relu(scaled_linear(x, w1))
+        y = scaled_linear(h, w2)
         loss = (y - x @ teacher.t()).square().mean()
         loss.backward()
         opt.step()
@@ -117,8 +153,9 @@ def train(tokens=512, inner=256, hidden=640, outer=128, steps=60, seed=0, device
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=60)
+    ap.add_argument("--gated", action="store_true", help="a gated hidden layer in bf16 instead of relu in 8 bits")
     a = ap.parse_args(argv)
-    losses = train(steps=a.steps)
+    losses = train(steps=a.steps, gated=a.gated)
     for i in range(0, len(losses), max(1, len(losses) // 10)):
         print(f"step {i:4d}  loss {losses[i]:.4f}")
     print(f"step {len(losses) - 1:4d}  loss {losses[-1]:.4f}")
