@@ -31,7 +31,7 @@ def act(name, g):
         s = torch.sigmoid(g)
         return g * s, s + g * s * (1 - s)
     if name == "gelu":
-        cdf = torch.special.ndtr(g)
+        cdf = torch.special.erfc(-g / math.sqrt(2)) / 2  # (torch's ndtr is 0 below -8.3)
         return g * cdf, cdf + g * torch.exp(-g * g / 2) / math.sqrt(2 * math.pi)
     c = math.sqrt(8 / math.pi)
     s = torch.sigmoid(c * (g + 0.044715 * g ** 3))
