@@ -61,6 +61,29 @@ bwgemm_status_t encode_operand16(CUtensorMap* map, CUtensorMap* map3, const void
     return st;
 }
 
+// 8-bit integers in boxes of 128 x box_rows (map), and of two whole 128s of K (map3); as above.
+bwgemm_status_t encode_bytes(CUtensorMap* map, CUtensorMap* map3, const void* data, int64_t ld, int64_t rows, int64_t K,
+                             uint32_t box_rows, CUtensorMapSwizzle swizzle)
+{
+    if (K >= 256) {
+        const cuuint64_t dims3[3] = {128, cuuint64_t(rows), cuuint64_t(K / 128)};
+        const cuuint64_t strides3[2] = {cuuint64_t(ld), 128};
+        const cuuint32_t box3[3] = {128, box_rows, 2};
+        const bwgemm_status_t st = encode(map3, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, data, dims3, strides3, box3, swizzle,
+                                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+        if (st != BWGEMM_OK)
+            return st;
+    }
+    const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(ld)};
+    const cuuint32_t box[2] = {128, box_rows};
+    const bwgemm_status_t st = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, data, dims, strides, box, swizzle,
+                                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    if (K < 256)
+        *map3 = *map;
+    return st;
+}
+
 bwgemm_status_t encode_result16(CUtensorMap* map, const bwgemm_matrix_t& x, int dtype, int64_t rows, int64_t cols)
 {
     const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
@@ -87,6 +110,8 @@ double lanes_step_us(const LanesVariant& v)
     return v.cg == 2 ? 0.57 : v.bn == 128 ? 0.46 : v.bn == 64 ? 0.37 : 0.25;
 }
 
+constexpr int64_t kNoWorkspaceRows = 32;  // 8-bit integers: so few rows of X take no workspace
+
 LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N, int64_t K,
                      const bwgemm_plan_options_t* opts, uint64_t workspace_bytes)
 {
@@ -95,7 +120,7 @@ LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N,
     LanesPlan best = {};
     for (int i = 0; i < kNumLanesVariants; ++i) {
         const LanesVariant& v = kLanesVariants[i];
-        if (v.mode != mode)
+        if (v.mode != mode || (mode == kLanesInt8 && M <= kNoWorkspaceRows && !lanes_widens(v.bn)))
             continue;
         const int W = v.cg == 2 ? capped(max_pairs, 2, opts) : capped(num_sms, 1, opts);
         if (W < 1)
@@ -622,7 +647,7 @@ bwgemm_status_t bwgemm_run_integer_workspace(int64_t M, int64_t N, int64_t K, ui
         return BWGEMM_ERR_INVALID_ARG;
     if (!fits(M) || !fits(N) || !fits(K) || M > kMostElements / round_up(std::max<int64_t>(K, 1), 128))
         return BWGEMM_ERR_UNSUPPORTED;
-    if (M > 0 && N > 0 && K > 0 && !takes_few_rows(kLanesInt8, M, N, K))
+    if (M > kNoWorkspaceRows && N > 0 && K > 0)
         *bytes = uint64_t(round_up(M * round_up(K, 128) * 2, 256));  // A as fp16
     return BWGEMM_OK;
 }
@@ -694,18 +719,22 @@ bwgemm_status_t bwgemm_run_integer(bwgemm_plan_t plan, const int8_t* A, const fl
     p.out[0] = C;
     p.ldo[0] = ldc;
     LanesMaps maps;
-    const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(N)};
-    const cuuint64_t strides[1] = {cuuint64_t(ldb)};
-    const cuuint32_t box[2] = {128, uint32_t(p.l_rows)};
-    if ((st = encode(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, B, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B)) != BWGEMM_OK ||
-        (st = encode_operand16(&maps.x, &maps.x3, workspace, ldy, BWGEMM_FP16, M, ldy, uint32_t(v.bn / v.cg))) != BWGEMM_OK)
+    p.l_chunks = int32_t(K / 128);
+    if ((st = encode_bytes(&maps.w, &maps.w3, B, ldb, N, K, uint32_t(p.l_rows), CU_TENSOR_MAP_SWIZZLE_128B)) != BWGEMM_OK)
         return st;
-    maps.w2 = maps.w3 = maps.w23 = maps.w;
-    const WidenParams wp = {A, lda, int32_t(M), int32_t(K), static_cast<uint16_t*>(workspace), ldy};
-    if (launch_widen(wp, s, pdl) != cudaSuccess)
-        return BWGEMM_ERR_CUDA;
-    plan->launches += 1;
+    maps.w2 = maps.w23 = maps.w;
+    if (lanes_widens(v.bn)) {
+        if ((st = encode_bytes(&maps.x, &maps.x3, A, lda, M, K, uint32_t(v.bn), CU_TENSOR_MAP_SWIZZLE_NONE)) != BWGEMM_OK)
+            return st;
+    } else {
+        if ((st = encode_operand16(&maps.x, &maps.x3, workspace, ldy, BWGEMM_FP16, M, ldy, uint32_t(v.bn / v.cg))) !=
+            BWGEMM_OK)
+            return st;
+        const WidenParams wp = {A, lda, int32_t(M), int32_t(K), static_cast<uint16_t*>(workspace), ldy};
+        if (launch_widen(wp, s, pdl) != cudaSuccess)
+            return BWGEMM_ERR_CUDA;
+        plan->launches += 1;
+    }
     if (launch_lanes(sel.variant, maps, p, sel.workers * v.cg, s, pdl) != cudaSuccess)
         return BWGEMM_ERR_CUDA;
     plan->launches += 1;

@@ -75,7 +75,7 @@ struct LanesParams {
     int32_t lrows, crows, K;     // rows of the weights and of X
     int32_t num_kb;              // ceil(K / 128)
     int32_t l_rows;              // weight rows per tile: a multiple of 8, at most 64, 128 or (pair) 256
-    int32_t l_chunks, c_chunks;  // whole 64-element chunks of the 16-bit operands' rows (0: no 3-D views)
+    int32_t l_chunks, c_chunks;  // whole chunks of the weights' and X's rows: of 64 elements, of 128 integers
     int32_t num_l, num_c;        // tiles along the weights' rows and X's
     int32_t raster_group;
     int32_t dp_tiles, sk_tiles;  // as in ScaledParams
@@ -104,8 +104,14 @@ constexpr LanesVariant kLanesVariants[] = {
 };
 constexpr int kNumLanesVariants = int(sizeof(kLanesVariants) / sizeof(kLanesVariants[0]));
 
-// w / w2: the weights (gated: of G and U) in boxes of 64 elements (int8: 128) x l_rows; w3, w23:
-// in two whole chunks; x, x3: X in boxes of 64 x (bn / cg).
+// Whether the 8-bit integers' tiles of `bn` rows of X take them as they are (else launch_widen's fp16).
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+constexpr bool lanes_widens(int bn) { return bn <= 32; }
+
+// w / w2: the weights (gated: of G and U) in boxes of a chunk x l_rows; w3, w23: of two whole
+// chunks; x, x3: X so, in bn / cg rows.
 struct LanesMaps {
     CUtensorMap w, w2, w3, w23, x, x3;
 };

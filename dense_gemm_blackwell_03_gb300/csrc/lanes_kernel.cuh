@@ -17,20 +17,21 @@
 // and become fp16 on the last stretch: four warps take a row each into registers, widen
 // it (xor 0x80 makes u = x + 128, a byte permutation 0x6400 | u = 1024 + u, one
 // subtraction 1024 + u - 1152 = x, all exact) and store it to TMEM, from where the MMA
-// reads its A operand.  X, the smaller or at least the shared operand, is widened before
-// (launch_widen) and comes through shared memory as fp16.
+// reads its A operand.  X goes through shared memory as fp16: in tiles of up to 32 rows it comes
+// as bytes too and is widened from one part of shared memory to another; in wider ones it is widened once before (launch_widen).
 //
 //   warp 0      TMA producer: a ring of stages of 128 of K of the weights (gated: and of X)
 //   warp 1      TMEM allocator and MMA issuer (in the even CTA of a pair)
-//   warp 2      kLanesInt8: TMA producer of X's ring
-//   warps 4..   kLanesInt8: groups of four converting warps, a TMEM lane quarter each; two
+//   warp 2      kLanesInt8: TMA producer of X's ring, or with one or three more what widens X
+//               into it
+//   then        kLanesInt8: groups of four converting warps, a TMEM lane quarter each; two
 //               groups take turns, so that one's waits overlap the other's work
 //   then        epilogue: four warps, eight from 128 columns on
 //
 // The integers' two rings: what bounds few rows of X is how many bytes of weights are on
 // their way, so those get most of the shared memory, and a stage is free as soon as it is
-// in registers.  They do not depend on the kernel that widens X, which lets this one start
-// only when all before it is done: their copies run while it works.
+// in registers.  They do not depend on launch_widen, which lets this kernel start only when
+// all before it is done: where it ran, their copies do not wait for it.
 //
 // Work: whole tiles, and the last, partial wave spread over all workers in K steps; the
 // warp that completes a tile's K adds the pieces in worker order (as in the block-scaled
@@ -53,22 +54,28 @@ struct LanesConfig {
     static constexpr int kXRows = BN / CG;                    // rows of X this CTA copies
     static constexpr int kLBytes = kGated ? 2 * 64 * kLanesK * 2 : 128 * kLanesK;
     static constexpr int kXBytes = kXRows * kLanesK * 2;
-    // The rings (gated: one, of both operands).  A step is what one barrier round trip between
-    // producers and MMA warp covers: kStep stages of the weights, each widened by a group of
-    // converting warps into its part of a TMEM slot, with X's part in shared memory.  The MMA warp's
-    // way through a step is some 600 cycles beside its MMAs, hence two stages where tiles are
-    // narrow (64 x 28672 x 8192: 49 us with one).  A stage past the end of K is passed on
-    // empty, so that each group meets every phase of its barriers.
+    // The rings (gated: one, of both operands).  A step is what one barrier round trip covers:
+    // kStep blocks of 128 of K, each widened by a group of converting warps into its part of a
+    // TMEM slot, with X's part in shared memory.  A warp's way through a barrier, its copies or
+    // MMAs and the arrivals is some 300 to 600 cycles, hence two blocks where tiles are narrow
+    // (64 x 28672 x 8192: 49 us with two blocks a step, 55 with one).
     static constexpr int kRingBytes = 222 * 1024;
     static constexpr int kStep = !kGated && BN <= 64 ? 2 : 1;
     static constexpr int kXStep = kStep * kXBytes;
     static constexpr int kXStages = kGated ? kRingBytes / (kLBytes + kXBytes) : 3;
     static constexpr int kConvGroups = kGated ? 0 : kStep;
-    static constexpr int kFit = (kRingBytes - kXStages * kXStep) / kLBytes;
-    static constexpr int kLStages = kGated ? kXStages : (kFit > 10 ? 10 : kFit) / kStep * kStep;
+    // X's bytes of a step, copied with its weights, and the warps that widen them: eight pieces
+    // of 16 a lane and step
+    static constexpr bool kWidens = !kGated && lanes_widens(BN);
+    static constexpr int kRawStep = kWidens ? BN * kStep * kLanesK : 0;
+    static constexpr int kXWarps = kWidens ? BN / 16 : 0;
+    static constexpr int kLStep = kStep * kLBytes;
+    static constexpr int kFit = (kRingBytes - kXStages * kXStep) / (kLStep + kRawStep);
+    static constexpr int kLStages = kGated ? kXStages : kFit > 10 / kStep ? 10 / kStep : kFit;
     static constexpr int kConvWarps = 4 * kConvGroups;
     static constexpr int kEpiWarps = lanes_epi_warps(BN);
-    static constexpr int kFirstEpi = 4 + kConvWarps;
+    static constexpr int kFirstConv = 4;
+    static constexpr int kFirstEpi = kFirstConv + kConvWarps;
     static constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
     static constexpr int kCols = BN / (kEpiWarps / 4);        // columns per epilogue warp
     static constexpr int kPiece = kCols < 32 ? kCols : 32;    // of which it reads this many at a time
@@ -81,11 +88,12 @@ struct LanesConfig {
     static_assert(kTmemCols >= 32 && kTmemCols <= 512, "TMEM");
     static constexpr size_t kPartialFloats = lanes_partial_floats(MODE, BN);
     static constexpr int kOffL = 0;
-    static constexpr int kOffX = kLStages * kLBytes;
-    static constexpr int kOffScale = kOffX + kXStages * kXStep;  // a warp's 32 scales of X
+    static constexpr int kOffX = kLStages * kLStep;
+    static constexpr int kOffRaw = kOffX + kXStages * kXStep;
+    static constexpr int kOffScale = kOffRaw + kLStages * kRawStep;  // a warp's 32 scales of X
     static constexpr int kOffBar = kOffScale + kEpiWarps * 128;
     // full, empty, wfull, wempty, acc_full, acc_empty, drain
-    static constexpr int kNumBars = 2 * kXStages + 2 * kLStages + 2 * kBufs + 1;
+    static constexpr int kNumBars = 2 * (kXStages + kLStages + kBufs) + 1;
     static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars;
     static constexpr int kOffAbort = kOffTmemSlot + 4;
     static constexpr int kSmemBytes = kOffAbort + 4 + 1024;
@@ -131,7 +139,7 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
     const uint32_t sX = base + Cfg::kOffX;
     const uint32_t bar_full = base + Cfg::kOffBar;              // X has landed, the weights (widened) are there
     const uint32_t bar_empty = bar_full + 8 * XS;
-    const uint32_t bar_wfull = bar_empty + 8 * XS;              // 8-bit weights have landed
+    const uint32_t bar_wfull = bar_empty + 8 * XS;              // 8-bit weights (and X) have landed
     const uint32_t bar_wempty = bar_wfull + 8 * LS;
     const uint32_t bar_acc_full = bar_wempty + 8 * LS;
     const uint32_t bar_acc_empty = bar_acc_full + 8 * Cfg::kBufs;
@@ -141,12 +149,12 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
 
     if (threadIdx.x == 64) {
         for (int s = 0; s < XS; ++s) {
-            ptx::mbar_init(bar_full + 8 * s, GATED ? 1 : 1 + CG * Cfg::kConvWarps);  // a producer, and the converting warps
+            ptx::mbar_init(bar_full + 8 * s, GATED ? 1 : (Cfg::kWidens ? Cfg::kXWarps : 1) + CG * Cfg::kConvWarps);
             ptx::mbar_init(bar_empty + 8 * s, 1);
         }
-        for (int s = 0; s < LS; ++s) {
+        for (int s = 0; !GATED && s < LS; ++s) {
             ptx::mbar_init(bar_wfull + 8 * s, 1);
-            ptx::mbar_init(bar_wempty + 8 * s, 4);
+            ptx::mbar_init(bar_wempty + 8 * s, Cfg::kConvWarps + Cfg::kXWarps);
         }
         for (int b = 0; b < Cfg::kBufs; ++b) {
             ptx::mbar_init(bar_acc_full + 8 * b, 1);
@@ -158,7 +166,7 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
     }
     if (warp == 0 && lane == 0) {
         ptx::prefetch_tensormap(&maps.w);
-        ptx::prefetch_tensormap(&maps.x3);
+        ptx::prefetch_tensormap(Cfg::kWidens ? &maps.x : &maps.x3);
         if (GATED) {
             ptx::prefetch_tensormap(&maps.w3);
             ptx::prefetch_tensormap(&maps.w23);
@@ -206,9 +214,8 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
         bool ok = true;
         while (ok && iter.next(p, seg)) {
             const int l_row = (seg.l_blk * CG + int(rank)) * l_rows;
-            const int kb1 = seg.kb0 + (seg.kb1 - seg.kb0 + Cfg::kStep - 1) / Cfg::kStep * Cfg::kStep;
 #pragma unroll 1
-            for (int kb = seg.kb0; kb < kb1; ++kb, ++n) {
+            for (int kb = seg.kb0; kb < seg.kb1; kb += Cfg::kStep, ++n) {
                 ok = warp_wait((GATED ? bar_empty : bar_wempty) + 8 * s, phase ^ 1u, p, abort_flag, kStatusProducerTimeout);
                 if (!ok)
                     break;
@@ -217,7 +224,7 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
                 if (!stall)
                     arm(s, phase);
                 if (!stall && ptx::elect_one()) {
-                    const uint32_t dL = sL + uint32_t(s * Cfg::kLBytes);
+                    const uint32_t dL = sL + uint32_t(s * Cfg::kLStep);
                     const int k = kb * kLanesK;
                     if constexpr (GATED) {
                         const uint32_t fb = bar_full + 8 * s;
@@ -236,11 +243,23 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
                         }
                         load_x(sX + uint32_t(s * Cfg::kXBytes), fb, seg.c_blk * BN, kb);
                     } else {
-                        if (kb < seg.kb1) {
-                            ptx::mbar_arrive_expect_tx(bar_wfull + 8 * s, uint32_t(l_rows * 128));
-                            ptx::tma_load_2d(dL, &maps.w, bar_wfull + 8 * s, k, l_row);
+                        // a step's blocks in one copy where all lie in whole 128s of K
+                        const uint32_t wb = bar_wfull + 8 * s, dR = base + uint32_t(Cfg::kOffRaw + s * Cfg::kRawStep);
+                        const int count = min(Cfg::kStep, seg.kb1 - kb);
+                        const int x_row = seg.c_blk * BN;
+                        ptx::mbar_arrive_expect_tx(wb, uint32_t(count * kLanesK * (l_rows + (Cfg::kWidens ? BN : 0))));
+                        if (Cfg::kWidens && n == 0)  // (launch_widen has waited for what was before it)
+                            ptx::grid_dependency_wait();
+                        if (Cfg::kStep == 2 && count == 2 && kb + 2 <= p.l_chunks) {
+                            ptx::tma_load_3d(dL, &maps.w3, wb, 0, l_row, kb);
+                            if (Cfg::kWidens)
+                                ptx::tma_load_3d(dR, &maps.x3, wb, 0, x_row, kb);
                         } else {
-                            ptx::mbar_arrive(bar_wfull + 8 * s);
+                            for (int i = 0; i < count; ++i) {
+                                ptx::tma_load_2d(dL + uint32_t(i * l_rows * kLanesK), &maps.w, wb, k + i * kLanesK, l_row);
+                                if (Cfg::kWidens)
+                                    ptx::tma_load_2d(dR + uint32_t(i * BN * kLanesK), &maps.x, wb, k + i * kLanesK, x_row);
+                            }
                         }
                     }
                 }
@@ -251,7 +270,66 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
                 }
             }
         }
-    } else if (!GATED && warp == 2) {
+    } else if (Cfg::kWidens && warp >= 2 && warp < 2 + Cfg::kXWarps) {
+        // --------------------------------- X's bytes to fp16, within shared memory
+        // A row's step is 256 integers, 16 pieces; a warp takes two rows at a time.  Eight
+        // lanes next to each other take four pieces of both, of different chunks: neither
+        // their reads (rows of 128 bytes) nor their writes (pieces by row mod 8) share a bank.
+        constexpr int PIECES = 8, APART = 2 * (Cfg::kXWarps > 0 ? Cfg::kXWarps : 1);
+        const int odd = (lane >> 2) & 1, block = lane >> 4, chunk = ((lane >> 3) & 1) ^ odd;
+        const int r0 = 2 * (warp - 2) + odd;  // this lane's rows: r0, r0 + APART, ...
+        const uint32_t from0 = base + uint32_t(Cfg::kOffRaw + (block * BN + r0) * kLanesK + chunk * 64 + (lane & 3) * 16);
+        // the piece's place: 16-byte pieces c0 and c0 + 1 of its rows in the block's chunk
+        const uint32_t to0 = sX + uint32_t(block * Cfg::kXBytes + chunk * (Cfg::kXRows * 128) + r0 * 128);
+        const uint32_t c0 = uint32_t(2 * (lane & 3));
+        int s = 0, ws = 0;
+        uint32_t phase = 0, wphase = 0;
+        bool ok = true;
+        while (ok && iter.next(p, seg)) {
+#pragma unroll 1
+            for (int kb = seg.kb0; kb < seg.kb1; kb += Cfg::kStep) {
+                ok = warp_wait(bar_wfull + 8 * ws, wphase, p, abort_flag, kStatusMmaTimeout);
+                if (!ok)
+                    break;
+                uint4 v[PIECES];
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i)
+                    ptx::ld_shared_v4(from0 + uint32_t(ws * Cfg::kRawStep + i * APART * kLanesK), v[i].x, v[i].y, v[i].z, v[i].w);
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(bar_wempty + 8 * ws);
+                ok = warp_wait(bar_empty + 8 * s, phase ^ 1u, p, abort_flag, kStatusMmaTimeout);
+                if (!ok)
+                    break;
+                if (kb + block < seg.kb1) {
+#pragma unroll
+                    for (int i = 0; i < PIECES; ++i) {
+                        uint4 a, b;
+                        widen4(v[i].x, a.x, a.y);
+                        widen4(v[i].y, a.z, a.w);
+                        widen4(v[i].z, b.x, b.y);
+                        widen4(v[i].w, b.z, b.w);
+                        const uint32_t to = to0 + uint32_t(s * Cfg::kXStep + i * APART * 128);
+                        const uint32_t swz = uint32_t((r0 + i * APART) & 7);
+                        ptx::st_shared_v4(to + ((c0 ^ swz) << 4), a.x, a.y, a.z, a.w);
+                        ptx::st_shared_v4(to + (((c0 + 1) ^ swz) << 4), b.x, b.y, b.z, b.w);
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(bar_full + 8 * s);
+                if (++ws == LS) {
+                    ws = 0;
+                    wphase ^= 1u;
+                }
+                if (++s == XS) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (!GATED && !Cfg::kWidens && warp == 2) {
         // ------------------------------------------------------ TMA producer of X
         const uint32_t leader_full = CG == 2 ? ptx::map_to_cta(bar_full, 0) : bar_full;
         ptx::grid_dependency_wait();  // what X is widened by
@@ -343,14 +421,14 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
                 bphase ^= 1u;
             }
         }
-    } else if (!GATED && warp >= 4 && warp < Cfg::kFirstEpi) {
+    } else if (!GATED && warp >= Cfg::kFirstConv && warp < Cfg::kFirstEpi) {
         // ------------------------------------------------- 8-bit weights to fp16
-        const int group = (warp - 4) >> 2, q = warp & 3;
+        const int group = (warp - Cfg::kFirstConv) >> 2, q = warp & 3;
         const int row = 32 * q + lane;
         const uint32_t leader_full = CG == 2 ? ptx::map_to_cta(bar_full, 0) : bar_full;
-        const uint32_t src0 = sL + uint32_t(row * 128);
+        const uint32_t src0 = sL + uint32_t(group * l_rows * kLanesK + row * 128);
         const uint32_t dst0 = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(Cfg::kACol0);
-        int s = group, a = 0;
+        int s = 0, a = 0;
         uint32_t phase = 0, aphase = 0;
         bool ok = true;
         while (ok && iter.next(p, seg)) {
@@ -359,7 +437,7 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
                 ok = warp_wait(bar_wfull + 8 * s, phase, p, abort_flag, kStatusMmaTimeout);
                 if (!ok)
                     break;
-                const uint32_t src = src0 + uint32_t(s * Cfg::kLBytes);
+                const uint32_t src = src0 + uint32_t(s * Cfg::kLStep);
                 uint32_t w[8][4];
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
@@ -391,9 +469,8 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
                     else
                         ptx::mbar_arrive(bar_full + 8 * a);
                 }
-                s += Cfg::kStep;
-                if (s >= LS) {
-                    s -= LS;
+                if (++s == LS) {
+                    s = 0;
                     phase ^= 1u;
                 }
                 if (++a == XS) {
@@ -596,7 +673,7 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
             __syncwarp();
             drain_wait(bar_drain, 0u, kDrainNs);
         }
-        if (warp == 0 || (!GATED && warp == 2)) {
+        if (warp == 0 || (!GATED && !Cfg::kWidens && warp == 2)) {
             const uint32_t bar = GATED || warp == 2 ? bar_full : bar_wfull;
 #pragma unroll 1
             for (int s = 0; s < (GATED || warp == 2 ? XS : LS); ++s)

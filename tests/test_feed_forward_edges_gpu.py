@@ -393,9 +393,9 @@ def test_int8_refusals(plan):
     f = torch.zeros(64 * 64, device="cuda")
     ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda").data_ptr()
     at, s, host = q.data_ptr(), f.data_ptr(), np.zeros(64).ctypes.data // 16 * 16
-    need = binding._workspace_bytes("bwgemm_run_integer_workspace", 20, 64, 256)
+    need = binding._workspace_bytes("bwgemm_run_integer_workspace", 40, 64, 256)
 
-    def raw(A=at, sa=s, B=at, sb=s, C=s, M=20, N=64, K=256, lda=256, ldb=256, ldc=64, out=0, workspace=ws, size=need):
+    def raw(A=at, sa=s, B=at, sb=s, C=s, M=40, N=64, K=256, lda=256, ldb=256, ldc=64, out=0, workspace=ws, size=need):
         return plan.lib.bwgemm_run_integer(plan.handle, A, sa, B, sb, C, M, N, K, lda, ldb, ldc, out, workspace, size, None)
     assert raw(M=0) == raw(N=0) == raw(K=0, A=None, B=None, sa=None, sb=None, workspace=None, size=0) == 0
     for bad in (dict(A=None), dict(sa=None), dict(B=None), dict(sb=None), dict(C=None), dict(M=-1), dict(N=-1), dict(K=-1), dict(lda=255),

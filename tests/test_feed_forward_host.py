@@ -87,16 +87,19 @@ def test_backward_workspace(lib):
 def test_integer_workspace(lib):
     name = "bwgemm_run_integer_workspace"
     assert lib.bwgemm_run_integer_workspace(1, 1, 1, None) == INVALID
-    for sizes in ((0, 5, 5), (5, 0, 5), (5, 5, 0), (1, 8192, 8192), (8, 28672, 8192)):
+    for sizes in ((0, 5, 5), (50, 0, 5), (50, 5, 0), (1, 8192, 8192), (32, 28672, 8192), (8, 16, 1 << 20)):
         assert workspace(lib, name, *sizes) == (0, 0)
     assert workspace(lib, name, 5, 5, -1)[0] == INVALID
     assert workspace(lib, name, 1 << 31, 5, 5)[0] == workspace(lib, name, (1 << 31) - 256, 1, (1 << 31) - 256)[0] == UNSUP
-    for M, N, K in ((17, 5, 5), (9, 28672, 8192), (4096, 1, 129)):  # A as fp16, rows padded to 128
+    for M, N, K in ((33, 5, 5), (40, 28672, 8192), (4096, 1, 129)):  # A as fp16, rows padded to 128
         rc, n = workspace(lib, name, M, N, K)
         need = M * (-(-K // 128) * 128) * 2
         assert rc == 0 and need <= n < need + 256
-    # (8 rows of a K whose 32-bit sums could overflow go through tiles)
-    assert workspace(lib, name, 8, 16, 131071) == (0, 0) and workspace(lib, name, 8, 16, 131072)[1] > 0
+
+
+def test_few_rows_of_integers_whose_sums_fit():
+    # 32-bit sums of products of up to 2^14
+    assert binding.select_int8(SMS, 8, 16, 131071)["lanes"] == 2 and binding.select_int8(SMS, 8, 16, 131072)["lanes"] == 1
 
 
 # ------------------------------------------------------------ division of the work
@@ -310,11 +313,11 @@ def test_integers_describe_their_operands(plan):
     call = plan.lib.calls[-1]
     assert [call[k] for k in ("A", "sa", "B", "sb", "C", "M", "N", "K", "lda", "ldb", "ldc", "out", "workspace", "workspace_bytes")] == [
         q.data_ptr(), s.data_ptr(), b.data_ptr(), sb.data_ptr(), c.data_ptr(), 3, 40, 20, 32, 48, 40, binding.FP16, None, 0]
-    out = z(17, 61, dtype=torch.float32, wide=80)
-    assert plan.gemm_int8(z(17, 20, dtype=torch.int8, wide=32), torch.zeros(17), z(61, 20, dtype=torch.int8, wide=32),
+    out = z(37, 61, dtype=torch.float32, wide=80)
+    assert plan.gemm_int8(z(37, 20, dtype=torch.int8, wide=32), torch.zeros(37), z(61, 20, dtype=torch.int8, wide=32),
                           torch.zeros(61), out=out) is out
     call = plan.lib.calls[-1]
-    assert call["ldc"] == 80 and call["out"] == binding.FP32 and call["workspace_bytes"] == 17 * 128 * 2
+    assert call["ldc"] == 80 and call["out"] == binding.FP32 and call["workspace_bytes"] == 37 * 128 * 2
     assert call["workspace"] is not None
     q0, s0 = plan.quantize_int8(z(3, 0))  # rows without a value: as rows of zeros
     assert q0.shape == (3, 0) and (s0 == torch.tensor(2.0 ** -100 / 127)).all()
