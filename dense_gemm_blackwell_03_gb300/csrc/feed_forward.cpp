@@ -110,7 +110,13 @@ double lanes_step_us(const LanesVariant& v)
     return v.cg == 2 ? 0.57 : v.bn == 128 ? 0.46 : v.bn == 64 ? 0.37 : 0.25;
 }
 
-constexpr int64_t kNoWorkspaceRows = 32;  // 8-bit integers: so few rows of X take no workspace
+// Whether a product of 8-bit integers takes X as it is at every division of its work: there
+// is no workspace for its fp16 then.  Up to 32 rows, but for large weights, whose bytes come
+// faster than a step of 32 rows is widened (see lanes_kernel.cuh).
+bool widens_always(int64_t M, int64_t N, int64_t K)
+{
+    return M <= 16 || (M <= 32 && double(N) * double(K) <= 64e6);
+}
 
 LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N, int64_t K,
                      const bwgemm_plan_options_t* opts, uint64_t workspace_bytes)
@@ -120,7 +126,9 @@ LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N,
     LanesPlan best = {};
     for (int i = 0; i < kNumLanesVariants; ++i) {
         const LanesVariant& v = kLanesVariants[i];
-        if (v.mode != mode || (mode == kLanesInt8 && M <= kNoWorkspaceRows && !lanes_widens(v.bn)))
+        if (v.mode != mode)
+            continue;
+        if (mode == kLanesInt8 && (widens_always(M, N, K) ? !v.widens : v.widens && double(N) * double(K) > 64e6))
             continue;
         const int W = v.cg == 2 ? capped(max_pairs, 2, opts) : capped(num_sms, 1, opts);
         if (W < 1)
@@ -647,7 +655,7 @@ bwgemm_status_t bwgemm_run_integer_workspace(int64_t M, int64_t N, int64_t K, ui
         return BWGEMM_ERR_INVALID_ARG;
     if (!fits(M) || !fits(N) || !fits(K) || M > kMostElements / round_up(std::max<int64_t>(K, 1), 128))
         return BWGEMM_ERR_UNSUPPORTED;
-    if (M > kNoWorkspaceRows && N > 0 && K > 0)
+    if (M > 0 && N > 0 && K > 0 && !takes_few_rows(kLanesInt8, M, N, K) && !widens_always(M, N, K))
         *bytes = uint64_t(round_up(M * round_up(K, 128) * 2, 256));  // A as fp16
     return BWGEMM_OK;
 }
@@ -723,7 +731,7 @@ bwgemm_status_t bwgemm_run_integer(bwgemm_plan_t plan, const int8_t* A, const fl
     if ((st = encode_bytes(&maps.w, &maps.w3, B, ldb, N, K, uint32_t(p.l_rows), CU_TENSOR_MAP_SWIZZLE_128B)) != BWGEMM_OK)
         return st;
     maps.w2 = maps.w23 = maps.w;
-    if (lanes_widens(v.bn)) {
+    if (v.widens) {
         if ((st = encode_bytes(&maps.x, &maps.x3, A, lda, M, K, uint32_t(v.bn), CU_TENSOR_MAP_SWIZZLE_NONE)) != BWGEMM_OK)
             return st;
     } else {

@@ -96,19 +96,14 @@ struct LanesParams {
 
 struct LanesVariant {
     int mode, cg, bn;
+    bool widens = false;  // takes X as 8-bit integers (else launch_widen's fp16)
 };
 constexpr LanesVariant kLanesVariants[] = {
-    {kLanesGated, 1, 16}, {kLanesGated, 1, 32}, {kLanesGated, 1, 64}, {kLanesGated, 1, 128},
-    {kLanesInt8, 1, 16},  {kLanesInt8, 1, 32},  {kLanesInt8, 1, 64},  {kLanesInt8, 1, 128},
-    {kLanesInt8, 2, 256},
+    {kLanesGated, 1, 16},      {kLanesGated, 1, 32},      {kLanesGated, 1, 64}, {kLanesGated, 1, 128},
+    {kLanesInt8, 1, 16, true}, {kLanesInt8, 1, 32, true}, {kLanesInt8, 1, 32},  {kLanesInt8, 1, 64},
+    {kLanesInt8, 1, 128},      {kLanesInt8, 2, 256},
 };
 constexpr int kNumLanesVariants = int(sizeof(kLanesVariants) / sizeof(kLanesVariants[0]));
-
-// Whether the 8-bit integers' tiles of `bn` rows of X take them as they are (else launch_widen's fp16).
-#ifdef __CUDACC__
-__host__ __device__
-#endif
-constexpr bool lanes_widens(int bn) { return bn <= 32; }
 
 // w / w2: the weights (gated: of G and U) in boxes of a chunk x l_rows; w3, w23: of two whole
 // chunks; x, x3: X so, in bn / cg rows.

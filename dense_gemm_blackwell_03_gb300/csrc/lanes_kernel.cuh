@@ -17,13 +17,16 @@
 // and become fp16 on the last stretch: four warps take a row each into registers, widen
 // it (xor 0x80 makes u = x + 128, a byte permutation 0x6400 | u = 1024 + u, one
 // subtraction 1024 + u - 1152 = x, all exact) and store it to TMEM, from where the MMA
-// reads its A operand.  X goes through shared memory as fp16: in tiles of up to 32 rows it comes
-// as bytes too and is widened from one part of shared memory to another; in wider ones it is widened once before (launch_widen).
+// reads its A operand.  X goes through shared memory as fp16, widened once before
+// (launch_widen) or, of up to 32 rows a tile (WIDENS), by two warps from one part of shared
+// memory to another.  That saves a launch and the workspace, but takes them 870 (16 rows) and
+// 1250 (32 rows) cycles a step, the latter more than the weights of 256 of K take from HBM:
+// 32 x 28672 x 8192 51 us, 44 when widened before; 64 x 4096 x 4096 13.8 and 14.5 us, and 4 us less
+// of host time.
 //
 //   warp 0      TMA producer: a ring of stages of 128 of K of the weights (gated: and of X)
 //   warp 1      TMEM allocator and MMA issuer (in the even CTA of a pair)
-//   warp 2      kLanesInt8: TMA producer of X's ring, or with one or three more what widens X
-//               into it
+//   warp 2      kLanesInt8: TMA producer of X's ring, or with warp 3 what widens X into it
 //   then        kLanesInt8: groups of four converting warps, a TMEM lane quarter each; two
 //               groups take turns, so that one's waits overlap the other's work
 //   then        epilogue: four warps, eight from 128 columns on
@@ -46,7 +49,7 @@ namespace bwgemm {
 
 constexpr int kLanesK = 128;  // of K per stage
 
-template <int MODE, int CG, int BN>
+template <int MODE, int CG, int BN, bool WIDENS>
 struct LanesConfig {
     static constexpr bool kGated = MODE == kLanesGated;
     static_assert(CG == 1 || (!kGated && BN == 256), "pairs: 8-bit integers, 256 rows of X");
@@ -64,11 +67,11 @@ struct LanesConfig {
     static constexpr int kXStep = kStep * kXBytes;
     static constexpr int kXStages = kGated ? kRingBytes / (kLBytes + kXBytes) : 3;
     static constexpr int kConvGroups = kGated ? 0 : kStep;
-    // X's bytes of a step, copied with its weights, and the warps that widen them: eight pieces
-    // of 16 a lane and step
-    static constexpr bool kWidens = !kGated && lanes_widens(BN);
+    // X's bytes of a step, copied with its weights, and the warps that widen them
+    static constexpr bool kWidens = WIDENS;
+    static_assert(!WIDENS || (!kGated && BN <= 32), "widened by two warps");
     static constexpr int kRawStep = kWidens ? BN * kStep * kLanesK : 0;
-    static constexpr int kXWarps = kWidens ? BN / 16 : 0;
+    static constexpr int kXWarps = kWidens ? 2 : 0;
     static constexpr int kLStep = kStep * kLBytes;
     static constexpr int kFit = (kRingBytes - kXStages * kXStep) / (kLStep + kRawStep);
     static constexpr int kLStages = kGated ? kXStages : kFit > 10 / kStep ? 10 / kStep : kFit;
@@ -118,11 +121,11 @@ __device__ __forceinline__ uint16_t round16(float v, int dtype)
     return dtype == BWGEMM_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
 
-template <int MODE, int CG, int BN>
-__global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
+template <int MODE, int CG, int BN, bool WIDENS>
+__global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1)
     lanes_kernel(const __grid_constant__ LanesMaps maps, const LanesParams p)
 {
-    using Cfg = LanesConfig<MODE, CG, BN>;
+    using Cfg = LanesConfig<MODE, CG, BN, WIDENS>;
     constexpr bool GATED = Cfg::kGated;
     constexpr int XS = Cfg::kXStages, LS = Cfg::kLStages;
     extern __shared__ uint8_t smem_raw[];
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN>::kThreads, 1)
         // A row's step is 256 integers, 16 pieces; a warp takes two rows at a time.  Eight
         // lanes next to each other take four pieces of both, of different chunks: neither
         // their reads (rows of 128 bytes) nor their writes (pieces by row mod 8) share a bank.
-        constexpr int PIECES = 8, APART = 2 * (Cfg::kXWarps > 0 ? Cfg::kXWarps : 1);
+        constexpr int PIECES = BN / 4, APART = 4;  // of 16 integers, for each lane and step; rows between them
         const int odd = (lane >> 2) & 1, block = lane >> 4, chunk = ((lane >> 3) & 1) ^ odd;
         const int r0 = 2 * (warp - 2) + odd;  // this lane's rows: r0, r0 + APART, ...
         const uint32_t from0 = base + uint32_t(Cfg::kOffRaw + (block * BN + r0) * kLanesK + chunk * 64 + (lane & 3) * 16);

@@ -5,11 +5,11 @@
 namespace bwgemm {
 namespace {
 
-template <int MODE, int CG, int BN>
+template <int MODE, int CG, int BN, bool WIDENS = false>
 cudaError_t launch_one(const LanesMaps& maps, const LanesParams& p, int grid, cudaStream_t stream, bool pdl)
 {
-    using Cfg = LanesConfig<MODE, CG, BN>;
-    auto kernel = lanes_kernel<MODE, CG, BN>;
+    using Cfg = LanesConfig<MODE, CG, BN, WIDENS>;
+    auto kernel = lanes_kernel<MODE, CG, BN, WIDENS>;
     if (grid % CG != 0)
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> allowed{0};
@@ -44,17 +44,18 @@ cudaError_t launch_one(const LanesMaps& maps, const LanesParams& p, int grid, cu
 
 cudaError_t launch_lanes(int idx, const LanesMaps& maps, const LanesParams& p, int grid, cudaStream_t stream, bool pdl)
 {
-    static_assert(kNumLanesVariants == 9, "one case per variant below, in the order of kLanesVariants");
+    static_assert(kNumLanesVariants == 10, "one case per variant below, in the order of kLanesVariants");
     switch (idx) {
     case 0: return launch_one<kLanesGated, 1, 16>(maps, p, grid, stream, pdl);
     case 1: return launch_one<kLanesGated, 1, 32>(maps, p, grid, stream, pdl);
     case 2: return launch_one<kLanesGated, 1, 64>(maps, p, grid, stream, pdl);
     case 3: return launch_one<kLanesGated, 1, 128>(maps, p, grid, stream, pdl);
-    case 4: return launch_one<kLanesInt8, 1, 16>(maps, p, grid, stream, pdl);
-    case 5: return launch_one<kLanesInt8, 1, 32>(maps, p, grid, stream, pdl);
-    case 6: return launch_one<kLanesInt8, 1, 64>(maps, p, grid, stream, pdl);
-    case 7: return launch_one<kLanesInt8, 1, 128>(maps, p, grid, stream, pdl);
-    case 8: return launch_one<kLanesInt8, 2, 256>(maps, p, grid, stream, pdl);
+    case 4: return launch_one<kLanesInt8, 1, 16, true>(maps, p, grid, stream, pdl);
+    case 5: return launch_one<kLanesInt8, 1, 32, true>(maps, p, grid, stream, pdl);
+    case 6: return launch_one<kLanesInt8, 1, 32>(maps, p, grid, stream, pdl);
+    case 7: return launch_one<kLanesInt8, 1, 64>(maps, p, grid, stream, pdl);
+    case 8: return launch_one<kLanesInt8, 1, 128>(maps, p, grid, stream, pdl);
+    case 9: return launch_one<kLanesInt8, 2, 256>(maps, p, grid, stream, pdl);
     default: return cudaErrorInvalidValue;
     }
 }

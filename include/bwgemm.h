@@ -658,7 +658,7 @@ bwgemm_status_t bwgemm_quantize_integer(bwgemm_plan_t plan, const void* X, bwgem
  *   C : M x N bf16, fp16 or fp32 (`out`), row stride ldc elements, 16-byte aligned, ldc a
  *       multiple of 16 bytes
  *   workspace : device memory, 256-byte aligned, of at least bwgemm_run_integer_workspace()
- *       bytes (else BWGEMM_ERR_WORKSPACE; NULL where that is 0, as for M <= 32), holding
+ *       bytes (else BWGEMM_ERR_WORKSPACE; NULL where that is 0, as for M <= 16), holding
  *       nothing of use before or after
  *
  * Sums are fp32: exact as long as none passes 2^24 in magnitude (K <= 1024 for any operands),
