@@ -3,7 +3,8 @@
 //
 // The weights' bytes are the time: each is read once.  16 weight rows are the rows of
 // mma.sync's m16n8k32 (integers: exact 32-bit sums) or m16n8k16 (bf16, fp16), rows of X its
-// 8 columns.  In the gated form rows 0 to 7 are Wg's and 8 to 15 the same rows of Wu: a lane's
+// 8 columns.  (The integer instruction is slow on this GPU: one row of X, 8192 x 8192, keeps
+// the tensor pipe busy 56 % of the time; one and two rows take dot products instead.)  In the gated form rows 0 to 7 are Wg's and 8 to 15 the same rows of Wu: a lane's
 // accumulator then holds G in its first half and U of the same outputs in its second.
 // The contraction does not care which K a position stands for as long as both operands
 // agree, so lane (g, q) takes whole 16-byte pieces: bytes 16 q and 64 + 16 q of rows g and
@@ -11,7 +12,9 @@
 //
 // A CTA takes 16 weight rows, its eight warps the blocks of their K in turn, kFewRing blocks
 // in flight each (asynchronous copies that every lane makes and reads for itself: nobody
-// waits for anybody), and their sums meet in shared memory in warp order.
+// waits for anybody), and their sums meet in shared memory in warp order.  Measured at one
+// row: integers 8192 x 8192 12.5 us (5.4 TB/s), 28672 x 8192 36.9 (6.4 TB/s); gated 10240 x 8192
+// 50.2 (6.7 TB/s, 98 % of the copy rate).  Rings of four blocks: 15.9 us on 8192 x 8192.
 #include "activation.cuh"
 #include "feed_forward.h"
 #include "gemm_kernel.cuh"
@@ -62,8 +65,20 @@ __device__ __forceinline__ uint16_t round_to(float v, int dtype)
     return dtype == BWGEMM_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
 
-// NT: groups of 8 rows of X (1 or 2).
-template <int KIND, int NT, int kFewWarps>
+// One lane's part of 16 bytes of a weight row and of a row of X.
+__device__ __forceinline__ void dot_piece(uint32_t& d, const uint4& w, const uint4& x)
+{
+    int v = int(d);
+    v = __dp4a(int(w.x), int(x.x), v);
+    v = __dp4a(int(w.y), int(x.y), v);
+    v = __dp4a(int(w.z), int(x.z), v);
+    v = __dp4a(int(w.w), int(x.w), v);
+    d = uint32_t(v);
+}
+
+// NT: groups of 8 rows of X (1 or 2).  DOTS: no matrix instructions, but a dot product of four
+// integers at a time for each of DOTS rows of X (0: none).
+template <int KIND, int NT, int DOTS, int kFewWarps>
 __global__ void __launch_bounds__(32 * kFewWarps, 32 / kFewWarps) few_rows_kernel(const FewRowsParams p)
 {
     constexpr bool INT8 = KIND == kFewInt8;
@@ -76,13 +91,15 @@ __global__ void __launch_bounds__(32 * kFewWarps, 32 / kFewWarps) few_rows_kerne
     const uint8_t* const w0 = p.w[0] + int64_t(min(n0 + g, p.N - 1)) * p.ldw[0];
     const uint8_t* const w1 = INT8 ? p.w[0] + int64_t(min(n0 + 8 + g, p.N - 1)) * p.ldw[0]
                                    : p.w[1] + int64_t(min(n0 + g, p.N - 1)) * p.ldw[1];
-    const uint8_t* x_at[NT];
+    static_assert(DOTS == 0 || (INT8 && NT == 1 && DOTS <= 2), "integers, few rows");
+    constexpr int XT = DOTS > 0 ? DOTS : NT;  // rows of X whose pieces a lane loads
+    const uint8_t* x_at[XT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-        x_at[t] = p.x + int64_t(min(8 * t + g, p.M - 1)) * p.ldx;
-    uint32_t sum[NT][4];
+    for (int t = 0; t < XT; ++t)
+        x_at[t] = p.x + int64_t(min(DOTS > 0 ? t : 8 * t + g, p.M - 1)) * p.ldx;
+    uint32_t sum[XT][4];  // (DOTS: of weight rows g and g + 8, in 0 and 1)
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < XT; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             sum[t][i] = 0u;
@@ -108,9 +125,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 32 / kFewWarps) few_rows_kerne
     int slot = 0;
 #pragma unroll 1
     for (int kb = warp; kb < whole; kb += kFewWarps) {
-        uint4 x[NT][2];
+        uint4 x[XT][2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < XT; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 x[t][h] = ptx::ld_global_ca_v4(x_at[t] + int64_t(kb) * 128 + 64 * h + 16 * q);
@@ -125,8 +142,14 @@ __global__ void __launch_bounds__(32 * kFewWarps, 32 / kFewWarps) few_rows_kerne
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                mma_piece<KIND>(sum[t], lo[h], hi[h], x[t][h]);
+            for (int t = 0; t < XT; ++t) {
+                if constexpr (DOTS > 0) {
+                    dot_piece(sum[t][0], lo[h], x[t][h]);
+                    dot_piece(sum[t][1], hi[h], x[t][h]);
+                } else {
+                    mma_piece<KIND>(sum[t], lo[h], hi[h], x[t][h]);
+                }
+            }
         fetch(kb + kFewRing * kFewWarps, slot);
         slot = slot + 1 == kFewRing ? 0 : slot + 1;
     }
@@ -136,8 +159,15 @@ __global__ void __launch_bounds__(32 * kFewWarps, 32 / kFewWarps) few_rows_kerne
             const int64_t k = int64_t(whole) * 128 + 64 * h + 16 * q;
             const uint4 lo = load_ragged(w0, k, p.row_bytes), hi = load_ragged(w1, k, p.row_bytes);
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                mma_piece<KIND>(sum[t], lo, hi, load_ragged(x_at[t], k, p.row_bytes));
+            for (int t = 0; t < XT; ++t) {
+                const uint4 x = load_ragged(x_at[t], k, p.row_bytes);
+                if constexpr (DOTS > 0) {
+                    dot_piece(sum[t][0], lo, x);
+                    dot_piece(sum[t][1], hi, x);
+                } else {
+                    mma_piece<KIND>(sum[t], lo, hi, x);
+                }
+            }
         }
     }
 
@@ -145,12 +175,25 @@ __global__ void __launch_bounds__(32 * kFewWarps, 32 / kFewWarps) few_rows_kerne
     ptx::cp_async_wait_all();
     __syncthreads();
     uint32_t* const part = reinterpret_cast<uint32_t*>(few_smem);
-    constexpr int kX = 8 * NT;
+    constexpr int kX = DOTS > 0 ? DOTS : 8 * NT;
+    if constexpr (DOTS > 0) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < DOTS; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            part[(warp * kX + 8 * t + 2 * q + (i & 1)) * 16 + g + (i >> 1) * 8] = sum[t][i];
+            for (int i = 0; i < 2; ++i) {
+                int v = int(sum[t][i]);
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                if (q == 0)
+                    part[(warp * kX + t) * 16 + g + 8 * i] = uint32_t(v);
+            }
+    } else {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                part[(warp * kX + 8 * t + 2 * q + (i & 1)) * 16 + g + (i >> 1) * 8] = sum[t][i];
+    }
     __syncthreads();
     const int r = int(threadIdx.x) % ROWS, m = int(threadIdx.x) / ROWS, n = n0 + r;
     if (m >= min(p.M, kX) || n >= p.N)
@@ -187,11 +230,11 @@ __global__ void __launch_bounds__(32 * kFewWarps, 32 / kFewWarps) few_rows_kerne
     }
 }
 
-template <int KIND, int NT, int WARPS>
+template <int KIND, int NT, int DOTS, int WARPS>
 cudaError_t launch_one(const FewRowsParams& p, cudaStream_t stream, bool pdl)
 {
     constexpr int kRows = few_rows(KIND), kSmem = WARPS * kFewRing * kFewBlock;
-    auto kernel = few_rows_kernel<KIND, NT, WARPS>;
+    auto kernel = few_rows_kernel<KIND, NT, DOTS, WARPS>;
     static std::atomic<uint64_t> allowed{0};
     cudaError_t err = allow_smem(kernel, kSmem, allowed);
     if (err != cudaSuccess)
@@ -209,13 +252,13 @@ cudaError_t launch_one(const FewRowsParams& p, cudaStream_t stream, bool pdl)
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int KIND, int NT>
+template <int KIND, int NT, int DOTS = 0>
 cudaError_t launch_warps(int warps, const FewRowsParams& p, cudaStream_t stream, bool pdl)
 {
     switch (warps) {
-    case 8: return launch_one<KIND, NT, 8>(p, stream, pdl);
-    case 16: return launch_one<KIND, NT, 16>(p, stream, pdl);
-    case 32: return launch_one<KIND, NT, 32>(p, stream, pdl);
+    case 8: return launch_one<KIND, NT, DOTS, 8>(p, stream, pdl);
+    case 16: return launch_one<KIND, NT, DOTS, 16>(p, stream, pdl);
+    case 32: return launch_one<KIND, NT, DOTS, 32>(p, stream, pdl);
     default: return cudaErrorInvalidValue;
     }
 }
@@ -224,6 +267,11 @@ cudaError_t launch_warps(int warps, const FewRowsParams& p, cudaStream_t stream,
 
 cudaError_t launch_few_rows(int kind, int warps, const FewRowsParams& p, cudaStream_t stream, bool pdl)
 {
+    // (us, dot products against matrix instructions: 1 x 8192 x 8192 12.5 and 14.2, 2 rows 12.6 and
+    // 14.2, 4 rows 14.2 and 14.2; 1 x 512 x 28672 8.3 and 10.9)
+    if (kind == kFewInt8 && p.M <= 2)
+        return p.M == 1 ? launch_warps<kFewInt8, 1, 1>(warps, p, stream, pdl)
+                        : launch_warps<kFewInt8, 1, 2>(warps, p, stream, pdl);
     switch (2 * kind + (p.M > 8)) {
     case 2 * kFewInt8: return launch_warps<kFewInt8, 1>(warps, p, stream, pdl);
     case 2 * kFewInt8 + 1: return launch_warps<kFewInt8, 2>(warps, p, stream, pdl);
