@@ -6,11 +6,11 @@
 // is within 127 * 2^-24 < 2^-17 of it, so it is right but for values that close to the middle
 // of two integers:
 //
-// * bf16: x and a are integers X, A < 2^8 times powers of two, and where x / a lies in
-//   [2^-j-1, 2^-j + 1) the quotient's distance from a middle is a multiple of 2^-j / A: 0 or, as
-//   no middle lies below j = 8, more than 2^-16.  One fma that adds 384 rounds it to a multiple of 2^-15:
-//   to the middle itself from within 2^-17, never to it from beyond 2^-16; ties then go to
-//   the even integer by themselves.
+// * bf16: x = X 2^i and a = A 2^k with integers X, A < 2^8, so the quotient's distance from a
+//   middle is a multiple of 2^d / A, d = i - k: 0, or more than 2^-16, as quotients of 1/2 and
+//   more have d >= -8.  One fma that adds 384 rounds the quotient to a multiple of 2^-15: to the
+//   middle itself from within 2^-17, never to it from beyond 2^-16; ties then go to the even
+//   integer by themselves.
 // * fp16: 127 x and r a are exact in fp32 and so is the rest e = 127 x - r a (a multiple of
 //   x's last place, at most a / 2 or so: 20 bits); 2 |e| against a decides.
 // * fp32: 254 |x| against (2 L + 1) a, both as the sum of two fp32 values.
@@ -18,6 +18,9 @@
 // Bound by HBM: a row is read once, held in registers between the maximum and the
 // rounding (up to 8 pieces of 16 bytes a thread; what a longer row has beyond that is
 // read again, from L2), by a warp, 128, 256 or 512 threads according to its length.
+// 8192 x 8192 bf16 30.7 us (96 % of the copy rate; 39.8 with the test of every value's rest that
+// fp16 takes, before the fp32 pairs), fp16 33.2, fp32 52.7 (49.3 at the copy rate); 28672 x 1024
+// 13.7 (22.6 with eight pieces a lane for rows of 128).
 #include <type_traits>
 
 #include "feed_forward.h"
