@@ -533,7 +533,8 @@ def check_args(A_ptr, B_ptr, C_ptr, M, N, K, lda, ldb, ldc, dtype=BF16) -> int:
 
 class Plan:
     """A bwgemm plan on one CUDA device (see ``bwgemm_create_plan``), for one thread and one
-    stream at a time: its launches share a workspace and a status word."""
+    stream at a time: its launches, a captured graph's replays among them, share a workspace and
+    a status word."""
 
     def __init__(self, device: int | None = None, **opts):
         import torch

@@ -4,8 +4,9 @@
 // The weights' bytes are the time: each is read once.  16 weight rows are the rows of
 // mma.sync's m16n8k32 (integers: exact 32-bit sums) or m16n8k16 (bf16, fp16), rows of X its
 // 8 columns.  (The integer instruction is slow on this GPU: one row of X, 8192 x 8192, keeps
-// the tensor pipe busy 56 % of the time; one and two rows take dot products instead.)  In the gated form rows 0 to 7 are Wg's and 8 to 15 the same rows of Wu: a lane's
-// accumulator then holds G in its first half and U of the same outputs in its second.
+// the tensor pipe busy 56 % of the time; one and two rows take dot products instead.)  In the
+// gated form rows 0 to 7 are Wg's and 8 to 15 the same rows of Wu: a lane's accumulator then
+// holds G in its first half and U of the same outputs in its second.
 // The contraction does not care which K a position stands for as long as both operands
 // agree, so lane (g, q) takes whole 16-byte pieces: bytes 16 q and 64 + 16 q of rows g and
 // g + 8 of a 128-byte block, and of rows g (and g + 8) of X; four MMAs consume it.

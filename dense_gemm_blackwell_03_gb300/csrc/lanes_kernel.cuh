@@ -37,8 +37,10 @@
 // all before it is done: where it ran, their copies do not wait for it.
 //
 // Measured (us, and what bounds it): gated 64 x 28672 x 8192 147 to 150 (HBM, 93 % of the copy
-// rate); integers 64 x 28672 x 8192 47 (5 TB/s; 95 steps a CTA of 0.37 us, then the pieces of
-// 72 tiles are added), 8192 x 28672 x 8192, pairs, 2040 (1.89 PFLOP/s, the fp16 rate).
+// rate); integers 64 x 28672 x 8192 47 (5 TB/s: 95 blocks of 128 of K a CTA at HBM's 0.37 us each,
+// the rest is widening X, the first bytes' way and the last tile's epilogue; a second set of
+// converting warps that takes every other step 50, tiles of 256 weight rows on CTA pairs 53),
+// 8192 x 28672 x 8192, pairs, 2060 (1.87 PFLOP/s, the fp16 rate).
 //
 // Work: whole tiles, and the last, partial wave spread over all workers in K steps; the
 // warp that completes a tile's K adds the pieces in worker order (as in the block-scaled

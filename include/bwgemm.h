@@ -23,7 +23,9 @@
  *
  * Threading: a plan may be used from one host thread at a time and on one
  * stream at a time (its split-K workspace and status word are shared by its
- * launches).  Different plans are independent.
+ * launches).  A captured graph's replays are launches of the plan they were
+ * captured with: of two graphs of one plan, one runs after the other.
+ * Different plans are independent.
  *
  * Nothing is thrown across this boundary; every entry point returns a status.
  */
@@ -643,8 +645,8 @@ bwgemm_status_t bwgemm_gated_backward_workspace(int64_t M, int64_t N, uint64_t* 
  * of its fp32 value.  A row holding a NaN or an infinity gets the scale NaN and zeros.
  *
  * X and q 16-byte aligned; ldx a multiple of 16 bytes, ldq (bytes between rows) of 16;
- * scales one per row, 4-byte aligned.  Device memory as for bwgemm_run.  Asynchronous, one
- * launch (none for an empty X), no allocation, capturable.
+ * scales one per row, 4-byte aligned; neither they nor q may overlap X.  Device memory as for
+ * bwgemm_run.  Asynchronous, one launch (none for an empty X), no allocation, capturable.
  */
 bwgemm_status_t bwgemm_quantize_integer(bwgemm_plan_t plan, const void* X, bwgemm_dtype_t dtype, int64_t rows,
                                      int64_t cols, int64_t ldx, int8_t* q, int64_t ldq, float* scales, void* stream);
@@ -656,7 +658,7 @@ bwgemm_status_t bwgemm_quantize_integer(bwgemm_plan_t plan, const void* X, bwgem
  *
  *   A, B : 16-byte aligned, lda and ldb multiples of 16;  scales 4-byte aligned
  *   C : M x N bf16, fp16 or fp32 (`out`), row stride ldc elements, 16-byte aligned, ldc a
- *       multiple of 16 bytes
+ *       multiple of 16 bytes; must not overlap the operands, their scales or the workspace
  *   workspace : device memory, 256-byte aligned, of at least bwgemm_run_integer_workspace()
  *       bytes (else BWGEMM_ERR_WORKSPACE; NULL where that is 0, as for M <= 16), holding
  *       nothing of use before or after

@@ -542,6 +542,46 @@ def test_the_first_module_call_of_a_stream_inside_a_capture(plan):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_two_graphs_of_one_plan_in_turns(plan):
+    # one after the other on a stream, as launches of their plan: tiles in pieces use its workspace
+    work = [all_calls(plan, *s) for s in SIZES[1:]]
+    want = [run() for run in work]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for run in work:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            got.append(run())
+    for outputs in got:
+        for t in outputs:
+            t.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(10):
+            for g in graphs:
+                g.replay()
+    torch.cuda.synchronize()
+    for outputs, w in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(outputs, w))
+    assert plan.status() == 0
+
+
+@pytest.mark.parametrize("M", [5, 40, 200])
+def test_one_tensor_in_two_places(plan, M):
+    from dense_gemm_blackwell_03_gb300.linear_training import gated_linear
+    x, w, other = ref.layer(M, 136, 200, torch.bfloat16, M)
+    apart = [t.clone().requires_grad_() for t in (x, w, w)]
+    dh = torch.ones(1, 1, dtype=torch.bfloat16, device="cuda").expand(M, 136)  # a sum's gradient: one element
+    want = torch.autograd.grad(gated_linear(*apart), apart, dh)
+    x.requires_grad_()
+    w.requires_grad_()
+    dx, dw = torch.autograd.grad(gated_linear(x, w, w), (x, w), dh)
+    assert torch.equal(dx, want[0]) and torch.equal(dw, want[1] + want[2])
+    q, s = plan.quantize_int8(x.detach())
+    check(plan.gemm_int8(q, s, q, s), *ref.product_int8(q, s, q, s, torch.bfloat16))
+
+
 @pytest.mark.parametrize("op", ["gated", "int8", "backward", "rows"])
 def test_weights_written_just_before_on_the_stream(plan, op):
     # kernels that start early read nothing that the kernel before them still writes
