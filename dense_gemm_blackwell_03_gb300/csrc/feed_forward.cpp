@@ -101,21 +101,39 @@ struct LanesPlan {
     double us;
 };
 
-// Microseconds of 128 of K of a tile on its CTA or pair, weights at hand: the way of a step
-// through its barriers, the MMAs, and the widening.  Fitted to 4 to 333 rows on eight shapes.
+// What a launch takes in microseconds, fitted to 20 to 400 rows on eight shapes (1024 x 8192 to
+// 14336 x 4096): a call without its K steps; 128 of K of a tile on its CTA or pair, weights at
+// hand (the way through its barriers, the MMAs, and the widening); and, where tiles are cut into
+// pieces, a piece's way out and the others' in again by the warps that come last.
+double lanes_base_us(const LanesVariant& v)
+{
+    return v.mode == kLanesGated ? 6.0 : v.widens ? 5.0 : 9.0;  // (9: launch_widen before it)
+}
+
 double lanes_step_us(const LanesVariant& v)
 {
     if (v.mode == kLanesGated)
-        return v.bn == 128 ? 0.83 : v.bn == 64 ? 0.54 : v.bn == 32 ? 0.42 : 0.36;
-    return v.cg == 2 ? 0.57 : v.bn == 128 ? 0.46 : v.bn == 64 ? 0.37 : 0.25;
+        return v.bn == 128 ? 0.78 : v.bn == 64 ? 0.51 : v.bn == 32 ? 0.41 : 0.36;
+    return v.cg == 2 ? 0.58 : v.bn == 128 ? 0.375 : v.bn >= 32 ? 0.27 : 0.24;
 }
 
+double lanes_join_us(const LanesVariant& v, int pieces)
+{
+    const int groups = std::max(v.bn / (lanes_epi_warps(v.bn) / 4) / 32, 1);  // of columns that a warp adds one after the other
+    if (v.mode == kLanesGated)
+        return (v.bn == 128 ? 20.0 : v.bn == 64 ? 15.0 : v.bn == 32 ? 7.5 : 4.0) + groups * std::max(pieces - 4, 0);
+    return 2.5 + 0.55 * groups * pieces;
+}
+
+// Weights from which on tiles of 32 rows of X take it widened before: their bytes come faster
+// than a step of 32 rows is widened (see lanes_kernel.cuh).
+constexpr double kWidenedBefore = 100e6;
+
 // Whether a product of 8-bit integers takes X as it is at every division of its work: there
-// is no workspace for its fp16 then.  Up to 32 rows, but for large weights, whose bytes come
-// faster than a step of 32 rows is widened (see lanes_kernel.cuh).
+// is no workspace for its fp16 then.
 bool widens_always(int64_t M, int64_t N, int64_t K)
 {
-    return M <= 16 || (M <= 32 && double(N) * double(K) <= 64e6);
+    return M <= 16 || (M <= 32 && double(N) * double(K) <= kWidenedBefore);
 }
 
 LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N, int64_t K,
@@ -128,7 +146,7 @@ LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N,
         const LanesVariant& v = kLanesVariants[i];
         if (v.mode != mode)
             continue;
-        if (mode == kLanesInt8 && (widens_always(M, N, K) ? !v.widens : v.widens && double(N) * double(K) > 64e6))
+        if (mode == kLanesInt8 && (widens_always(M, N, K) ? !v.widens : v.widens && double(N) * double(K) > kWidenedBefore))
             continue;
         const int W = v.cg == 2 ? capped(max_pairs, 2, opts) : capped(num_sms, 1, opts);
         if (W < 1)
@@ -155,8 +173,9 @@ LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N,
             const uint64_t slot_bytes = uint64_t(lanes_partial_floats(mode, v.bn)) * 4 * v.cg;
             const bool room = kCounterRegionBytes + uint64_t(W) * 2 * slot_bytes <= workspace_bytes &&
                               uint64_t(rest) * v.cg * lanes_epi_warps(v.bn) * 4 <= kCounterRegionBytes;
-            // (spread: over all workers, or, where there is no full wave, over 8, 4 or 2 a tile)
-            for (int spread = 0; spread <= (rest > 0 && room && rest * kb < (1ll << 30) ? (full == 0 ? 4 : 1) : 0); ++spread) {
+            // (spread: over all workers, or, where there is no full wave, over as many a tile as
+            // there are for each, or half as many: a worker then has one piece, not two)
+            for (int spread = 0; spread <= (rest > 0 && room && rest * kb < (1ll << 30) ? (full == 0 ? 3 : 1) : 0); ++spread) {
                 s.workers = int(std::min<int64_t>(tiles, W));
                 s.dp_tiles = int(tiles);
                 s.sk_tiles = s.sk_iters = 0;
@@ -166,20 +185,23 @@ LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N,
                     s.sk_iters = int(rest * kb);
                     s.workers = full == 0 ? std::max(std::min(W, s.sk_iters / 4), 1) : W;
                     if (spread > 1)
-                        s.workers = int(std::min<int64_t>(s.workers, rest << (5 - spread)));
+                        s.workers = int(std::max<int64_t>(s.workers / rest / (spread - 1), 1) * rest);
+                    if (s.workers > W)
+                        continue;
                 }
-                const double us = lanes_step_us(v);
-                double t = double((s.dp_tiles + s.workers - 1) / s.workers) * double(kb) * us;
-                if (spread)
-                    t += double((s.sk_iters + s.workers - 1) / s.workers) * us;
+                const double us = lanes_step_us(v), whole = double((s.dp_tiles + s.workers - 1) / s.workers) * double(kb) * us;
+                const double steps = whole + (spread ? double((s.sk_iters + s.workers - 1) / s.workers) * us : 0.0);
                 // the weights once from HBM; bound by that, the form with the least work of its own
-                t = std::max(t, weights / 6.5e6) + 0.1 * t;
+                double t = lanes_base_us(v) + std::max(steps, weights / 6.5e6 + 0.1 * steps);
                 if (spread) {
-                    // a piece's partial tile out, the fence, the counter, and the pieces of a tile
-                    // in again by the warps that come last, a few at a time
-                    const int cols = v.bn / (lanes_epi_warps(v.bn) / 4), width = std::min(cols, 32);
-                    const int pieces = int((s.workers + rest - 1) / rest) + 1;
-                    t += 7.0 + 0.8 * (cols / width) * std::ceil(double(pieces) / lanes_flight(mode, width));
+                    // two pieces a worker: what the second's steps do not cover of the first's; whole
+                    // tiles, which come after them, cover them but for what delays their own
+                    const bool one = s.workers % rest == 0;
+                    const double join = lanes_join_us(v, int((s.workers + rest - 1) / rest) + (one ? 0 : 1));
+                    if (full > 0)
+                        t += std::max((mode == kLanesGated ? 1.0 : 0.5) * join, 2.0 * join - whole);
+                    else
+                        t += join + (one ? 0.0 : std::max(0.0, join - steps / 2));
                 }
                 if (best.workers == 0 || t < best.us) {
                     s.us = t;
@@ -188,7 +210,8 @@ LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N,
             }
         }
     }
-    best.raster = best.num_c <= 2 ? std::max(best.num_l, 1) : std::min(8, best.num_l);
+    // groups of eight tile rows, all columns of one before the next: weights are read again from L2
+    best.raster = std::max(std::min(8, best.num_l), 1);
     return best;
 }
 
@@ -297,27 +320,27 @@ GatedPlan plan_gated(int num_sms, int max_pairs, int64_t M, int64_t N, int64_t K
     if (pairs < 1 || g.num_r * g.num_c >= (1ll << 31))
         return g;
     g.workers = int(std::min<int64_t>(g.num_r * g.num_c, pairs));
-    // measured, lanes against pairs: 64 x 28672 x 8192 149 and 158 us, 128 x 28672 x 8192 165 and 159,
-    // 64 x 10240 x 8192 71 and 93, 100 x 10240 x 8192 113 and 93, 200 x 4096 x 4096 33 and 24,
-    // 333 x 1000 x 5005 27 and 29
+    // measured, lanes against pairs: 64 x 28672 x 8192 147 and 158 us, 128 x 28672 x 8192 165 and 159,
+    // 64 x 10240 x 8192 72 and 93, 100 x 10240 x 8192 98 and 94, 100 x 4096 x 4096 25.1 and 24.5, 200 x
+    // 4096 x 4096 32 and 24, 200 x 2048 x 8192 38 and 42, 333 x 1000 x 5005 27 and 29
     const double waves = double((g.num_r * g.num_c + pairs - 1) / pairs), t = waves * double(blocks_of(K)) * 0.6;
-    const double us = std::max(t, double(N) * double(K) * 4 / 6.5e6) + 0.1 * t;
+    const double us = 5.0 + std::max(t, double(N) * double(K) * 4 / 6.5e6) + 0.1 * t;
     g.lanes = g.l.workers > 0 && g.l.us < us;
     return g;
 }
 
 // Whether the kernel for few rows takes the product.  Measured in us, it against tiles: integers
-// 8 x 28672 x 8192 44 and 46, 16 x 28672 x 8192 59 and 46, 12 x 8192 x 8192 23.2 and 20.4, 16 x 4096 x
-// 4096 8.3 and 14.7; gated 1 x 10240 x 8192 51.7 and 56.5, 2 55.3 and 56.5, 4 62 and 57, 8 x 8192 x
-// 8192 45.0 and 42.9, 16 x 4096 x 4096 15.1 and 16.6.
+// 8 x 8192 x 8192 15.3 and 16.6, 8 x 28672 x 8192 44 and 40, 3 x 28672 x 8192 39.5 and 38.8, 16 x 4096 x
+// 4096 8.8 and 10.5, 16 x 5120 x 5120 14.7 and 11.5; gated 2 x 28672 x 8192 135.7 and 140.8, 2 x 8192 x
+// 8192 43.0 and 42.5, 16 x 4096 x 4096 15.2 and 16.6, 4 x 5120 x 5120 24.9 and 20.0.
 bool takes_few_rows(int mode, int64_t M, int64_t N, int64_t K)
 {
     if (M > kFewMost)
         return false;
     const double weights = double(N) * double(K);
     if (mode == kLanesInt8)
-        return K <= kFewIntegerK && (M <= 8 || weights <= 48e6);
-    return M <= 2 || weights <= 32e6;
+        return K <= kFewIntegerK && (M <= 2 || weights <= (M <= 8 ? 100e6 : 20e6));
+    return M <= 2 || weights <= 20e6;
 }
 
 // Its warps per CTA: eight, so that many CTAs share an SM; more where there are too few of

@@ -113,11 +113,6 @@ struct LanesMaps {
 cudaError_t launch_lanes(int idx, const LanesMaps& maps, const LanesParams& p, int grid, cudaStream_t stream, bool pdl);
 // Epilogue warps of a variant, each with an arrival counter per tile and CTA.
 constexpr int lanes_epi_warps(int bn) { return bn >= 128 ? 8 : 4; }
-// Pieces of a tile that a warp has on their way at once when it adds them, `width` columns each.
-#ifdef __CUDACC__
-__host__ __device__
-#endif
-constexpr int lanes_flight(int mode, int width) { return 64 / ((mode == kLanesGated ? 2 : 1) * width); }
 // fp32 sums of a CTA's partial tile.
 constexpr int lanes_partial_floats(int mode, int bn) { return mode == kLanesGated ? 2 * 128 * bn : 128 * bn; }
 

@@ -18,15 +18,16 @@
 // it (xor 0x80 makes u = x + 128, a byte permutation 0x6400 | u = 1024 + u, one
 // subtraction 1024 + u - 1152 = x, all exact) and store it to TMEM, from where the MMA
 // reads its A operand.  X goes through shared memory as fp16, widened once before
-// (launch_widen) or, of up to 32 rows a tile (WIDENS), by two warps from one part of shared
-// memory to another.  That saves a launch and the workspace, but takes them 870 (16 rows) and
-// 1250 (32 rows) cycles a step, the latter more than the weights of 256 of K take from HBM:
-// 32 x 28672 x 8192 51 us, 44 when widened before; 64 x 4096 x 4096 13.8 and 14.5 us, and 4 us less
-// of host time.
+// (launch_widen) or, of up to 32 rows a tile (WIDENS), by a warp for every eight rows from one
+// part of shared memory to another: no second launch (4 us of GPU and of host time each) and no
+// workspace, but more work a step.  32 x 28672 x 8192 44.2 us, 43.1 when widened before; 48 x
+// 8192 x 8192 23.8 and 23.9; 333 x 1000 x 5005 16.1 (18.2 with two warps).  At 16 rows four warps
+// instead of two lose 5 %.
 //
 //   warp 0      TMA producer of the weights' ring (gated: of X's rows too)
 //   warp 1      TMEM allocator and MMA issuer (in the even CTA of a pair)
-//   warp 2      kLanesInt8: TMA producer of X's ring, or with warp 3 what widens X into it
+//   warp 2      kLanesInt8: TMA producer of X's ring, or with warp 3 and the last two (of 32
+//               rows a tile) what widens X into it
 //   then        kLanesInt8: groups of four converting warps, a TMEM lane quarter each and a
 //               group per 128 of K of a step
 //   then        epilogue: four warps, eight from 128 columns on
@@ -37,9 +38,10 @@
 // all before it is done: where it ran, their copies do not wait for it.
 //
 // Measured (us, and what bounds it): gated 64 x 28672 x 8192 147 to 150 (HBM, 93 % of the copy
-// rate); integers 64 x 28672 x 8192 47 (5 TB/s: 95 blocks of 128 of K a CTA at HBM's 0.37 us each,
-// the rest is widening X, the first bytes' way and the last tile's epilogue; a second set of
-// converting warps that takes every other step 50, tiles of 256 weight rows on CTA pairs 53),
+// rate); integers 64 x 28672 x 8192 47 (5 TB/s: 36 us of weights at HBM's rate, 4 to widen X before,
+// the rest is the launch, the first bytes' way and the last tile's epilogue; without MMAs, widening and
+// TMEM stores it takes as long.  A second set of converting warps that takes every other step: 50,
+// tiles of 256 weight rows on CTA pairs 53, on one CTA 51),
 // 8192 x 28672 x 8192, pairs, 2060 (1.87 PFLOP/s, the fp16 rate).
 //
 // Work: whole tiles, and the last, partial wave spread over all workers in K steps; the
@@ -75,9 +77,9 @@ struct LanesConfig {
     static constexpr int kConvGroups = kGated ? 0 : kStep;
     // X's bytes of a step, copied with its weights, and the warps that widen them
     static constexpr bool kWidens = WIDENS;
-    static_assert(!WIDENS || (!kGated && BN <= 32), "widened by two warps");
+    static_assert(!WIDENS || (!kGated && BN <= 32), "integers, few rows of X");
     static constexpr int kRawStep = kWidens ? BN * kStep * kLanesK : 0;
-    static constexpr int kXWarps = kWidens ? 2 : 0;
+    static constexpr int kXWarps = kWidens ? BN / 8 : 0;
     static constexpr int kLStep = kStep * kLBytes;
     static constexpr int kFit = (kRingBytes - kXStages * kXStep) / (kLStep + kRawStep);
     static constexpr int kLStages = kGated ? kXStages : kFit > 10 / kStep ? 10 / kStep : kFit;
@@ -85,7 +87,8 @@ struct LanesConfig {
     static constexpr int kEpiWarps = lanes_epi_warps(BN);
     static constexpr int kFirstConv = 4;
     static constexpr int kFirstEpi = kFirstConv + kConvWarps;
-    static constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+    static constexpr int kLastX = kFirstEpi + kEpiWarps;  // what widens X beside warps 2 and 3
+    static constexpr int kThreads = 32 * (kLastX + (kXWarps > 2 ? kXWarps - 2 : 0));
     static constexpr int kCols = BN / (kEpiWarps / 4);        // columns per epilogue warp
     static constexpr int kPiece = kCols < 32 ? kCols : 32;    // of which it reads this many at a time
     static constexpr int kAccCols = kGated ? 2 * BN : BN;
@@ -279,14 +282,14 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
                 }
             }
         }
-    } else if (Cfg::kWidens && warp >= 2 && warp < 2 + Cfg::kXWarps) {
+    } else if (Cfg::kWidens && ((warp >= 2 && warp < Cfg::kFirstConv) || warp >= Cfg::kLastX)) {
         // --------------------------------- X's bytes to fp16, within shared memory
         // A row's step is 256 integers, 16 pieces; a warp takes two rows at a time.  Eight
         // lanes next to each other take four pieces of both, of different chunks: neither
         // their reads (rows of 128 bytes) nor their writes (pieces by row mod 8) share a bank.
-        constexpr int PIECES = BN / 4, APART = 4;  // of 16 integers, for each lane and step; rows between them
+        constexpr int PIECES = 4, APART = BN / 4;  // of 16 integers, for each lane and step; rows between them
         const int odd = (lane >> 2) & 1, block = lane >> 4, chunk = ((lane >> 3) & 1) ^ odd;
-        const int r0 = 2 * (warp - 2) + odd;  // this lane's rows: r0, r0 + APART, ...
+        const int r0 = 2 * (warp < Cfg::kFirstConv ? warp - 2 : warp - Cfg::kLastX + 2) + odd;  // this lane's rows: r0, r0 + APART, ...
         const uint32_t from0 = base + uint32_t(Cfg::kOffRaw + (block * BN + r0) * kLanesK + chunk * 64 + (lane & 3) * 16);
         // the piece's place: 16-byte pieces c0 and c0 + 1 of its rows in the block's chunk
         const uint32_t to0 = sX + uint32_t(block * Cfg::kXBytes + chunk * (Cfg::kXRows * 128) + r0 * 128);
@@ -447,10 +450,17 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
                 if (!ok)
                     break;
                 const uint32_t src = src0 + uint32_t(s * Cfg::kLStep);
-                uint32_t w[8][4];
+                // 16-byte pieces in registers: all eight of a row, or half of them where registers
+                // are short (32 rows a tile 22.4 us on 48 x 8192 x 8192, 23.0 with all; from 128 on
+                // all are 1 % faster)
+                constexpr int HELD = BN <= 64 ? 4 : 8;
+                uint32_t w[HELD][4];
+                auto take = [&](int from) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    ptx::ld_shared_v4(src + (uint32_t(c ^ (row & 7)) << 4), w[c][0], w[c][1], w[c][2], w[c][3]);
+                    for (int c = 0; c < HELD; ++c)
+                        ptx::ld_shared_v4(src + (uint32_t((from + c) ^ (row & 7)) << 4), w[c][0], w[c][1], w[c][2], w[c][3]);
+                };
+                take(0);
                 ok = warp_wait(bar_empty + 8 * a, aphase ^ 1u, p, abort_flag, kStatusMmaTimeout);
                 if (!ok)
                     break;
@@ -460,8 +470,10 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
                     uint32_t r[32];
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        widen4(w[4 * half + i / 4][i % 4], r[2 * i], r[2 * i + 1]);
-                    if (half == 0) {  // the stage is in registers
+                        widen4(w[(4 * half + i / 4) % HELD][i % 4], r[2 * i], r[2 * i + 1]);
+                    if (HELD == 4 && half == 0)
+                        take(4);
+                    if (half == (HELD == 4 ? 1 : 0)) {  // the stage is in registers
                         __syncwarp();
                         if (lane == 0)
                             ptx::mbar_arrive(bar_wempty + 8 * s);
@@ -488,7 +500,7 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
                 }
             }
         }
-    } else if (warp >= Cfg::kFirstEpi) {
+    } else if (warp >= Cfg::kFirstEpi && warp < Cfg::kLastX) {
         // ------------------------------------------------------------ epilogue
         ptx::grid_dependency_wait();
         constexpr int P = Cfg::kPiece;
@@ -633,8 +645,9 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
 #pragma unroll
                     for (int j = 0; j < P; ++j)
                         f[i][j] = 0.f;
-                // pieces on their way at once, added in order
-                constexpr int FLIGHT = lanes_flight(MODE, P);
+                // pieces on their way at once, added in order (two of 32 columns take registers that
+                // the integers' other warps lack: 48 x 8192 x 8192 23.9 us, 23.0 with one)
+                constexpr int FLIGHT = 32 / P;
 #pragma unroll 1
                 for (int w = w0; w <= w1; w += FLIGHT) {
                     uint4 x[FLIGHT][MATS][P / 4];
