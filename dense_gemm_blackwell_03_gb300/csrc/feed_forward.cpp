@@ -33,10 +33,10 @@ CUtensorMapDataType type16(int dtype)
 }
 
 // A 16-bit operand in boxes of two whole 64-element chunks x box_rows (map3), and of one
-// (map), which is read at the end of rows that are no multiple of 128.  A map that no copy
-// uses is a copy of the other.
+// (map), which is read at and past the end of rows that are no multiple of `step`, the columns
+// that its tiles advance by.  A map that no copy uses is a copy of the other.
 bwgemm_status_t encode_operand16(CUtensorMap* map, CUtensorMap* map3, const void* data, int64_t ld, int dtype, int64_t rows,
-                                 int64_t cols, uint32_t box_rows)
+                                 int64_t cols, uint32_t box_rows, int64_t step = 128)
 {
     const int64_t chunks = cols / 64;
     if (chunks >= 2) {
@@ -48,7 +48,7 @@ bwgemm_status_t encode_operand16(CUtensorMap* map, CUtensorMap* map3, const void
         if (st != BWGEMM_OK)
             return st;
         *map = *map3;
-        if (cols % 128 == 0)
+        if (cols % step == 0)
             return BWGEMM_OK;
     }
     const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
@@ -613,17 +613,18 @@ bwgemm_status_t bwgemm_gated_backward(bwgemm_plan_t plan, const bwgemm_matrix_t*
     p.timeout_ns = limit_ns(plan);
     p.status = plan->d_status;
     p.stall_kblock = plan->opts.stall_kblock;
-    // dG and dU: rows of tokens, K-major for dX, stored K x rows for the weights
+    // dG and dU: rows of tokens, K-major for dX, stored K x rows for the weights.  A pair's second
+    // CTA reads past rows that end in the first one's half of a tile.
     PairMaps maps;
     for (int i = 0; i < 2; ++i)
-        if ((st = encode_operand16(&maps.a[i], &maps.a3[i], d[i], ldd, dtype, M, N, 128)) != BWGEMM_OK)
+        if ((st = encode_operand16(&maps.a[i], &maps.a3[i], d[i], ldd, dtype, M, N, 128, pair_tile(sel.cg))) != BWGEMM_OK)
             return st;
     const bwgemm_matrix_t* const b[3] = {of_x ? Wg : nullptr, of_x ? Wu : nullptr, of_w ? X : nullptr};
     const bwgemm_matrix_t* const out[3] = {of_x ? dX : nullptr, of_w ? dWg : nullptr, of_w ? dWu : nullptr};
     for (int i = 0; i < 3; ++i) {
         maps.b[i] = maps.b3[i] = maps.out[i] = maps.a[0];  // where there is none, none is read
-        if (b[i] && (st = encode_operand16(&maps.b[i], &maps.b3[i], b[i]->data, b[i]->ld, dtype, i < 2 ? N : M, K, 128)) !=
-                        BWGEMM_OK)
+        if (b[i] && (st = encode_operand16(&maps.b[i], &maps.b3[i], b[i]->data, b[i]->ld, dtype, i < 2 ? N : M, K, 128,
+                                           pair_tile(sel.cg))) != BWGEMM_OK)
             return st;
         if (!out[i])
             continue;

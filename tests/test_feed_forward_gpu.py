@@ -224,6 +224,14 @@ def test_backward_slices_and_many_tiles(plan, M, N, K):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("M,N,K", [(1856, 2752, 384), (1500, 2944, 1152), (1500, 2944, 512), (700, 2944, 4096)])
+def test_backward_pairs_whose_rows_end_in_half_a_tile(plan, M, N, K):
+    # N, K or both 128 past a multiple of 256: the pair's second CTA reads past whole rows
+    if torch.cuda.get_device_properties(0).multi_processor_count == 152:
+        assert {p["tile"] for p in binding.select_gated_backward(152, M, N, K, 76)} == {256}
+    check_backward(plan, M, N, K, seed=K)
+
+
 def test_backward_of_one_side_alone(plan):
     (dh, g, u, x, wg, wu), (dx, dwg, dwu) = check_backward(plan, 130, 200, 264)
     only_x = plan.gated_linear_backward(dh, g, u, None, wg, wu, weight_grads=False)
