@@ -195,11 +195,13 @@ LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N,
                 double t = lanes_base_us(v) + std::max(steps, weights / 6.5e6 + 0.1 * steps);
                 if (spread) {
                     // two pieces a worker: what the second's steps do not cover of the first's; whole
-                    // tiles, which come after them, cover them but for what delays their own
+                    // tiles, which come after them, cover them but for what delays their own, and no
+                    // more of them than TMEM has buffers for
                     const bool one = s.workers % rest == 0;
                     const double join = lanes_join_us(v, int((s.workers + rest - 1) / rest) + (one ? 0 : 1));
                     if (full > 0)
-                        t += std::max((mode == kLanesGated ? 1.0 : 0.5) * join, 2.0 * join - whole);
+                        t += std::max((mode == kLanesGated ? 1.0 : 0.5) * join,
+                                      2.0 * join - std::min(whole, (v.bn == 256 ? 1 : 2) * double(kb) * us));
                     else
                         t += join + (one ? 0.0 : std::max(0.0, join - steps / 2));
                 }

@@ -42,7 +42,8 @@
 // the rest is the launch, the first bytes' way and the last tile's epilogue; without MMAs, widening and
 // TMEM stores it takes as long.  A second set of converting warps that takes every other step: 50,
 // tiles of 256 weight rows on CTA pairs 53, on one CTA 51),
-// 8192 x 28672 x 8192, pairs, 2060 (1.87 PFLOP/s, the fp16 rate).
+// 8192 x 28672 x 8192, pairs, 2030 to 2070 (1.9 PFLOP/s, the fp16 rate under the power cap; 4096 x 8192
+// x 8192 288, 304 with sums handed back after their stores).
 //
 // Work: whole tiles, and the last, partial wave spread over all workers in K steps; the
 // warp that completes a tile's K adds the pieces in worker order (as in the block-scaled
@@ -70,7 +71,9 @@ struct LanesConfig {
     // TMEM slot, with X's part in shared memory.  A warp's way through a barrier, its copies or
     // MMAs and the arrivals is some 300 to 600 cycles, hence two blocks where tiles are narrow
     // (64 x 28672 x 8192: 49 us with two blocks a step, 55 with one).
-    static constexpr int kRingBytes = 222 * 1024;
+    // kLanesInt8: 16-bit results of 32 weight rows x 32 rows of X, turned on their way out, per epilogue warp
+    static constexpr int kTurnBytes = kGated ? 0 : 2048;
+    static constexpr int kRingBytes = 222 * 1024 - lanes_epi_warps(BN) * kTurnBytes;
     static constexpr int kStep = !kGated && BN <= 64 ? 2 : 1;
     static constexpr int kXStep = kStep * kXBytes;
     static constexpr int kXStages = kGated ? kRingBytes / (kLBytes + kXBytes) : 3;
@@ -102,8 +105,10 @@ struct LanesConfig {
     static constexpr int kOffL = 0;
     static constexpr int kOffX = kLStages * kLStep;
     static constexpr int kOffRaw = kOffX + kXStages * kXStep;
-    static constexpr int kOffScale = kOffRaw + kLStages * kRawStep;  // a warp's 32 scales of X
-    static constexpr int kOffBar = kOffScale + kEpiWarps * 128;
+    static constexpr int kOffTurn = kOffRaw + kLStages * kRawStep;
+    static constexpr int kScaleBytes = kGated ? 0 : 4 * kCols;
+    static constexpr int kOffScale = kOffTurn + kEpiWarps * kTurnBytes;  // X's scales of a warp's columns
+    static constexpr int kOffBar = kOffScale + kEpiWarps * kScaleBytes;
     // full, empty, wfull, wempty, acc_full, acc_empty, drain
     static constexpr int kNumBars = 2 * (kXStages + kLStages + kBufs) + 1;
     static constexpr int kOffTmemSlot = kOffBar + 8 * kNumBars;
@@ -511,7 +516,8 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
         // M = 64: row 16 q + i of the weights in lane i of quarter q, lanes 16 to 31 unused
         const int row = GATED ? 16 * q + lane : 32 * q + lane;
         const bool in_tile = row < l_rows && (!GATED || lane < 16);
-        const uint32_t scale_buf = base + uint32_t(Cfg::kOffScale + e * 128);
+        const uint32_t scale_buf = base + uint32_t(Cfg::kOffScale + e * Cfg::kScaleBytes);
+        const uint32_t turn = base + uint32_t(Cfg::kOffTurn + e * Cfg::kTurnBytes);
         int b = 0;
         uint32_t bphase = 0;
         bool ok = true;
@@ -520,6 +526,41 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
             const int m0 = seg.c_blk * BN + col;                        // its row of column 0
             const bool live = in_tile && n < p.lrows;
             const float ls = !GATED && live ? p.ls[n] : 0.f;
+            if constexpr (!GATED) {
+                for (int c = lane; c < Cfg::kCols; c += 32)
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(scale_buf + 4 * c), "f"(m0 + c < p.crows ? p.cs[m0 + c] : 0.f)
+                                 : "memory");
+                __syncwarp();
+            }
+            // P rows of X from column c on, 32 columns of the result each, in this warp's `turn`: out in
+            // 16-byte pieces (4096 x 4096 x 1024 39 us, 45 with a store of 64 bytes for each row and warp)
+            auto turn_out = [&](int c) {
+                __syncwarp();
+                const int m = m0 + c, count = p.crows - m;
+                const int piece = 8 * (lane & 3), n8 = n - lane + piece;  // of 8 columns
+                const int left = row - lane + piece < l_rows ? p.lrows - n8 : 0;
+                uint16_t* dst = static_cast<uint16_t*>(p.out[0]) + int64_t(m) * p.ldo[0] + n8;
+#pragma unroll
+                for (int j = lane >> 2; j < P; j += 8) {
+                    uint4 w;
+                    ptx::ld_shared_v4(turn + uint32_t(j * 64 + 2 * piece), w.x, w.y, w.z, w.w);
+                    if (j >= count)
+                        continue;
+                    uint16_t* at = dst + j * p.ldo[0];
+                    if (left >= 8) {
+                        *reinterpret_cast<uint4*>(at) = w;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 7; ++k)
+                            if (k < left)
+                                at[k] = uint16_t((&w.x)[k / 2] >> (16 * (k % 2)));
+                    }
+                }
+                __syncwarp();
+            };
+            auto turn_in = [&](int j, uint16_t h) {
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + uint32_t(j * 64 + 2 * lane)), "h"(h) : "memory");
+            };
             // P columns of finished sums (gated: of G, then of U) from column c of the warp's on
             auto finish = [&](int c, const float(&v)[MATS][P]) {
                 const int m = m0 + c, count = p.crows - m;
@@ -541,34 +582,29 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
                 } else {
                     if (count <= 0)
                         return;
-                    __syncwarp();
-                    const float cs = lane < count && lane < P ? p.cs[m + lane] : 0.f;
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(scale_buf + 4 * lane), "f"(cs) : "memory");
-                    __syncwarp();
-                    if (!live)
-                        return;
                     // (the sum times its token's scale) times its channel's: neither product
                     // leaves fp32's range where the result does not
                     if (p.out_type == BWGEMM_FP32) {
+                        if (!live)
+                            return;
                         float* dst = static_cast<float*>(p.out[0]) + int64_t(m) * p.ldo[0] + n;
 #pragma unroll
                         for (int j = 0; j < P; j += 4) {
-                            const float4 f = ptx::ld_shared_f32x4(scale_buf + 4 * j);
+                            const float4 f = ptx::ld_shared_f32x4(scale_buf + 4 * (c + j));
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 if (j + k < count)
                                     dst[(j + k) * p.ldo[0]] = v[0][j + k] * (&f.x)[k] * ls;
                         }
                     } else {
-                        uint16_t* dst = static_cast<uint16_t*>(p.out[0]) + int64_t(m) * p.ldo[0] + n;
 #pragma unroll
                         for (int j = 0; j < P; j += 4) {
-                            const float4 f = ptx::ld_shared_f32x4(scale_buf + 4 * j);
+                            const float4 f = ptx::ld_shared_f32x4(scale_buf + 4 * (c + j));
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                if (j + k < count)
-                                    dst[(j + k) * p.ldo[0]] = round16(v[0][j + k] * (&f.x)[k] * ls, p.out_type);
+                                turn_in(j + k, round16(v[0][j + k] * (&f.x)[k] * ls, p.out_type));
                         }
+                        turn_out(c);
                     }
                 }
             };
@@ -585,6 +621,39 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
             constexpr size_t kStride = Cfg::kPartialFloats;
             constexpr size_t kWarpFloats = size_t(MATS) * 32 * Cfg::kCols;
             const size_t mine = size_t(e) * kWarpFloats + 4 * lane;
+            if constexpr (Cfg::kBufs == 1) {
+                if (seg.whole && p.out_type != BWGEMM_FP32) {
+                    // one buffer of sums: rounded and packed in registers, and handed back before they
+                    // go out (32 us)
+                    uint32_t w[Cfg::kCols / 2];
+#pragma unroll
+                    for (int c = 0; c < Cfg::kCols; c += P) {
+                        uint32_t v[P];
+                        ptx::tmem_ld_32x32b_x32(taddr + uint32_t(c), v);
+                        ptx::tmem_ld_wait();
+                        if (c + P >= Cfg::kCols)
+                            hand_back<CG>(empty, lane);
+#pragma unroll
+                        for (int j = 0; j < P; j += 4) {
+                            const float4 f = ptx::ld_shared_f32x4(scale_buf + 4 * (c + j));
+#pragma unroll
+                            for (int k = 0; k < 4; k += 2)
+                                w[(c + j + k) / 2] = pack2(__float_as_uint(__uint_as_float(v[j + k]) * (&f.x)[k] * ls),
+                                                           __float_as_uint(__uint_as_float(v[j + k + 1]) * (&f.x)[k + 1] * ls), p.out_type);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < Cfg::kCols; c += P) {
+                        if (m0 + c >= p.crows)
+                            break;
+#pragma unroll
+                        for (int j = 0; j < P; ++j)
+                            turn_in(j, uint16_t(w[(c + j) / 2] >> (16 * (j % 2))));
+                        turn_out(c);
+                    }
+                    continue;
+                }
+            }
             float* const part = p.partials + ((size_t(worker) * 2 + seg.slot) * CG + rank) * kStride + mine;
 #pragma unroll 1
             for (int c = 0; c < Cfg::kCols; c += P) {
