@@ -221,28 +221,35 @@ LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N,
 // The gradients' products.  No workers where there is no division.
 struct PairPlan {
     PairProduct prod[2];
+    int early;
     int cg;
     int workers;  // CTAs or pairs
 };
 
-// The longest worker's cycles when `workers` take the units of both products in turn.
-int64_t pair_cycles(const PairProduct (&d)[2], int64_t workers, int64_t step)
+// The longest worker's cycles when `workers` share the units of both products as pair_unit has
+// it, and the count of early ones that makes them fewest.
+int64_t pair_cycles(const PairProduct (&d)[2], int64_t workers, int64_t step, int* early)
 {
-    int64_t most = 0;
-    const int64_t first = d[0].units % workers;
-    // the workers that the last of dX's, and of the weights', units end at, and the ones after
-    for (int64_t w : {int64_t(0), first, (first + d[1].units) % workers, workers - 1}) {
-        int64_t cycles = 0;
-        for (int i = 0; i < 2; ++i) {
-            if (d[i].units == 0)
-                continue;
-            const int64_t before = i == 0 ? 0 : d[0].units;  // units t = before.. with t % workers == w
-            auto upto = [&](int64_t t) { return t / workers + (t % workers > w ? 1 : 0); };
-            cycles += (upto(before + d[i].units) - upto(before)) * ((d[i].steps + d[i].splits - 1) / d[i].splits * step + 500);
+    int64_t unit[2], best = -1;
+    for (int i = 0; i < 2; ++i)
+        unit[i] = (d[i].steps + d[i].splits - 1) / d[i].splits * step + 500;
+    const int64_t turns = d[0].units / workers, rest = d[0].units % workers, others = workers - rest;
+    const int64_t even = rest > 0 ? unit[0] / unit[1] : 0, most = (d[1].units + others - 1) / others;
+    for (int64_t e : {int64_t(0), even, even + 1}) {
+        if (e > 0 && (rest == 0 || d[1].units == 0))
+            continue;
+        e = std::min(e, most);
+        const int64_t left = std::max<int64_t>(d[1].units - e * others, 0);
+        // of those with one more of the first product's, and of the others
+        const int64_t with = (turns + 1) * unit[0] + (left + workers - 1) / workers * unit[1];
+        const int64_t without = turns * unit[0] + (e + (left + workers - 1 - rest) / workers) * unit[1];
+        const int64_t cycles = rest > 0 ? std::max(with, without) : without;
+        if (best < 0 || cycles < best) {
+            best = cycles;
+            *early = int(e);
         }
-        most = std::max(most, cycles);
     }
-    return most;
+    return best;
 }
 
 // Tiles of 256 on CTA pairs (1024 SM cycles per 128 of K, bound by the MMAs) or of 128 on
@@ -280,13 +287,13 @@ PairPlan plan_backward(int64_t M, int64_t N, int64_t K, bool of_x, bool of_w, in
                 // partial sums lie by unit, of both products where either has slices
                 if ((sx > 1 || sw > 1) && int64_t(sw > 1 ? x.units + w.units : x.units) > room)
                     continue;
-                int64_t cycles = pair_cycles(s.prod, workers, g == 2 ? 1024 : 740);
+                s.workers = int(std::min<int64_t>(x.units + w.units, workers));
+                int64_t cycles = pair_cycles(s.prod, s.workers, g == 2 ? 1024 : 740, &s.early);
                 for (int i = 0; i < 2; ++i)
                     if (s.prod[i].splits > 1)
                         cycles += 3000 + s.prod[i].units * tile * tile * 4 / 1250;
                 if (best.workers == 0 || cycles < best_cycles) {
                     best_cycles = cycles;
-                    s.workers = int(std::min<int64_t>(x.units + w.units, workers));
                     best = s;
                 }
                 if (tiles[1] == 0)
@@ -607,6 +614,7 @@ bwgemm_status_t bwgemm_gated_backward(bwgemm_plan_t plan, const bwgemm_matrix_t*
     PairParams p = {};
     p.prod[0] = sel.prod[0];
     p.prod[1] = sel.prod[1];
+    p.early = sel.early;
     p.steps_k = int32_t(blocks_of(N));
     p.chunks_a = int32_t(N / 64);
     p.chunks_b = int32_t(K / 64);

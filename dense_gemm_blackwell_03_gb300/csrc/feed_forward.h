@@ -37,6 +37,7 @@ struct PairProduct {
 
 struct PairParams {
     PairProduct prod[2];
+    int32_t early;               // units of the second product for who has fewer of the first's
     int32_t steps_k;             // of one term of dX: ceil(N / 128)
     int32_t chunks_a, chunks_b;  // whole 64-element chunks of the operands' rows (0: no a3 / b3)
     float* partials;             // the slices' fp32 sums, by unit

@@ -56,7 +56,7 @@ cudaError_t launch_form(const PairMaps& maps, const PairParams& p, int grid, cud
 // dU = dH act(G), dG = dH U act'(G): three reads and two writes of rows x cols, eight
 // values a thread, rounded to 16 bits as the operands that the products need.  Bound by HBM
 // (2048 x 4096 20 us cold, of which 12 are its bytes).
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 256, kGradPieces = 2;  // a thread has two pieces on their way
 
 __device__ __forceinline__ float2 unpack16(uint32_t w, int dtype)
 {
@@ -71,35 +71,50 @@ __global__ void __launch_bounds__(kGradThreads) gate_grad_kernel(const GateGradP
     const int64_t per_row = (p.cols + 7) / 8, pieces = per_row * p.rows;
     const int64_t step = int64_t(gridDim.x) * kGradThreads;
 #pragma unroll 1
-    for (int64_t i = int64_t(blockIdx.x) * kGradThreads + threadIdx.x; i < pieces; i += step) {
-        const int64_t row = i / per_row, col = (i - row * per_row) * 8;
-        uint4 dh, g, u, dg, du;
-        if (col + 8 <= p.cols) {
-            dh = ptx::ld_global_cg_v4(p.dh + row * p.lddh + col);
-            g = ptx::ld_global_cg_v4(p.g + row * p.ldg + col);
-            u = ptx::ld_global_cg_v4(p.u + row * p.ldu + col);
-        } else {  // nothing is read past a row's end
-            dh = g = u = make_uint4(0u, 0u, 0u, 0u);
+    for (int64_t i = int64_t(blockIdx.x) * kGradThreads + threadIdx.x; i < pieces; i += kGradPieces * step) {
+        int64_t row[kGradPieces], col[kGradPieces];
+        uint4 dh[kGradPieces], g[kGradPieces], u[kGradPieces];
 #pragma unroll
-            for (int k = 0; k < 7; ++k)
-                if (col + k < p.cols) {
-                    reinterpret_cast<uint16_t*>(&dh)[k] = p.dh[row * p.lddh + col + k];
-                    reinterpret_cast<uint16_t*>(&g)[k] = p.g[row * p.ldg + col + k];
-                    reinterpret_cast<uint16_t*>(&u)[k] = p.u[row * p.ldu + col + k];
-                }
+        for (int n = 0; n < kGradPieces; ++n) {
+            const int64_t at = i + n * step;
+            row[n] = at / per_row;
+            col[n] = (at - row[n] * per_row) * 8;
+            if (at >= pieces)
+                continue;
+            if (col[n] + 8 <= p.cols) {
+                dh[n] = ptx::ld_global_cg_v4(p.dh + row[n] * p.lddh + col[n]);
+                g[n] = ptx::ld_global_cg_v4(p.g + row[n] * p.ldg + col[n]);
+                u[n] = ptx::ld_global_cg_v4(p.u + row[n] * p.ldu + col[n]);
+            } else {  // nothing is read past a row's end
+                dh[n] = g[n] = u[n] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int k = 0; k < 7; ++k)
+                    if (col[n] + k < p.cols) {
+                        reinterpret_cast<uint16_t*>(&dh[n])[k] = p.dh[row[n] * p.lddh + col[n] + k];
+                        reinterpret_cast<uint16_t*>(&g[n])[k] = p.g[row[n] * p.ldg + col[n] + k];
+                        reinterpret_cast<uint16_t*>(&u[n])[k] = p.u[row[n] * p.ldu + col[n] + k];
+                    }
+            }
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 fh = unpack16((&dh.x)[k], p.dtype), fg = unpack16((&g.x)[k], p.dtype), fu = unpack16((&u.x)[k], p.dtype);
-            float2 value, slope;
-            activate_slope(fg.x, p.activation, value.x, slope.x);
-            activate_slope(fg.y, p.activation, value.y, slope.y);
-            (&dg.x)[k] = pack2(__float_as_uint(fh.x * fu.x * slope.x), __float_as_uint(fh.y * fu.y * slope.y), p.dtype);
-            (&du.x)[k] = pack2(__float_as_uint(fh.x * value.x), __float_as_uint(fh.y * value.y), p.dtype);
+        for (int n = 0; n < kGradPieces; ++n) {
+            if (i + n * step >= pieces)
+                break;
+            uint4 dg, du;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 fh = unpack16((&dh[n].x)[k], p.dtype), fg = unpack16((&g[n].x)[k], p.dtype),
+                             fu = unpack16((&u[n].x)[k], p.dtype);
+                float2 value, slope;
+                activate_slope(fg.x, p.activation, value.x, slope.x);
+                activate_slope(fg.y, p.activation, value.y, slope.y);
+                (&dg.x)[k] = pack2(__float_as_uint(fh.x * fu.x * slope.x), __float_as_uint(fh.y * fu.y * slope.y), p.dtype);
+                (&du.x)[k] = pack2(__float_as_uint(fh.x * value.x), __float_as_uint(fh.y * value.y), p.dtype);
+            }
+            // the workspace's rows are whole pieces: what lies past the end is not read as a value
+            *reinterpret_cast<uint4*>(p.dg + row[n] * p.ldd + col[n]) = dg;
+            *reinterpret_cast<uint4*>(p.du + row[n] * p.ldd + col[n]) = du;
         }
-        // the workspace's rows are whole pieces: what lies past the end is not read as a value
-        *reinterpret_cast<uint4*>(p.dg + row * p.ldd + col) = dg;
-        *reinterpret_cast<uint4*>(p.du + row * p.ldd + col) = du;
     }
 }
 
@@ -119,7 +134,7 @@ cudaError_t launch_gate_grad(const GateGradParams& p, cudaStream_t stream, bool 
 {
     const int64_t pieces = (p.cols + 7) / 8 * p.rows;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(std::min<int64_t>((pieces + kGradThreads - 1) / kGradThreads, 1 << 20)), 1, 1);
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>((pieces + kGradPieces * kGradThreads - 1) / (kGradPieces * kGradThreads), 1 << 20)), 1, 1);
     cfg.blockDim = dim3(kGradThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -47,8 +47,12 @@ __device__ __forceinline__ PairTile pair_tile_at(const PairParams& p, int t)
     const PairProduct& d = p.prod[x.which];
     t -= x.which ? p.prod[0].units : 0;
     const int i = t / d.splits, slice = t - i * d.splits;
-    x.k0 = int(int64_t(slice) * d.steps / d.splits);
-    x.k1 = int(int64_t(slice + 1) * d.steps / d.splits);
+    x.k0 = 0;
+    x.k1 = d.steps;
+    if (d.splits > 1) {
+        x.k0 = int(int64_t(slice) * d.steps / d.splits);
+        x.k1 = int(int64_t(slice + 1) * d.steps / d.splits);
+    }
     // groups of 8 tile rows (of all results), walked down before stepping along the columns
     const int rows = d.num_r * d.results;
     const int per_group = 8 * d.num_c;
@@ -61,6 +65,43 @@ __device__ __forceinline__ PairTile pair_tile_at(const PairParams& p, int t)
     x.r = r - x.result * d.num_r;
     return x;
 }
+
+// The i-th unit of a worker, of `total`.  dX's units (the first product's) are dealt in turn; then those
+// who got none in the last turn take `early` of the weights' tiles each, as one of dX's units
+// is many times their length, and all take the rest in turn.
+__device__ __forceinline__ int pair_unit(const PairParams& p, int worker, int workers, int i)
+{
+    const int first = p.prod[0].units, rest = first % workers;
+    const int mine = first / workers + (worker < rest ? 1 : 0);
+    if (i < mine)
+        return worker + i * workers;
+    i -= mine;
+    if (worker >= rest) {
+        if (i < p.early)
+            return first + worker - rest + i * (workers - rest);
+        i -= p.early;
+    }
+    return first + p.early * (workers - rest) + worker + i * workers;
+}
+
+// A worker's units one after the other.  The divisions that find a tile take as long as a step's
+// MMAs: next() after a tile's first step, so that they overlap the rest.
+struct PairWalk {
+    PairTile x;
+    int i = 0, t;
+    __device__ __forceinline__ PairWalk(const PairParams& p, int worker, int workers, int total)
+    {
+        t = pair_unit(p, worker, workers, 0);
+        if (t < total)
+            x = pair_tile_at(p, t);
+    }
+    __device__ __forceinline__ void next(const PairParams& p, int worker, int workers, int total)
+    {
+        t = pair_unit(p, worker, workers, ++i);
+        if (t < total)
+            x = pair_tile_at(p, t);
+    }
+};
 
 // A box of 128 rows x 128 elements of an operand: whole chunks in one copy, else chunk by
 // chunk (zeros past the row's end, and past the last row).
@@ -154,8 +195,8 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
         uint32_t phase = 0;
         bool ok = true;
 #pragma unroll 1
-        for (int t = worker; ok && t < total; t += workers) {
-            const PairTile x = pair_tile_at(p, t);
+        for (PairWalk walk(p, worker, workers, total); ok && walk.t < total;) {
+            const PairTile x = walk.x;
             const int a0 = x.r * TILE + int(rank) * 128;
             const int b0 = FORM == kPairGated ? x.c * COLS : x.c * TILE + int(rank) * 128;
 #pragma unroll 1
@@ -184,6 +225,8 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                     pair_load<CG>(dB, &maps.b[zb], &maps.b3[zb], p.chunks_b, fb, B_MN ? k : b0, B_MN ? b0 : k);
                 }
                 __syncwarp();
+                if (i == x.k0)
+                    walk.next(p, worker, workers, total);
                 if (++s == STAGES) {
                     s = 0;
                     phase ^= 1u;
@@ -200,8 +243,8 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
         uint32_t phase = 0, bphase = 0;
         bool ok = true;
 #pragma unroll 1
-        for (int t = worker; ok && t < total; t += workers) {
-            const PairTile x = pair_tile_at(p, t);
+        for (PairWalk walk(p, worker, workers, total); ok && walk.t < total;) {
+            const PairTile x = walk.x;
             ok = warp_wait(bar_acc_empty + 8 * b, bphase ^ 1u, p, abort_flag, kStatusMmaTimeout);
 #pragma unroll 1
             for (int i = x.k0; ok && i < x.k1; ++i) {
@@ -237,6 +280,8 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
                     }
                 }
                 __syncwarp();
+                if (i == x.k0)
+                    walk.next(p, worker, workers, total);
                 if (++s == STAGES) {
                     s = 0;
                     phase ^= 1u;
@@ -260,21 +305,31 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
         auto put = [&](const uint32_t (&w)[32], const PairProduct& d, int z, int row0, int col) {
             if (row0 >= d.rows || col >= d.cols)
                 return;
-            if ((d.cols & 7) != 0 && col + 64 > d.cols) {
-                // a TMA store clips a row's end only in whole 16-byte pieces
-                if (row0 + lane < d.rows) {
-                    uint16_t* dst = p.out[z] + int64_t(row0 + lane) * p.ldo[z] + col;
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (col + i < d.cols)
-                            dst[i] = uint16_t((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xFFFFu));
-                }
-                return;
-            }
             if (lane == 0)
                 ptx::bulk_wait_group_read<0>();  // the store before has read the staging block
             __syncwarp();
             ortho_stage(w, sb, lane);
+            if ((d.cols & 7) != 0 && col + 64 > d.cols) {
+                // a TMA store clips a row's end only in whole 16-byte pieces: eight lanes a row
+                __syncwarp();
+                const int c = col + 8 * (lane & 7), left = d.cols - c;
+#pragma unroll 1
+                for (int r = lane >> 3; r < 32 && row0 + r < d.rows; r += 4) {
+                    uint4 v;
+                    ptx::ld_shared_v4(sb + uint32_t(r * 128 + (((lane ^ r) & 7) << 4)), v.x, v.y, v.z, v.w);
+                    uint16_t* dst = p.out[z] + int64_t(row0 + r) * p.ldo[z] + c;
+                    if (left >= 8) {
+                        *reinterpret_cast<uint4*>(dst) = v;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 7; ++i)
+                            if (i < left)
+                                dst[i] = uint16_t((&v.x)[i / 2] >> (16 * (i % 2)));
+                    }
+                }
+                __syncwarp();
+                return;
+            }
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -283,7 +338,7 @@ __global__ void __launch_bounds__(OrthoConfig<CG>::kThreads, 1)
             }
         };
 #pragma unroll 1
-        for (int t = worker; ok && t < total; t += workers) {
+        for (int i = 0, t; ok && (t = pair_unit(p, worker, workers, i)) < total; ++i) {
             const PairTile x = pair_tile_at(p, t);
             const PairProduct& d = p.prod[x.which];
             const int row0 = x.r * TILE + int(rank) * 128 + 32 * q;
