@@ -38,11 +38,11 @@
 // all before it is done: where it ran, their copies do not wait for it.
 //
 // Measured (us, and what bounds it): gated 64 x 28672 x 8192 147 to 150 (HBM, 93 % of the copy
-// rate); integers 64 x 28672 x 8192 47 (5 TB/s: 36 us of weights at HBM's rate, 4 to widen X before,
+// rate); integers 64 x 28672 x 8192 46 (5.2 TB/s: 36 us of weights at HBM's rate, 4 to widen X before,
 // the rest is the launch, the first bytes' way and the last tile's epilogue; without MMAs, widening and
 // TMEM stores it takes as long.  A second set of converting warps that takes every other step: 50,
 // tiles of 256 weight rows on CTA pairs 53, on one CTA 51),
-// 8192 x 28672 x 8192, pairs, 2030 to 2070 (1.9 PFLOP/s, the fp16 rate under the power cap; 4096 x 8192
+// 8192 x 28672 x 8192, pairs, 1910 to 2070 (1.86 to 2.01 PFLOP/s, the fp16 rate under the power cap; 4096 x 8192
 // x 8192 288, 304 with sums handed back after their stores).
 //
 // Work: whole tiles, and the last, partial wave spread over all workers in K steps; the
