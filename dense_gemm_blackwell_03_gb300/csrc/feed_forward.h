@@ -88,6 +88,7 @@ struct LanesParams {
     int32_t activation;
     void* out[3];                // C; kLanesGated: H, G, U (G null: not kept)
     int64_t ldo[3];
+    int32_t turned;              // kLanesInt8: the lanes are A's rows, "X" is B: lanes are rows of C
     uint64_t timeout_ns;
     uint32_t* status;
     float* partials;

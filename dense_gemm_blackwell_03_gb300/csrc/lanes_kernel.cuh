@@ -2,7 +2,8 @@
 // on few rows of X, and the product of 8-bit integers at any size.
 //
 //   kLanesGated   H[m, n] = act(G) * U,  G = X Wg^T, U = X Wu^T      bf16 or fp16
-//   kLanesInt8    C[m, n] = sx[m] * sw[n] * sum_k X[m, k] * W[n, k]  8-bit integers
+//   kLanesInt8    C[m, n] = sx[m] * sw[n] * sum_k X[m, k] * W[n, k]  8-bit integers (turned: X
+//                 in the lanes and W in its place, where there are fewer of W's rows)
 //
 // The accumulator holds the result transposed: a TMEM lane per weight row, a column per
 // row of X (16 to 256), so that one to a few hundred tokens cost no more tensor time than
@@ -135,7 +136,9 @@ __device__ __forceinline__ uint16_t round16(float v, int dtype)
     return dtype == BWGEMM_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
 
-template <int MODE, int CG, int BN, bool WIDENS>
+// TURNED: p.turned of the pairs, whose epilogue is the longer the more it has of both ways out
+// (6978 x 3467 x 128 32 us, 37 with both in one kernel).
+template <int MODE, int CG, int BN, bool WIDENS, bool TURNED = false>
 __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1)
     lanes_kernel(const __grid_constant__ LanesMaps maps, const LanesParams p)
 {
@@ -152,6 +155,7 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
     const int worker = int(blockIdx.x) / CG;
     const int workers = int(gridDim.x) / CG;
     const int l_rows = p.l_rows;  // of this CTA
+    const bool turned = CG == 2 ? TURNED : p.turned != 0;
     const uint32_t sL = base + Cfg::kOffL;
     const uint32_t sX = base + Cfg::kOffX;
     const uint32_t bar_full = base + Cfg::kOffBar;              // X has landed, the weights (widened) are there
@@ -561,6 +565,60 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
             auto turn_in = [&](int j, uint16_t h) {
                 asm volatile("st.shared.u16 [%0], %1;" ::"r"(turn + uint32_t(j * 64 + 2 * lane)), "h"(h) : "memory");
             };
+            // Where p.turned, a lane is a row of the result: its columns c + 8 k .. to its place, or by
+            // way of shared memory for eight rows of 64 bytes at a time (pairs: 4096 x 4000 x 1024 33.6 us,
+            // 38.4 without; smaller tiles are 2 % slower so); and of 32 bits P columns
+            auto row_in = [&](int k, uint4 w) {
+                ptx::st_shared_v4(turn + uint32_t(lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)), w.x, w.y, w.z, w.w);
+            };
+            auto rows_out = [&](int c) {
+                __syncwarp();
+                const int piece = 8 * (lane & 3), left = p.crows - (m0 + c + piece);
+#pragma unroll
+                for (int r = lane >> 2; r < 32; r += 8) {
+                    uint4 w;
+                    ptx::ld_shared_v4(turn + uint32_t(r * 64 + (((lane ^ (r >> 1)) & 3) << 4)), w.x, w.y, w.z, w.w);
+                    if (row - lane + r >= l_rows || n - lane + r >= p.lrows)
+                        continue;
+                    uint16_t* at = static_cast<uint16_t*>(p.out[0]) + int64_t(n - lane + r) * p.ldo[0] + m0 + c + piece;
+                    if (left >= 8) {
+                        *reinterpret_cast<uint4*>(at) = w;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 7; ++k)
+                            if (k < left)
+                                at[k] = uint16_t((&w.x)[k / 2] >> (16 * (k % 2)));
+                    }
+                }
+                __syncwarp();
+            };
+            auto row_out = [&](int c, int k, uint4 w) {
+                const int left = live ? p.crows - (m0 + c + 8 * k) : 0;
+                uint16_t* at = static_cast<uint16_t*>(p.out[0]) + int64_t(n) * p.ldo[0] + m0 + c + 8 * k;
+                if (left >= 8) {
+                    *reinterpret_cast<uint4*>(at) = w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 7; ++i)
+                        if (i < left)
+                            at[i] = uint16_t((&w.x)[i / 2] >> (16 * (i % 2)));
+                }
+            };
+            auto row_out32 = [&](int c, const float(&f)[P]) {
+                const int left = live ? p.crows - (m0 + c) : 0;
+                float* dst = static_cast<float*>(p.out[0]) + int64_t(n) * p.ldo[0] + m0 + c;
+#pragma unroll
+                for (int j = 0; j < P; j += 4) {
+                    if (left >= j + 4) {
+                        *reinterpret_cast<float4*>(dst + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 3; ++k)
+                            if (j + k < left)
+                                dst[j + k] = f[j + k];
+                    }
+                }
+            };
             // P columns of finished sums (gated: of G, then of U) from column c of the warp's on
             auto finish = [&](int c, const float(&v)[MATS][P]) {
                 const int m = m0 + c, count = p.crows - m;
@@ -584,7 +642,27 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
                         return;
                     // (the sum times its token's scale) times its channel's: neither product
                     // leaves fp32's range where the result does not
-                    if (p.out_type == BWGEMM_FP32) {
+                    if (turned) {
+                        float r[P];
+#pragma unroll
+                        for (int j = 0; j < P; j += 4) {
+                            const float4 f = ptx::ld_shared_f32x4(scale_buf + 4 * (c + j));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                r[j + k] = v[0][j + k] * ls * (&f.x)[k];
+                        }
+                        if (p.out_type == BWGEMM_FP32) {
+                            row_out32(c, r);
+                        } else {
+                            uint32_t w[P / 2];
+#pragma unroll
+                            for (int j = 0; j < P / 2; ++j)
+                                w[j] = pack2(__float_as_uint(r[2 * j]), __float_as_uint(r[2 * j + 1]), p.out_type);
+#pragma unroll
+                            for (int k = 0; k < P / 8; ++k)
+                                row_out(c, k, make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+                        }
+                    } else if (p.out_type == BWGEMM_FP32) {
                         if (!live)
                             return;
                         float* dst = static_cast<float*>(p.out[0]) + int64_t(m) * p.ldo[0] + n;
@@ -638,18 +716,31 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
                             const float4 f = ptx::ld_shared_f32x4(scale_buf + 4 * (c + j));
 #pragma unroll
                             for (int k = 0; k < 4; k += 2)
-                                w[(c + j + k) / 2] = pack2(__float_as_uint(__uint_as_float(v[j + k]) * (&f.x)[k] * ls),
-                                                           __float_as_uint(__uint_as_float(v[j + k + 1]) * (&f.x)[k + 1] * ls), p.out_type);
+                            {  // a token's scale first
+                                const float a = turned ? ls : (&f.x)[k], a1 = turned ? ls : (&f.x)[k + 1];
+                                const float b = turned ? (&f.x)[k] : ls, b1 = turned ? (&f.x)[k + 1] : ls;
+                                w[(c + j + k) / 2] = pack2(__float_as_uint(__uint_as_float(v[j + k]) * a * b),
+                                                           __float_as_uint(__uint_as_float(v[j + k + 1]) * a1 * b1), p.out_type);
+                            }
                         }
                     }
 #pragma unroll
                     for (int c = 0; c < Cfg::kCols; c += P) {
                         if (m0 + c >= p.crows)
                             break;
+                        if (turned) {
 #pragma unroll
-                        for (int j = 0; j < P; ++j)
-                            turn_in(j, uint16_t(w[(c + j) / 2] >> (16 * (j % 2))));
-                        turn_out(c);
+                            for (int k = 0; k < P / 8; ++k) {
+                                const int i = c / 2 + 4 * k;
+                                row_in(k, make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]));
+                            }
+                            rows_out(c);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < P; ++j)
+                                turn_in(j, uint16_t(w[(c + j) / 2] >> (16 * (j % 2))));
+                            turn_out(c);
+                        }
                     }
                     continue;
                 }

@@ -5,11 +5,11 @@
 namespace bwgemm {
 namespace {
 
-template <int MODE, int CG, int BN, bool WIDENS = false>
+template <int MODE, int CG, int BN, bool WIDENS = false, bool TURNED = false>
 cudaError_t launch_one(const LanesMaps& maps, const LanesParams& p, int grid, cudaStream_t stream, bool pdl)
 {
     using Cfg = LanesConfig<MODE, CG, BN, WIDENS>;
-    auto kernel = lanes_kernel<MODE, CG, BN, WIDENS>;
+    auto kernel = lanes_kernel<MODE, CG, BN, WIDENS, TURNED>;
     if (grid % CG != 0)
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> allowed{0};
@@ -55,7 +55,9 @@ cudaError_t launch_lanes(int idx, const LanesMaps& maps, const LanesParams& p, i
     case 6: return launch_one<kLanesInt8, 1, 32>(maps, p, grid, stream, pdl);
     case 7: return launch_one<kLanesInt8, 1, 64>(maps, p, grid, stream, pdl);
     case 8: return launch_one<kLanesInt8, 1, 128>(maps, p, grid, stream, pdl);
-    case 9: return launch_one<kLanesInt8, 2, 256>(maps, p, grid, stream, pdl);
+    case 9:
+        return p.turned ? launch_one<kLanesInt8, 2, 256, false, true>(maps, p, grid, stream, pdl)
+                        : launch_one<kLanesInt8, 2, 256>(maps, p, grid, stream, pdl);
     default: return cudaErrorInvalidValue;
     }
 }

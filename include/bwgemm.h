@@ -679,7 +679,8 @@ bwgemm_status_t bwgemm_run_integer_workspace(int64_t M, int64_t N, int64_t K, ui
 /* How bwgemm_gated and bwgemm_run_integer divide a product (for inspection and tests). */
 typedef struct {
     int32_t lanes;    /* 0: X's rows fill the tiles' rows (bwgemm_gated); 1: the weights'  */
-                      /* rows do; 2: the kernel for at most 16 rows of X (no tiles)       */
+                      /* rows do; 2: the kernel for at most 16 rows of X (no tiles);      */
+                      /* 3: as 1, with A for the weights and B for X (bwgemm_run_integer) */
     int32_t tile_w;   /* weight rows per tile (bwgemm_gated: of each weight)              */
     int32_t tile_x;   /* rows of X per tile                                               */
     int32_t dp_tiles; /* tiles computed whole                                             */

@@ -123,4 +123,8 @@ def product_int8(a, sa, b, sb, dtype):
 def check(got, want, bound):
     assert got.shape == want.shape
     off = (got.double() - want).abs() - bound
+    if got.dtype == torch.float16:
+        # from 65520 on, the middle of the largest value 65504 and 2^16, fp16 rounds to infinity
+        infinite = got.isinf() & (got.double().sign() == want.sign()) & (want.abs() + bound >= 65520)
+        off = torch.where(infinite, torch.zeros_like(off), off)
     assert bool((off <= 0).all()), f"{int((~(off <= 0)).sum())} of {off.numel()} values past their bound, worst by {float(off.max()):.3g}"

@@ -107,6 +107,23 @@ def test_int8_pairs_whole_and_in_pieces(M, N, K):
             assert p.status() == 0, s
 
 
+@pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("cap", [0, 4, 152])
+@pytest.mark.parametrize("M,N,K", [(700, 33, 300), (300, 65, 5000), (1001, 131, 1001), (3000, 260, 700), (513, 400, 1300),
+                                   (3000, 1400, 1100)])
+def test_int8_with_more_rows_than_columns(M, N, K, cap, out):
+    # A's rows in the lanes: whole tiles and pieces, every width, odd ends
+    assert binding.select_int8(sms(), M, N, K, max_ctas=cap)["lanes"] == 3
+    (a, sa, b, sb), (want, bound) = int8_case(M, N, K, out, seed=cap)
+    hold = torch.full((M + 2, -(-N // 8) * 8 + 24), 7.0, dtype=T[out], device="cuda")
+    with binding.Plan(0, max_ctas=cap) as p:
+        p.gemm_int8(a, sa, b, sb, out=hold[1:M + 1, 8:8 + N])
+        assert p.status() == 0
+    check(hold[1:M + 1, 8:8 + N], want, bound)
+    hold[1:M + 1, 8:8 + N] = 7
+    assert bool((hold == 7).all())
+
+
 @pytest.mark.parametrize("cap", [1, 2, 7])
 def test_few_ctas_give_right_results(cap):
     with binding.Plan(0, max_ctas=cap) as p:

@@ -91,9 +91,10 @@ def test_integer_workspace(lib):
         assert workspace(lib, name, *sizes) == (0, 0)
     assert workspace(lib, name, 5, 5, -1)[0] == INVALID
     assert workspace(lib, name, 1 << 31, 5, 5)[0] == workspace(lib, name, (1 << 31) - 256, 1, (1 << 31) - 256)[0] == UNSUP
-    for M, N, K in ((33, 5, 5), (17, 28672, 8192), (4096, 1, 129)):  # A as fp16, rows padded to 128
+    # A as fp16, or B where it has far fewer rows, but more than 32; rows padded to 128
+    for M, N, K in ((33, 5, 5), (17, 28672, 8192), (4096, 1, 129), (4096, 33, 129), (300, 300, 300), (300, 299, 300)):
         rc, n = workspace(lib, name, M, N, K)
-        need = M * (-(-K // 128) * 128) * 2
+        need = (33 if N == 33 else M) * (-(-K // 128) * 128) * 2
         assert rc == 0 and need <= n < need + 256
 
 
@@ -130,7 +131,9 @@ def test_every_plan_covers_its_product_in_bounds(opts):
                 continue
             ctas = 2 if s["tile_x"] == 256 else 1
             assert s["tile_x"] in widths and s["tile_w"] % 8 == 0 and 8 <= s["tile_w"] <= most * ctas
-            tiles = cdiv(N, s["tile_w"]) * cdiv(M, s["tile_x"])
+            rows, cols = (M, N) if s["lanes"] == 3 else (N, M)
+            assert s["lanes"] == 1 or (s["lanes"] == 3 and select is binding.select_int8 and M > N > 32)
+            tiles = cdiv(rows, s["tile_w"]) * cdiv(cols, s["tile_x"])
             assert s["dp_tiles"] + s["sk_tiles"] == tiles
             assert 1 <= s["workers"] <= (min(76, cap // 2) if ctas == 2 else cap)
             if s["sk_tiles"]:
