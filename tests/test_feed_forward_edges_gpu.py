@@ -627,6 +627,30 @@ def test_weights_written_just_before_on_the_stream(plan, op):
                 check(t, v, e)
 
 
+@pytest.mark.parametrize("M,N,K", [(6000, 40, 2048), (4000, 600, 1024)])
+def test_tokens_written_just_before_in_the_lanes(plan, M, N, K):
+    # A's bytes are copied before the kernel that widens B has ended
+    assert binding.select_int8(sms(), M, N, K)["lanes"] == 3
+    b, sb = plan.quantize_int8(torch.randn(N, K, device="cuda"))
+    rest = torch.randn(M, K, device="cuda")
+    held = [plan.quantize_int8(rest * (i + 1)) for i in range(2)]
+    want = [plan.gemm_int8(q, s, b, sb) for q, s in held]
+    torch.cuda.synchronize()
+    got, flush = [], torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    a, sa = (torch.empty_like(t) for t in held[0])
+    for i in range(8):
+        x = rest * (i % 2 + 1)
+        flush.add_(1)
+        q, s = plan.quantize_int8(x)
+        got.append(plan.gemm_int8(q, s, b, sb))
+        a.copy_(held[i % 2][0])  # by a kernel that knows nothing of an early start
+        sa.copy_(held[i % 2][1])
+        got.append(plan.gemm_int8(a, sa, b, sb))
+    torch.cuda.synchronize()
+    for i, c in enumerate(got):
+        assert torch.equal(c, want[i // 2 % 2])
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("tokens", [1, 5, 70, 600])
 def test_a_feed_forward_block_served(plan, tokens):
