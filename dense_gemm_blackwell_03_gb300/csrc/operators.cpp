@@ -118,8 +118,8 @@ ScaledPlan plan_scaled(int num_sms, int64_t M, int64_t N, int64_t K, bool b_squa
                 continue;
             s.num_l = int(nl);
             s.num_c = int(nc);
-            // whole tiles, or whole tiles for the full waves and the rest in K
-            // iterations over all workers, at least four K blocks a piece
+            // whole tiles, or whole tiles for the full waves and the rest in K iterations
+            // over all workers; without a full wave over as many as have four K blocks each
             const int64_t full = tiles / W * W, rest = tiles - full;
             const uint64_t slot_bytes = uint64_t(128) * v.bn * 4;
             const bool room = kCounterRegionBytes + uint64_t(W) * 2 * slot_bytes <= workspace_bytes &&
@@ -134,6 +134,9 @@ ScaledPlan plan_scaled(int num_sms, int64_t M, int64_t N, int64_t K, bool b_squa
                     s.sk_tiles = int(rest);
                     s.sk_iters = int32_t(rest * kb);
                     s.workers = full == 0 ? std::max(std::min(W, s.sk_iters / 4), 1) : W;
+                    // the kernel adds the pieces of all workers from a tile's first to its last: each has one
+                    if (s.sk_iters < s.workers)
+                        continue;
                 }
                 const double us = block_us(v, s.l_rows);
                 double t = double((s.dp_tiles + s.workers - 1) / s.workers) * double(kb) * us;
