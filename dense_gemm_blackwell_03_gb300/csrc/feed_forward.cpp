@@ -177,14 +177,14 @@ LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N,
                 continue;
             s.num_l = int(nl);
             s.num_c = int(nc);
-            // whole tiles, or whole tiles for the full waves and the rest in K steps over all
-            // workers, at least four a piece
+            // whole tiles, or whole tiles for the full waves and the rest in K steps over all workers
             const int64_t full = tiles / W * W, rest = tiles - full;
             const uint64_t slot_bytes = uint64_t(lanes_partial_floats(mode, v.bn)) * 4 * v.cg;
             const bool room = kCounterRegionBytes + uint64_t(W) * 2 * slot_bytes <= workspace_bytes &&
                               uint64_t(rest) * v.cg * lanes_epi_warps(v.bn) * 4 <= kCounterRegionBytes;
-            // (spread: over all workers, or, where there is no full wave, over as many a tile as
-            // there are for each, or half as many: a worker then has one piece, not two)
+            // (spread: over all workers, or, where there is no full wave, over all that have four
+            // steps each, over as many a tile as there are for each, or half as many: a worker
+            // then has one piece, not two)
             for (int spread = 0; spread <= (rest > 0 && room && rest * kb < (1ll << 30) ? (full == 0 ? 3 : 1) : 0); ++spread) {
                 s.workers = int(std::min<int64_t>(tiles, W));
                 s.dp_tiles = int(tiles);
@@ -196,7 +196,8 @@ LanesPlan plan_lanes(int mode, int num_sms, int max_pairs, int64_t M, int64_t N,
                     s.workers = full == 0 ? std::max(std::min(W, s.sk_iters / 4), 1) : W;
                     if (spread > 1)
                         s.workers = int(std::max<int64_t>(s.workers / rest / (spread - 1), 1) * rest);
-                    if (s.workers > W)
+                    // the kernel adds the pieces of all workers from a tile's first to its last: each has one
+                    if (s.workers > W || s.sk_iters < s.workers)
                         continue;
                 }
                 const double us = lanes_step_us(v), whole = double((s.dp_tiles + s.workers - 1) / s.workers) * double(kb) * us;

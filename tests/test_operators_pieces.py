@@ -29,6 +29,17 @@ def test_every_worker_of_a_scaled_product_has_a_step(M):
             assert c["sk_tiles"] == 0 or c["workers"] <= c["sk_tiles"] * blocks(K), (cap, M, N, K)
 
 
+@pytest.mark.parametrize("select,rows", [(binding.select_gated, 64), (binding.select_int8, 128), (binding.select_int8, 256)])
+def test_every_worker_of_a_product_with_the_weights_in_the_lanes_has_a_step(select, rows):
+    # (with joins as dear as they are no plan comes near to it)
+    for cap in (2, 5, 20, 80, 152):
+        for more in {1, 2, cap // 2, cap - 1} - {0, cap}:
+            for M in (17, 64, 200):
+                for kb in range(1, cap // more + 2):
+                    c = select(152, M, rows * (cap + more), 128 * kb, max_ctas=cap)
+                    assert c["sk_tiles"] == 0 or c["workers"] <= c["sk_tiles"] * kb, (cap, more, M, kb)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("blocks_k", [-3, -1, 0])
 def test_a_scaled_product_takes_nothing_from_an_earlier_call(blocks_k):
