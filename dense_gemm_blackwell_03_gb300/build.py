@@ -25,7 +25,7 @@ SOURCES = ["gemm_sm103.cu", "skinny_sm103.cu", "wholek_sm103.cu", "api.cpp", "pl
            "gated_sm103.cu", "lanes_sm103.cu", "int8_sm103.cu", "few_rows_sm103.cu", "feed_forward.cpp"]
 HEADERS = ["ptx.cuh", "gemm_kernel.cuh", "skinny_kernel.cuh", "wholek_kernel.cuh", "kernel_params.h", "internal.h", "tuned_table.h",
            "plan.h", "operators.h", "scaled_kernel.cuh", "ortho_kernel.cuh", "pipeline.cuh", "operators_host.h", "feed_forward.h", "activation.cuh",
-           "pair_kernel.cuh", "lanes_kernel.cuh"]
+           "pair_kernel.cuh", "lanes_kernel.cuh", "int8_scales.cuh"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

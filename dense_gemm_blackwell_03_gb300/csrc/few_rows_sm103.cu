@@ -19,6 +19,7 @@
 #include "activation.cuh"
 #include "feed_forward.h"
 #include "gemm_kernel.cuh"
+#include "int8_scales.cuh"
 
 namespace bwgemm {
 namespace {
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 32 / kFewWarps) few_rows_kerne
         }
     };
     if constexpr (INT8) {
-        const float v = total(r) * p.cs[m] * p.ls[n];
+        const float v = scaled_sum(total(r), p.cs[m], p.ls[n]);
         const int64_t at = int64_t(m) * p.ldo[0] + n;
         if (p.out_type == BWGEMM_FP32)
             static_cast<float*>(p.out[0])[at] = v;

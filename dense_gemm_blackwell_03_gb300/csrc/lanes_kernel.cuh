@@ -53,6 +53,7 @@
 
 #include "activation.cuh"
 #include "feed_forward.h"
+#include "int8_scales.cuh"
 #include "scaled_kernel.cuh"
 
 namespace bwgemm {
@@ -530,12 +531,32 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
             const int m0 = seg.c_blk * BN + col;                        // its row of column 0
             const bool live = in_tile && n < p.lrows;
             const float ls = !GATED && live ? p.ls[n] : 0.f;
+            bool large = !GATED && turned && large_scale(ls);  // of the warp's tokens
             if constexpr (!GATED) {
-                for (int c = lane; c < Cfg::kCols; c += 32)
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(scale_buf + 4 * c), "f"(m0 + c < p.crows ? p.cs[m0 + c] : 0.f)
-                                 : "memory");
+                for (int c = lane; c < Cfg::kCols; c += 32) {
+                    const float f = m0 + c < p.crows ? p.cs[m0 + c] : 0.f;
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(scale_buf + 4 * c), "f"(f) : "memory");
+                    large = large || (!turned && large_scale(f));
+                }
+                large = __any_sync(0xffffffffu, large);
                 __syncwarp();
             }
+            // sums of P columns from c on, scaled
+            auto scale = [&](const float(&v)[P], int c, float(&r)[P]) {
+#pragma unroll
+                for (int j = 0; j < P; j += 4) {
+                    const float4 f = ptx::ld_shared_f32x4(scale_buf + 4 * (c + j));
+                    if (!large) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            r[j + k] = turned ? v[j + k] * ls * (&f.x)[k] : v[j + k] * (&f.x)[k] * ls;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            r[j + k] = scaled_sum(v[j + k], turned ? ls : (&f.x)[k], turned ? (&f.x)[k] : ls);
+                    }
+                }
+            };
             // P rows of X from column c on, 32 columns of the result each, in this warp's `turn`: out in
             // 16-byte pieces (4096 x 4096 x 1024 39 us, 45 with a store of 64 bytes for each row and warp)
             auto turn_out = [&](int c) {
@@ -640,17 +661,9 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
                 } else {
                     if (count <= 0)
                         return;
-                    // (the sum times its token's scale) times its channel's: neither product
-                    // leaves fp32's range where the result does not
+                    float r[P];
+                    scale(v[0], c, r);
                     if (turned) {
-                        float r[P];
-#pragma unroll
-                        for (int j = 0; j < P; j += 4) {
-                            const float4 f = ptx::ld_shared_f32x4(scale_buf + 4 * (c + j));
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                r[j + k] = v[0][j + k] * ls * (&f.x)[k];
-                        }
                         if (p.out_type == BWGEMM_FP32) {
                             row_out32(c, r);
                         } else {
@@ -667,21 +680,13 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
                             return;
                         float* dst = static_cast<float*>(p.out[0]) + int64_t(m) * p.ldo[0] + n;
 #pragma unroll
-                        for (int j = 0; j < P; j += 4) {
-                            const float4 f = ptx::ld_shared_f32x4(scale_buf + 4 * (c + j));
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (j + k < count)
-                                    dst[(j + k) * p.ldo[0]] = v[0][j + k] * (&f.x)[k] * ls;
-                        }
+                        for (int j = 0; j < P; ++j)
+                            if (j < count)
+                                dst[j * p.ldo[0]] = r[j];
                     } else {
 #pragma unroll
-                        for (int j = 0; j < P; j += 4) {
-                            const float4 f = ptx::ld_shared_f32x4(scale_buf + 4 * (c + j));
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                turn_in(j + k, round16(v[0][j + k] * (&f.x)[k] * ls, p.out_type));
-                        }
+                        for (int j = 0; j < P; ++j)
+                            turn_in(j, round16(r[j], p.out_type));
                         turn_out(c);
                     }
                 }
@@ -711,18 +716,14 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
                         ptx::tmem_ld_wait();
                         if (c + P >= Cfg::kCols)
                             hand_back<CG>(empty, lane);
+                        float f[P], r[P];
 #pragma unroll
-                        for (int j = 0; j < P; j += 4) {
-                            const float4 f = ptx::ld_shared_f32x4(scale_buf + 4 * (c + j));
+                        for (int j = 0; j < P; ++j)
+                            f[j] = __uint_as_float(v[j]);
+                        scale(f, c, r);
 #pragma unroll
-                            for (int k = 0; k < 4; k += 2)
-                            {  // a token's scale first
-                                const float a = turned ? ls : (&f.x)[k], a1 = turned ? ls : (&f.x)[k + 1];
-                                const float b = turned ? (&f.x)[k] : ls, b1 = turned ? (&f.x)[k + 1] : ls;
-                                w[(c + j + k) / 2] = pack2(__float_as_uint(__uint_as_float(v[j + k]) * a * b),
-                                                           __float_as_uint(__uint_as_float(v[j + k + 1]) * a1 * b1), p.out_type);
-                            }
-                        }
+                        for (int j = 0; j < P / 2; ++j)
+                            w[c / 2 + j] = pack2(__float_as_uint(r[2 * j]), __float_as_uint(r[2 * j + 1]), p.out_type);
                     }
 #pragma unroll
                     for (int c = 0; c < Cfg::kCols; c += P) {

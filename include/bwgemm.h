@@ -665,7 +665,8 @@ bwgemm_status_t bwgemm_quantize_integer(bwgemm_plan_t plan, const void* X, bwgem
  *
  * Sums are fp32: exact as long as none passes 2^24 in magnitude (K <= 1024 for any operands),
  * beyond that rounded as fp32 sums are.  The sum is multiplied with scale_a, then with
- * scale_b.  Everything else -- device memory, empty sizes (K == 0: C = 0), asynchrony, capture,
+ * scale_b (the other way round where scale_a is above 2^80 in magnitude), each product rounded to
+ * fp32: scales of any size give the results that are in range.  Everything else -- device memory, empty sizes (K == 0: C = 0), asynchrony, capture,
  * status after a timeout, the plan's workspace -- is as for bwgemm_run; sums are in a fixed
  * order for a shape.
  */
