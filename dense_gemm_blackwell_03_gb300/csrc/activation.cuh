@@ -2,8 +2,8 @@
 //
 // silu(g) = g s(g) and gelu_tanh(g) = g (1 + tanh z) / 2 = g s(2 z) with the logistic
 // function s(t) = 1 / (1 + exp(-t)) and z = sqrt(2 / pi) (g + 0.044715 g^3); gelu(g) = g Phi(g).
-// exp and the quotient are CUDA's fast ones, good to a few 2^-23 -- results are rounded
-// to 2^-9 or 2^-12 after them.
+// The quotient is CUDA's fast one, good to 2 ulp, and so is exp, whose error grows with its argument:
+// 2 + 1.2 |t| ulp, 2^-16 at the ends of its range -- results are rounded to 2^-9 or 2^-12 after them.
 #pragma once
 
 #include <cstdint>
@@ -12,10 +12,12 @@
 
 namespace bwgemm {
 
-// s(t); 0 and 1 at the ends: exp(-t) past fp32 is inf, and 1 / inf = 0.
+// s(t), as exp(t) / (1 + exp(t)) for t < 0: nothing overflows, and what is below fp32's normal
+// numbers (t < -87.3) is as coarse as they are; 0 from t = -104 on.
 __device__ __forceinline__ float logistic(float t)
 {
-    return __fdividef(1.f, 1.f + __expf(-t));
+    const float e = __expf(-fabsf(t));
+    return __fdividef(t < 0.f ? e : 1.f, 1.f + e);
 }
 
 constexpr float kGeluC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
