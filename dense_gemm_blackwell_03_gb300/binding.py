@@ -884,7 +884,8 @@ class Plan:
     def gemm_int8(self, A, scale_a, B, scale_b, out=None, out_dtype=None, stream=None):
         """``bwgemm_run_integer``: ``out = scale_a[:, None] * scale_b * (A @ B.T)`` of int8 CUDA tensors A
         (M x K) and B (N x K) with a scale per row, as `quantize_int8` returns them.  `out_dtype`:
-        bf16 (default), fp16 or fp32."""
+        bf16 (default), fp16 or fp32.  Sums of at most 16 rows of A are 32-bit integers at most sizes, all
+        others fp32, exact up to 2^24 (``bwgemm_run_integer`` has the sizes and the error past it)."""
         torch = _torch()
         if stream is not None:
             with torch.cuda.stream(stream):

@@ -13,8 +13,9 @@
 // lanes -- a thread has both G and U of its outputs.
 //
 // 8-bit integers: the tensor cores of sm_103a have none, but an fp16 holds every 8-bit
-// integer exactly, their products are exact in fp32 and so are sums up to 2^24 (longer
-// ones round as fp32 does).  So the weights travel as bytes -- HBM, L2 and shared memory --
+// integer exactly, their products are exact in fp32 and so are sums up to 2^24.  (Past it the
+// tensor cores cut off the last bits of what they add: 512 x 2048 x 131072, all 127, 5.1e-5 too
+// small.)  So the weights travel as bytes -- HBM, L2 and shared memory --
 // and become fp16 on the last stretch: four warps take a row each into registers, widen
 // it (xor 0x80 makes u = x + 128, a byte permutation 0x6400 | u = 1024 + u, one
 // subtraction 1024 + u - 1152 = x, all exact) and store it to TMEM, from where the MMA

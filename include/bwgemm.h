@@ -663,12 +663,17 @@ bwgemm_status_t bwgemm_quantize_integer(bwgemm_plan_t plan, const void* X, bwgem
  *       bytes (else BWGEMM_ERR_WORKSPACE; NULL where that is 0, as for M <= 16), holding
  *       nothing of use before or after
  *
- * Sums are fp32: exact as long as none passes 2^24 in magnitude (K <= 1024 for any operands),
- * beyond that rounded as fp32 sums are.  The sum is multiplied with scale_a, then with
- * scale_b (the other way round where scale_a is above 2^80 in magnitude), each product rounded to
- * fp32: scales of any size give the results that are in range.  Everything else -- device memory, empty sizes (K == 0: C = 0), asynchrony, capture,
- * status after a timeout, the plan's workspace -- is as for bwgemm_run; sums are in a fixed
- * order for a shape.
+ * Sums of few rows of A (M <= 2; M <= 8 where N K <= 10^8, M <= 16 where N K <= 2 10^7; K <= 131071
+ * for all) are 32-bit integers, exact, rounded to fp32 once.  All others are the tensor cores' fp32:
+ * exact as long as no sum of a part of the products passes 2^24 in magnitude (K <= 1024 for any
+ * operands); past it the last bits of what is added are cut off, not rounded, up to K 2^-24 of the
+ * sum of magnitudes (all values 127: 3.0e-5 too small at K = 8192, 5.1e-5 at 131072).  A row's
+ * result can so differ between a small batch and a larger one.
+ *
+ * The sum is multiplied with scale_a, then with scale_b (the other way round where scale_a is above
+ * 2^80 in magnitude), each product rounded to fp32: scales of any size give what is in range.
+ * Everything else -- device memory, empty sizes (K == 0: C = 0), asynchrony, capture, status after a
+ * timeout, the plan's workspace -- is as for bwgemm_run; sums are in a fixed order for a shape.
  */
 bwgemm_status_t bwgemm_run_integer(bwgemm_plan_t plan, const int8_t* A, const float* scale_a, const int8_t* B,
                                 const float* scale_b, void* C, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb,
