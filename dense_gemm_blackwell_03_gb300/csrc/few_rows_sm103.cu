@@ -14,8 +14,8 @@
 // A CTA takes 16 weight rows, its eight warps the blocks of their K in turn, kFewRing blocks
 // in flight each (asynchronous copies that every lane makes and reads for itself: nobody
 // waits for anybody), and their sums meet in shared memory in warp order.  Measured at one
-// row: integers 8192 x 8192 12.5 us (5.4 TB/s), 28672 x 8192 36.9 (6.4 TB/s); gated 10240 x 8192
-// 50.2 (6.7 TB/s, 98 % of the copy rate).  Rings of four blocks: 15.9 us on 8192 x 8192.
+// row: integers 8192 x 8192 12.5 to 12.9 us (5.3 TB/s), 28672 x 8192 36.9 (6.4 TB/s); gated 10240 x 8192
+// 50 to 52 (6.6 TB/s, 95 to 98 % of the copy rate).  Rings of four blocks: 15.9 us on 8192 x 8192.
 #include "activation.cuh"
 #include "feed_forward.h"
 #include "gemm_kernel.cuh"

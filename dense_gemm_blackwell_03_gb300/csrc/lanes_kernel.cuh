@@ -23,7 +23,7 @@
 // (launch_widen) or, of up to 32 rows a tile (WIDENS), by a warp for every eight rows from one
 // part of shared memory to another: no second launch (4 us of GPU and of host time each) and no
 // workspace, but more work a step.  32 x 28672 x 8192 44.2 us, 43.1 when widened before; 48 x
-// 8192 x 8192 23.8 and 23.9; 333 x 1000 x 5005 16.1 (18.2 with two warps).  At 16 rows four warps
+// 8192 x 8192 22.2, 23.9 when widened before; 333 x 1000 x 5005 14.9 (18.2 with two warps).  At 16 rows four warps
 // instead of two lose 5 %.
 //
 //   warp 0      TMA producer of the weights' ring (gated: of X's rows too)
@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(LanesConfig<MODE, CG, BN, WIDENS>::kThreads, 1
             if constexpr (Cfg::kBufs == 1) {
                 if (seg.whole && p.out_type != BWGEMM_FP32) {
                     // one buffer of sums: rounded and packed in registers, and handed back before they
-                    // go out (32 us)
+                    // go out (4096 x 4096 x 1024 33 us; 39 with the buffer handed back after its stores)
                     uint32_t w[Cfg::kCols / 2];
 #pragma unroll
                     for (int c = 0; c < Cfg::kCols; c += P) {

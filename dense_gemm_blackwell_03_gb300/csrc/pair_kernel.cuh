@@ -22,7 +22,7 @@
 //
 // What bounds it: the MMAs, 1024 cycles per 128 of K of a 256 x 256 tile; the epilogue
 // of a tile (other TMEM buffer) overlaps the next tile's.  Measured: gated 8192 x 28672 x 8192
-// 4340 to 4470 us (1.72 to 1.77 PFLOP/s, the sustained rate under the power cap), tensor pipe 88 %
+// 4220 to 4470 us (1.72 to 1.82 PFLOP/s, the sustained rate under the power cap), tensor pipe 88 %
 // active on 4096 x 8192 x 2048; gradients of 4096 x 28672 x 8192 4530 to 4820 us with the pass
 // that makes dG and dU (1.60 to 1.70), tensor pipe 87 % active on 2048 x 4096 x 2048.  Each stage of
 // the ring holds 128 of K of both operands (64 KiB per CTA), one 32 KiB copy each where the box lies

@@ -11,6 +11,8 @@ Each tensor is read once by ``quantize``, which writes both directions (the colu
 only where a gradient reads them).
 ``gated_linear(x, w_gate, w_up)`` is the gated layer ``act(x @ w_gate.T) * (x @ w_up.T)``
 in 16 bits, with its gradients by ``gated_linear_backward``.
+A training step may be captured into a CUDA graph; no autograd graph of the same weights
+from outside the capture may live meanwhile, as autograd would leave the capturing stream for theirs.
 ``OrthogonalMomentum`` updates the weights with ``orthogonalize`` of their
 momentum.  ``python -m dense_gemm_blackwell_03_gb300.linear_training`` fits a
 small two-layer network to a teacher and prints the loss; with ``--gated`` its
