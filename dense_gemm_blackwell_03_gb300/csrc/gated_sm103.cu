@@ -1,5 +1,7 @@
 // gated_sm103.cu -- the gated feed-forward layer's large products (pair_kernel.cuh), and
 // the gradients of its two projections.
+#include <cfloat>
+
 #include "pair_kernel.cuh"
 
 namespace bwgemm {
@@ -64,6 +66,16 @@ __device__ __forceinline__ float2 unpack16(uint32_t w, int dtype)
                                 : __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// dH U act'(G).  A slope can be tiny, so where dH U leaves fp32's range the larger of the two
+// meets the slope first.
+__device__ __forceinline__ float gate_grad(float dh, float u, float slope)
+{
+    const float p = dh * u;
+    if (__builtin_expect(fabsf(p) <= FLT_MAX, 1))
+        return p * slope;
+    return fabsf(dh) > fabsf(u) ? dh * slope * u : u * slope * dh;
+}
+
 __global__ void __launch_bounds__(kGradThreads) gate_grad_kernel(const GateGradParams p)
 {
     ptx::grid_dependency_wait();
@@ -108,7 +120,8 @@ __global__ void __launch_bounds__(kGradThreads) gate_grad_kernel(const GateGradP
                 float2 value, slope;
                 activate_slope(fg.x, p.activation, value.x, slope.x);
                 activate_slope(fg.y, p.activation, value.y, slope.y);
-                (&dg.x)[k] = pack2(__float_as_uint(fh.x * fu.x * slope.x), __float_as_uint(fh.y * fu.y * slope.y), p.dtype);
+                (&dg.x)[k] = pack2(__float_as_uint(gate_grad(fh.x, fu.x, slope.x)),
+                                   __float_as_uint(gate_grad(fh.y, fu.y, slope.y)), p.dtype);
                 (&du.x)[k] = pack2(__float_as_uint(fh.x * value.x), __float_as_uint(fh.y * value.y), p.dtype);
             }
             // the workspace's rows are whole pieces: what lies past the end is not read as a value

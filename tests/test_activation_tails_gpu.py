@@ -85,3 +85,26 @@ def test_small_slopes_times_a_large_gradient(plan, act, M):
         check(got[:, 3], want, bound + 2.0 ** -8 * (want.abs() + bound))
         assert not got[:, :3].any() and not got[:, 4:].any()
         assert int((want.abs() > 100 * bound).sum()) > N // 2
+
+
+@pytest.mark.parametrize("swap", [False, True])
+@pytest.mark.parametrize("act", sorted(POINTS))
+def test_a_gradient_and_a_factor_whose_product_passes_fp32(plan, act, swap):
+    # dH U is 2^150, the slope brings dH U act'(G) back
+    points = {"silu": torch.arange(-100.0, -30.0, 0.5), "gelu_tanh": -torch.arange(6.0, 10.0, 0.0625), "gelu": -torch.arange(7.0, 13.0, 0.125)}
+    g = points[act].bfloat16().cuda()
+    N = len(g)
+    g = torch.cat([g, torch.full((-N % 8,), -300.0, dtype=torch.bfloat16, device="cuda")])[None]
+    dh, up = torch.full_like(g, 2.0 ** (50 if swap else 100)), torch.full_like(g, 2.0 ** (100 if swap else 50))
+    x = torch.zeros(1, 16, dtype=torch.bfloat16, device="cuda")
+    x[:, 3] = 1
+    _, dwg, _ = plan.gated_linear_backward(dh, g, up, x, None, None, act, input_grad=False)
+    _, slope, _, es = tail(act, g[0].double())
+    want, bound = slope * 2.0 ** 150, es * 2.0 ** 150
+    bound = bound + 2.0 ** -8 * (want.abs() + bound)
+    far = want.abs() - bound >= 3.3961775292304e38
+    assert int(far.sum()) < N // 2 and bool(dwg[:, 3][far].isinf().all())
+    near = ~far & (want.abs() + bound >= 3.38e38)
+    fine = ~far & ~near
+    check(dwg[:, 3][fine], want[fine], bound[fine])
+    assert not dwg[:, 3].isnan().any() and not dwg[N:].any()
